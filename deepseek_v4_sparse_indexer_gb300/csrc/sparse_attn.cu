@@ -992,67 +992,42 @@ __global__ void __launch_bounds__(attn_threads(GW), 1) sparse_attn_kernel(const 
     }
 }
 
-constexpr int kMergeMaxPieces = 128;   // one per thread of the merge block; a unit has at most kMaxTopK / 64 + 2 tiles
-static_assert((kMaxTopK + TR - 1) / TR + (kNSwa + TR - 1) / TR <= kMergeMaxPieces, "merge: one thread per piece");
+constexpr int kMergeThreads = 128;     // one block per (unit, head): four dims a thread
 
-// Combines the pieces of the remainder units that straddle a share boundary.
-// Block (v, h): head h of remainder unit v, whose tiles [v nt, (v+1) nt) of the
-// remainder tile space lie in the shares of CTAs c0 .. c1 (share c: tiles
-// [c T / g, (c+1) T / g)); a unit inside one share was written directly.
-// O = sum_k 2^(m_k - M) O_k / sum_k 2^(m_k - M) l_k, lse = (M + log2 L) ln 2.
-__global__ void __launch_bounds__(128) attn_merge_kernel(const __grid_constant__ AttnArgs a, int nt, int g_rem, int G) {
-    pdl_launch_dependents();
-    pdl_wait();
-    const int v = blockIdx.x / kNHead;
-    const int h = blockIdx.x - v * kNHead;
-    const long long u_rem0 = static_cast<long long>(a.units / G) * G;
-    const long long T = (a.units - u_rem0) * nt;
-    const long long vs = static_cast<long long>(v) * nt, ve = vs + nt;
-    auto share_of = [&](long long x) -> int { return static_cast<int>(((x + 1) * g_rem - 1) / T); };
-    const int c0 = share_of(vs), c1 = share_of(ve - 1);
-    if (c0 == c1) return;                                   // whole inside one share
-    const float *wo = static_cast<const float *>(a.ws);
-    const float *ml = wo + 2LL * G * kNHead * kHeadDim;    // (m, l) after the 2 G O slots
-    // Share c0 holds the unit's start: its first piece (slot 0) when the share
-    // starts exactly there, else its last (slot 1); later shares: their first.
-    auto piece_slot = [&](int c) -> long long {
-        return c == c0 ? 2LL * c + (static_cast<long long>(c) * T / g_rem == vs ? 0 : 1) : 2LL * c;
-    };
+// Combines one head's pieces of a unit: O = sum_k 2^(m_k - M) O_k / L with
+// L = sum_k 2^(m_k - M) l_k; also returns M and L (0 when every piece is
+// empty).  Piece i's partial is slot(i) of the workspace; np <= kMaxAttnCtas.
+// One round trip for the first kEarly pieces: threads load the (m, l) pairs and
+// every thread its four dims of those pieces' O rows, all in flight together;
+// pieces past kEarly then load eight at a time.  The sums run in piece order,
+// as a sequential loop would.
+template <typename Slot>
+DS4A_DEV float4 merge_pieces(const float *wo, const float *ml, int h, int np, Slot slot, float &M, float &L) {
     const float NEG_INF = -__int_as_float(0x7f800000);
-    // One round trip for the first kEarly pieces: thread i < np loads piece
-    // i's (m, l) and every thread its four dims of those pieces' O rows, all in
-    // flight together; pieces past kEarly (top_k > 896) then load eight at a
-    // time.  The sums run in piece order, as a sequential loop would.
     constexpr int kEarly = 16;
-    __shared__ float s_w[kMergeMaxPieces], s_l[kMergeMaxPieces];
-    __shared__ float s_max[4];
-    const int np = c1 - c0 + 1;                              // <= tiles per unit <= kMergeMaxPieces
+    __shared__ float s_w[kMaxAttnCtas], s_l[kMaxAttnCtas];
+    __shared__ float s_max[kMergeThreads / 32];
     const int d = threadIdx.x * 4;
     float4 oe[kEarly];
 #pragma unroll
     for (int j = 0; j < kEarly; ++j)
-        oe[j] = j < np ? *reinterpret_cast<const float4 *>(wo + (piece_slot(c0 + j) * kNHead + h) * kHeadDim + d)
+        oe[j] = j < np ? *reinterpret_cast<const float4 *>(wo + (slot(j) * kNHead + h) * kHeadDim + d)
                        : make_float4(0.f, 0.f, 0.f, 0.f);
-    float mk = NEG_INF, lk = 0.f;
-    if (threadIdx.x < np) {
-        const float2 p = *reinterpret_cast<const float2 *>(ml + (piece_slot(c0 + threadIdx.x) * kNHead + h) * 2);
-        if (p.y > 0.f) {
-            mk = p.x;
-            lk = p.y;
-        }
+    float m = NEG_INF;
+    for (int i = threadIdx.x; i < np; i += kMergeThreads) {
+        const float2 p = *reinterpret_cast<const float2 *>(ml + (slot(i) * kNHead + h) * 2);
+        s_w[i] = p.y > 0.f ? p.x : NEG_INF;
+        s_l[i] = p.y > 0.f ? p.y : 0.f;
+        m = fmaxf(m, s_w[i]);
     }
-    float M = mk;
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-    if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = M;
+    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+    if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = m;
     __syncthreads();
     M = fmaxf(fmaxf(s_max[0], s_max[1]), fmaxf(s_max[2], s_max[3]));
-    if (threadIdx.x < np) {
-        s_w[threadIdx.x] = mk == NEG_INF ? 0.f : exp2f(mk - M);
-        s_l[threadIdx.x] = lk;
-    }
+    for (int i = threadIdx.x; i < np; i += kMergeThreads) s_w[i] = s_w[i] == NEG_INF ? 0.f : exp2f(s_w[i] - M);
     __syncthreads();
-    float L = 0.f;
+    L = 0.f;
     for (int i = 0; i < np; ++i) L += s_w[i] * s_l[i];
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -1069,9 +1044,8 @@ __global__ void __launch_bounds__(128) attn_merge_kernel(const __grid_constant__
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const int i = i0 + j;
-            o[j] = (i < np && s_w[i] != 0.f)
-                       ? *reinterpret_cast<const float4 *>(wo + (piece_slot(c0 + i) * kNHead + h) * kHeadDim + d)
-                       : make_float4(0.f, 0.f, 0.f, 0.f);
+            o[j] = (i < np && s_w[i] != 0.f) ? *reinterpret_cast<const float4 *>(wo + (slot(i) * kNHead + h) * kHeadDim + d)
+                                             : make_float4(0.f, 0.f, 0.f, 0.f);
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -1089,10 +1063,41 @@ __global__ void __launch_bounds__(128) attn_merge_kernel(const __grid_constant__
     acc.y *= inv;
     acc.z *= inv;
     acc.w *= inv;
+    return acc;
+}
+DS4A_DEV float merged_lse(float M, float L) {
+    return L > 0.f ? (M + log2f(L)) * 0.6931471805599453f : -__int_as_float(0x7f800000);
+}
+
+// Combines the pieces of the remainder units that straddle a share boundary.
+// Block (v, h): head h of remainder unit v, whose tiles [v nt, (v+1) nt) of the
+// remainder tile space lie in the shares of CTAs c0 .. c1 (share c: tiles
+// [c T / g, (c+1) T / g)); a unit inside one share was written directly.
+__global__ void __launch_bounds__(kMergeThreads) attn_merge_kernel(const __grid_constant__ AttnArgs a, int nt, int g_rem,
+                                                                   int G) {
+    pdl_launch_dependents();
+    pdl_wait();
+    const int v = blockIdx.x / kNHead;
+    const int h = blockIdx.x - v * kNHead;
+    const long long u_rem0 = static_cast<long long>(a.units / G) * G;
+    const long long T = (a.units - u_rem0) * nt;
+    const long long vs = static_cast<long long>(v) * nt, ve = vs + nt;
+    auto share_of = [&](long long x) -> int { return static_cast<int>(((x + 1) * g_rem - 1) / T); };
+    const int c0 = share_of(vs), c1 = share_of(ve - 1);
+    if (c0 == c1) return;                                   // whole inside one share
+    const float *wo = static_cast<const float *>(a.ws);
+    const float *ml = wo + 2LL * G * kNHead * kHeadDim;    // (m, l) after the 2 G O slots
+    // Share c0 holds the unit's start: its first piece (slot 0) when the share
+    // starts exactly there, else its last (slot 1); later shares: their first.
+    auto piece_slot = [&](int i) -> long long {
+        const int c = c0 + i;
+        return i == 0 ? 2LL * c + (static_cast<long long>(c) * T / g_rem == vs ? 0 : 1) : 2LL * c;
+    };
+    float M, L;
+    const float4 acc = merge_pieces(wo, ml, h, c1 - c0 + 1, piece_slot, M, L);
     const long long u = u_rem0 + v;
-    *reinterpret_cast<float4 *>(a.out + (u * kNHead + h) * kHeadDim + d) = acc;
-    if (a.lse && threadIdx.x == 0)
-        a.lse[u * kNHead + h] = L > 0.f ? (M + log2f(L)) * 0.6931471805599453f : NEG_INF;
+    *reinterpret_cast<float4 *>(a.out + (u * kNHead + h) * kHeadDim + threadIdx.x * 4) = acc;
+    if (a.lse && threadIdx.x == 0) a.lse[u * kNHead + h] = merged_lse(M, L);
 }
 
 // Tiles per unit in the tile space: the top_k compressed rows and the raw window.
@@ -1126,7 +1131,7 @@ cudaError_t launch_sparse_attn(const AttnArgs &a, int num_sms, cudaStream_t s) {
     const int g_rem = static_cast<int>(t_rem < G ? t_rem : G);
     e = launch_k(kern, dim3(static_cast<unsigned>(G)), dim3(attn_threads(gw)), kSmemBytes, s, a, nt, g_rem);
     if (e != cudaSuccess || g_rem <= 1) return e;
-    return launch_k(attn_merge_kernel, dim3(static_cast<unsigned>(u_rem * kNHead)), dim3(128), 0, s, a, nt, g_rem,
+    return launch_k(attn_merge_kernel, dim3(static_cast<unsigned>(u_rem * kNHead)), dim3(kMergeThreads), 0, s, a, nt, g_rem,
                     static_cast<int>(G));
 }
 
