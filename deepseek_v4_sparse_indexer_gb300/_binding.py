@@ -28,7 +28,11 @@ DS4A_OP_SPARSE_ATTN_DECODE = 2
 DS4A_OP_SPARSE_ATTN_PREFILL = 3
 DS4A_OP_DENSE_ATTN_DECODE = 4
 DS4A_OP_INDEXER_TOPK = 5
+DS4A_OP_PAGED_ATTN_DECODE = 6
 DS4A_OP_FLAG_128_HEADS = 0x100
+DS4A_BF16, DS4A_F16, DS4A_F32, DS4A_E4M3 = 0, 1, 2, 3
+DS4A_ROPE_NEIGHBOURS, DS4A_ROPE_HALVES = 0, 1
+DS4A_MIN_PAGE, DS4A_MAX_PAGE, DS4A_MAX_PLAN_SEQS = 8, 4096, 16384
 
 N_HEAD, HEAD_DIM, N_IDX_HEAD, IDX_DIM, N_SWA = 64, 512, 64, 128, 128
 
@@ -38,7 +42,8 @@ EXPORTS = ("ds4a_strerror", "ds4a_version", "ds4a_workspace_bytes", "ds4a_get_de
            "ds4a_topk_select_noalloc", "ds4a_sparse_attn_decode", "ds4a_sparse_attn_prefill",
            "ds4a_dense_attn_decode", "ds4a_kv_push_raw", "ds4a_compressor_pool",
            "ds4a_sparse_attn_decode_heads", "ds4a_sparse_attn_prefill_heads", "ds4a_dense_attn_decode_heads",
-           "ds4a_rows_to_fp8", "ds4a_sparse_attn_decode_fp8", "ds4a_sparse_attn_prefill_fp8", "ds4a_indexer_topk")
+           "ds4a_rows_to_fp8", "ds4a_sparse_attn_decode_fp8", "ds4a_sparse_attn_prefill_fp8", "ds4a_indexer_topk",
+           "ds4a_paged_plan", "ds4a_qk_norm_rope", "ds4a_paged_attn_decode")
 DS4A_TOPK_NOALLOC_SCRATCH_BYTES = 8 << 20
 DS4A_MAX_TOP_K = 2048
 
@@ -115,6 +120,15 @@ def load(build_if_missing: bool = True):
     L.ds4a_sparse_attn_prefill_fp8.argtypes = [_vp, _vp, _vp, _vp, _i32, _vp, _vp, _i32, _vp, _i32, _i32, _f32, _vp,
                                                _vp, _i32, _vp, _sz, _vp]
     L.ds4a_sparse_attn_prefill_fp8.restype = _i32
+    L.ds4a_paged_plan.argtypes = [_vp, _vp, _i32, _i32, _i32, _vp, _i32, _vp, _vp, _vp, _i64, _i32, _vp, _vp, _vp, _vp,
+                                  _vp, _vp, _vp, _i32, _vp, _vp, _i32, _vp]
+    L.ds4a_paged_plan.restype = _i32
+    L.ds4a_qk_norm_rope.argtypes = [_vp, _i32, _i64, _vp, _i32, _i64, _vp, _vp, _i32, _i32, _f32, _vp, _vp, _vp, _vp,
+                                    _i32, _vp, _vp, _i64, _i32, _i32, _i32, _vp]
+    L.ds4a_qk_norm_rope.restype = _i32
+    L.ds4a_paged_attn_decode.argtypes = [_i32, _vp, _vp, _i32, _vp, _i32, _i32, _vp, _i64, _i32, _vp, _vp, _vp, _i32,
+                                         _vp, _i32, _vp, _vp, _f32, _vp, _vp, _i32, _vp, _sz, _vp]
+    L.ds4a_paged_attn_decode.restype = _i32
     _lib = L
     return L
 
@@ -497,3 +511,172 @@ def ds4a_sparse_attn_prefill_fp8(q, q_pos, rows8, row_scale, idx, count, raw, ra
                                              ws.numel() * ws.element_size() if ws is not None else 0,
                                              _stream(stream))
     _check(st, "ds4a_sparse_attn_prefill_fp8")
+
+
+# ----------------------------------------------------------------------------
+# Paged caches
+# ----------------------------------------------------------------------------
+
+_TYPES = {torch.bfloat16: DS4A_BF16, torch.float16: DS4A_F16, torch.float32: DS4A_F32, torch.uint8: DS4A_E4M3}
+
+
+def _req_ints(device, **tensors):
+    """Each tensor is contiguous int32 on `device`; (tensor, shape) also checks the shape."""
+    for name, (t, shape) in tensors.items():
+        if t.dtype != torch.int32 or t.device != device or not t.is_contiguous():
+            raise ValueError(f"{name}: must be a contiguous int32 tensor on {device}")
+        if t.shape != shape:
+            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+def _req_table(table, U, device):
+    if table.dtype != torch.int32 or table.device != device or table.dim() != 2 or table.shape[0] != U \
+            or table.shape[1] < 1 or (table.shape[1] > 1 and table.stride(1) != 1):
+        raise ValueError(f"table: int32 [{U}, max_pages] on {device}, entries of a row contiguous")
+    return table.stride(0) if U > 1 else table.shape[1]
+
+
+def _device_of(t, name):
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a CUDA tensor")
+    return t.device
+
+
+def _launch(device, stream, name, *args):
+    """Calls entry point `name` with the tensors' device current and a stream of that device."""
+    f = getattr(load(), name)
+    if device.index == torch.cuda.current_device():
+        st = f(*args, _stream(stream))
+    else:
+        with torch.cuda.device(device):
+            st = f(*args, _stream(stream))
+    _check(st, name)
+
+
+def ds4a_paged_plan(past, add, ratio, page_size, free_pages, free_head, table, n_rows, n_raw, cu_tok, cu_row, tok_pos,
+                    raw_slot, row_pos, row_slot, free_head_out, ring=None, stream=None):
+    """Block tables and slot maps of one step from the request lengths, all int32:
+    past, add [B]; free_pages [n_free], free_head [1]; table [B, max_pages]
+    (updated); n_rows, n_raw [B], cu_tok, cu_row [B + 1], tok_pos, raw_slot
+    [T_cap], row_pos, row_slot [R_cap] and free_head_out [1] (written; may be
+    free_head); ring [B] or None."""
+    dev = _device_of(past, "past")
+    B = past.numel()
+    T, R, n_free = tok_pos.numel(), row_pos.numel(), free_pages.numel()
+    _req_ints(dev, past=(past, (B,)), add=(add, (B,)), free_pages=(free_pages, (n_free,)), free_head=(free_head, (1,)),
+              free_head_out=(free_head_out, (1,)), n_rows=(n_rows, (B,)), n_raw=(n_raw, (B,)),
+              cu_tok=(cu_tok, (B + 1,)), cu_row=(cu_row, (B + 1,)), tok_pos=(tok_pos, (T,)), raw_slot=(raw_slot, (T,)),
+              row_pos=(row_pos, (R,)), row_slot=(row_slot, (R,)))
+    if ring is not None:
+        _req_ints(dev, ring=(ring, (B,)))
+    stride = _req_table(table, B, dev)
+    _launch(dev, stream, "ds4a_paged_plan", past.data_ptr(), add.data_ptr(), B, ratio, page_size, free_pages.data_ptr(),
+            n_free, free_head.data_ptr(), free_head_out.data_ptr(), table.data_ptr(), stride, table.shape[1],
+            None if ring is None else ring.data_ptr(), n_rows.data_ptr(), n_raw.data_ptr(), cu_tok.data_ptr(),
+            cu_row.data_ptr(), tok_pos.data_ptr(), raw_slot.data_ptr(), T, row_pos.data_ptr(), row_slot.data_ptr(), R)
+
+
+def ds4a_qk_norm_rope(q, k, pos, inv_freq, eps, q_weight, k_weight, q_out, k_out, k_slot=None, k_scale=None,
+                      style=DS4A_ROPE_NEIGHBOURS, stream=None):
+    """RMS norm and tail rotation of q [T,H,D] and of the key rows k [T,D] (bf16,
+    fp16 or fp32; heads contiguous, any token stride; either may be None), D =
+    512 or 128.  pos i32 [T] (negative: padding, nothing written); inv_freq f64
+    [n_rot / 2]; q_weight, k_weight f32 [D] or None; q_out bf16 [T,H,D]
+    (written); k_out [rows,D] bf16, fp16 or uint8 E4M3 codes with k_scale f32
+    [rows] (row k_slot[t] written; k_slot i32 [T], None: row t)."""
+    x = q if q is not None else k
+    if x is None:
+        raise ValueError("q and k: at least one is needed")
+    dev = _device_of(x, "q" if q is not None else "k")
+    T, D = pos.numel(), x.shape[-1]
+    H = q_type = k_type = k_out_type = q_stride = k_stride = k_rows = 0
+    if pos.dtype != torch.int32 or pos.device != dev or not pos.is_contiguous() or pos.dim() != 1:
+        raise ValueError("pos: contiguous int32 [T]")
+    if inv_freq.dtype != torch.float64 or inv_freq.device != dev or not inv_freq.is_contiguous() or inv_freq.dim() != 1:
+        raise ValueError("inv_freq: contiguous float64 [n_rot / 2]")
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None and (w.dtype != torch.float32 or w.device != dev or not w.is_contiguous() or w.shape != (D,)):
+            raise ValueError(f"{name}: contiguous float32 [{D}]")
+    if q is not None:
+        q_type = _TYPES.get(q.dtype, -1)
+        if not DS4A_BF16 <= q_type <= DS4A_F32 or q.device != dev or q.dim() != 3 or q.shape[0] != T or q.stride(2) != 1 \
+                or (q.shape[1] > 1 and q.stride(1) != D):
+            raise ValueError("q: bf16, fp16 or fp32 [T, H, D] with contiguous heads")
+        H = q.shape[1]
+        q_stride = q.stride(0) if T > 1 else H * D
+        if q_out is None or q_out.dtype != torch.bfloat16 or q_out.device != dev or not q_out.is_contiguous() \
+                or q_out.shape != q.shape:
+            raise ValueError("q_out: contiguous bf16 [T, H, D]")
+    if k is not None:
+        k_type = _TYPES.get(k.dtype, -1)
+        if not DS4A_BF16 <= k_type <= DS4A_F32 or k.device != dev or k.shape != (T, D) or k.stride(1) != 1:
+            raise ValueError("k: bf16, fp16 or fp32 [T, D] with contiguous rows")
+        k_stride = k.stride(0) if T > 1 else D
+        k_out_type = _TYPES.get(None if k_out is None else k_out.dtype, -1)
+        if k_out_type not in (DS4A_BF16, DS4A_F16, DS4A_E4M3) or k_out.device != dev or not k_out.is_contiguous() \
+                or k_out.dim() != 2 or k_out.shape[1] != D:
+            raise ValueError("k_out: contiguous bf16, fp16 or uint8 [rows, D]")
+        k_rows = k_out.shape[0]
+        if k_out_type == DS4A_E4M3 and (k_scale is None or k_scale.dtype != torch.float32 or k_scale.device != dev
+                                        or not k_scale.is_contiguous() or k_scale.shape != (k_rows,)):
+            raise ValueError("k_scale: contiguous float32 [rows]")
+        if k_slot is not None:
+            _req_ints(dev, k_slot=(k_slot, (T,)))
+    _launch(dev, stream, "ds4a_qk_norm_rope", q.data_ptr() if q is not None else None, q_type, q_stride,
+            k.data_ptr() if k is not None else None, k_type, k_stride, pos.data_ptr(), inv_freq.data_ptr(),
+            2 * inv_freq.numel(), style, eps, None if q_weight is None else q_weight.data_ptr(),
+            None if k_weight is None else k_weight.data_ptr(), q_out.data_ptr() if q is not None else None,
+            k_out.data_ptr() if k is not None else None, k_out_type,
+            k_scale.data_ptr() if k_out_type == DS4A_E4M3 else None, None if k_slot is None else k_slot.data_ptr(),
+            k_rows, T, H, D)
+
+
+def ds4a_paged_attn_decode(q, rows, table, n_rows, raw, n_raw, scale, out, lse=None, ws=None, idx=None, count=None,
+                           row_scale=None, ring=None, stream=None):
+    """Attention of one new token per unit over paged rows and the raw window: q
+    bf16 [U,H,512] (H = 64 or 128); rows bf16 [n_pages,P,512], or uint8 E4M3
+    codes with row_scale f32 [n_pages,P]; table i32 [U,max_pages]; n_rows i32
+    [U]; raw fp16 [n_ring,128,512]; n_raw i32 [U]; ring i32 [U] or None (ring u);
+    idx i32 [U,top_k] and count i32 [U]: the listed rows only, None: all rows;
+    out bf16 [U,H,512]; lse f32 [U,H] or None; ws uint8 workspace of
+    ds4a_workspace_bytes(DS4A_OP_PAGED_ATTN_DECODE, U, 1, max_pages * P, top_k)."""
+    dev = _device_of(q, "q")
+    U = q.shape[0]
+    if q.dtype != torch.bfloat16 or q.dim() != 3 or q.shape[2] != HEAD_DIM or not q.is_contiguous():
+        raise ValueError("q: contiguous bf16 [U, H, 512]")
+    if out.dtype != torch.bfloat16 or out.device != dev or out.shape != q.shape or not out.is_contiguous():
+        raise ValueError("out: contiguous bf16 [U, H, 512]")
+    if rows.dtype not in (torch.bfloat16, torch.uint8) or rows.device != dev or rows.dim() != 3 \
+            or rows.shape[2] != HEAD_DIM or not rows.is_contiguous():
+        raise ValueError("rows: contiguous bf16 or uint8 [n_pages, page_size, 512]")
+    fp8 = rows.dtype == torch.uint8
+    if fp8 and (row_scale is None or row_scale.dtype != torch.float32 or row_scale.device != dev
+                or row_scale.shape != rows.shape[:2] or not row_scale.is_contiguous()):
+        raise ValueError("row_scale: contiguous float32 [n_pages, page_size]")
+    if raw.dtype != torch.float16 or raw.device != dev or raw.dim() != 3 or raw.shape[1:] != (N_SWA, HEAD_DIM) \
+            or not raw.is_contiguous():
+        raise ValueError("raw: contiguous fp16 [n_ring, 128, 512]")
+    stride = _req_table(table, U, dev)
+    _req_ints(dev, n_rows=(n_rows, (U,)), n_raw=(n_raw, (U,)))
+    if ring is not None:
+        _req_ints(dev, ring=(ring, (U,)))
+    elif raw.shape[0] < U:
+        raise ValueError("raw: a ring per unit, or give ring")
+    top_k = 0
+    if (idx is None) != (count is None):
+        raise ValueError("idx and count go together")
+    if idx is not None:
+        top_k = idx.shape[-1]
+        _req_ints(dev, idx=(idx, (U, top_k)), count=(count, (U,)))
+    if lse is not None and (lse.dtype != torch.float32 or lse.device != dev or lse.shape != q.shape[:2]
+                            or not lse.is_contiguous()):
+        raise ValueError("lse: contiguous float32 [U, H]")
+    if ws is not None and (ws.device != dev or not ws.is_contiguous()):
+        raise ValueError("ws: a contiguous tensor on the same device")
+    _launch(dev, stream, "ds4a_paged_attn_decode", q.shape[1], q.data_ptr(), rows.data_ptr(),
+            DS4A_E4M3 if fp8 else DS4A_BF16, row_scale.data_ptr() if fp8 else None, rows.shape[0], rows.shape[1],
+            table.data_ptr(), stride, table.shape[1], n_rows.data_ptr(), None if idx is None else idx.data_ptr(),
+            None if count is None else count.data_ptr(), top_k, raw.data_ptr(), raw.shape[0],
+            None if ring is None else ring.data_ptr(), n_raw.data_ptr(), scale, out.data_ptr(),
+            None if lse is None else lse.data_ptr(), U, None if ws is None else ws.data_ptr(),
+            0 if ws is None else ws.numel() * ws.element_size())

@@ -91,6 +91,21 @@ ds4a_status take_injected() {
     return c;
 }
 
+// log2 of a page size, -1 for one that is not allowed.
+int page_shift(int page_size) {
+    if (page_size < DS4A_MIN_PAGE || page_size > DS4A_MAX_PAGE || (page_size & (page_size - 1))) return -1;
+    int s = 0;
+    while ((1 << s) < page_size) ++s;
+    return s;
+}
+
+// The paged attention counts its 64-row tiles and its q rows in 32 bits (U:
+// units x 64-head halves).
+bool paged_attn_sizes_ok(long long U, long long N_cap, int top_k) {
+    const long long tiles = ((top_k ? top_k : N_cap) + 63) / 64 + 2;
+    return U * tiles < (1LL << 31) && U * kNHead < (1LL << 31);
+}
+
 }  // namespace
 
 namespace ds4a {
@@ -148,7 +163,7 @@ size_t ds4a_workspace_bytes(int op, int U, int Q, int N_cap, int top_k) {
     const int h = (op & DS4A_OP_FLAG_128_HEADS) ? 2 : 1;
     op &= ~DS4A_OP_FLAG_128_HEADS;
     if (h == 2 && op != DS4A_OP_SPARSE_ATTN_DECODE && op != DS4A_OP_SPARSE_ATTN_PREFILL &&
-        op != DS4A_OP_DENSE_ATTN_DECODE)
+        op != DS4A_OP_DENSE_ATTN_DECODE && op != DS4A_OP_PAGED_ATTN_DECODE)
         return static_cast<size_t>(-1);
     if (static_cast<long long>(U) * h > 0x7fffffffLL) return static_cast<size_t>(-1);
     U *= h;
@@ -170,6 +185,9 @@ size_t ds4a_workspace_bytes(int op, int U, int Q, int N_cap, int top_k) {
         if (units > 0x7fffffffLL) return static_cast<size_t>(-1);
         return attn_ws_bytes(static_cast<int>(units), top_k);
     }
+    case DS4A_OP_PAGED_ATTN_DECODE:
+        if (top_k < 0 || top_k > DS4A_MAX_TOP_K || !paged_attn_sizes_ok(U, N_cap, top_k)) return static_cast<size_t>(-1);
+        return paged_attn_ws_bytes(U / h, h, top_k ? top_k : N_cap);
     default: return static_cast<size_t>(-1);
     }
 }
@@ -558,6 +576,151 @@ ds4a_status ds4a_compressor_pool(const float *kv, const float *score, int ratio,
     return launch_compressor_pool(kv, score, ratio, width, out, U, static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? DS4A_OK
                : DS4A_ECUDA;
+}
+
+ds4a_status ds4a_paged_plan(const int32_t *past, const int32_t *add, int B, int ratio, int page_size,
+                            const int32_t *free_pages, int n_free, const int32_t *free_head, int32_t *free_head_out,
+                            int32_t *table, int64_t table_stride, int max_pages, const int32_t *ring, int32_t *n_rows,
+                            int32_t *n_raw, int32_t *cu_tok, int32_t *cu_row, int32_t *tok_pos, int32_t *raw_slot,
+                            int T_cap, int32_t *row_pos, int32_t *row_slot, int R_cap, void *stream) {
+    const NvtxRange nvtx_range("ds4a_paged_plan");
+    if (ds4a_status inj = take_injected()) return inj;
+    if (!past || !add || !free_head || !free_head_out || !table || !n_rows || !n_raw || !cu_tok || !cu_row ||
+        !tok_pos || !raw_slot || !row_pos || !row_slot || n_free < 0 || (n_free > 0 && !free_pages))
+        return DS4A_EINVAL;
+    const int shift = page_shift(page_size);
+    if (B < 1 || B > DS4A_MAX_PLAN_SEQS || ratio < 1 || shift < 0 || max_pages < 1 || table_stride < max_pages ||
+        T_cap < 1 || R_cap < 1)
+        return DS4A_EINVAL;
+    DevInfo *di = nullptr;
+    if (ds4a_status st = current_device(&di)) return st;
+    const PagedPlanArgs a{past,   add,    B,      ratio,    shift, free_pages, n_free,   free_head,
+                          free_head_out,  table,  table_stride,  max_pages, ring,  n_rows,     n_raw,    cu_tok,
+                          cu_row, tok_pos, raw_slot, T_cap,  row_pos, row_slot, R_cap,    di->status};
+    return launch_paged_plan(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? DS4A_OK : DS4A_ECUDA;
+}
+
+ds4a_status ds4a_qk_norm_rope(const void *q, int q_type, int64_t q_tok_stride, const void *k, int k_type,
+                              int64_t k_tok_stride, const int32_t *pos, const double *inv_freq, int n_rot, int style,
+                              float eps, const float *q_weight, const float *k_weight, uint16_t *q_out, void *k_out,
+                              int k_out_type, float *k_scale, const int32_t *k_slot, int64_t k_out_rows, int T,
+                              int n_head, int head_dim, void *stream) {
+    const NvtxRange nvtx_range("ds4a_qk_norm_rope");
+    if (ds4a_status inj = take_injected()) return inj;
+    if (T < 0) return DS4A_EINVAL;
+    if (T == 0) return DS4A_OK;                            // an empty tensor may have no address
+    if ((!q && !k) || !pos || !inv_freq) return DS4A_EINVAL;
+    if (head_dim != 512 && head_dim != 128) return DS4A_EUNSUPPORTED;
+    if ((n_rot != 16 && n_rot != 32 && n_rot != 64 && n_rot != 128) || n_rot > head_dim) return DS4A_EUNSUPPORTED;
+    if (style != DS4A_ROPE_NEIGHBOURS && style != DS4A_ROPE_HALVES) return DS4A_EINVAL;
+    if (!(eps > 0.f) || eps > 3e38f || !aligned(inv_freq, 8)) return DS4A_EINVAL;
+    if (q_weight && !aligned(q_weight, 16)) return DS4A_EINVAL;
+    if (k_weight && !aligned(k_weight, 16)) return DS4A_EINVAL;
+    if (q) {
+        if (q_type != DS4A_BF16 && q_type != DS4A_F16 && q_type != DS4A_F32) return DS4A_EUNSUPPORTED;
+        if (!q_out || n_head < 1 || !aligned(q, 16) || !aligned(q_out, 16)) return DS4A_EINVAL;
+        const int64_t row = static_cast<int64_t>(n_head) * head_dim;
+        if (T > 1 && (q_tok_stride < row || q_tok_stride % (q_type == DS4A_F32 ? 4 : 8))) return DS4A_EINVAL;
+        if (static_cast<int64_t>(T) * n_head >= (1LL << 31)) return DS4A_EINVAL;
+        if (q_out == q && (q_type != DS4A_BF16 || (T > 1 && q_tok_stride != row))) return DS4A_EINVAL;
+    }
+    if (k) {
+        if (k_type != DS4A_BF16 && k_type != DS4A_F16 && k_type != DS4A_F32) return DS4A_EUNSUPPORTED;
+        if (k_out_type != DS4A_BF16 && k_out_type != DS4A_F16 && k_out_type != DS4A_E4M3) return DS4A_EUNSUPPORTED;
+        if (k_out_type == DS4A_E4M3 && head_dim != 512) return DS4A_EUNSUPPORTED;
+        if (k_out_type == DS4A_E4M3 && (!k_scale || !aligned(k_scale, 4))) return DS4A_EINVAL;
+        if (!k_out || k_out == k || !aligned(k, 16) || !aligned(k_out, 16)) return DS4A_EINVAL;
+        if (T > 1 && (k_tok_stride < head_dim || k_tok_stride % (k_type == DS4A_F32 ? 4 : 8))) return DS4A_EINVAL;
+        if (k_out_rows < 0 || (!k_slot && k_out_rows < T)) return DS4A_EINVAL;
+    }
+    DevInfo *di = nullptr;
+    if (ds4a_status st = current_device(&di)) return st;
+    NormRopeArgs a{};
+    a.q = q;
+    a.q_type = q_type;
+    a.q_stride = q_tok_stride;
+    a.k = k;
+    a.k_type = k_type;
+    a.k_stride = k_tok_stride;
+    a.pos = pos;
+    a.inv_freq = inv_freq;
+    a.n_rot = n_rot;
+    a.style = style;
+    a.eps = eps;
+    a.q_weight = q_weight;
+    a.k_weight = k_weight;
+    a.q_out = q_out;
+    a.k_out = k_out;
+    a.k_out_type = k_out_type;
+    a.k_scale = k_scale;
+    a.k_slot = k_slot;
+    a.k_rows = k_out_rows;
+    a.T = T;
+    a.n_head = q ? n_head : 0;
+    a.status = di->status;
+    return launch_qk_norm_rope(a, head_dim, di->sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? DS4A_OK
+                                                                                                     : DS4A_ECUDA;
+}
+
+ds4a_status ds4a_paged_attn_decode(int n_head, const uint16_t *q, const void *rows, int rows_type,
+                                   const float *row_scale, int n_pages, int page_size, const int32_t *table,
+                                   int64_t table_stride, int max_pages, const int32_t *n_rows, const int32_t *idx,
+                                   const int32_t *count, int top_k, const uint16_t *raw, int n_ring,
+                                   const int32_t *ring, const int32_t *n_raw, float scale, uint16_t *out, float *lse,
+                                   int U, void *ws, size_t ws_bytes, void *stream) {
+    const NvtxRange nvtx_range("ds4a_paged_attn_decode");
+    if (ds4a_status inj = take_injected()) return inj;
+    if (n_head != 64 && n_head != 128) return DS4A_EUNSUPPORTED;
+    if (rows_type != DS4A_BF16 && rows_type != DS4A_E4M3) return DS4A_EUNSUPPORTED;
+    const int hsplit = n_head / kNHead, shift = page_shift(page_size);
+    if (!q || !rows || !table || !n_rows || !raw || !n_raw || !out || U < 1 || shift < 0) return DS4A_EINVAL;
+    if ((idx == nullptr) != (count == nullptr) || (idx == nullptr) != (top_k == 0)) return DS4A_EINVAL;
+    if (top_k < 0 || top_k > DS4A_MAX_TOP_K || n_pages < 1 || n_ring < 1 || max_pages < 1 || table_stride < max_pages)
+        return DS4A_EINVAL;
+    if (!aligned(q, 16) || !aligned(rows, 16) || !aligned(raw, 16) || !aligned(out, 16)) return DS4A_EINVAL;
+    if (rows_type == DS4A_E4M3 && (!row_scale || !aligned(row_scale, 4))) return DS4A_EINVAL;
+    if (!(scale == scale)) return DS4A_EINVAL;
+    const long long cap = static_cast<long long>(max_pages) << shift, pool = static_cast<long long>(n_pages) << shift;
+    const long long raws = static_cast<long long>(n_ring) * kNSwa;
+    if (cap >= (1LL << 31) || pool >= (1LL << 31) || raws >= (1LL << 31)) return DS4A_EINVAL;
+    if (!paged_attn_sizes_ok(static_cast<long long>(U) * hsplit, cap, top_k)) return DS4A_EINVAL;
+    const int list_cap = top_k ? top_k : static_cast<int>(cap);
+    const size_t need = paged_attn_ws_bytes(U, hsplit, list_cap);
+    if (need && (!ws || ws_bytes < need || !aligned(ws, 256))) return DS4A_EWORKSPACE;
+    DevInfo *di = nullptr;
+    if (ds4a_status st = current_device(&di)) return st;
+    AttnArgs a{};
+    a.q = q;
+    a.rows = static_cast<const uint16_t *>(rows);
+    a.rows8 = rows_type == DS4A_E4M3 ? static_cast<const uint8_t *>(rows) : nullptr;
+    a.row_scale = row_scale;
+    a.N_cap = static_cast<int>(cap);
+    a.idx = idx;
+    a.count = count;
+    a.top_k = list_cap;
+    a.raw = raw;
+    a.raw_per_unit = kNSwa;
+    a.n_raw = n_raw;
+    a.scale = scale;
+    a.lse = lse;
+    a.units = U * hsplit;
+    a.hsplit = hsplit;
+    a.ws = need ? ws : nullptr;
+    a.status = di->status;
+    a.table = table;
+    a.table_stride = table_stride;
+    a.page_shift = shift;
+    a.n_pages = n_pages;
+    a.n_rows = n_rows;
+    a.ring = ring;
+    a.n_ring = n_ring;
+    a.out16 = out;
+    if (!encode_2d_sw128(&a.tm_q, false, q, kHeadDim, static_cast<unsigned long long>(a.units) * kNHead, 64, 64))
+        return DS4A_EINVAL;
+    a.tma_rows = !a.rows8 && encode_2d_sw128(&a.tm_rows, false, rows, kHeadDim, static_cast<unsigned long long>(pool), 64,
+                                             page_size < 64 ? static_cast<unsigned>(page_size) : 64u);
+    a.tma_raw = encode_2d_sw128(&a.tm_raw, true, raw, kHeadDim, static_cast<unsigned long long>(raws), 64, 64);
+    return launch_paged_attn(a, di->sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? DS4A_OK : DS4A_ECUDA;
 }
 
 }  // extern "C"

@@ -110,8 +110,20 @@ struct AttnArgs {
     int hsplit;                  // 1 (64 heads) or 2 (128 heads: two sub-units per row-side unit)
     void *ws;
     uint32_t *status;
+    // Paged rows (launch_paged_attn): pool row of unit u's row r = page table[u][r >> shift], row r & mask of it
+    const int32_t *table;        // [row-side units][table_stride]
+    long long table_stride;
+    int page_shift, n_pages;
+    const int32_t *n_rows;       // [row-side units]: rows that exist (N_cap: the most a table can name)
+    const int32_t *ring;         // [row-side units] raw ring of a unit, or null: unit u has ring u
+    int n_ring;
+    uint16_t *out16;             // bf16 [units][64][512] (instead of out)
 };
 size_t attn_ws_bytes(int units, int top_k);
+// Paged decode attention: U row-side units whose lists hold at most list_cap
+// compressed rows (top_k, or N_cap for dense lists; AttnArgs.top_k).
+size_t paged_attn_ws_bytes(int U, int hsplit, int list_cap);
+cudaError_t launch_paged_attn(const AttnArgs &a, int num_sms, cudaStream_t s);
 cudaError_t launch_debug_wait(uint32_t *status, unsigned long long limit_ns, cudaStream_t s);
 cudaError_t launch_sparse_attn(const AttnArgs &a, int num_sms, cudaStream_t s);
 
@@ -121,6 +133,52 @@ cudaError_t launch_kv_push_raw(const float *kv, uint16_t *raw, long long raw_uni
 cudaError_t launch_compressor_pool(const float *kv, const float *score, int ratio, int width, float *out, int U,
                                    cudaStream_t s);
 cudaError_t launch_rows_to_fp8(const float *x, long long n_rows, uint8_t *codes, float *row_scale, cudaStream_t s);
+
+// ---- paged cache: block tables and slot maps, norm and rotation ---------------
+struct PagedPlanArgs {
+    const int32_t *past, *add;   // [B]
+    int B, ratio, shift;         // shift: log2 of the page size
+    const int32_t *free_pages;
+    int n_free;
+    const int32_t *free_head;
+    int32_t *free_head_out;
+    int32_t *table;
+    long long table_stride;
+    int max_pages;
+    const int32_t *ring;         // [B] or null: sequence b has ring b
+    int32_t *n_rows, *n_raw;     // [B]
+    int32_t *cu_tok, *cu_row;    // [B + 1]
+    int32_t *tok_pos, *raw_slot;
+    int T_cap;
+    int32_t *row_pos, *row_slot;
+    int R_cap;
+    uint32_t *status;
+};
+cudaError_t launch_paged_plan(const PagedPlanArgs &a, cudaStream_t s);
+
+struct NormRopeArgs {
+    const void *q;               // [T][n_head][D] (token stride q_stride) or null
+    int q_type;
+    long long q_stride;
+    const void *k;               // [T][D] (token stride k_stride) or null
+    int k_type;
+    long long k_stride;
+    const int32_t *pos;          // [T]
+    const double *inv_freq;      // [n_rot / 2]
+    int n_rot, style;
+    float eps;
+    const float *q_weight, *k_weight;   // [D] or null
+    uint16_t *q_out;             // bf16 [T][n_head][D]
+    void *k_out;                 // [k_rows][D]
+    int k_out_type;
+    float *k_scale;              // [k_rows], E4M3 only
+    const int32_t *k_slot;       // [T] or null: row t
+    long long k_rows;
+    int T, n_head;
+    int heads_per_warp, q_groups;   // set by the launcher
+    uint32_t *status;
+};
+cudaError_t launch_qk_norm_rope(NormRopeArgs a, int head_dim, int num_sms, cudaStream_t s);
 
 // ---- shared host helpers of the C ABI -------------------------------------
 // Optional NVTX range around each C-ABI op (one range per call, named after

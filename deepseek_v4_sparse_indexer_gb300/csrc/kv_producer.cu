@@ -18,6 +18,7 @@
 #include <cuda_fp16.h>
 
 #include "common.cuh"
+#include "fp8_rows.cuh"
 #include "internal.h"
 
 namespace ds4a {
@@ -146,29 +147,10 @@ __global__ void __launch_bounds__(kPoolThreads) compressor_pool_kernel(const flo
 
 // One warp per row of 512 fp32 values; lane l owns elements 16l .. 16l+15.
 //   amax  = max |x| over the row (fmaxf skips NaN);
-//   e     = the smallest integer with amax <= 448 * 2^e, within [-126, 127]
-//           (0 when amax is 0 or infinite): with amax = m * 2^k, m in [0.5, 1),
-//           e = k - 9 if m <= 0.875 (448 = 0.875 * 2^9), else k - 8;
+//   e     = fp8_row_exponent(amax);
 //   codes = E4M3 of x * 2^-e, rounded to nearest even, saturating at 448
 //           (the scaling by a power of two is exact).
 constexpr int kFp8RowsPerBlock = 4;
-
-DS4A_DEV int fp8_row_exponent(float amax) {
-    const uint32_t b = __float_as_uint(amax);
-    const int field = static_cast<int>(b >> 23);
-    if (amax == 0.f || field >= 255) return 0;            // zero, infinity
-    if (field == 0) return -126;                           // subnormal: below 448 * 2^-127
-    const int k = field - 126;                             // amax = m * 2^k, m in [0.5, 1)
-    int e = (b & 0x7FFFFFu) <= 0x600000u ? k - 9 : k - 8;  // m <= 0.875 <=> fraction <= 0.75 * 2^23
-    return e < -126 ? -126 : (e > 127 ? 127 : e);
-}
-
-DS4A_DEV uint32_t e4m3x4(float a, float b, float c, float d) {
-    uint16_t lo, hi;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));   // a -> low byte
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
-    return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
-}
 
 __global__ void __launch_bounds__(32 * kFp8RowsPerBlock) rows_to_fp8_kernel(const float *__restrict__ x,
                                                                           long long n_rows, uint8_t *codes,

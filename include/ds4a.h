@@ -83,8 +83,24 @@ typedef int ds4a_status;
 #define DS4A_OP_SPARSE_ATTN_PREFILL 3
 #define DS4A_OP_DENSE_ATTN_DECODE 4
 #define DS4A_OP_INDEXER_TOPK 5
+#define DS4A_OP_PAGED_ATTN_DECODE 6
 /* OR-ed into an attention op: the workspace of the 128-head (Pro shape) call. */
 #define DS4A_OP_FLAG_128_HEADS 0x100
+
+/* Element types, where a call takes more than one. */
+#define DS4A_BF16 0
+#define DS4A_F16 1
+#define DS4A_F32 2
+#define DS4A_E4M3 3             /* the FP8 row store: codes and a scale per row */
+
+/* Which dims of a head's last n_rot rotate together (ds4a_qk_norm_rope). */
+#define DS4A_ROPE_NEIGHBOURS 0  /* dim 2i of the tail with dim 2i + 1          */
+#define DS4A_ROPE_HALVES 1      /* dim i of the tail with dim n_rot / 2 + i    */
+
+/* Page sizes of a paged cache: a power of two of rows in this range. */
+#define DS4A_MIN_PAGE 8
+#define DS4A_MAX_PAGE 4096
+#define DS4A_MAX_PLAN_SEQS 16384 /* sequences of one ds4a_paged_plan call       */
 
 /* Human-readable text of a status code (static storage). */
 const char *ds4a_strerror(ds4a_status status);
@@ -466,6 +482,158 @@ ds4a_status ds4a_sparse_attn_prefill_fp8(const uint16_t *q, const int32_t *q_pos
                                          const uint16_t *raw, int32_t raw_pos0, int n_raw_rows,
                                          float scale, float *out, float *lse, int T,
                                          void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * 5. Paged caches.  A serving program keeps the compressed rows (and indexer
+ *    keys) of all its sequences in pages of one pool per layer, so that
+ *    sequences can grow and end without moving rows.  A page holds `page_size`
+ *    rows (a power of two, DS4A_MIN_PAGE .. DS4A_MAX_PAGE); a pool is
+ *    [n_pages][page_size][...], contiguous; row r of sequence u is row
+ *    r % page_size of page table[u * table_stride + r / page_size].  Table
+ *    entries are read only for rows that exist, so those behind a sequence's
+ *    last page may hold anything; a page may appear in several sequences'
+ *    tables.  A slot is a row of the pool counted from its start,
+ *    page * page_size + row.
+ */
+
+/*
+ * 5a. Block tables and slot maps of one step from the request lengths.
+ *    Sequence b has past[b] tokens in the cache and add[b] new ones in this
+ *    step; a layer keeps one compressed row per `ratio` tokens (§3-2: 4 or
+ *    128), so the sequence has floor(past[b] / ratio) rows before the step and
+ *    floor((past[b] + add[b]) / ratio) after it.  Pages the new rows need are
+ *    taken from the free list in sequence order.
+ *
+ *    past, add    int32 [B] (device).  A negative length, or an add that takes
+ *                 the sequence past 2^31 - 1 tokens, sets DS4A_DEV_BOUNDS and
+ *                 counts as 0.
+ *    free_pages   int32 [n_free] (device): page numbers to allocate from, from
+ *                 free_pages[*free_head] on.  n_free may be 0 (NULL).
+ *    free_head    int32 [1] (device).   free_head_out  int32 [1] (device,
+ *                 written): *free_head plus the pages taken; may be free_head
+ *                 itself.
+ *    table        int32 [B] rows of max_pages entries, table_stride apart
+ *                 (device, updated): the entries of the step's new pages are
+ *                 written, the others left as they were.
+ *    ring         int32 [B] or NULL (device): sequence b's raw-window ring
+ *                 (ring b when NULL), 0 <= ring < 2^24.
+ *    n_rows, n_raw    int32 [B] (device, written): rows and raw-window rows
+ *                 (min(past + add, 128)) after the step.
+ *    cu_tok, cu_row   int32 [B + 1] (device, written): exclusive sums of the
+ *                 new tokens and of the new rows; token cu_tok[b] + i is new
+ *                 token i of sequence b, row cu_row[b] + i its new row i.
+ *    tok_pos, raw_slot  int32 [T_cap] (device, written): a token's position and
+ *                 its row in the raw rings seen as one [n_ring * 128][512]
+ *                 buffer: ring * 128 + position % 128, or -1 for a token that
+ *                 a later one of the same step replaces (only a chunk's last
+ *                 128 tokens are kept).
+ *    row_pos, row_slot  int32 [R_cap] (device, written): a new row's position
+ *                 (that of its last token, (row + 1) * ratio - 1) and slot.
+ *    Entries behind the last token or row are written as -1, so that a step
+ *    captured with fixed capacities skips them downstream (5b).  Too many
+ *    tokens or rows for T_cap or R_cap, a free list that runs out and a sequence
+ *    that outgrows max_pages set DS4A_DEV_BOUNDS; rows without a page get slot
+ *    -1 (and table entry -1 where the free list ran out).
+ *    Sizes: 1 <= B <= DS4A_MAX_PLAN_SEQS, ratio >= 1, max_pages >= 1,
+ *    table_stride >= max_pages, n_free >= 0, T_cap >= 1, R_cap >= 1.
+ */
+ds4a_status ds4a_paged_plan(const int32_t *past, const int32_t *add, int B, int ratio,
+                            int page_size, const int32_t *free_pages, int n_free,
+                            const int32_t *free_head, int32_t *free_head_out, int32_t *table,
+                            int64_t table_stride, int max_pages, const int32_t *ring,
+                            int32_t *n_rows, int32_t *n_raw, int32_t *cu_tok, int32_t *cu_row,
+                            int32_t *tok_pos, int32_t *raw_slot, int T_cap, int32_t *row_pos,
+                            int32_t *row_slot, int R_cap, void *stream);
+
+/*
+ * 5b. Norm and rotation of queries and keys (§2: RoPE on the last n_rot dims
+ *    of a head; §3-2: a pooled row is RMS-normalised and its tail rotated
+ *    before it is stored): what turns projections into the rotated q, raw
+ *    rows, compressed rows, indexer queries and indexer keys that the other
+ *    calls take.  For every query head, and for the token's key row:
+ *
+ *      y[d] = x[d] * weight[d] / sqrt(mean_d x[d]^2 + eps)
+ *      (y[a], y[b]) = (y[a] cos t - y[b] sin t, y[a] sin t + y[b] cos t),
+ *      t = pos * inv_freq[i], for the n_rot / 2 pairs (a, b) of the last n_rot
+ *      dims: a = D - n_rot + 2i, b = a + 1 (DS4A_ROPE_NEIGHBOURS) or
+ *      a = D - n_rot + i, b = a + n_rot / 2 (DS4A_ROPE_HALVES).
+ *
+ *    Sums and products in fp32, the angle in fp64 (the whole turns of a far
+ *    position are removed there), one rounding at the end.  A row whose sum of
+ *    squares passes the fp32 range gives zeros.
+ *
+ *    q        bf16, fp16 or fp32 (q_type) [T] tokens of n_head heads of
+ *             head_dim contiguous elements, tokens q_tok_stride elements apart
+ *             (device); or NULL: keys only.
+ *    k        bf16, fp16 or fp32 (k_type) [T] rows of head_dim elements,
+ *             k_tok_stride apart (device); or NULL: queries only.
+ *    pos      int32 [T] (device).  A token with a negative position is padding:
+ *             its rows of q_out and k_out are left as they were.
+ *    inv_freq fp64 [n_rot / 2] (device).   n_rot 16, 32, 64 or 128, at most
+ *             head_dim.
+ *    q_weight, k_weight  fp32 [head_dim] or NULL: all ones (device).
+ *    q_out    bf16 [T][n_head][head_dim], contiguous (device, written); may be q
+ *             itself when q is bf16 and contiguous.
+ *    k_out    bf16, fp16 or E4M3 (k_out_type) [k_out_rows][head_dim],
+ *             contiguous (device, written): a key's row is k_slot[t], so that it
+ *             goes straight into a raw ring (fp16), a paged store (bf16) or the
+ *             FP8 row store (E4M3, head_dim 512; quantised as in 4c, its scale
+ *             in k_scale[slot], fp32 [k_out_rows]).  k_out is not k.
+ *    k_slot   int32 [T] (device), or NULL: row t.  A negative slot stores no
+ *             key; one past the store sets DS4A_DEV_BOUNDS and stores none.  The
+ *             slots of one call are distinct.
+ *    head_dim 512 or 128; n_head >= 1 (ignored when q is NULL); T >= 0 (0:
+ *             nothing is launched); eps > 0.  q, k, the weights and the outputs
+ *             are 16-byte aligned and the strides whole multiples of 16 bytes.
+ */
+ds4a_status ds4a_qk_norm_rope(const void *q, int q_type, int64_t q_tok_stride, const void *k,
+                              int k_type, int64_t k_tok_stride, const int32_t *pos,
+                              const double *inv_freq, int n_rot, int style, float eps,
+                              const float *q_weight, const float *k_weight, uint16_t *q_out,
+                              void *k_out, int k_out_type, float *k_scale, const int32_t *k_slot,
+                              int64_t k_out_rows, int T, int n_head, int head_dim, void *stream);
+
+/*
+ * 5d. Attention of one new token per sequence over paged rows: 3a and 3c (one
+ *    joint softmax over compressed rows and the raw window, fp32 softmax and
+ *    accumulation) with the rows read through a block table, ragged lengths
+ *    and bf16 output.  The batch is cut into equal shares of 64-row tiles by
+ *    the lengths found on the device, a unit cut by a share boundary is
+ *    computed in pieces, and a second kernel joins them.
+ *
+ *    n_head   64 or 128 (else DS4A_EUNSUPPORTED).
+ *    q        bf16 [U][n_head][512] (device).
+ *    rows     rows_type DS4A_BF16: bf16 [n_pages][page_size][512].  DS4A_E4M3:
+ *             uint8 codes of that shape, and row_scale fp32
+ *             [n_pages][page_size] (powers of two, as in 3e) (device).
+ *    table    int32 [U] rows of max_pages entries, table_stride apart (device).
+ *    n_rows   int32 [U] (device): rows of unit u, 0 .. max_pages * page_size.
+ *    idx, count, top_k   both NULL and 0: the unit attends to all its rows
+ *             (3c).  Else int32 [U][top_k] row numbers within the unit and
+ *             int32 [U] (device), as from ds4a_topk_select (3a).
+ *    raw      fp16 [n_ring][128][512] raw-window rings, contiguous (device).
+ *    ring     int32 [U] (device): unit u's ring; NULL: ring u.
+ *    n_raw    int32 [U], 0..128 (device).
+ *    out      bf16 [U][n_head][512] (device).  lse  fp32 [U][n_head] or NULL.
+ *             A unit with no row at all (padding of a captured batch) gives
+ *             out = 0, lse = -inf.
+ *    ws       workspace of ds4a_workspace_bytes(DS4A_OP_PAGED_ATTN_DECODE [|
+ *             DS4A_OP_FLAG_128_HEADS], U, 1, max_pages * page_size, top_k)
+ *             bytes, 256-byte aligned (device).
+ *    A length outside its range is clamped, a ring outside [0, n_ring) gives no
+ *    raw rows, and a listed row that is not one of the unit's rows or whose
+ *    page is not one of the pool's is masked; each sets DS4A_DEV_BOUNDS.
+ *    q, rows, raw and out are 16-byte aligned.  max_pages * page_size and
+ *    n_pages * page_size are below 2^31.
+ */
+ds4a_status ds4a_paged_attn_decode(int n_head, const uint16_t *q, const void *rows, int rows_type,
+                                   const float *row_scale, int n_pages, int page_size,
+                                   const int32_t *table, int64_t table_stride, int max_pages,
+                                   const int32_t *n_rows, const int32_t *idx,
+                                   const int32_t *count, int top_k, const uint16_t *raw,
+                                   int n_ring, const int32_t *ring, const int32_t *n_raw,
+                                   float scale, uint16_t *out, float *lse, int U, void *ws,
+                                   size_t ws_bytes, void *stream);
 
 #ifdef __cplusplus
 }
