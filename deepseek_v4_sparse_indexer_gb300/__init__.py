@@ -12,7 +12,8 @@ from ._binding import (Ds4aError, load, ds4a_version, ds4a_workspace_bytes, ds4a
                        ds4a_kv_push_raw, ds4a_compressor_pool, ds4a_sparse_attn_decode_heads,
                        ds4a_sparse_attn_prefill_heads, ds4a_dense_attn_decode_heads, ds4a_rows_to_fp8,
                        ds4a_sparse_attn_decode_fp8, ds4a_sparse_attn_prefill_fp8, ds4a_indexer_topk,
-                       ds4a_paged_plan, ds4a_qk_norm_rope, ds4a_paged_attn_decode, DS4A_OP_PAGED_ATTN_DECODE,
+                       ds4a_paged_plan, ds4a_qk_norm_rope, ds4a_paged_indexer_score, ds4a_paged_attn_decode,
+                       DS4A_OP_PAGED_ATTN_DECODE,
                        DS4A_OP_FLAG_128_HEADS, DS4A_ROPE_NEIGHBOURS, DS4A_ROPE_HALVES)
 from .step import DecodeStep, PrefillStep, DenseStep, ProducerStep, DEFAULT_SCALE
 
@@ -21,7 +22,8 @@ __all__ = ["Ds4aError", "load", "ds4a_version", "ds4a_workspace_bytes", "ds4a_ge
            "ds4a_sparse_attn_prefill", "ds4a_dense_attn_decode", "ds4a_kv_push_raw", "ds4a_compressor_pool",
            "ds4a_sparse_attn_decode_heads", "ds4a_sparse_attn_prefill_heads", "ds4a_dense_attn_decode_heads",
            "ds4a_rows_to_fp8", "ds4a_sparse_attn_decode_fp8", "ds4a_sparse_attn_prefill_fp8", "ds4a_indexer_topk",
-           "ds4a_paged_plan", "ds4a_qk_norm_rope", "ds4a_paged_attn_decode", "DS4A_OP_PAGED_ATTN_DECODE",
+           "ds4a_paged_plan", "ds4a_qk_norm_rope", "ds4a_paged_indexer_score", "ds4a_paged_attn_decode",
+           "DS4A_OP_PAGED_ATTN_DECODE",
            "DS4A_OP_FLAG_128_HEADS", "DS4A_ROPE_NEIGHBOURS", "DS4A_ROPE_HALVES",
            "DecodeStep", "PrefillStep", "DenseStep", "ProducerStep",
            "DEFAULT_SCALE"]

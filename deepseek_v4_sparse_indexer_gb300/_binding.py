@@ -43,7 +43,7 @@ EXPORTS = ("ds4a_strerror", "ds4a_version", "ds4a_workspace_bytes", "ds4a_get_de
            "ds4a_dense_attn_decode", "ds4a_kv_push_raw", "ds4a_compressor_pool",
            "ds4a_sparse_attn_decode_heads", "ds4a_sparse_attn_prefill_heads", "ds4a_dense_attn_decode_heads",
            "ds4a_rows_to_fp8", "ds4a_sparse_attn_decode_fp8", "ds4a_sparse_attn_prefill_fp8", "ds4a_indexer_topk",
-           "ds4a_paged_plan", "ds4a_qk_norm_rope", "ds4a_paged_attn_decode")
+           "ds4a_paged_plan", "ds4a_qk_norm_rope", "ds4a_paged_indexer_score", "ds4a_paged_attn_decode")
 DS4A_TOPK_NOALLOC_SCRATCH_BYTES = 8 << 20
 DS4A_MAX_TOP_K = 2048
 
@@ -126,6 +126,8 @@ def load(build_if_missing: bool = True):
     L.ds4a_qk_norm_rope.argtypes = [_vp, _i32, _i64, _vp, _i32, _i64, _vp, _vp, _i32, _i32, _f32, _vp, _vp, _vp, _vp,
                                     _i32, _vp, _vp, _i64, _i32, _i32, _i32, _vp]
     L.ds4a_qk_norm_rope.restype = _i32
+    L.ds4a_paged_indexer_score.argtypes = [_vp, _vp, _vp, _i32, _i32, _vp, _i64, _i32, _vp, _vp, _i32, _i32, _vp]
+    L.ds4a_paged_indexer_score.restype = _i32
     L.ds4a_paged_attn_decode.argtypes = [_i32, _vp, _vp, _i32, _vp, _i32, _i32, _vp, _i64, _i32, _vp, _vp, _vp, _i32,
                                          _vp, _i32, _vp, _vp, _f32, _vp, _vp, _i32, _vp, _sz, _vp]
     L.ds4a_paged_attn_decode.restype = _i32
@@ -629,6 +631,26 @@ def ds4a_qk_norm_rope(q, k, pos, inv_freq, eps, q_weight, k_weight, q_out, k_out
             k_out.data_ptr() if k is not None else None, k_out_type,
             k_scale.data_ptr() if k_out_type == DS4A_E4M3 else None, None if k_slot is None else k_slot.data_ptr(),
             k_rows, T, H, D)
+
+
+def ds4a_paged_indexer_score(iq, w, ik, table, n_rows, scores, stream=None):
+    """Indexer scores of one query per unit over paged keys: iq bf16 [U,1,64,128];
+    w f32 [U,1,64]; ik bf16 [n_pages,P,128]; table i32 [U,max_pages]; n_rows i32
+    [U]; scores f32 [U,1,N_cap] (written for r < n_rows[u])."""
+    dev = _device_of(iq, "iq")
+    U, N_cap = scores.shape[0], scores.shape[-1]
+    if iq.dtype != torch.bfloat16 or iq.shape != (U, 1, N_IDX_HEAD, IDX_DIM) or not iq.is_contiguous():
+        raise ValueError("iq: contiguous bf16 [U, 1, 64, 128]")
+    if w.dtype != torch.float32 or w.device != dev or w.shape != (U, 1, N_IDX_HEAD) or not w.is_contiguous():
+        raise ValueError("w: contiguous float32 [U, 1, 64]")
+    if ik.dtype != torch.bfloat16 or ik.device != dev or ik.dim() != 3 or ik.shape[2] != IDX_DIM or not ik.is_contiguous():
+        raise ValueError("ik: contiguous bf16 [n_pages, page_size, 128]")
+    if scores.dtype != torch.float32 or scores.device != dev or scores.shape != (U, 1, N_cap) or not scores.is_contiguous():
+        raise ValueError("scores: contiguous float32 [U, 1, N_cap]")
+    stride = _req_table(table, U, dev)
+    _req_ints(dev, n_rows=(n_rows, (U,)))
+    _launch(dev, stream, "ds4a_paged_indexer_score", iq.data_ptr(), w.data_ptr(), ik.data_ptr(), ik.shape[0], ik.shape[1],
+            table.data_ptr(), stride, table.shape[1], n_rows.data_ptr(), scores.data_ptr(), U, N_cap)
 
 
 def ds4a_paged_attn_decode(q, rows, table, n_rows, raw, n_raw, scale, out, lse=None, ws=None, idx=None, count=None,

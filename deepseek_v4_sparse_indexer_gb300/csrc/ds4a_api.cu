@@ -662,6 +662,43 @@ ds4a_status ds4a_qk_norm_rope(const void *q, int q_type, int64_t q_tok_stride, c
                                                                                                      : DS4A_ECUDA;
 }
 
+ds4a_status ds4a_paged_indexer_score(const uint16_t *iq, const float *w, const uint16_t *ik, int n_pages,
+                                     int page_size, const int32_t *table, int64_t table_stride, int max_pages,
+                                     const int32_t *n_rows, float *scores, int U, int N_cap, void *stream) {
+    const NvtxRange nvtx_range("ds4a_paged_indexer_score");
+    if (ds4a_status inj = take_injected()) return inj;
+    const int shift = page_shift(page_size);
+    if (!iq || !w || !ik || !table || !n_rows || !scores || shift < 0) return DS4A_EINVAL;
+    if (U < 1 || U > (1 << 24) || N_cap < 1 || n_pages < 1 || max_pages < 1 || table_stride < max_pages)
+        return DS4A_EINVAL;
+    if (!aligned(iq, 16) || !aligned(ik, 16) || !aligned(w, 4) || !aligned(scores, 4)) return DS4A_EINVAL;
+    const long long cap = static_cast<long long>(max_pages) << shift, pool = static_cast<long long>(n_pages) << shift;
+    if (cap >= (1LL << 31) || pool >= (1LL << 31)) return DS4A_EINVAL;
+    IndexerArgs a{};
+    a.row_lim = static_cast<int>(cap < N_cap ? cap : N_cap);
+    // the tiles of a batch are counted in 32 bits
+    if (static_cast<long long>(U) * ((a.row_lim + 127) / 128) >= (1LL << 31)) return DS4A_EINVAL;
+    DevInfo *di = nullptr;
+    if (ds4a_status st = current_device(&di)) return st;
+    a.w = w;
+    a.n_rows = n_rows;
+    a.scores = scores;
+    a.status = di->status;
+    a.U = U;
+    a.Q = 1;
+    a.N_cap = N_cap;
+    a.table = table;
+    a.table_stride = table_stride;
+    a.page_shift = shift;
+    a.n_pages = n_pages;
+    indexer_plan(a, di->sms);
+    if (!encode_2d_sw128(&a.tm_ik, false, ik, kIdxDim, static_cast<unsigned long long>(pool), 64,
+                         page_size < 128 ? static_cast<unsigned>(page_size) : 128u) ||
+        !encode_2d_sw128(&a.tm_iq, false, iq, kIdxDim, static_cast<unsigned long long>(U) * kNIdxHead, 64, kNIdxHead))
+        return DS4A_EINVAL;
+    return launch_indexer_score(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? DS4A_OK : DS4A_ECUDA;
+}
+
 ds4a_status ds4a_paged_attn_decode(int n_head, const uint16_t *q, const void *rows, int rows_type,
                                    const float *row_scale, int n_pages, int page_size, const int32_t *table,
                                    int64_t table_stride, int max_pages, const int32_t *n_rows, const int32_t *idx,

@@ -26,6 +26,14 @@
 // together and a CTA reloads its iq block only where its share crosses into
 // the next (unit, group).
 //
+// Paged keys (PAGED, decode only): row r of unit u is row r % P of page
+// table[u][r / P] of one pool.  The whole producer warp works on a tile: lane i
+// looks up the page of the tile's i-th piece (a page of up to 64 rows,
+// or 128 rows of a larger one) one tile ahead and loads that piece's two boxes; a
+// piece past the unit's rows or outside the pool is read past the end of the
+// tensor map, which fills zeros and reads nothing.  The batch is ragged, so the
+// shares are cut from the tiles that exist: every CTA scans the units' lengths.
+//
 // The decode scan is HBM-bound (256 B of keys per row for 16 kFLOP); the
 // prefill chunk (G = 4) is tensor-bound.  Every wait is bounded: on timeout
 // the kernel flags DS4A_DEV_TIMEOUT, waits (bounded) for its copies and
@@ -124,6 +132,75 @@ DS4A_DEV Item next_item(const IndexerArgs &a, long long &lin, long long hi) {
     m.t0 = m.first;
     m.t1 = min(end, nt);
     return m;
+}
+
+// A CTA's walk over its share.  Unpaged: tiles [lin, hi) of the U * n_groups *
+// nt_cap tiles.  Paged: lin..hi counts the share's tiles that exist, the next of
+// which is tile `off` of unit u or of a later one.
+struct Walk {
+    long long lin, hi;
+    int u, off;
+};
+template <bool PAGED>
+DS4A_DEV Item next_of(const IndexerArgs &a, Walk &w) {
+    if constexpr (!PAGED) return next_item(a, w.lin, w.hi);
+    Item m;
+    m.u = w.u++;
+    m.g = 0;
+    const int nt = (min(max(a.n_rows[m.u], 0), a.row_lim) + kTileRows - 1) / kTileRows;
+    m.t0 = m.first = w.off;
+    m.t1 = static_cast<int>(min(static_cast<long long>(nt), w.off + (w.hi - w.lin)));
+    w.lin += m.t1 - m.t0;
+    w.off = 0;
+    return m;
+}
+
+// Paged: this CTA's share [c T / G, (c + 1) T / G) of the batch's T tiles, found
+// by a scan over all units' lengths.  The whole block calls it.
+DS4A_DEV Walk paged_share(const IndexerArgs &a) {
+    __shared__ int s_warp[32];
+    __shared__ int s_at[2];
+    const int n_thr = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (a.U + n_thr - 1) / n_thr, u0 = min(tid * per, a.U), u1 = min(u0 + per, a.U);
+    int sum = 0;
+    bool ok = true;
+    for (int u = u0; u < u1; ++u) {
+        const int n = a.n_rows[u];
+        ok = ok && n >= 0 && n <= a.row_lim;
+        sum += (min(max(n, 0), a.row_lim) + kTileRows - 1) / kTileRows;
+    }
+    if (!ok && blockIdx.x == 0) report(a.status, DS4A_DEV_BOUNDS);
+    int inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += v;
+    }
+    if (lane == 31) s_warp[warp] = inc;
+    __syncthreads();
+    int start = inc - sum, T = 0;
+    for (int w = 0; w < (n_thr >> 5); ++w) {
+        const int v = s_warp[w];
+        if (w < warp) start += v;
+        T += v;
+    }
+    const long long lo = static_cast<long long>(T) * blockIdx.x / gridDim.x;
+    const long long hi = static_cast<long long>(T) * (blockIdx.x + 1) / gridDim.x;
+    for (int u = u0; u < u1; ++u) {
+        const int nt = (min(max(a.n_rows[u], 0), a.row_lim) + kTileRows - 1) / kTileRows;
+        if (start <= lo && lo < start + nt) {
+            s_at[0] = u;
+            s_at[1] = static_cast<int>(lo - start);
+        }
+        start += nt;
+    }
+    __syncthreads();
+    Walk w;
+    w.lin = 0;
+    w.hi = hi - lo;                                 // 0: nothing, and s_at may be unset
+    w.u = s_at[0];
+    w.off = s_at[1];
+    return w;
 }
 
 // Bounded wait that ignores the abort flag (used to drain in-flight work).
@@ -254,7 +331,7 @@ DS4A_DEV void prefetch_share_head(const IndexerArgs &a, long long lo, long long 
     }
 }
 
-template <int G>
+template <int G, bool PAGED>
 __global__ void __launch_bounds__(IdxCfg<G>::kThreads, 1)
     indexer_score_kernel(const __grid_constant__ IndexerArgs a) {
     pdl_launch_dependents();
@@ -307,9 +384,14 @@ __global__ void __launch_bounds__(IdxCfg<G>::kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    long long share_lo, share_hi;
-    cta_share(a, share_lo, share_hi);
-    if (warp != 0) pdl_wait();                         // the set-up above reads no global memory
+    Walk share;
+    if constexpr (PAGED) {
+        pdl_wait();                                    // the lengths may come from the kernel before
+        share = paged_share(a);
+    } else {
+        cta_share(a, share.lin, share.hi);
+        if (warp != 0) pdl_wait();                     // the set-up above reads no global memory
+    }
     const uint32_t tmem_base = *tmem_slot;
 
     if (warp < C::kFirstEpiWarp) {
@@ -317,9 +399,11 @@ __global__ void __launch_bounds__(IdxCfg<G>::kThreads, 1)
     }
     if (warp == 0) {
         // ------------------------------------------------------------ TMA producer
-        if (lane == 0) prefetch_share_head(a, share_lo, share_hi, G);
-        pdl_wait();
-        if (lane == 0) {
+        if constexpr (!PAGED) {
+            if (lane == 0) prefetch_share_head(a, share.lin, share.hi, G);
+            pdl_wait();
+        }
+        if (PAGED || lane == 0) {
             // Decode (G = 1) reads every key tile once: stream it through L2.  A
             // prefill chunk's query groups all read the same key tiles: keep
             // them in L2 (evict-first keys were re-read from DRAM once the
@@ -331,24 +415,52 @@ __global__ void __launch_bounds__(IdxCfg<G>::kThreads, 1)
             bool used_s[C::kStages] = {}, used_b[C::kBBufs] = {};
             uint32_t par_s[C::kStages] = {}, par_b[C::kBBufs] = {};
             bool ok = true;
-            for (long long lin = share_lo; ok && lin < share_hi;) {
-                const Item m = next_item(a, lin, share_hi);
+            // Paged: the whole warp waits and each lane loads its piece of a tile.
+            auto wait_free = [&](uint64_t *bar, uint32_t parity) -> bool {
+                const bool r = mbar_wait_hint(bar, parity, abort_flag);
+                if constexpr (PAGED) return __all_sync(0xffffffffu, r);
+                return r;
+            };
+            const int box = PAGED ? min(kTileRows, 1 << a.page_shift) : kTileRows;
+            const int pool_end = PAGED ? a.n_pages << a.page_shift : 0;
+            auto piece_row = [&](const Item &m, int t) -> int {   // pool row of this lane's piece of tile t
+                const int r = t * kTileRows + lane * box;
+                if (lane * box >= kTileRows || t >= m.t1 || r >= min(a.n_rows[m.u], a.row_lim)) return pool_end;
+                const int page = __ldg(a.table + m.u * a.table_stride + (r >> a.page_shift));
+                return page < 0 || page >= a.n_pages ? pool_end : (page << a.page_shift) + (r & ((1 << a.page_shift) - 1));
+            };
+            Walk walk = share;
+            while (ok && walk.lin < walk.hi) {
+                const Item m = next_of<PAGED>(a, walk);
                 if (m.t0 >= m.t1) continue;
-                if (!mbar_wait_hint(&b_empty[bb], bph ^ 1, abort_flag)) { ok = false; break; }
-                mbar_arrive_expect_tx(&b_full[bb], C::kBBytes);
-                const int qrow = (m.u * a.Q + m.g * G) * kNIdxHead;
-                uint8_t *dstB = sB + bb * C::kBBytes;
-                tma_load_2d(dstB, &a.tm_iq, &b_full[bb], 0, qrow, pol_keep);
-                tma_load_2d(dstB + C::kBSub, &a.tm_iq, &b_full[bb], 64, qrow, pol_keep);
+                int y = PAGED ? piece_row(m, m.t0) : 0;
+                if (!wait_free(&b_empty[bb], bph ^ 1)) { ok = false; break; }
+                if (!PAGED || lane == 0) {
+                    mbar_arrive_expect_tx(&b_full[bb], C::kBBytes);
+                    const int qrow = (m.u * a.Q + m.g * G) * kNIdxHead;
+                    uint8_t *dstB = sB + bb * C::kBBytes;
+                    tma_load_2d(dstB, &a.tm_iq, &b_full[bb], 0, qrow, pol_keep);
+                    tma_load_2d(dstB + C::kBSub, &a.tm_iq, &b_full[bb], 64, qrow, pol_keep);
+                }
                 used_b[bb] = true;
                 par_b[bb] = bph;
                 if (++bb == C::kBBufs) { bb = 0; bph ^= 1; }
                 for (int t = m.t0; t < m.t1; ++t) {
-                    if (!mbar_wait_hint(&a_empty[s], sph ^ 1, abort_flag)) { ok = false; break; }
-                    mbar_arrive_expect_tx(&a_full[s], C::kABytes);
+                    const int y_next = PAGED ? piece_row(m, t + 1) : 0;
+                    if (!wait_free(&a_empty[s], sph ^ 1)) { ok = false; break; }
+                    if (!PAGED || lane == 0) mbar_arrive_expect_tx(&a_full[s], C::kABytes);
                     uint8_t *dstA = sA + s * C::kABytes;
-                    tma_load_3d(dstA, &a.tm_ik, &a_full[s], 0, t * kTileRows, m.u, pol_stream);
-                    tma_load_3d(dstA + C::kASub, &a.tm_ik, &a_full[s], 64, t * kTileRows, m.u, pol_stream);
+                    if constexpr (PAGED) {
+                        __syncwarp();
+                        if (lane * box < kTileRows) {
+                            tma_load_2d(dstA + lane * box * 128, &a.tm_ik, &a_full[s], 0, y, pol_stream);
+                            tma_load_2d(dstA + C::kASub + lane * box * 128, &a.tm_ik, &a_full[s], 64, y, pol_stream);
+                        }
+                        y = y_next;
+                    } else {
+                        tma_load_3d(dstA, &a.tm_ik, &a_full[s], 0, t * kTileRows, m.u, pol_stream);
+                        tma_load_3d(dstA + C::kASub, &a.tm_ik, &a_full[s], 64, t * kTileRows, m.u, pol_stream);
+                    }
                     used_s[s] = true;
                     par_s[s] = sph;
                     if (++s == C::kStages) { s = 0; sph ^= 1; }
@@ -371,8 +483,9 @@ __global__ void __launch_bounds__(IdxCfg<G>::kThreads, 1)
             int s = 0, bb = 0, ab = 0;
             uint32_t sph = 0, bph = 0, aph = 0;
             bool ok = true;
-            for (long long lin = share_lo; ok && lin < share_hi;) {
-                const Item m = next_item(a, lin, share_hi);
+            Walk walk = share;
+            while (ok && walk.lin < walk.hi) {
+                const Item m = next_of<PAGED>(a, walk);
                 if (m.t0 >= m.t1) continue;
                 if (!mbar_wait_hint(&b_full[bb], bph, abort_flag)) { ok = false; break; }
                 const uint32_t b_addr = smem_u32(sB + bb * C::kBBytes);
@@ -428,16 +541,19 @@ __global__ void __launch_bounds__(IdxCfg<G>::kThreads, 1)
             eph ^= 1;
             return r;
         };
-        for (long long lin = share_lo; ok && lin < share_hi;) {
-            const Item m = next_item(a, lin, share_hi);
+        Walk walk = share;
+        while (ok && walk.lin < walk.hi) {
+            const Item m = next_of<PAGED>(a, walk);
             const int nr_raw = a.n_rows[m.u];
-            // Reported once per unit: by the item holding its first tile.
-            if ((nr_raw < 0 || nr_raw > a.N_cap) && e == 0 && lane == 0 && m.first == 0 && m.g == 0)
+            // Reported once per unit: by the item holding its first tile (paged: by
+            // the scan of the lengths).
+            if (!PAGED && (nr_raw < 0 || nr_raw > a.N_cap) && e == 0 && lane == 0 && m.first == 0 && m.g == 0)
                 report(a.status, DS4A_DEV_BOUNDS);
             if (m.t0 >= m.t1) continue;
-            const int nr = nr_raw < 0 ? 0 : (nr_raw > a.N_cap ? a.N_cap : nr_raw);
+            const int n_most = PAGED ? a.row_lim : a.N_cap;
+            const int nr = nr_raw < 0 ? 0 : (nr_raw > n_most ? n_most : nr_raw);
             const int q0 = m.g * G + half * C::kQPerEpiWarp;
-            if (a.fused) {
+            if (!PAGED && a.fused) {
                 // Fused selection: a fresh histogram per query of the group once
                 // every epilogue warp is done with the previous item, and the
                 // threshold other CTAs may already have raised for these rows.
@@ -491,10 +607,19 @@ __global__ void __launch_bounds__(IdxCfg<G>::kThreads, 1)
             // store at the end of each tile.
             const int32_t *rp = a.row_pos ? a.row_pos + static_cast<long long>(m.u) * a.N_cap : nullptr;
             int rpos_next = 0;
+            // Paged: whether the row's page is one of the pool's, looked up as far ahead.
+            auto page_ok = [&](int row) -> bool {
+                if (!PAGED || row >= nr) return true;
+                const int page = __ldg(a.table + m.u * a.table_stride + (row >> a.page_shift));
+                return page >= 0 && page < a.n_pages;
+            };
+            bool in_pool_next = PAGED ? page_ok(m.t0 * kTileRows + row_in_tile) : true;
             if (rp && m.t0 * kTileRows + row_in_tile < nr) rpos_next = __ldg(rp + m.t0 * kTileRows + row_in_tile);
             for (int t = m.t0; t < m.t1; ++t) {
                 const int row = t * kTileRows + row_in_tile;
                 const int rpos = rpos_next;
+                const bool in_pool = in_pool_next;
+                if (PAGED && t + 1 < m.t1) in_pool_next = page_ok(row + kTileRows);
                 if (rp && t + 1 < m.t1 && row + kTileRows < nr) rpos_next = __ldg(rp + row + kTileRows);
                 // Warp-uniform outcome: the tcgen05.ld below is .sync.aligned.
                 if (!__all_sync(0xffffffffu, mbar_wait_hint(&acc_full[ab], aph, abort_flag))) { ok = false; break; }
@@ -516,7 +641,7 @@ __global__ void __launch_bounds__(IdxCfg<G>::kThreads, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&acc_empty[ab]);
-                if (a.fused) {
+                if (!PAGED && a.fused) {
                     // Keep the row as a candidate when its key reaches the query's
                     // threshold, and count it in the query's histogram.  The
                     // threshold is a bin edge with at least top_k counted keys at
@@ -555,14 +680,18 @@ __global__ void __launch_bounds__(IdxCfg<G>::kThreads, 1)
                         const int qq = q0 + j;
                         if (qq < a.Q) {
                             float out = sc[j];
-                            if (a.q_pos && rpos > qpos[j]) out = -__int_as_float(0x7f800000);
+                            if (PAGED && !in_pool) {
+                                out = -__int_as_float(0x7f800000);
+                                report(a.status, DS4A_DEV_BOUNDS);
+                            }
+                            if (!PAGED && a.q_pos && rpos > qpos[j]) out = -__int_as_float(0x7f800000);
                             a.scores[(static_cast<long long>(m.u) * a.Q + qq) * a.N_cap + row] = out;
                         }
                     }
                 }
                 if (++ab == C::kAccBufs) { ab = 0; aph ^= 1; }
             }
-            if (a.fused && ok) {
+            if (!PAGED && a.fused && ok) {
 #pragma unroll
                 for (int j = 0; j < C::kQPerEpiWarp; ++j) {
                     if (qn[j]) flush(j);
@@ -587,21 +716,21 @@ __global__ void __launch_bounds__(IdxCfg<G>::kThreads, 1)
     }
 }
 
-template <int G>
+template <int G, bool PAGED>
 cudaError_t launch_g(const IndexerArgs &a, cudaStream_t s) {
     using C = IdxCfg<G>;
-    cudaError_t e = cudaFuncSetAttribute(indexer_score_kernel<G>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaError_t e = cudaFuncSetAttribute(indexer_score_kernel<G, PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          C::kSmemBytes);
     if (e != cudaSuccess) return e;
     if constexpr (C::kSplitRegs) {
         // setmaxnreg.inc draws on the registers the block was launched with: the
         // split must fit in them, or the raising warps would wait forever.
         cudaFuncAttributes fa;
-        e = cudaFuncGetAttributes(&fa, indexer_score_kernel<G>);
+        e = cudaFuncGetAttributes(&fa, indexer_score_kernel<G, PAGED>);
         if (e != cudaSuccess) return e;
         if (fa.numRegs * C::kThreads < C::kRegsNeeded) return cudaErrorInvalidConfiguration;
     }
-    return launch_k(indexer_score_kernel<G>, dim3(a.grid), dim3(C::kThreads), C::kSmemBytes, s, a);
+    return launch_k(indexer_score_kernel<G, PAGED>, dim3(a.grid), dim3(C::kThreads), C::kSmemBytes, s, a);
 }
 
 // Zeroes the fused selection's per-row counters.  A kernel rather than a
@@ -636,8 +765,9 @@ void indexer_plan(IndexerArgs &a, int num_sms) {
 }
 
 cudaError_t launch_indexer_score(const IndexerArgs &a, cudaStream_t s) {
-    if (a.G == 4) return launch_g<4>(a, s);
-    return launch_g<1>(a, s);
+    if (a.table) return launch_g<1, true>(a, s);
+    if (a.G == 4) return launch_g<4, false>(a, s);
+    return launch_g<1, false>(a, s);
 }
 
 }  // namespace ds4a

@@ -39,6 +39,12 @@ struct IndexerArgs {
     int nt_cap;                 // 128-row tiles per (unit, group): ceil(N_cap / 128)
     long long total_tiles;      // U * n_groups * nt_cap, split evenly over the CTAs
     int grid;
+    // Paged keys (null table: not paged; Q = 1): tm_ik is the pool, 2-D (128,
+    // n_pages << page_shift), box (64, rows of a page up to 128)
+    const int32_t *table;       // [U][table_stride]
+    long long table_stride;
+    int page_shift, n_pages;
+    int row_lim;                // rows a unit can have: min(N_cap, what its table names)
 };
 cudaError_t launch_indexer_score(const IndexerArgs &a, cudaStream_t s);
 cudaError_t launch_clear_counters(uint32_t *c, long long n, int num_sms, cudaStream_t s);

@@ -594,6 +594,27 @@ ds4a_status ds4a_qk_norm_rope(const void *q, int q_type, int64_t q_tok_stride, c
                               int64_t k_out_rows, int T, int n_head, int head_dim, void *stream);
 
 /*
+ * 5c. Indexer score over paged keys, one query per unit: 1 with the keys read
+ *    through a block table (the same arithmetic, and the same bits as 1 over
+ *    contiguous keys).  ds4a_topk_select then selects over the scores.
+ *
+ *    iq       bf16 [U][64][128], w  fp32 [U][64], contiguous (device).
+ *    ik       bf16 [n_pages][page_size][128], contiguous, 16-byte aligned
+ *             (device).
+ *    table    int32 [U] rows of max_pages entries, table_stride apart (device).
+ *    n_rows   int32 [U] (device): 0 <= n_rows[u] <= min(N_cap, max_pages *
+ *             page_size); a count outside sets DS4A_DEV_BOUNDS and is clamped.
+ *    scores   fp32 [U][N_cap] (device), written for r < n_rows[u], the others
+ *             left as they were.  A row whose page is not one of the pool's gets
+ *             -inf and sets DS4A_DEV_BOUNDS.
+ *    max_pages * page_size and n_pages * page_size are below 2^31.
+ */
+ds4a_status ds4a_paged_indexer_score(const uint16_t *iq, const float *w, const uint16_t *ik,
+                                     int n_pages, int page_size, const int32_t *table,
+                                     int64_t table_stride, int max_pages, const int32_t *n_rows,
+                                     float *scores, int U, int N_cap, void *stream);
+
+/*
  * 5d. Attention of one new token per sequence over paged rows: 3a and 3c (one
  *    joint softmax over compressed rows and the raw window, fp32 softmax and
  *    accumulation) with the rows read through a block table, ragged lengths

@@ -25,6 +25,8 @@ PLAN = dict(past=FAKE, add=FAKE, B=2, ratio=4, page_size=64, free_pages=FAKE, n_
 ROPE = dict(q=FAKE, q_type=B.DS4A_BF16, q_tok_stride=64 * 512, k=2 * FAKE, k_type=B.DS4A_F32, k_tok_stride=512, pos=FAKE,
             inv_freq=FAKE, n_rot=64, style=0, eps=1e-6, q_weight=None, k_weight=None, q_out=3 * FAKE, k_out=4 * FAKE,
             k_out_type=B.DS4A_F16, k_scale=None, k_slot=FAKE, k_out_rows=128, T=4, n_head=64, head_dim=512)
+SCORE = dict(iq=FAKE, w=FAKE, ik=FAKE, n_pages=9, page_size=64, table=FAKE, table_stride=4, max_pages=4, n_rows=FAKE,
+             scores=FAKE, U=2, N_cap=256)
 ATTN = dict(n_head=64, q=FAKE, rows=FAKE, rows_type=B.DS4A_BF16, row_scale=None, n_pages=9, page_size=64, table=FAKE,
             table_stride=4, max_pages=4, n_rows=FAKE, idx=None, count=None, top_k=0, raw=FAKE, n_ring=2, ring=None,
             n_raw=FAKE, scale=0.04, out=FAKE, lse=None, U=2, ws=FAKE, ws_bytes=1 << 30)
@@ -65,6 +67,15 @@ def test_rope_of_no_token_launches_nothing(lib):
 
 
 @pytest.mark.parametrize("change", [
+    dict(iq=None), dict(w=None), dict(ik=None), dict(table=None), dict(n_rows=None), dict(scores=None), dict(n_pages=0),
+    dict(page_size=0), dict(page_size=96), dict(max_pages=0), dict(table_stride=3), dict(U=0), dict(U=(1 << 24) + 1),
+    dict(N_cap=0), dict(iq=FAKE + 8), dict(ik=FAKE + 2), dict(w=FAKE + 2), dict(scores=FAKE + 1), dict(n_pages=1 << 25),
+    dict(max_pages=1 << 25, table_stride=1 << 25), dict(U=1 << 20, N_cap=1 << 24, max_pages=1 << 18, table_stride=1 << 18)])
+def test_indexer_rejects(lib, change):
+    assert call(lib.ds4a_paged_indexer_score, SCORE, **change) == B.DS4A_EINVAL
+
+
+@pytest.mark.parametrize("change", [
     dict(q=None), dict(rows=None), dict(table=None), dict(n_rows=None), dict(raw=None), dict(n_raw=None), dict(out=None),
     dict(U=0), dict(page_size=4), dict(page_size=100), dict(idx=FAKE), dict(count=FAKE), dict(top_k=4),
     dict(idx=FAKE, count=FAKE), dict(idx=FAKE, count=FAKE, top_k=B.DS4A_MAX_TOP_K + 1), dict(n_pages=0), dict(n_ring=0),
@@ -98,7 +109,7 @@ def test_attention_workspace(lib, heads, flag):
 
 
 @pytest.mark.parametrize("name,args", [("ds4a_paged_plan", PLAN), ("ds4a_qk_norm_rope", ROPE),
-                                       ("ds4a_paged_attn_decode", ATTN)])
+                                       ("ds4a_paged_indexer_score", SCORE), ("ds4a_paged_attn_decode", ATTN)])
 def test_injected_error(lib, name, args):
     lib.ds4a_debug_inject_error(B.DS4A_ECUDA)
     assert call(getattr(lib, name), args) == B.DS4A_ECUDA
