@@ -522,37 +522,50 @@ def ds4a_sparse_attn_prefill_fp8(q, q_pos, rows8, row_scale, idx, count, raw, ra
 _TYPES = {torch.bfloat16: DS4A_BF16, torch.float16: DS4A_F16, torch.float32: DS4A_F32, torch.uint8: DS4A_E4M3}
 
 
-def _req_ints(device, **tensors):
-    """Each tensor is contiguous int32 on `device`; (tensor, shape) also checks the shape."""
-    for name, (t, shape) in tensors.items():
-        if t.dtype != torch.int32 or t.device != device or not t.is_contiguous():
-            raise ValueError(f"{name}: must be a contiguous int32 tensor on {device}")
-        if t.shape != shape:
-            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+# These calls are a few microseconds of GPU work, so the checks go by the cheap
+# properties: the device's index and the element count (a contiguous tensor of
+# the right count is the right memory whatever its shape).
+
+def _req_ints(dev, *tensors):
+    """Each (name, tensor, n) is contiguous int32 on device index `dev` with n elements."""
+    for name, t, n in tensors:
+        if t.dtype is not torch.int32 or t.get_device() != dev or t.numel() != n or not t.is_contiguous():
+            raise ValueError(f"{name}: must be contiguous int32 on cuda:{dev} with {n} elements")
 
 
-def _req_table(table, U, device):
-    if table.dtype != torch.int32 or table.device != device or table.dim() != 2 or table.shape[0] != U \
-            or table.shape[1] < 1 or (table.shape[1] > 1 and table.stride(1) != 1):
-        raise ValueError(f"table: int32 [{U}, max_pages] on {device}, entries of a row contiguous")
-    return table.stride(0) if U > 1 else table.shape[1]
+def _table_stride(table, U, dev):
+    if table.dtype is not torch.int32 or table.get_device() != dev or table.dim() != 2:
+        raise ValueError(f"table: int32 [{U}, max_pages] on cuda:{dev}")
+    n, cols = table.shape
+    rows, one = table.stride()
+    if n != U or cols < 1 or (cols > 1 and one != 1):
+        raise ValueError(f"table: int32 [{U}, max_pages], entries of a row contiguous")
+    return rows if U > 1 else cols, cols
 
 
-def _device_of(t, name):
-    if not t.is_cuda:
+def _device_index(t, name):
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError(f"{name}: must be a CUDA tensor")
-    return t.device
+    return dev
 
 
-def _launch(device, stream, name, *args):
-    """Calls entry point `name` with the tensors' device current and a stream of that device."""
-    f = getattr(load(), name)
-    if device.index == torch.cuda.current_device():
-        st = f(*args, _stream(stream))
+def _opt(t):
+    return None if t is None else t.data_ptr()
+
+
+def _launch(dev, stream, name, *args):
+    """Calls entry point `name` with device index `dev` current, on `stream` or that device's current stream."""
+    f = getattr(_lib or load(), name)
+    # torch.cuda.current_stream() builds a Stream object: 2.8 us of a 4 us call
+    raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    if dev == torch.cuda.current_device():
+        st = f(*args, raw)
     else:
-        with torch.cuda.device(device):
-            st = f(*args, _stream(stream))
-    _check(st, name)
+        with torch.cuda.device(dev):
+            st = f(*args, raw)
+    if st != DS4A_OK:
+        raise Ds4aError(st, name)
 
 
 def ds4a_paged_plan(past, add, ratio, page_size, free_pages, free_head, table, n_rows, n_raw, cu_tok, cu_row, tok_pos,
@@ -562,19 +575,18 @@ def ds4a_paged_plan(past, add, ratio, page_size, free_pages, free_head, table, n
     (updated); n_rows, n_raw [B], cu_tok, cu_row [B + 1], tok_pos, raw_slot
     [T_cap], row_pos, row_slot [R_cap] and free_head_out [1] (written; may be
     free_head); ring [B] or None."""
-    dev = _device_of(past, "past")
-    B = past.numel()
-    T, R, n_free = tok_pos.numel(), row_pos.numel(), free_pages.numel()
-    _req_ints(dev, past=(past, (B,)), add=(add, (B,)), free_pages=(free_pages, (n_free,)), free_head=(free_head, (1,)),
-              free_head_out=(free_head_out, (1,)), n_rows=(n_rows, (B,)), n_raw=(n_raw, (B,)),
-              cu_tok=(cu_tok, (B + 1,)), cu_row=(cu_row, (B + 1,)), tok_pos=(tok_pos, (T,)), raw_slot=(raw_slot, (T,)),
-              row_pos=(row_pos, (R,)), row_slot=(row_slot, (R,)))
+    dev = _device_index(past, "past")
+    B, T, R, n_free = past.numel(), tok_pos.numel(), row_pos.numel(), free_pages.numel()
+    _req_ints(dev, ("past", past, B), ("add", add, B), ("free_pages", free_pages, n_free), ("free_head", free_head, 1),
+              ("free_head_out", free_head_out, 1), ("n_rows", n_rows, B), ("n_raw", n_raw, B), ("cu_tok", cu_tok, B + 1),
+              ("cu_row", cu_row, B + 1), ("tok_pos", tok_pos, T), ("raw_slot", raw_slot, T), ("row_pos", row_pos, R),
+              ("row_slot", row_slot, R))
     if ring is not None:
-        _req_ints(dev, ring=(ring, (B,)))
-    stride = _req_table(table, B, dev)
+        _req_ints(dev, ("ring", ring, B))
+    stride, max_pages = _table_stride(table, B, dev)
     _launch(dev, stream, "ds4a_paged_plan", past.data_ptr(), add.data_ptr(), B, ratio, page_size, free_pages.data_ptr(),
-            n_free, free_head.data_ptr(), free_head_out.data_ptr(), table.data_ptr(), stride, table.shape[1],
-            None if ring is None else ring.data_ptr(), n_rows.data_ptr(), n_raw.data_ptr(), cu_tok.data_ptr(),
+            n_free, free_head.data_ptr(), free_head_out.data_ptr(), table.data_ptr(), stride, max_pages,
+            _opt(ring), n_rows.data_ptr(), n_raw.data_ptr(), cu_tok.data_ptr(),
             cu_row.data_ptr(), tok_pos.data_ptr(), raw_slot.data_ptr(), T, row_pos.data_ptr(), row_slot.data_ptr(), R)
 
 
@@ -589,68 +601,78 @@ def ds4a_qk_norm_rope(q, k, pos, inv_freq, eps, q_weight, k_weight, q_out, k_out
     x = q if q is not None else k
     if x is None:
         raise ValueError("q and k: at least one is needed")
-    dev = _device_of(x, "q" if q is not None else "k")
+    dev = _device_index(x, "q" if q is not None else "k")
     T, D = pos.numel(), x.shape[-1]
     H = q_type = k_type = k_out_type = q_stride = k_stride = k_rows = 0
-    if pos.dtype != torch.int32 or pos.device != dev or not pos.is_contiguous() or pos.dim() != 1:
-        raise ValueError("pos: contiguous int32 [T]")
-    if inv_freq.dtype != torch.float64 or inv_freq.device != dev or not inv_freq.is_contiguous() or inv_freq.dim() != 1:
+    _req_ints(dev, ("pos", pos, T))
+    if inv_freq.dtype is not torch.float64 or inv_freq.get_device() != dev or not inv_freq.is_contiguous():
         raise ValueError("inv_freq: contiguous float64 [n_rot / 2]")
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None and (w.dtype != torch.float32 or w.device != dev or not w.is_contiguous() or w.shape != (D,)):
-            raise ValueError(f"{name}: contiguous float32 [{D}]")
+    for w in (q_weight, k_weight):
+        if w is not None and (w.dtype is not torch.float32 or w.get_device() != dev or w.numel() != D
+                              or not w.is_contiguous()):
+            raise ValueError(f"q_weight, k_weight: contiguous float32 [{D}]")
     if q is not None:
         q_type = _TYPES.get(q.dtype, -1)
-        if not DS4A_BF16 <= q_type <= DS4A_F32 or q.device != dev or q.dim() != 3 or q.shape[0] != T or q.stride(2) != 1 \
-                or (q.shape[1] > 1 and q.stride(1) != D):
-            raise ValueError("q: bf16, fp16 or fp32 [T, H, D] with contiguous heads")
-        H = q.shape[1]
-        q_stride = q.stride(0) if T > 1 else H * D
-        if q_out is None or q_out.dtype != torch.bfloat16 or q_out.device != dev or not q_out.is_contiguous() \
-                or q_out.shape != q.shape:
+        if not DS4A_BF16 <= q_type <= DS4A_F32 or q.dim() != 3:
+            raise ValueError("q: bf16, fp16 or fp32 [T, H, D]")
+        n, H, _ = q.shape
+        q_stride, head, one = q.stride()
+        if n != T or one != 1 or (H > 1 and head != D):
+            raise ValueError("q: [T, H, D] with contiguous heads")
+        if T <= 1:
+            q_stride = H * D
+        if q_out is None or q_out.dtype is not torch.bfloat16 or q_out.get_device() != dev \
+                or q_out.numel() != T * H * D or not q_out.is_contiguous():
             raise ValueError("q_out: contiguous bf16 [T, H, D]")
     if k is not None:
         k_type = _TYPES.get(k.dtype, -1)
-        if not DS4A_BF16 <= k_type <= DS4A_F32 or k.device != dev or k.shape != (T, D) or k.stride(1) != 1:
-            raise ValueError("k: bf16, fp16 or fp32 [T, D] with contiguous rows")
-        k_stride = k.stride(0) if T > 1 else D
+        if not DS4A_BF16 <= k_type <= DS4A_F32 or k.get_device() != dev or k.dim() != 2 or k.shape != (T, D):
+            raise ValueError("k: bf16, fp16 or fp32 [T, D]")
+        k_stride, one = k.stride()
+        if one != 1:
+            raise ValueError("k: contiguous rows")
+        if T <= 1:
+            k_stride = D
         k_out_type = _TYPES.get(None if k_out is None else k_out.dtype, -1)
-        if k_out_type not in (DS4A_BF16, DS4A_F16, DS4A_E4M3) or k_out.device != dev or not k_out.is_contiguous() \
-                or k_out.dim() != 2 or k_out.shape[1] != D:
+        if k_out_type not in (DS4A_BF16, DS4A_F16, DS4A_E4M3) or k_out.get_device() != dev or k_out.dim() != 2 \
+                or k_out.shape[1] != D or not k_out.is_contiguous():
             raise ValueError("k_out: contiguous bf16, fp16 or uint8 [rows, D]")
         k_rows = k_out.shape[0]
-        if k_out_type == DS4A_E4M3 and (k_scale is None or k_scale.dtype != torch.float32 or k_scale.device != dev
-                                        or not k_scale.is_contiguous() or k_scale.shape != (k_rows,)):
+        if k_out_type == DS4A_E4M3 and (k_scale is None or k_scale.dtype is not torch.float32
+                                        or k_scale.get_device() != dev or k_scale.numel() != k_rows
+                                        or not k_scale.is_contiguous()):
             raise ValueError("k_scale: contiguous float32 [rows]")
         if k_slot is not None:
-            _req_ints(dev, k_slot=(k_slot, (T,)))
-    _launch(dev, stream, "ds4a_qk_norm_rope", q.data_ptr() if q is not None else None, q_type, q_stride,
-            k.data_ptr() if k is not None else None, k_type, k_stride, pos.data_ptr(), inv_freq.data_ptr(),
-            2 * inv_freq.numel(), style, eps, None if q_weight is None else q_weight.data_ptr(),
-            None if k_weight is None else k_weight.data_ptr(), q_out.data_ptr() if q is not None else None,
-            k_out.data_ptr() if k is not None else None, k_out_type,
-            k_scale.data_ptr() if k_out_type == DS4A_E4M3 else None, None if k_slot is None else k_slot.data_ptr(),
-            k_rows, T, H, D)
+            _req_ints(dev, ("k_slot", k_slot, T))
+    _launch(dev, stream, "ds4a_qk_norm_rope", _opt(q), q_type, q_stride, _opt(k), k_type, k_stride, pos.data_ptr(),
+            inv_freq.data_ptr(), 2 * inv_freq.numel(), style, eps, _opt(q_weight), _opt(k_weight),
+            q_out.data_ptr() if q is not None else None, k_out.data_ptr() if k is not None else None, k_out_type,
+            k_scale.data_ptr() if k_out_type == DS4A_E4M3 else None, _opt(k_slot), k_rows, T, H, D)
 
 
 def ds4a_paged_indexer_score(iq, w, ik, table, n_rows, scores, stream=None):
     """Indexer scores of one query per unit over paged keys: iq bf16 [U,1,64,128];
     w f32 [U,1,64]; ik bf16 [n_pages,P,128]; table i32 [U,max_pages]; n_rows i32
     [U]; scores f32 [U,1,N_cap] (written for r < n_rows[u])."""
-    dev = _device_of(iq, "iq")
-    U, N_cap = scores.shape[0], scores.shape[-1]
-    if iq.dtype != torch.bfloat16 or iq.shape != (U, 1, N_IDX_HEAD, IDX_DIM) or not iq.is_contiguous():
-        raise ValueError("iq: contiguous bf16 [U, 1, 64, 128]")
-    if w.dtype != torch.float32 or w.device != dev or w.shape != (U, 1, N_IDX_HEAD) or not w.is_contiguous():
-        raise ValueError("w: contiguous float32 [U, 1, 64]")
-    if ik.dtype != torch.bfloat16 or ik.device != dev or ik.dim() != 3 or ik.shape[2] != IDX_DIM or not ik.is_contiguous():
-        raise ValueError("ik: contiguous bf16 [n_pages, page_size, 128]")
-    if scores.dtype != torch.float32 or scores.device != dev or scores.shape != (U, 1, N_cap) or not scores.is_contiguous():
+    dev = _device_index(iq, "iq")
+    if scores.dim() != 3:
+        raise ValueError("scores: [U, 1, N_cap]")
+    U, one, N_cap = scores.shape
+    if one != 1 or scores.dtype is not torch.float32 or scores.get_device() != dev or not scores.is_contiguous():
         raise ValueError("scores: contiguous float32 [U, 1, N_cap]")
-    stride = _req_table(table, U, dev)
-    _req_ints(dev, n_rows=(n_rows, (U,)))
-    _launch(dev, stream, "ds4a_paged_indexer_score", iq.data_ptr(), w.data_ptr(), ik.data_ptr(), ik.shape[0], ik.shape[1],
-            table.data_ptr(), stride, table.shape[1], n_rows.data_ptr(), scores.data_ptr(), U, N_cap)
+    if iq.dtype is not torch.bfloat16 or iq.numel() != U * N_IDX_HEAD * IDX_DIM or not iq.is_contiguous():
+        raise ValueError("iq: contiguous bf16 [U, 1, 64, 128]")
+    if w.dtype is not torch.float32 or w.get_device() != dev or w.numel() != U * N_IDX_HEAD or not w.is_contiguous():
+        raise ValueError("w: contiguous float32 [U, 1, 64]")
+    if ik.dtype is not torch.bfloat16 or ik.get_device() != dev or ik.dim() != 3 or not ik.is_contiguous():
+        raise ValueError("ik: contiguous bf16 [n_pages, page_size, 128]")
+    n_pages, page_size, width = ik.shape
+    if width != IDX_DIM:
+        raise ValueError("ik: contiguous bf16 [n_pages, page_size, 128]")
+    _req_ints(dev, ("n_rows", n_rows, U))
+    stride, max_pages = _table_stride(table, U, dev)
+    _launch(dev, stream, "ds4a_paged_indexer_score", iq.data_ptr(), w.data_ptr(), ik.data_ptr(), n_pages, page_size,
+            table.data_ptr(), stride, max_pages, n_rows.data_ptr(), scores.data_ptr(), U, N_cap)
 
 
 def ds4a_paged_attn_decode(q, rows, table, n_rows, raw, n_raw, scale, out, lse=None, ws=None, idx=None, count=None,
@@ -662,43 +684,50 @@ def ds4a_paged_attn_decode(q, rows, table, n_rows, raw, n_raw, scale, out, lse=N
     idx i32 [U,top_k] and count i32 [U]: the listed rows only, None: all rows;
     out bf16 [U,H,512]; lse f32 [U,H] or None; ws uint8 workspace of
     ds4a_workspace_bytes(DS4A_OP_PAGED_ATTN_DECODE, U, 1, max_pages * P, top_k)."""
-    dev = _device_of(q, "q")
-    U = q.shape[0]
-    if q.dtype != torch.bfloat16 or q.dim() != 3 or q.shape[2] != HEAD_DIM or not q.is_contiguous():
+    dev = _device_index(q, "q")
+    if q.dtype is not torch.bfloat16 or q.dim() != 3 or not q.is_contiguous():
         raise ValueError("q: contiguous bf16 [U, H, 512]")
-    if out.dtype != torch.bfloat16 or out.device != dev or out.shape != q.shape or not out.is_contiguous():
+    U, H, width = q.shape
+    if width != HEAD_DIM:
+        raise ValueError("q: contiguous bf16 [U, H, 512]")
+    if out.dtype is not torch.bfloat16 or out.get_device() != dev or out.numel() != U * H * HEAD_DIM \
+            or not out.is_contiguous():
         raise ValueError("out: contiguous bf16 [U, H, 512]")
-    if rows.dtype not in (torch.bfloat16, torch.uint8) or rows.device != dev or rows.dim() != 3 \
-            or rows.shape[2] != HEAD_DIM or not rows.is_contiguous():
+    fp8 = rows.dtype is torch.uint8
+    if not (fp8 or rows.dtype is torch.bfloat16) or rows.get_device() != dev or rows.dim() != 3 \
+            or not rows.is_contiguous():
         raise ValueError("rows: contiguous bf16 or uint8 [n_pages, page_size, 512]")
-    fp8 = rows.dtype == torch.uint8
-    if fp8 and (row_scale is None or row_scale.dtype != torch.float32 or row_scale.device != dev
-                or row_scale.shape != rows.shape[:2] or not row_scale.is_contiguous()):
+    n_pages, page_size, width = rows.shape
+    if width != HEAD_DIM:
+        raise ValueError("rows: contiguous bf16 or uint8 [n_pages, page_size, 512]")
+    if fp8 and (row_scale is None or row_scale.dtype is not torch.float32 or row_scale.get_device() != dev
+                or row_scale.numel() != n_pages * page_size or not row_scale.is_contiguous()):
         raise ValueError("row_scale: contiguous float32 [n_pages, page_size]")
-    if raw.dtype != torch.float16 or raw.device != dev or raw.dim() != 3 or raw.shape[1:] != (N_SWA, HEAD_DIM) \
+    if raw.dtype is not torch.float16 or raw.get_device() != dev or raw.dim() != 3 or raw.shape[1:] != (N_SWA, HEAD_DIM) \
             or not raw.is_contiguous():
         raise ValueError("raw: contiguous fp16 [n_ring, 128, 512]")
-    stride = _req_table(table, U, dev)
-    _req_ints(dev, n_rows=(n_rows, (U,)), n_raw=(n_raw, (U,)))
+    n_ring = raw.shape[0]
+    stride, max_pages = _table_stride(table, U, dev)
+    _req_ints(dev, ("n_rows", n_rows, U), ("n_raw", n_raw, U))
     if ring is not None:
-        _req_ints(dev, ring=(ring, (U,)))
-    elif raw.shape[0] < U:
+        _req_ints(dev, ("ring", ring, U))
+    elif n_ring < U:
         raise ValueError("raw: a ring per unit, or give ring")
     top_k = 0
     if (idx is None) != (count is None):
         raise ValueError("idx and count go together")
     if idx is not None:
         top_k = idx.shape[-1]
-        _req_ints(dev, idx=(idx, (U, top_k)), count=(count, (U,)))
-    if lse is not None and (lse.dtype != torch.float32 or lse.device != dev or lse.shape != q.shape[:2]
+        _req_ints(dev, ("idx", idx, U * top_k), ("count", count, U))
+    if lse is not None and (lse.dtype is not torch.float32 or lse.get_device() != dev or lse.numel() != U * H
                             or not lse.is_contiguous()):
         raise ValueError("lse: contiguous float32 [U, H]")
-    if ws is not None and (ws.device != dev or not ws.is_contiguous()):
-        raise ValueError("ws: a contiguous tensor on the same device")
-    _launch(dev, stream, "ds4a_paged_attn_decode", q.shape[1], q.data_ptr(), rows.data_ptr(),
-            DS4A_E4M3 if fp8 else DS4A_BF16, row_scale.data_ptr() if fp8 else None, rows.shape[0], rows.shape[1],
-            table.data_ptr(), stride, table.shape[1], n_rows.data_ptr(), None if idx is None else idx.data_ptr(),
-            None if count is None else count.data_ptr(), top_k, raw.data_ptr(), raw.shape[0],
-            None if ring is None else ring.data_ptr(), n_raw.data_ptr(), scale, out.data_ptr(),
-            None if lse is None else lse.data_ptr(), U, None if ws is None else ws.data_ptr(),
-            0 if ws is None else ws.numel() * ws.element_size())
+    ws_ptr, ws_bytes = None, 0
+    if ws is not None:
+        if ws.get_device() != dev or not ws.is_contiguous():
+            raise ValueError("ws: a contiguous tensor on the same device")
+        ws_ptr, ws_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
+    _launch(dev, stream, "ds4a_paged_attn_decode", H, q.data_ptr(), rows.data_ptr(), DS4A_E4M3 if fp8 else DS4A_BF16,
+            row_scale.data_ptr() if fp8 else None, n_pages, page_size, table.data_ptr(), stride, max_pages,
+            n_rows.data_ptr(), _opt(idx), _opt(count), top_k, raw.data_ptr(), n_ring, _opt(ring), n_raw.data_ptr(), scale,
+            out.data_ptr(), _opt(lse), U, ws_ptr, ws_bytes)

@@ -99,11 +99,10 @@ int page_shift(int page_size) {
     return s;
 }
 
-// The paged attention counts its 64-row tiles and its q rows in 32 bits (U:
-// units x 64-head halves).
-bool paged_attn_sizes_ok(long long U, long long N_cap, int top_k) {
-    const long long tiles = ((top_k ? top_k : N_cap) + 63) / 64 + 2;
-    return U * tiles < (1LL << 31) && U * kNHead < (1LL << 31);
+// The paged attention counts its tiles and its q rows in 32 bits (U: units x
+// 64-head halves).
+bool paged_attn_sizes_ok(long long U, int list_cap) {
+    return U * paged_attn_tiles(list_cap) < (1LL << 31) && U * kNHead < (1LL << 31);
 }
 
 }  // namespace
@@ -138,6 +137,27 @@ bool encode_2d_sw128(CUtensorMap *m, bool f16, const void *base, unsigned long l
     return f(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base),
              dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+namespace {
+bool encode_rows_nd(CUtensorMap *m, bool f16, const void *base, int rank, const cuuint64_t *dims,
+                    const cuuint64_t *strides, const cuuint32_t *box) {
+    EncodeTiledFn f = encode_fn();
+    if (!f) return false;
+    const cuuint32_t es[4] = {1, 1, 1, 1};
+    return f(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank,
+             const_cast<void *>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+}  // namespace
+bool encode_row_blocks(CUtensorMap *m, bool f16, const void *base, unsigned long long rows, unsigned box_rows) {
+    const cuuint64_t dims[3] = {64, rows, kHeadDim / 64}, strides[2] = {kHeadDim * 2, 128};
+    const cuuint32_t box[3] = {64, box_rows, kHeadDim / 64};
+    return encode_rows_nd(m, f16, base, 3, dims, strides, box);
+}
+bool encode_row_groups(CUtensorMap *m, bool f16, const void *base, unsigned long long rows, unsigned box_rows) {
+    const cuuint64_t dims[4] = {64, 8, kHeadDim / 64, rows / 8}, strides[3] = {kHeadDim * 2, 128, 8 * kHeadDim * 2};
+    const cuuint32_t box[4] = {64, 8, kHeadDim / 64, box_rows / 8};
+    return encode_rows_nd(m, f16, base, 4, dims, strides, box);
 }
 }  // namespace ds4a
 
@@ -186,7 +206,8 @@ size_t ds4a_workspace_bytes(int op, int U, int Q, int N_cap, int top_k) {
         return attn_ws_bytes(static_cast<int>(units), top_k);
     }
     case DS4A_OP_PAGED_ATTN_DECODE:
-        if (top_k < 0 || top_k > DS4A_MAX_TOP_K || !paged_attn_sizes_ok(U, N_cap, top_k)) return static_cast<size_t>(-1);
+        if (top_k < 0 || top_k > DS4A_MAX_TOP_K || !paged_attn_sizes_ok(U, top_k ? top_k : N_cap))
+            return static_cast<size_t>(-1);
         return paged_attn_ws_bytes(U / h, h, top_k ? top_k : N_cap);
     default: return static_cast<size_t>(-1);
     }
@@ -720,43 +741,43 @@ ds4a_status ds4a_paged_attn_decode(int n_head, const uint16_t *q, const void *ro
     const long long cap = static_cast<long long>(max_pages) << shift, pool = static_cast<long long>(n_pages) << shift;
     const long long raws = static_cast<long long>(n_ring) * kNSwa;
     if (cap >= (1LL << 31) || pool >= (1LL << 31) || raws >= (1LL << 31)) return DS4A_EINVAL;
-    if (!paged_attn_sizes_ok(static_cast<long long>(U) * hsplit, cap, top_k)) return DS4A_EINVAL;
     const int list_cap = top_k ? top_k : static_cast<int>(cap);
+    if (!paged_attn_sizes_ok(static_cast<long long>(U) * hsplit, list_cap)) return DS4A_EINVAL;
     const size_t need = paged_attn_ws_bytes(U, hsplit, list_cap);
     if (need && (!ws || ws_bytes < need || !aligned(ws, 256))) return DS4A_EWORKSPACE;
     DevInfo *di = nullptr;
     if (ds4a_status st = current_device(&di)) return st;
-    AttnArgs a{};
+    PagedAttnArgs a{};
     a.q = q;
     a.rows = static_cast<const uint16_t *>(rows);
     a.rows8 = rows_type == DS4A_E4M3 ? static_cast<const uint8_t *>(rows) : nullptr;
     a.row_scale = row_scale;
-    a.N_cap = static_cast<int>(cap);
-    a.idx = idx;
-    a.count = count;
-    a.top_k = list_cap;
-    a.raw = raw;
-    a.raw_per_unit = kNSwa;
-    a.n_raw = n_raw;
-    a.scale = scale;
-    a.lse = lse;
-    a.units = U * hsplit;
-    a.hsplit = hsplit;
-    a.ws = need ? ws : nullptr;
-    a.status = di->status;
     a.table = table;
     a.table_stride = table_stride;
     a.page_shift = shift;
     a.n_pages = n_pages;
     a.n_rows = n_rows;
+    a.N_cap = static_cast<int>(cap);
+    a.idx = idx;
+    a.count = count;
+    a.list_cap = list_cap;
+    a.raw = raw;
     a.ring = ring;
     a.n_ring = n_ring;
-    a.out16 = out;
-    if (!encode_2d_sw128(&a.tm_q, false, q, kHeadDim, static_cast<unsigned long long>(a.units) * kNHead, 64, 64))
+    a.n_raw = n_raw;
+    a.scale = scale;
+    a.out = out;
+    a.lse = lse;
+    a.U = U;
+    a.hsplit = hsplit;
+    a.ws = need ? ws : nullptr;
+    a.status = di->status;
+    a.tma_rows = !a.rows8 && !idx;
+    if (!encode_row_blocks(&a.tm_q, false, q, static_cast<unsigned long long>(U) * n_head, kNHead) ||
+        !encode_row_groups(&a.tm_raw, true, raw, static_cast<unsigned long long>(raws), 16) ||
+        (a.tma_rows && !encode_row_groups(&a.tm_rows, false, rows, static_cast<unsigned long long>(pool),
+                                          page_size < 16 ? static_cast<unsigned>(page_size) : 16u)))
         return DS4A_EINVAL;
-    a.tma_rows = !a.rows8 && encode_2d_sw128(&a.tm_rows, false, rows, kHeadDim, static_cast<unsigned long long>(pool), 64,
-                                             page_size < 64 ? static_cast<unsigned>(page_size) : 64u);
-    a.tma_raw = encode_2d_sw128(&a.tm_raw, true, raw, kHeadDim, static_cast<unsigned long long>(raws), 64, 64);
     return launch_paged_attn(a, di->sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? DS4A_OK : DS4A_ECUDA;
 }
 

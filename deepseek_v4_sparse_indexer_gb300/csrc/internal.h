@@ -116,20 +116,8 @@ struct AttnArgs {
     int hsplit;                  // 1 (64 heads) or 2 (128 heads: two sub-units per row-side unit)
     void *ws;
     uint32_t *status;
-    // Paged rows (launch_paged_attn): pool row of unit u's row r = page table[u][r >> shift], row r & mask of it
-    const int32_t *table;        // [row-side units][table_stride]
-    long long table_stride;
-    int page_shift, n_pages;
-    const int32_t *n_rows;       // [row-side units]: rows that exist (N_cap: the most a table can name)
-    const int32_t *ring;         // [row-side units] raw ring of a unit, or null: unit u has ring u
-    int n_ring;
-    uint16_t *out16;             // bf16 [units][64][512] (instead of out)
 };
 size_t attn_ws_bytes(int units, int top_k);
-// Paged decode attention: U row-side units whose lists hold at most list_cap
-// compressed rows (top_k, or N_cap for dense lists; AttnArgs.top_k).
-size_t paged_attn_ws_bytes(int U, int hsplit, int list_cap);
-cudaError_t launch_paged_attn(const AttnArgs &a, int num_sms, cudaStream_t s);
 cudaError_t launch_debug_wait(uint32_t *status, unsigned long long limit_ns, cudaStream_t s);
 cudaError_t launch_sparse_attn(const AttnArgs &a, int num_sms, cudaStream_t s);
 
@@ -161,6 +149,38 @@ struct PagedPlanArgs {
     uint32_t *status;
 };
 cudaError_t launch_paged_plan(const PagedPlanArgs &a, cudaStream_t s);
+
+struct PagedAttnArgs {
+    CUtensorMap tm_q;            // bf16 (64 dims, U * hsplit * 64 rows, 8 column blocks), box (64, 64, 8), 128B swizzle
+    CUtensorMap tm_rows;         // bf16 (64 dims, 8 rows, 8 column blocks, groups of 8 rows) of the pool, box of 16 rows (8
+                                 // with pages of 8 rows); unused unless tma_rows
+    CUtensorMap tm_raw;          // the same of the raw rings, fp16, box of 16 rows
+    int tma_rows;
+    const uint16_t *q;           // [U * hsplit][64][512] bf16
+    const uint16_t *rows;        // bf16 pool (unused with rows8)
+    const uint8_t *rows8;        // E4M3 pool or null
+    const float *row_scale;      // E4M3: scale per pool row
+    const int32_t *table;        // [U][table_stride]: row r of unit u is row r & mask of page table[u][r >> page_shift]
+    long long table_stride;
+    int page_shift, n_pages;
+    const int32_t *n_rows;       // [U]: rows that exist
+    int N_cap;                   // the most a unit's table can name
+    const int32_t *idx, *count;  // [U][list_cap], [U]; null: all rows
+    int list_cap;                // the most a unit's list can hold (dense: N_cap)
+    const uint16_t *raw;         // fp16 [n_ring][128][512]
+    const int32_t *ring;         // [U] or null: unit u has ring u
+    int n_ring;
+    const int32_t *n_raw;        // [U]
+    float scale;
+    uint16_t *out;               // bf16 [U * hsplit][64][512]
+    float *lse;                  // [U * hsplit][64] or null
+    int U, hsplit;               // units; 1 (64 heads) or 2 (128)
+    void *ws;
+    uint32_t *status;
+};
+long long paged_attn_tiles(int list_cap);   // the most tiles a unit can have
+size_t paged_attn_ws_bytes(int U, int hsplit, int list_cap);
+cudaError_t launch_paged_attn(const PagedAttnArgs &a, int num_sms, cudaStream_t s);
 
 struct NormRopeArgs {
     const void *q;               // [T][n_head][D] (token stride q_stride) or null
@@ -213,5 +233,12 @@ int take_injected_error();
 // cols*2 bytes) with the 128-byte swizzle.  False if the driver rejects it.
 bool encode_2d_sw128(CUtensorMap *m, bool f16, const void *base, unsigned long long cols, unsigned long long rows,
                      unsigned box_cols, unsigned box_rows);
+// Tensor maps over a row-major [rows][512] 16-bit matrix with the 128-byte
+// swizzle, whose boxes land as 128-byte-wide column blocks.  blocks: (64 dims,
+// rows, 8 blocks), box (64, box_rows, 8): block behind block.  groups (rows a
+// multiple of 8): (64 dims, 8 rows, 8 blocks, groups of 8 rows), box (64, 8, 8,
+// box_rows / 8): 8-row group behind group, each of eight 1 KB blocks.
+bool encode_row_blocks(CUtensorMap *m, bool f16, const void *base, unsigned long long rows, unsigned box_rows);
+bool encode_row_groups(CUtensorMap *m, bool f16, const void *base, unsigned long long rows, unsigned box_rows);
 
 }  // namespace ds4a

@@ -18,11 +18,15 @@
 //
 // One thread-block cluster (one CTA for a small step): every CTA scans all the
 // lengths (at most 16,384 sequences: three prefix arrays in shared memory, 128
-// KB of loads from L2 per CTA) instead of waiting for one that does, then the
-// CTAs take the tokens, rows and pages in turn, four consecutive ones per thread
-// (one binary search each).  The cluster barrier between the reads of *head and
-// its update lets the caller update it in place.  Bound: launch and the latency
-// of load -> scan -> search -> store.
+// KB of loads from L2 per CTA) instead of waiting for one that does.  The four
+// kinds of output (sequences, new pages, tokens, rows) are cut into blocks of
+// consecutive items that the warps take in turn, so that a small step's loads
+// of all four are in flight at once; a lane's next item is 32 further on, mostly
+// in the same sequence, whose lengths it still holds (a search and three loads
+// for every four items, one int4 store each, took 22 us on 256 chunks of up to
+// 2,048 tokens).  The cluster barrier between the reads of *head and its update
+// lets the caller update it in place.  Bound: the latency of load -> scan ->
+// search -> load -> store.
 //
 // The kernel never lets its dependents launch early: the top-k kernels read the
 // row counts it writes before their own dependency wait.
@@ -34,21 +38,44 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
+static_assert(kWarps == 32, "one lane per warp in the scan of the warps' sums");
 
 struct Sums {
-    long long tok, row, page;
+    int tok, row, page;
 };
+// Sums of lengths saturate at 2^31 - 1 (past every capacity, so flagged).
+DS4A_DEV int add_sat(int x, int y) {
+    const uint32_t v = static_cast<uint32_t>(x) + static_cast<uint32_t>(y);   // both >= 0: no wrap
+    return v > 0x7fffffffu ? 0x7fffffff : static_cast<int>(v);
+}
+DS4A_DEV Sums add_sat(const Sums &x, const Sums &y) {
+    return {add_sat(x.tok, y.tok), add_sat(x.row, y.row), add_sat(x.page, y.page)};
+}
+// Inclusive sums over the warp's lanes.
+DS4A_DEV Sums scan_warp(Sums v, int lane) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const Sums t = {__shfl_up_sync(0xffffffffu, v.tok, o), __shfl_up_sync(0xffffffffu, v.row, o),
+                        __shfl_up_sync(0xffffffffu, v.page, o)};
+        if (lane >= o) v = add_sat(v, t);
+    }
+    return v;
+}
 
-DS4A_DEV int div_up_shift(int n, int shift) { return static_cast<int>((static_cast<long long>(n) + (1 << shift) - 1) >> shift); }
+DS4A_DEV int pages_of(int rows, int shift) {
+    return static_cast<int>((static_cast<long long>(rows) + (1 << shift) - 1) >> shift);
+}
 
+struct Seq {
+    int past, add;
+    bool ok;
+};
 // Lengths of sequence b: negative ones, and a sum past 2^31 - 1, count as 0.
-DS4A_DEV bool seq_lengths(const PagedPlanArgs &a, int b, int &past, int &add) {
-    past = a.past[b];
-    add = a.add[b];
-    bool ok = true;
-    if (past < 0) past = 0, ok = false;
-    if (add < 0 || static_cast<long long>(past) + add > 0x7fffffffLL) add = 0, ok = false;
-    return ok;
+DS4A_DEV Seq seq_of(const PagedPlanArgs &a, int b) {
+    Seq s = {a.past[b], a.add[b], true};
+    if (s.past < 0) s.past = 0, s.ok = false;
+    if (s.add < 0 || s.past > 0x7fffffff - s.add) s.add = 0, s.ok = false;
+    return s;
 }
 
 // The last index b in [0, n) with cu[b] <= x (cu[0] = 0 <= x).
@@ -62,165 +89,168 @@ DS4A_DEV int find_seq(const int *cu, int n, int x) {
     return lo;
 }
 
-DS4A_DEV void store4(int32_t *p, long long i, long long n, const int (&v)[4], bool vec) {
-    if (vec && i + 4 <= n) {
-        *reinterpret_cast<int4 *>(p + i) = make_int4(v[0], v[1], v[2], v[3]);
-        return;
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-        if (i + k < n) p[i + k] = v[k];
-}
-
 __global__ void __launch_bounds__(kThreads, 1) paged_plan_kernel(const __grid_constant__ PagedPlanArgs a) {
     extern __shared__ int smem[];
     const int B = a.B;
     int *cu_tok = smem, *cu_row = smem + (B + 1), *cu_page = smem + 2 * (B + 1);
     __shared__ Sums s_warp[kWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int cta = blockIdx.x, n_cta = gridDim.x;
     pdl_wait();
 
     // ---- exclusive sums: thread t takes sequences [t per, (t + 1) per)
+    const int head_in = a.free_head[0];
     const int per = (B + kThreads - 1) / kThreads;
     const int b0 = min(tid * per, B), b1 = min(b0 + per, B);
     Sums mine = {0, 0, 0};
     bool ok = true;
     for (int b = b0; b < b1; ++b) {
-        int past, add;
-        ok &= seq_lengths(a, b, past, add);
-        const int r0 = past / a.ratio, r1 = (past + add) / a.ratio;
-        // kept per sequence, turned into sums below
-        cu_tok[b + 1] = add;
-        cu_row[b + 1] = r1 - r0;
-        cu_page[b + 1] = div_up_shift(r1, a.shift) - div_up_shift(r0, a.shift);
-        mine.tok += add;
-        mine.row += r1 - r0;
-        mine.page += cu_page[b + 1];
+        const Seq s = seq_of(a, b);
+        ok = ok && s.ok;
+        const int r0 = s.past / a.ratio, r1 = (s.past + s.add) / a.ratio;
+        const Sums one = {s.add, r1 - r0, pages_of(r1, a.shift) - pages_of(r0, a.shift)};
+        cu_tok[b + 1] = one.tok;                 // summed below
+        cu_row[b + 1] = one.row;
+        cu_page[b + 1] = one.page;
+        mine = add_sat(mine, one);
     }
-    const int head_in = a.free_head[0];
-    Sums inc = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long t = __shfl_up_sync(0xffffffffu, inc.tok, o), r = __shfl_up_sync(0xffffffffu, inc.row, o),
-                        p = __shfl_up_sync(0xffffffffu, inc.page, o);
-        if (lane >= o) inc.tok += t, inc.row += r, inc.page += p;
-    }
+    const Sums inc = scan_warp(mine, lane);
     if (lane == 31) s_warp[warp] = inc;
     __syncthreads();
-    Sums base = {inc.tok - mine.tok, inc.row - mine.row, inc.page - mine.page}, tot = {0, 0, 0};
-    for (int w = 0; w < kWarps; ++w) {
-        const Sums v = s_warp[w];
-        if (w < warp) base.tok += v.tok, base.row += v.row, base.page += v.page;
-        tot.tok += v.tok, tot.row += v.row, tot.page += v.page;
-    }
-    // The 32-bit sums saturate (such a batch is past every capacity and flagged).
-    const long long kTop = 0x7fffffffLL;
+    // before this thread: the warps before (every warp scans the warps' sums) and
+    // the lanes before; a saturated sum cannot be taken apart, so both are shifts
+    const Sums wsum = scan_warp(s_warp[lane], lane);
+    const int pw = max(warp - 1, 0);
+    Sums base = {__shfl_sync(0xffffffffu, wsum.tok, pw), __shfl_sync(0xffffffffu, wsum.row, pw),
+                 __shfl_sync(0xffffffffu, wsum.page, pw)};
+    if (warp == 0) base = {0, 0, 0};
+    Sums left = {__shfl_up_sync(0xffffffffu, inc.tok, 1), __shfl_up_sync(0xffffffffu, inc.row, 1),
+                 __shfl_up_sync(0xffffffffu, inc.page, 1)};
+    if (lane == 0) left = {0, 0, 0};
+    base = add_sat(base, left);
     for (int b = b0; b < b1; ++b) {
-        base.tok += cu_tok[b + 1];
-        base.row += cu_row[b + 1];
-        base.page += cu_page[b + 1];
-        cu_tok[b + 1] = static_cast<int>(min(base.tok, kTop));
-        cu_row[b + 1] = static_cast<int>(min(base.row, kTop));
-        cu_page[b + 1] = static_cast<int>(min(base.page, kTop));
+        base = add_sat(base, {cu_tok[b + 1], cu_row[b + 1], cu_page[b + 1]});
+        cu_tok[b + 1] = base.tok;
+        cu_row[b + 1] = base.row;
+        cu_page[b + 1] = base.page;
     }
     if (tid == 0) cu_tok[0] = cu_row[0] = cu_page[0] = 0;
     __syncthreads();
     const int T = cu_tok[B], R = cu_row[B], G = cu_page[B];
     const int head = head_in < 0 ? 0 : head_in;
-    if (head_in < 0 || tot.tok > a.T_cap || tot.row > a.R_cap || static_cast<long long>(head) + tot.page > a.n_free)
-        ok = false;
+    const long long head_end = static_cast<long long>(head) + G;
+    if (head_in < 0 || T > a.T_cap || R > a.R_cap || head_end > a.n_free) ok = false;
 
     // Page `g` of the step's new pages (-1: the free list is used up).
     auto free_page = [&](int g) -> int {
         const long long at = static_cast<long long>(head) + g;
         return at < a.n_free ? a.free_pages[at] : -1;
     };
-    const long long first = static_cast<long long>(cta) * kThreads + tid, step = static_cast<long long>(n_cta) * kThreads;
-
-    // ---- per sequence
-    for (long long b = first; b <= B; b += step) {
-        a.cu_tok[b] = cu_tok[b];
-        a.cu_row[b] = cu_row[b];
-        if (b < B) {
-            int past, add;
-            seq_lengths(a, static_cast<int>(b), past, add);
-            const int len = past + add;
-            a.n_rows[b] = len / a.ratio;
-            a.n_raw[b] = len < kNSwa ? len : kNSwa;
-        }
-    }
-    // ---- new pages
-    for (long long g = first; g < G; g += step) {
-        const int b = find_seq(cu_page, B, static_cast<int>(g));
-        int past, add;
-        seq_lengths(a, b, past, add);
-        const long long i = div_up_shift(past / a.ratio, a.shift) + (g - cu_page[b]);
-        if (i >= a.max_pages) {
-            ok = false;
+    // ---- each kind in blocks of equal runs, at most one per warp; the warps of
+    // all CTAs take the blocks in turn
+    const int n_warps = gridDim.x * kWarps;
+    auto run_of = [&](int n) -> int {
+        return max(32, static_cast<int>(((static_cast<long long>(n) + n_warps - 1) / n_warps + 31) & ~31LL));
+    };
+    auto blocks_of = [](int n, int run) -> int { return static_cast<int>((static_cast<long long>(n) + run - 1) / run); };
+    const int run_tok = run_of(a.T_cap), run_row = run_of(a.R_cap), run_page = run_of(G), run_seq = run_of(B + 1);
+    const int nb_tok = blocks_of(a.T_cap, run_tok), nb_row = blocks_of(a.R_cap, run_row);
+    const int nb_page = blocks_of(G, run_page), nb_seq = blocks_of(B + 1, run_seq);
+    for (int blk = blockIdx.x * kWarps + warp; blk < nb_seq + nb_page + nb_tok + nb_row; blk += n_warps) {
+        int k = blk;
+        if (k < nb_tok) {                                  // ---- tokens
+            const int end = static_cast<int>(min((static_cast<long long>(k) + 1) * run_tok, static_cast<long long>(a.T_cap)));
+            int seq_end = 0, first = 0, kept = 0, ring = -1;
+            for (long long x = static_cast<long long>(k) * run_tok + lane; x < end; x += 32) {
+                int pos = -1, slot = -1;
+                if (x < T) {
+                    if (x >= seq_end) {
+                        const int b = find_seq(cu_tok, B, static_cast<int>(x));
+                        const Seq s = seq_of(a, b);
+                        seq_end = cu_tok[b + 1];
+                        first = s.past - cu_tok[b];
+                        kept = s.past + s.add - kNSwa;
+                        ring = a.ring ? a.ring[b] : b;
+                        if (ring < 0 || ring > (0x7fffffff >> 7)) ring = -1, ok = false;
+                    }
+                    pos = first + static_cast<int>(x);
+                    if (pos >= kept && ring >= 0) slot = ring * kNSwa + (pos & (kNSwa - 1));
+                }
+                a.tok_pos[x] = pos;
+                a.raw_slot[x] = slot;
+            }
             continue;
         }
-        a.table[b * a.table_stride + i] = free_page(static_cast<int>(g));
-    }
-    // ---- tokens
-    const bool vec_t = ((reinterpret_cast<uintptr_t>(a.tok_pos) | reinterpret_cast<uintptr_t>(a.raw_slot)) & 15) == 0;
-    for (long long t = 4 * first; t < a.T_cap; t += 4 * step) {
-        int pos[4], slot[4];
-        int b = -1, past = 0, end = 0, ring = 0, seq_end = 0;
+        k -= nb_tok;
+        if (k < nb_row) {                                  // ---- rows, four at a time: their pages load together
+            const int end = static_cast<int>(min((static_cast<long long>(k) + 1) * run_row, static_cast<long long>(a.R_cap)));
+            int seq_end = 0, first = 0, held = 0, taken = 0;
+            const int32_t *table = nullptr;
+            for (long long x0 = static_cast<long long>(k) * run_row + lane; x0 < end; x0 += 4 * 32) {
+                int j[4], page[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            pos[k] = slot[k] = -1;
-            if (t + k >= T) continue;
-            const int x = static_cast<int>(t) + k;
-            if (b < 0 || x >= seq_end) {
-                b = find_seq(cu_tok, B, x);
-                seq_end = cu_tok[b + 1];
-                int add;
-                seq_lengths(a, b, past, add);
-                end = past + add;
-                ring = a.ring ? a.ring[b] : b;
-                if (ring < 0 || ring > (0x7fffffff >> 7)) ring = -1, ok = false;
-            }
-            pos[k] = past + (x - cu_tok[b]);
-            if (pos[k] >= end - kNSwa && ring >= 0) slot[k] = ring * kNSwa + (pos[k] & (kNSwa - 1));
-        }
-        store4(a.tok_pos, t, a.T_cap, pos, vec_t);
-        store4(a.raw_slot, t, a.T_cap, slot, vec_t);
-    }
-    // ---- rows
-    const bool vec_r = ((reinterpret_cast<uintptr_t>(a.row_pos) | reinterpret_cast<uintptr_t>(a.row_slot)) & 15) == 0;
-    for (long long t = 4 * first; t < a.R_cap; t += 4 * step) {
-        int pos[4], slot[4];
-        int b = -1, old = 0, held = 0, seq_end = 0;
+                for (int q = 0; q < 4; ++q) {
+                    const long long x = x0 + 32 * q;
+                    j[q] = page[q] = -1;
+                    if (x >= end || x >= R) continue;
+                    if (x >= seq_end) {
+                        const int b = find_seq(cu_row, B, static_cast<int>(x));
+                        const int old = seq_of(a, b).past / a.ratio;
+                        seq_end = cu_row[b + 1];
+                        first = old - cu_row[b];
+                        held = pages_of(old, a.shift);
+                        taken = cu_page[b] - held;
+                        table = a.table + b * a.table_stride;
+                    }
+                    j[q] = first + static_cast<int>(x);
+                    const int i = j[q] >> a.shift;
+                    if (i < a.max_pages) page[q] = i >= held ? free_page(taken + i) : table[i];
+                }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            pos[k] = slot[k] = -1;
-            if (t + k >= R) continue;
-            const int x = static_cast<int>(t) + k;
-            if (b < 0 || x >= seq_end) {
-                b = find_seq(cu_row, B, x);
-                seq_end = cu_row[b + 1];
-                int past, add;
-                seq_lengths(a, b, past, add);
-                old = past / a.ratio;
-                held = div_up_shift(old, a.shift);
+                for (int q = 0; q < 4; ++q) {
+                    const long long x = x0 + 32 * q;
+                    if (x >= end) break;
+                    int pos = -1, slot = -1;
+                    if (j[q] >= 0) {
+                        pos = static_cast<int>((static_cast<long long>(j[q]) + 1) * a.ratio - 1);
+                        const long long at = (static_cast<long long>(page[q]) << a.shift) + (j[q] & ((1 << a.shift) - 1));
+                        if (page[q] < 0 || at > 0x7fffffffLL) ok = false;
+                        else slot = static_cast<int>(at);
+                    }
+                    a.row_pos[x] = pos;
+                    a.row_slot[x] = slot;
+                }
             }
-            const int j = old + (x - cu_row[b]), i = j >> a.shift;
-            pos[k] = static_cast<int>((static_cast<long long>(j) + 1) * a.ratio - 1);
-            int page = -1;
-            if (i < a.max_pages) page = i >= held ? free_page(cu_page[b] + i - held) : a.table[b * a.table_stride + i];
-            const long long at = (static_cast<long long>(page) << a.shift) + (j & ((1 << a.shift) - 1));
-            if (page < 0 || at > kTop) ok = false;
-            else slot[k] = static_cast<int>(at);
+            continue;
         }
-        store4(a.row_pos, t, a.R_cap, pos, vec_r);
-        store4(a.row_slot, t, a.R_cap, slot, vec_r);
+        k -= nb_row;
+        if (k < nb_page) {                                 // ---- new pages
+            const int end = static_cast<int>(min((static_cast<long long>(k) + 1) * run_page, static_cast<long long>(G)));
+            for (long long x = static_cast<long long>(k) * run_page + lane; x < end; x += 32) {
+                const int g = static_cast<int>(x), b = find_seq(cu_page, B, g);
+                const long long i = static_cast<long long>(pages_of(seq_of(a, b).past / a.ratio, a.shift)) + (g - cu_page[b]);
+                if (i < a.max_pages) a.table[b * a.table_stride + i] = free_page(g);
+                else ok = false;
+            }
+            continue;
+        }
+        k -= nb_page;                                      // ---- sequences
+        const int end = min((k + 1) * run_seq, B + 1);
+        for (int b = k * run_seq + lane; b < end; b += 32) {
+            a.cu_tok[b] = cu_tok[b];
+            a.cu_row[b] = cu_row[b];
+            if (b < B) {
+                const Seq s = seq_of(a, b);
+                const int len = s.past + s.add;
+                a.n_rows[b] = len / a.ratio;
+                a.n_raw[b] = len < kNSwa ? len : kNSwa;
+            }
+        }
     }
     if (!ok) report(a.status, DS4A_DEV_BOUNDS);
     // ---- the free list's new head, once every CTA has read the old one
-    if (n_cta > 1) cluster_sync_all();
-    if (cta == 0 && tid == 0)
-        a.free_head_out[0] = static_cast<int>(min(static_cast<long long>(head) + tot.page, static_cast<long long>(a.n_free)));
+    if (gridDim.x > 1) cluster_sync_all();
+    if (blockIdx.x == 0 && tid == 0)
+        a.free_head_out[0] = static_cast<int>(min(head_end, static_cast<long long>(max(a.n_free, head))));
 }
 
 }  // namespace
@@ -230,8 +260,8 @@ cudaError_t launch_paged_plan(const PagedPlanArgs &a, cudaStream_t s) {
     cudaError_t e = cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(smem));
     if (e != cudaSuccess) return e;
-    // One CTA covers 4,096 tokens and as many rows in one turn; eight for more.
-    const bool wide = static_cast<long long>(a.T_cap) + a.R_cap > 8LL * kThreads || a.B > 4 * kThreads;
+    // One CTA covers a few thousand tokens and rows; a cluster of eight for more.
+    const bool wide = static_cast<long long>(a.T_cap) + a.R_cap > 8LL * kThreads;
     if (!wide) return launch_k(paged_plan_kernel, dim3(1), dim3(kThreads), smem, s, a);
     return launch_k_cluster(paged_plan_kernel, dim3(8), dim3(kThreads), smem, 8, s, a);
 }

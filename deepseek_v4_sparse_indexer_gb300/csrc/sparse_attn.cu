@@ -53,24 +53,9 @@
 // (32 cycles for M=64, N=64, K=16).  Descriptors are advanced by adding the
 // byte offset / 16 to a base descriptor.
 //
-// Paged rows (PAGED): a unit's compressed row r is row r % P of page
-// table[u][r / P] of one pool; the gather warps look a tile's pages up one tile
-// ahead, and a whole tile of a dense row list is one TMA box per page piece
-// (64 rows of one page, or pages of 8, 16 or 32 rows, each box at its place in
-// the tile; a page outside the pool is read past the end of the tensor map,
-// which fills zeros).  The batch is ragged, so its tiles are dealt by the lengths
-// themselves: every CTA scans the units' tile counts and takes an equal,
-// contiguous share.  (The strided rounds of the unpaged schedule keep
-// neighbouring units' rows together in memory; pages have no such order, and
-// equal shares of the capacity would leave CTAs idle.)  128 heads: the two
-// 64-head halves of a share run on neighbouring CTAs, so that the second one's
-// rows come from L2.  The result is bf16, for the projection behind it.
-//
 // Every wait is bounded (DS4A_DEV_TIMEOUT); on timeout the CTA drains what it
 // issued (bounded), frees TMEM and returns.
-#include <cuda_fp16.h>
-
-#include "common.cuh"
+#include "attn_common.cuh"
 #include "internal.h"
 
 namespace ds4a {
@@ -123,17 +108,6 @@ __host__ __device__ constexpr uint32_t idesc_f16(bool f16_inputs, bool values) {
     return (1u << 4) | (fmt << 7) | (fmt << 10) | (values ? (1u << 15) : 0u) | ((n >> 3) << 17) | ((m >> 4) << 24);
 }
 
-// Shared-memory descriptor with explicit leading / stride byte offsets (128B swizzle).
-DS4A_DEV uint64_t sw128_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-    uint64_t d = 0;
-    d |= static_cast<uint64_t>((addr & 0x3FFFFu) >> 4);
-    d |= static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16;
-    d |= static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32;
-    d |= static_cast<uint64_t>(1) << 46;
-    d |= static_cast<uint64_t>(2) << 61;
-    return d;
-}
-
 DS4A_DEV void tma_load_2d_nohint(void *dst, const void *map, uint64_t *bar, int x, int y) {
     asm volatile(
         "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
@@ -141,113 +115,6 @@ DS4A_DEV void tma_load_2d_nohint(void *dst, const void *map, uint64_t *bar, int 
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar))
         : "memory");
 }
-DS4A_DEV void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-
-DS4A_DEV void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
-          "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
-          "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
-          "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr));
-}
-DS4A_DEV void tmem_wait_ld(uint32_t (&r)[32]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
-                   "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]),
-                   "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]),
-                   "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]),
-                   "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
-                 :
-                 : "memory");
-}
-DS4A_DEV void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
-        "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
-        "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-        : "memory");
-}
-DS4A_DEV void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// Eight E4M3 codes (two words) times a power-of-two scale as eight bf16
-// (four words, dims in order).  E4M3 -> f16 is exact, and so are the scaling
-// in fp32 and the rounding to bf16 of a value with at most four significant
-// bits (down to 2^-133, the smallest bf16 subnormal).
-DS4A_DEV void e4m3x8_to_bf16(uint32_t w0, uint32_t w1, float s, uint32_t (&o)[4]) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const uint32_t w = j < 2 ? w0 : w1;
-        const uint16_t pair = static_cast<uint16_t>(w >> (16 * (j & 1)));
-        uint32_t h2;
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(pair));
-        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h2));
-        o[j] = pack2<false>(f.x * s, f.y * s);
-    }
-}
-// 16-byte read-only load that bypasses L1 (rows are read once).  Volatile, so
-// that it stays ahead of the buffer wait that follows it.
-DS4A_DEV uint4 ld_nc_v4(const uint4 *p) {
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
-}
-DS4A_DEV void st_shared_v4(uint32_t addr, const uint32_t (&v)[4]) {
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
-                 : "memory");
-}
-
-// 2^x by the MUFU approximation (relative error ~2^-22; -inf -> +0).
-DS4A_DEV float ex2(float x) {
-    float y;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-// UMMA / commit issued by the elected lane of a converged warp.
-DS4A_DEV void umma_elect(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p, e;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "elect.sync _|e, 0xffffffff;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-DS4A_DEV void commit_elect(uint64_t *bar) {
-    asm volatile(
-        "{\n\t.reg .pred e;\n\t"
-        "elect.sync _|e, 0xffffffff;\n\t"
-        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
-        : "memory");
-}
-// Warp-wide bounded wait (hinted try_wait: a waiting issuer takes no issue slots).
-DS4A_DEV bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
-    return __all_sync(0xffffffffu, mbar_wait_hint(bar, parity, abort));
-}
-
-// Bulk prefetch of [p, p + bytes) into L2 (16-byte aligned, multiple of 16 bytes).
-DS4A_DEV void prefetch_l2(const void *p, uint32_t bytes) {
-    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
-}
-
-DS4A_DEV bool wait_drain(uint64_t *bar, uint32_t parity) {
-    const uint64_t t0 = globaltimer_ns();
-    while (!mbar_try_wait(bar, parity))
-        if (globaltimer_ns() - t0 > kWaitLimitNs) return false;
-    return true;
-}
-
 // What one work item covers: this CTA's piece of one unit.
 struct Item {
     int unit;            // 64-head sub-unit (q, out, lse); ru: its row-side unit
@@ -258,16 +125,9 @@ struct Item {
     int nrw;             // raw rows
     int ct;              // compressed tiles
     int t0, t1;          // tile range of this split
-    int lim;             // paged: listed rows lie in [0, lim)
     long long raw_row0;  // row index of the unit's raw row 0 in the raw buffer
     long long comp_row0; // row index of the unit's compressed row 0 in the rows buffer
 };
-
-// Paged workspace: two partial slots per CTA (O, then their (m, l)), then one
-// int4 per share.
-__host__ __device__ inline int4 *paged_merge_info(const AttnArgs &a, int ctas) {
-    return reinterpret_cast<int4 *>(static_cast<float *>(a.ws) + 2LL * ctas * kNHead * (kHeadDim + 2));
-}
 
 // Work schedule.  With G CTAs, the first R = floor(units / G) rounds of units
 // are dealt whole and strided (CTA c: units c, c + G, ...), so that the CTAs
@@ -282,7 +142,6 @@ struct Sched {
     int u_rem0;              // first remainder unit (R x G)
     long long rs, re;        // this CTA's remainder share: remainder tiles [rs, re)
     int v0;                  // its first remainder unit (relative to u_rem0)
-    int off0, end_last;      // paged: first tile of its first unit, end of its last one
 };
 
 DS4A_DEV Sched make_sched(const AttnArgs &a, int nt, int g_rem) {
@@ -307,110 +166,8 @@ DS4A_DEV Sched make_sched(const AttnArgs &a, int nt, int g_rem) {
     return sc;
 }
 
-// ---- paged: shares by the units' own lengths
-struct PagedLens {
-    int cnt, lim, nrw, ring;   // listed rows, rows that exist, raw rows, raw ring
-    bool ok;                   // every value lay in its range
-};
-DS4A_DEV PagedLens paged_lens(const AttnArgs &a, int u) {
-    PagedLens l;
-    const int n = a.n_rows[u], c = a.idx ? a.count[u] : n, r = a.n_raw[u];
-    l.ring = a.ring ? a.ring[u] : u;
-    l.lim = min(max(n, 0), a.N_cap);
-    l.cnt = min(max(c, 0), a.top_k);
-    l.nrw = min(max(r, 0), kNSwa);
-    l.ok = l.lim == n && l.cnt == c && l.nrw == r;
-    if (l.ring < 0 || l.ring >= a.n_ring) {
-        l.ok = l.ok && l.nrw == 0;     // a unit without raw rows needs no ring
-        l.nrw = l.ring = 0;
-    }
-    return l;
-}
-DS4A_DEV int paged_tiles(const PagedLens &l) { return (l.cnt + TR - 1) / TR + (l.nrw + TR - 1) / TR; }
-
-// Share c of the batch's tiles (units in order, a unit without rows counting as
-// one, so that some CTA writes its result): [c T / g, (c + 1) T / g) with
-// g = min(shares, T), found by a scan over all units' tile counts.  The whole
-// block calls it.  info[c] (for the merge): the share's first unit, that unit's
-// first tile and tile count in the batch, and T.
-DS4A_DEV Sched make_paged_sched(const AttnArgs &a, int4 *info) {
-    __shared__ int s_warp[32];
-    __shared__ int s_out[4];
-    const int U = a.units / a.hsplit, shares = gridDim.x / a.hsplit, c = blockIdx.x / a.hsplit;
-    const int n_thr = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int per = (U + n_thr - 1) / n_thr;
-    const int u_lo = min(tid * per, U), u_hi = min(u_lo + per, U);
-    int sum = 0;
-    for (int u = u_lo; u < u_hi; ++u) sum += max(paged_tiles(paged_lens(a, u)), 1);
-    int inc = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += v;
-    }
-    if (lane == 31) s_warp[warp] = inc;
-    __syncthreads();
-    int start = inc - sum, T = 0;
-    for (int w = 0; w < (n_thr >> 5); ++w) {
-        const int v = s_warp[w];
-        if (w < warp) start += v;
-        T += v;
-    }
-    const int g = min(shares, T);
-    const int lo = static_cast<int>(static_cast<long long>(c) * T / g);
-    const int hi = static_cast<int>(static_cast<long long>(c + 1) * T / g);
-    if (c < g) {
-        for (int u = u_lo; u < u_hi; ++u) {
-            const int w = max(paged_tiles(paged_lens(a, u)), 1);
-            if (start <= lo && lo < start + w) {
-                s_out[0] = u;
-                s_out[1] = lo - start;
-                if (info && blockIdx.x == c * a.hsplit) info[c] = make_int4(u, start, w, T);
-            }
-            if (start < hi && hi <= start + w) {
-                s_out[2] = u;
-                s_out[3] = hi - start;
-            }
-            start += w;
-        }
-    }
-    __syncthreads();
-    Sched sc;
-    sc.nt = sc.R = sc.u_rem0 = 0;
-    sc.rs = sc.re = 0;
-    sc.v0 = c < g ? s_out[0] : 0;
-    sc.off0 = c < g ? s_out[1] : 0;
-    sc.end_last = c < g ? s_out[3] : 0;
-    sc.n_pieces = c < g ? s_out[2] - s_out[0] + 1 : 0;
-    return sc;
-}
-
-DS4A_DEV Item make_paged_piece(const AttnArgs &a, const Sched &sc, int i) {
-    Item m;
-    const int u = sc.v0 + i;
-    const PagedLens l = paged_lens(a, u);
-    const int tiles = paged_tiles(l);
-    const int lt0 = i == 0 ? sc.off0 : 0, lt1 = i == sc.n_pieces - 1 ? sc.end_last : max(tiles, 1);
-    if (!l.ok && lt0 == 0 && threadIdx.x == 0) report(a.status, DS4A_DEV_BOUNDS);
-    m.ru = u;
-    m.unit = u * a.hsplit + static_cast<int>(blockIdx.x % a.hsplit);
-    m.split = lt0 > 0 || lt1 < max(tiles, 1);
-    m.slot = 2LL * blockIdx.x + (i == 0 ? 0 : 1);
-    m.cnt = l.cnt;
-    m.lim = l.lim;
-    m.nrw = l.nrw;
-    m.ct = (l.cnt + TR - 1) / TR;
-    m.t0 = lt0;
-    m.t1 = min(tiles, lt1);
-    m.raw_row0 = l.ring * a.raw_per_unit;
-    m.comp_row0 = 0;                                    // listed rows are turned into rows of the pool
-    return m;
-}
-
 // Piece i of this CTA's schedule.
-template <bool PAGED>
 DS4A_DEV Item make_piece(const AttnArgs &a, const Sched &sc, int i) {
-    if constexpr (PAGED) return make_paged_piece(a, sc, i);
     Item m;
     int lt0 = 0, lt1 = sc.nt;
     if (i < sc.R) {
@@ -450,20 +207,7 @@ DS4A_DEV Item make_piece(const AttnArgs &a, const Sched &sc, int i) {
     return m;
 }
 
-DS4A_DEV void tmem_ld16x256_x8(uint32_t taddr, uint32_t (&r)[32]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
-          "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
-          "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
-          "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr));
-}
-
-template <int GW, bool PAGED>
+template <int GW>
 __global__ void __launch_bounds__(attn_threads(GW), 1) sparse_attn_kernel(const __grid_constant__ AttnArgs a, int nt,
                                                                           int g_rem) {
     constexpr int kGatherWarps = GW;
@@ -521,24 +265,18 @@ __global__ void __launch_bounds__(attn_threads(GW), 1) sparse_attn_kernel(const 
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const long long n_slots = 2LL * gridDim.x;
-    Sched sc;
-    if constexpr (PAGED) {
-        pdl_wait();                              // the lengths may come from the kernel before
-        sc = make_paged_sched(a, a.ws ? paged_merge_info(a, gridDim.x) : nullptr);
-    } else {
-        sc = make_sched(a, nt, g_rem);
-        if (threadIdx.x == 0 && sc.n_pieces > 0) {
-            // q of the first piece into L2 while the previous kernel finishes
-            // (a prefetch cannot go stale: L2 is the point of coherence)
-            const long long u0 = sc.R > 0 ? blockIdx.x : sc.u_rem0 + sc.v0;
-            prefetch_l2(a.q + u0 * kNHead * kHeadDim, kNHead * kHeadDim * 2);
-        }
-        pdl_wait();                              // the set-up above reads no global memory
+    const Sched sc = make_sched(a, nt, g_rem);
+    if (threadIdx.x == 0 && sc.n_pieces > 0) {
+        // q of the first piece into L2 while the previous kernel finishes
+        // (a prefetch cannot go stale: L2 is the point of coherence)
+        const long long u0 = sc.R > 0 ? blockIdx.x : sc.u_rem0 + sc.v0;
+        prefetch_l2(a.q + u0 * kNHead * kHeadDim, kNHead * kHeadDim * 2);
     }
+    pdl_wait();                                  // the set-up above reads no global memory
     const uint32_t tmem = *tmem_slot;
     const float NEG_INF = -__int_as_float(0x7f800000);
     const int u_end = sc.n_pieces;               // pieces 0 .. n_pieces-1
+    const long long n_slots = 2LL * gridDim.x;
 
     if (warp >= kFirstGatherWarp) {
         // ------------------------------------------------------------ row gather
@@ -553,7 +291,7 @@ __global__ void __launch_bounds__(attn_threads(GW), 1) sparse_attn_kernel(const 
         bool ok = true;
         auto first_tile = [&](int u, Item &m) -> int {
             for (; u < u_end; ++u) {
-                m = make_piece<PAGED>(a, sc, u);
+                m = make_piece(a, sc, u);
                 if (m.t0 < m.t1) return u;
             }
             return u_end;
@@ -564,26 +302,6 @@ __global__ void __launch_bounds__(attn_threads(GW), 1) sparse_attn_kernel(const 
                 u = first_tile(u + 1, m);
                 t = u < u_end ? m.t0 : 0;
                 ++ordinal;
-            }
-        };
-        // Paged: the pool row of a unit's row v; -1 when v is not one of its rows or
-        // its page is not in the pool.
-        auto pool_row = [&](const Item &m, int v) -> int {
-            if (v < 0 || v >= m.lim) return -1;
-            const int page = __ldg(a.table + m.ru * a.table_stride + (v >> a.page_shift));
-            return page < 0 || page >= a.n_pages ? -1 : (page << a.page_shift) + (v & ((1 << a.page_shift) - 1));
-        };
-        // Paged, dense row lists: lane i < 64 / box of the first gather warp holds
-        // the pool row of piece i of the next whole tile (past the pool's end for a
-        // page outside it: its box is filled with zeros).
-        const int box = PAGED ? min(TR, 1 << a.page_shift) : TR;
-        int y_next = 0;
-        auto fetch_boxes = [&](const Item &m, int t) {
-            if constexpr (PAGED) {
-                if (gw == 0 && lane * box < TR && t < m.ct && (t + 1) * TR <= m.cnt) {
-                    const int y = pool_row(m, t * TR + lane * box);
-                    y_next = y < 0 ? a.n_pages << a.page_shift : y;
-                }
             }
         };
         // Row list entries of tile t for this lane (< 0: masked).
@@ -600,7 +318,6 @@ __global__ void __launch_bounds__(attn_threads(GW), 1) sparse_attn_kernel(const 
                     // no idx: the row list is 0 .. count-1 (dense attention)
                     const int jj = t * TR + r;
                     rv[k] = jj < m.cnt ? (a.idx ? __ldg(a.idx + static_cast<long long>(m.ru) * a.top_k + jj) : jj) : -1;
-                    if constexpr (PAGED) rv[k] = pool_row(m, rv[k]);
                 } else {
                     const int jj = (t - m.ct) * TR + r;
                     rv[k] = jj < m.nrw ? jj : -1;
@@ -608,9 +325,6 @@ __global__ void __launch_bounds__(attn_threads(GW), 1) sparse_attn_kernel(const 
             }
         };
         auto row_index = [&](const Item &m, int t, int v) -> int {
-            if constexpr (PAGED) {
-                if (t < m.ct) return v;
-            }
             if (t < m.ct) return (v < 0 || v >= a.N_cap) ? -1 : static_cast<int>(m.comp_row0 + v);
             return v < 0 ? -1 : static_cast<int>(m.raw_row0 + v);
         };
@@ -622,12 +336,8 @@ __global__ void __launch_bounds__(attn_threads(GW), 1) sparse_attn_kernel(const 
         auto prefetch_next = [&](int u, int t, const Item &m) {
             if (u >= u_end || a.idx || a.rows8 || t >= m.ct) return;
             const int nfirst = t * TR;
-            if constexpr (PAGED) {
-                if (a.tma_rows && nfirst + TR <= m.cnt && gw == 0 && lane * box < TR && y_next < a.n_pages << a.page_shift)
-                    prefetch_l2(a.rows + static_cast<long long>(y_next) * kHeadDim, static_cast<uint32_t>(box) * kHeadDim * 2);
-            } else if (a.tma_rows && nfirst + TR <= m.cnt && gw == 0 && lane == 0) {
+            if (a.tma_rows && nfirst + TR <= m.cnt && gw == 0 && lane == 0)
                 prefetch_l2(a.rows + (m.comp_row0 + nfirst) * kHeadDim, TR * kHeadDim * 2);
-            }
         };
         auto nibble = [](uint32_t bal) -> uint32_t {   // lanes 0, 8, 16, 24 -> bits 0..3
             return (bal & 1u) | ((bal >> 7) & 2u) | ((bal >> 14) & 4u) | ((bal >> 21) & 8u);
@@ -637,12 +347,7 @@ __global__ void __launch_bounds__(attn_threads(GW), 1) sparse_attn_kernel(const 
         int ct_ = cit < u_end ? cm.t0 : 0;
         uint32_t jt = 0;
         int rv[kGroupsPerWarp];
-        auto fetch_tile = [&]() {
-            if (cit >= u_end) return;
-            fetch_rows(cm, ct_, rv);
-            if (PAGED && !a.idx) fetch_boxes(cm, ct_);
-        };
-        fetch_tile();
+        if (cit < u_end) fetch_rows(cm, ct_, rv);
         while (ok && cit < u_end) {
             if (ct_ == cm.t0 && gw == 0) {
                 // First tile of an item: q (bf16) by TMA once the previous item's
@@ -705,11 +410,10 @@ __global__ void __launch_bounds__(attn_threads(GW), 1) sparse_attn_kernel(const 
             // The row list of the next tile: before the wait, except for a
             // cp.async tile, where it goes out right after the copies.
             const long long y_tma = (raw_tile ? cm.raw_row0 : cm.comp_row0) + first;
-            const int y_box = y_next;
             const bool early_next = fp8_tile || tma_tile;
             if (early_next) {
                 advance(cit, ct_, cm);
-                fetch_tile();
+                if (cit < u_end) fetch_rows(cm, ct_, rv);
                 prefetch_next(cit, ct_, cm);
             }
             const int xb = jt & 1;
@@ -724,16 +428,7 @@ __global__ void __launch_bounds__(attn_threads(GW), 1) sparse_attn_kernel(const 
                 if (lane == 0 && g < kRowGroups) sValid[xb * kRowGroups + g] = static_cast<uint8_t>(nibble(bal));
             }
             const uint32_t buf = smem_u32(sX) + xb * kXBuf;
-            if (PAGED && tma_tile && !raw_tile) {
-                if (gw == 0) {
-                    if (lane == 0) mbar_arrive_expect_tx(&x_full[xb], kXBuf);   // also this warp's arrival
-                    __syncwarp();
-                    if (lane * box < TR)
-                        for (int b = 0; b < 8; ++b)
-                            tma_load_2d_nohint(sX + xb * kXBuf + b * kXBlk + lane * box * 128, &a.tm_rows, &x_full[xb],
-                                               b * 64, y_box);
-                }
-            } else if (tma_tile && gw == 0 && lane == 0) {
+            if (tma_tile && gw == 0 && lane == 0) {
                 const int y = static_cast<int>(y_tma);
                 mbar_arrive_expect_tx(&x_full[xb], kXBuf);      // also this warp's arrival
                 for (int b = 0; b < 8; ++b)
@@ -785,7 +480,7 @@ __global__ void __launch_bounds__(attn_threads(GW), 1) sparse_attn_kernel(const 
                 }
                 cp_async_commit();
                 advance(cit, ct_, cm);
-                fetch_tile();
+                if (cit < u_end) fetch_rows(cm, ct_, rv);
                 prefetch_next(cit, ct_, cm);
                 cp_async_wait<0>();
             }
@@ -809,7 +504,7 @@ __global__ void __launch_bounds__(attn_threads(GW), 1) sparse_attn_kernel(const 
         const uint64_t dq = sw128_desc(smem_u32(sQ), 16, 1024), dx0 = sw128_desc(smem_u32(sX), 16, 1024);
         uint32_t js = 0;                                     // tile counter: buffers js & 1
         for (int i = 0; ok && i < sc.n_pieces; ++i) {
-            const Item m = make_piece<PAGED>(a, sc, i);
+            const Item m = make_piece(a, sc, i);
             if (m.t0 >= m.t1) continue;
             if (!(ok = warp_wait(q_full, qph, abort_flag))) break;
             qph ^= 1;
@@ -859,7 +554,7 @@ __global__ void __launch_bounds__(attn_threads(GW), 1) sparse_attn_kernel(const 
         const uint64_t dxv = sw128_desc(smem_u32(sX), kXBlk, 1024), dp = sw128_desc(smem_u32(sP), 16, 1024);
         uint32_t jv = 0;
         for (int i = 0; ok && i < sc.n_pieces; ++i) {
-            const Item m = make_piece<PAGED>(a, sc, i);
+            const Item m = make_piece(a, sc, i);
             if (m.t0 >= m.t1) continue;
             for (int t = m.t0; t < m.t1; ++t, ++jv) {
                 const int b = jv & 1;
@@ -931,17 +626,12 @@ __global__ void __launch_bounds__(attn_threads(GW), 1) sparse_attn_kernel(const 
             if (lane == 0) mbar_arrive(q16_ready);
         };
         for (int i = 0; ok && i < sc.n_pieces; ++i) {
-            const Item m = make_piece<PAGED>(a, sc, i);
+            const Item m = make_piece(a, sc, i);
             if (m.t0 >= m.t1) {
                 // Empty row set: out = 0, lse = -inf (or an empty partial).
                 if (!m.split) {
-                    if constexpr (PAGED) {
-                        uint32_t *o = reinterpret_cast<uint32_t *>(a.out16 + static_cast<long long>(m.unit) * kNHead * kHeadDim);
-                        for (int k = e; k < kNHead * kHeadDim / 2; k += kSoftmaxWarps * 32) o[k] = 0u;
-                    } else {
-                        float *o = a.out + static_cast<long long>(m.unit) * kNHead * kHeadDim;
-                        for (int k = e; k < kNHead * kHeadDim; k += kSoftmaxWarps * 32) o[k] = 0.f;
-                    }
+                    float *o = a.out + static_cast<long long>(m.unit) * kNHead * kHeadDim;
+                    for (int k = e; k < kNHead * kHeadDim; k += kSoftmaxWarps * 32) o[k] = 0.f;
                     if (a.lse && e < kNHead) a.lse[static_cast<long long>(m.unit) * kNHead + e] = NEG_INF;
                 } else if (e < kNHead) {
                     float *ml = static_cast<float *>(a.ws) + n_slots * kNHead * kHeadDim;
@@ -1133,8 +823,8 @@ __global__ void __launch_bounds__(attn_threads(GW), 1) sparse_attn_kernel(const 
             ok = __all_sync(0xffffffffu, mbar_wait(&x_empty[(jt - 1) & 1], ((jt - 1) >> 1) & 1, abort_flag));
             if (!ok) break;
             tc_fence_after();
-            float *obase = !PAGED && !m.split ? a.out + static_cast<long long>(m.unit) * kNHead * kHeadDim
-                                              : static_cast<float *>(a.ws) + slot * kNHead * kHeadDim;
+            float *obase = !m.split ? a.out + static_cast<long long>(m.unit) * kNHead * kHeadDim
+                                        : static_cast<float *>(a.ws) + slot * kNHead * kHeadDim;
             // 1/l of the 64 heads in registers: no shared load between the
             // global stores below.
             float il[kNHead];
@@ -1145,20 +835,6 @@ __global__ void __launch_bounds__(attn_threads(GW), 1) sparse_attn_kernel(const 
                 tmem_ld32(tmem + lane_off + kTmemO + c * 32, v);
                 tmem_wait_ld(v);
                 const int d = (c >> 1) * 128 + q4 * 32 + lane;
-                if (PAGED && !m.split) {
-                    // bf16, two dims a store: of each pair of heads an even lane takes
-                    // the first and an odd lane the second, with its neighbour's dim
-                    uint16_t *o = a.out16 + (static_cast<long long>(m.unit) * kNHead + (c & 1) * 32 + (lane & 1)) * kHeadDim + (d & ~1);
-#pragma unroll
-                    for (int k = 0; k < 32; k += 2) {
-                        const float x0 = __uint_as_float(v[k]) * ((c & 1) ? il[32 + k] : il[k]);
-                        const float x1 = __uint_as_float(v[k + 1]) * ((c & 1) ? il[33 + k] : il[k + 1]);
-                        const float other = __shfl_xor_sync(0xffffffffu, (lane & 1) ? x0 : x1, 1);
-                        *reinterpret_cast<uint32_t *>(o + k * kHeadDim) =
-                            (lane & 1) ? pack2<false>(other, x1) : pack2<false>(x0, other);
-                    }
-                    continue;
-                }
 #pragma unroll
                 for (int k = 0; k < 32; ++k) {
                     const int h = (c & 1) * 32 + k;
@@ -1256,10 +932,6 @@ DS4A_DEV float4 merge_pieces(const float *wo, const float *ml, int h, int np, Sl
     acc.w *= inv;
     return acc;
 }
-DS4A_DEV float merged_lse(float M, float L) {
-    return L > 0.f ? (M + log2f(L)) * 0.6931471805599453f : -__int_as_float(0x7f800000);
-}
-
 // Combines the pieces of the remainder units that straddle a share boundary.
 // Block (v, h): head h of remainder unit v, whose tiles [v nt, (v+1) nt) of the
 // remainder tile space lie in the shares of CTAs c0 .. c1 (share c: tiles
@@ -1291,36 +963,6 @@ __global__ void __launch_bounds__(kMergeThreads) attn_merge_kernel(const __grid_
     if (a.lse && threadIdx.x == 0) a.lse[u * kNHead + h] = merged_lse(M, L);
 }
 
-// The paged batch's merge.  Only a unit that holds a share boundary is in
-// pieces: block (b, head) looks at the boundary between shares b and b + 1 and
-// combines the unit around it when this is the unit's first boundary.
-__global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid_constant__ AttnArgs a, int shares) {
-    pdl_launch_dependents();
-    pdl_wait();
-    const int heads = kNHead * a.hsplit, ctas = shares * a.hsplit;
-    const int b = blockIdx.x / heads, head = blockIdx.x - b * heads;
-    const int half = head / kNHead, h = head - half * kNHead;
-    const int4 *info = paged_merge_info(a, ctas);
-    const int T = info[0].w;
-    const int g = min(shares, T);
-    if (b + 1 >= g) return;
-    const int4 first = info[b + 1];                         // share b + 1's first unit, its first tile, its tiles
-    auto share_start = [&](int c) -> int { return static_cast<int>(static_cast<long long>(c) * T / g); };
-    if (share_start(b + 1) == first.y || share_start(b) > first.y) return;   // no unit cut, or an earlier boundary's
-    const int c0 = b, c1 = static_cast<int>((static_cast<long long>(first.y + first.z) * g - 1) / T);
-    const bool at_start = share_start(b) == first.y;
-    auto piece_slot = [&](int i) -> long long {
-        return 2LL * ((c0 + i) * a.hsplit + half) + (i == 0 && !at_start ? 1 : 0);
-    };
-    const float *wo = static_cast<const float *>(a.ws);
-    float M, L;
-    const float4 acc = merge_pieces(wo, wo + 2LL * ctas * kNHead * kHeadDim, h, c1 - c0 + 1, piece_slot, M, L);
-    const long long row = (static_cast<long long>(first.x) * a.hsplit + half) * kNHead + h;
-    *reinterpret_cast<uint2 *>(a.out16 + row * kHeadDim + threadIdx.x * 4) =
-        make_uint2(pack2<false>(acc.x, acc.y), pack2<false>(acc.z, acc.w));
-    if (a.lse && threadIdx.x == 0) a.lse[row] = merged_lse(M, L);
-}
-
 // Tiles per unit in the tile space: the top_k compressed rows and the raw window.
 int attn_tiles_per_unit(int top_k) { return (top_k + TR - 1) / TR + (kNSwa + TR - 1) / TR; }
 
@@ -1337,7 +979,7 @@ size_t attn_ws_bytes(int units, int top_k) {
 cudaError_t launch_sparse_attn(const AttnArgs &a, int num_sms, cudaStream_t s) {
     const int gw = (a.idx == nullptr && a.rows8 == nullptr) ? kGatherWarpsDense : kGatherWarpsList;
     void (*kern)(AttnArgs, int, int) =
-        gw == kGatherWarpsDense ? sparse_attn_kernel<kGatherWarpsDense, false> : sparse_attn_kernel<kGatherWarpsList, false>;
+        gw == kGatherWarpsDense ? sparse_attn_kernel<kGatherWarpsDense> : sparse_attn_kernel<kGatherWarpsList>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     if (e != cudaSuccess) return e;
     const int nt = attn_tiles_per_unit(a.top_k);
@@ -1354,36 +996,6 @@ cudaError_t launch_sparse_attn(const AttnArgs &a, int num_sms, cudaStream_t s) {
     if (e != cudaSuccess || g_rem <= 1) return e;
     return launch_k(attn_merge_kernel, dim3(static_cast<unsigned>(u_rem * kNHead)), dim3(kMergeThreads), 0, s, a, nt, g_rem,
                     static_cast<int>(G));
-}
-
-namespace {
-// Shares of a paged batch of U units of at most list_cap compressed rows: at
-// most one per CTA (per pair of CTAs with 128 heads) and per 64-row tile.
-long long paged_shares(int U, int hsplit, int list_cap, int max_ctas) {
-    const long long T = static_cast<long long>(U) * attn_tiles_per_unit(list_cap);
-    const long long most = max_ctas / hsplit;
-    return T < most ? T : most;
-}
-}  // namespace
-
-size_t paged_attn_ws_bytes(int U, int hsplit, int list_cap) {
-    const long long ctas = paged_shares(U, hsplit, list_cap, kMaxAttnCtas) * hsplit;
-    if (ctas <= hsplit) return 0;                           // one share: every unit whole
-    return static_cast<size_t>(ctas) * (2 * kNHead * (kHeadDim + 2) * sizeof(float) + sizeof(int4));
-}
-
-cudaError_t launch_paged_attn(const AttnArgs &a, int num_sms, cudaStream_t s) {
-    const int gw = (a.idx == nullptr && a.rows8 == nullptr) ? kGatherWarpsDense : kGatherWarpsList;
-    void (*kern)(AttnArgs, int, int) =
-        gw == kGatherWarpsDense ? sparse_attn_kernel<kGatherWarpsDense, true> : sparse_attn_kernel<kGatherWarpsList, true>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-    if (e != cudaSuccess) return e;
-    const int shares = static_cast<int>(paged_shares(a.units / a.hsplit, a.hsplit, a.top_k,
-                                                     num_sms < kMaxAttnCtas ? num_sms : kMaxAttnCtas));
-    e = launch_k(kern, dim3(static_cast<unsigned>(shares * a.hsplit)), dim3(attn_threads(gw)), kSmemBytes, s, a, 0, 0);
-    if (e != cudaSuccess || shares <= 1) return e;
-    return launch_k(paged_merge_kernel, dim3(static_cast<unsigned>((shares - 1) * kNHead * a.hsplit)), dim3(kMergeThreads), 0,
-                    s, a, shares);
 }
 
 }  // namespace ds4a

@@ -97,7 +97,7 @@ def test_attention_unsupported(lib, change):
 def test_attention_workspace(lib, heads, flag):
     need = B.ds4a_workspace_bytes(B.DS4A_OP_PAGED_ATTN_DECODE | flag, 2, 1, 256, 0)
     slot = 2 * 64 * 514 * 4 + 16          # two partials and one share record per CTA
-    assert need == 2 * 6 * (heads // 64) * slot        # 2 units x (4 + 2) tiles
+    assert need == 2 * 9 * (heads // 64) * slot        # 2 units x (6 + 3) tiles of 48 rows
     for change in (dict(ws_bytes=need - 1), dict(ws=None), dict(ws=FAKE + 16)):
         assert call(lib.ds4a_paged_attn_decode, ATTN, n_head=heads, **change) == B.DS4A_EWORKSPACE
     most = 160 * slot
