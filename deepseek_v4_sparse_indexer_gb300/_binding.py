@@ -32,7 +32,7 @@ DS4A_OP_PAGED_ATTN_DECODE = 6
 DS4A_OP_FLAG_128_HEADS = 0x100
 DS4A_BF16, DS4A_F16, DS4A_F32, DS4A_E4M3 = 0, 1, 2, 3
 DS4A_ROPE_NEIGHBOURS, DS4A_ROPE_HALVES = 0, 1
-DS4A_MIN_PAGE, DS4A_MAX_PAGE, DS4A_MAX_PLAN_SEQS = 8, 4096, 16384
+DS4A_MIN_PAGE, DS4A_MAX_PAGE, DS4A_MAX_PLAN_SEQS = 8, 4096, 8192
 
 N_HEAD, HEAD_DIM, N_IDX_HEAD, IDX_DIM, N_SWA = 64, 512, 64, 128, 128
 

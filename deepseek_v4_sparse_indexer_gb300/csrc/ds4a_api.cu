@@ -615,10 +615,32 @@ ds4a_status ds4a_paged_plan(const int32_t *past, const int32_t *add, int B, int 
         return DS4A_EINVAL;
     DevInfo *di = nullptr;
     if (ds4a_status st = current_device(&di)) return st;
-    const PagedPlanArgs a{past,   add,    B,      ratio,    shift, free_pages, n_free,   free_head,
-                          free_head_out,  table,  table_stride,  max_pages, ring,  n_rows,     n_raw,    cu_tok,
-                          cu_row, tok_pos, raw_slot, T_cap,  row_pos, row_slot, R_cap,    di->status};
-    return launch_paged_plan(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? DS4A_OK : DS4A_ECUDA;
+    PagedPlanArgs a{};
+    a.past = past;
+    a.add = add;
+    a.B = B;
+    a.ratio = ratio;
+    a.shift = shift;
+    a.free_pages = free_pages;
+    a.n_free = n_free;
+    a.free_head = free_head;
+    a.free_head_out = free_head_out;
+    a.table = table;
+    a.table_stride = table_stride;
+    a.max_pages = max_pages;
+    a.ring = ring;
+    a.n_rows = n_rows;
+    a.n_raw = n_raw;
+    a.cu_tok = cu_tok;
+    a.cu_row = cu_row;
+    a.tok_pos = tok_pos;
+    a.raw_slot = raw_slot;
+    a.T_cap = T_cap;
+    a.row_pos = row_pos;
+    a.row_slot = row_slot;
+    a.R_cap = R_cap;
+    a.status = di->status;
+    return launch_paged_plan(a, di->sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? DS4A_OK : DS4A_ECUDA;
 }
 
 ds4a_status ds4a_qk_norm_rope(const void *q, int q_type, int64_t q_tok_stride, const void *k, int k_type,

@@ -147,8 +147,9 @@ struct PagedPlanArgs {
     int32_t *row_pos, *row_slot;
     int R_cap;
     uint32_t *status;
+    int cluster;                 // set by the launcher: the CTAs are one cluster
 };
-cudaError_t launch_paged_plan(const PagedPlanArgs &a, cudaStream_t s);
+cudaError_t launch_paged_plan(PagedPlanArgs a, int num_sms, cudaStream_t s);
 
 struct PagedAttnArgs {
     CUtensorMap tm_q;            // bf16 (64 dims, U * hsplit * 64 rows, 8 column blocks), box (64, 64, 8), 128B swizzle

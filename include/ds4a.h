@@ -100,7 +100,7 @@ typedef int ds4a_status;
 /* Page sizes of a paged cache: a power of two of rows in this range. */
 #define DS4A_MIN_PAGE 8
 #define DS4A_MAX_PAGE 4096
-#define DS4A_MAX_PLAN_SEQS 16384 /* sequences of one ds4a_paged_plan call       */
+#define DS4A_MAX_PLAN_SEQS 8192 /* sequences of one ds4a_paged_plan call        */
 
 /* Human-readable text of a status code (static storage). */
 const char *ds4a_strerror(ds4a_status status);

@@ -67,7 +67,7 @@ def status(lib):
     return lib.ds4a_get_device_status()
 
 
-@pytest.mark.parametrize("B", [1, 2, 33, 1025, 16384])
+@pytest.mark.parametrize("B", [1, 2, 33, 1025, 8192])
 @pytest.mark.parametrize("ratio,P", [(4, 64), (128, 8), (1, 4096), (3, 16)])
 def test_decode_steps(cuda_lib, B, ratio, P):
     rng = random.Random(B * 1000 + ratio)
