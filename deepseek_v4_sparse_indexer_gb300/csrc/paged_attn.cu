@@ -18,19 +18,20 @@
 // copies are issued before the previous one's have landed.
 //
 // Roles (one CTA per SM, persistent over its share of the batch's tiles):
-//   lookup   warp 6: turns a tile's rows (listed ones: row number, then page; dense
+//   lookup   warp 10: turns a tile's rows (listed ones: row number, then page; dense
 //            ones: page) into rows of the pool, up to three tiles ahead, and hands
 //            them over in shared memory, so that no other warp waits for a lookup;
 //            a dense list's pieces go into L2 on the way;
-//   gather   warps 7..: bring a tile's rows into one of three buffers.  Listed rows
+//   gather   warps 11..: bring a tile's rows into one of three buffers.  Listed rows
 //            and ragged ends: 16-byte cp.async, masked rows zero-filled, 4-row
 //            groups dealt to the warps.  Dense lists and the raw window: TMA, one box
 //            per 16 rows of a page (8 with pages of 8 rows), boxes past the list's end
 //            or outside the pool read past the end of the tensor map, which fills
 //            zeros.  FP8 rows: codes to registers, written out as exact bf16.
-//   logits   warp 4: S[64 heads x 48 rows] = q . X^T into one of two TMEM buffers;
-//   softmax  warps 0-3: S out of TMEM, running max (raised only past 2^8), P;
-//   values   warp 5: O^T[512 dims x 64 heads] += X^T . P^T in TMEM.
+//   logits   warp 8: S[64 heads x 48 rows] = q . X^T into one of two TMEM buffers;
+//   softmax  warps 0-3 and 4-7, tiles in turn: S out of TMEM, running max (raised
+//            only past 2^8), P;
+//   values   warp 9: O^T[512 dims x 64 heads] += X^T . P^T in TMEM.
 // A row tile is stored as 8-row groups of eight 8 x 64 column blocks (1 KB each,
 // 128B-swizzled), so that one box of a row matrix seen as (64 dims, 8 rows, 8
 // blocks, groups) lands as whole groups; the UMMA descriptors then step 8 KB from
@@ -53,16 +54,17 @@ namespace {
 
 constexpr int TR = 48;                        // rows per tile
 constexpr int kBufs = 3;                      // row buffers
-constexpr int kSoftmaxWarps = 4;              // warps 0-3: softmax + epilogue (TMEM lane quarters)
-constexpr int kMmaWarp = 4;                   // warp 4: TMEM owner + logits UMMA issuer
-constexpr int kPvWarp = 5;                    // warp 5: values UMMA issuer
-constexpr int kLookWarp = 6;                  // warp 6: row lookup
-constexpr int kFirstGatherWarp = 7;
+constexpr int kGroupWarps = 4;                // a softmax group: one warp per TMEM lane quarter
+constexpr int kSoftmaxWarps = 8;              // warps 0-3, 4-7: two groups, taking the tiles in turn; epilogue
+constexpr int kMmaWarp = 8;                   // warp 8: TMEM owner + logits UMMA issuer
+constexpr int kPvWarp = 9;                    // warp 9: values UMMA issuer
+constexpr int kLookWarp = 10;                 // warp 10: row lookup
+constexpr int kFirstGatherWarp = 11;
 constexpr int kRowGroups = TR / 4;            // 4-row groups of a tile, dealt round-robin to the gather warps
-// Gather warps: four copy bf16 rows (two tiles in flight); the expansion of FP8
-// codes is arithmetic, so eight.
-constexpr int kGatherWarpsBf16 = 4;
-constexpr int kGatherWarpsFp8 = 8;
+// Gather warps: five copy bf16 rows (two tiles in flight); the expansion of FP8
+// codes is arithmetic, so nine.
+constexpr int kGatherWarpsBf16 = 5;
+constexpr int kGatherWarpsFp8 = 9;
 constexpr int threads_of(int gw) { return (kFirstGatherWarp + gw) * 32; }
 constexpr int kQBlk = kNHead * 128;           // 64 heads x 64 dims: 8 KB
 constexpr int kXBlk = 1024;                   // 8 rows x 64 dims
@@ -76,9 +78,8 @@ constexpr int kOffRows = kOffP + 2 * kPBuf;   // [kBufs] looked-up tiles (RowSlo
 constexpr int kOffValid = kOffRows + kBufs * 256;   // [kBufs] bit r: tile row r is listed and in the pool
 constexpr int kOffAlpha = kOffValid + 32;
 constexpr int kOffFlag = kOffAlpha + 2 * kNHead * 4;
-constexpr int kOffInvL = kOffFlag + 2 * kSoftmaxWarps * 4;
-constexpr int kOffBar = kOffInvL + kNHead * 4;
-constexpr int kNumBars = 4 * kBufs + 6 + 7;
+constexpr int kOffBar = kOffFlag + 2 * kGroupWarps * 4;
+constexpr int kNumBars = 4 * kBufs + 6 + 6 + 3 + kSoftmaxWarps;
 constexpr int kOffMisc = kOffBar + kNumBars * 8;
 constexpr int kSmemBytes = kOffMisc + 16 + 1024;
 static_assert(kOffP % 1024 == 0 && kOffAlpha % 16 == 0 && kOffFlag % 16 == 0 && kOffBar % 8 == 0, "alignment");
@@ -285,7 +286,6 @@ __global__ void __launch_bounds__(threads_of(GW), 1) paged_attn_kernel(const __g
     uint2 *sValid = reinterpret_cast<uint2 *>(smem + kOffValid);
     float *sAlpha = reinterpret_cast<float *>(smem + kOffAlpha);        // [2][64] this tile's rescale factor per head
     uint32_t *sFlag = reinterpret_cast<uint32_t *>(smem + kOffFlag);    // [2][4] softmax warp raised a head's max
-    float *sInvL = reinterpret_cast<float *>(smem + kOffInvL);
     uint64_t *x_full = reinterpret_cast<uint64_t *>(smem + kOffBar);   // [kBufs] row tile landed
     uint64_t *x_empty = x_full + kBufs;                                // [kBufs] values GEMM done: row tile (and P) free
     uint64_t *r_full = x_empty + kBufs;                                // [kBufs] rows looked up
@@ -299,7 +299,9 @@ __global__ void __launch_bounds__(threads_of(GW), 1) paged_attn_kernel(const __g
     uint64_t *o_free = q16_ready + 1;
     uint64_t *drain = o_free + 1;
     uint64_t *drain_v = drain + 1;
-    uint64_t *grp = drain_v + 1;                                       // softmax-group barrier
+    uint64_t *grp = drain_v + 1;                                       // [2] barrier of a softmax group
+    uint64_t *all = grp + 2;                                           // barrier of both
+    uint64_t *tok = all + 1;                                           // [8] a softmax warp has set its heads' running max
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + kOffMisc);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kOffMisc + 4);
 
@@ -313,16 +315,18 @@ __global__ void __launch_bounds__(threads_of(GW), 1) paged_attn_kernel(const __g
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&s_full[b], 1);
-            mbar_init(&s_empty[b], kSoftmaxWarps);
-            mbar_init(&p_full[b], kSoftmaxWarps);
+            mbar_init(&s_empty[b], kGroupWarps);
+            mbar_init(&p_full[b], kGroupWarps);
+            mbar_init(&grp[b], kGroupWarps);
         }
         mbar_init(q_full, 1);
         mbar_init(q_free, 1 + kSoftmaxWarps);  // the item's last logits GEMM + each softmax warp past its q wait
-        mbar_init(q16_ready, kSoftmaxWarps);
+        mbar_init(q16_ready, kGroupWarps);
         mbar_init(o_free, kSoftmaxWarps);
         mbar_init(drain, 1);
         mbar_init(drain_v, 1);
-        mbar_init(grp, kSoftmaxWarps);
+        mbar_init(all, kSoftmaxWarps);
+        for (int w = 0; w < kSoftmaxWarps; ++w) mbar_init(&tok[w], 1);
         *abort_flag = 0;
         mbar_fence_init();
         tma_prefetch_desc(&a.tm_q);
@@ -444,7 +448,7 @@ __global__ void __launch_bounds__(threads_of(GW), 1) paged_attn_kernel(const __g
         auto wait_for = [&](uint64_t *bar, uint32_t parity) -> bool {
             if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
             settle(false);
-            return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
+            return __all_sync(0xffffffffu, mbar_wait_hint(bar, parity, abort_flag));
         };
         for (;;) {
             if (!(ok = wait_for(&r_full[xb], (rph >> xb) & 1))) break;
@@ -512,17 +516,21 @@ __global__ void __launch_bounds__(threads_of(GW), 1) paged_attn_kernel(const __g
             }
             const uint32_t buf = smem_u32(dst);
             if (!tma_tile && !fp8_tile) {
-                const uint16_t *base = (raw_tile ? a.raw : a.rows) + chunk * 8;
+                // One pair of addresses per row, the blocks at constant steps from it
+                // (a masked row copies no bytes; its address is q's).
+                const uint16_t *from[kGroups];
+                uint32_t to[kGroups];
+#pragma unroll
+                for (int k = 0; k < kGroups; ++k) {
+                    const int r = row_of(k);
+                    from[k] = (src[k] < 0 ? a.q : (raw_tile ? a.raw : a.rows) + static_cast<long long>(src[k]) * kHeadDim) + chunk * 8;
+                    to[k] = buf + (r >> 3) * kXGroup + (r & 7) * 128 + ((chunk ^ (r & 7)) << 4);
+                }
 #pragma unroll
                 for (int b = 0; b < 8; ++b) {
 #pragma unroll
-                    for (int k = 0; k < kGroups; ++k) {
-                        const int r = row_of(k);
-                        if (r < TR)
-                            cp_async16(buf + (r >> 3) * kXGroup + b * kXBlk + (r & 7) * 128 + ((chunk ^ (r & 7)) << 4),
-                                       src[k] >= 0 ? base + static_cast<long long>(src[k]) * kHeadDim + b * 64 : a.q,
-                                       src[k] >= 0 ? 16u : 0u);
-                    }
+                    for (int k = 0; k < kGroups; ++k)
+                        if (gw + k * GW < kRowGroups) cp_async16(to[k] + b * kXBlk, from[k] + b * 64, src[k] >= 0 ? 16u : 0u);
                 }
                 cp_async_commit();
                 settle(true);
@@ -664,38 +672,40 @@ __global__ void __launch_bounds__(threads_of(GW), 1) paged_attn_kernel(const __g
         __syncwarp();
     } else {
         // ------------------------------------------------------------ softmax + epilogue
-        // Warp w = TMEM lane quarter w.  Logits (16x256b loads): thread t holds
-        // heads h0 = 16w + t/4 and h1 = h0 + 8 for tile rows 8j + 2(t%4) + {0,1},
-        // j = 0..5 (registers 4j, 4j+1: h0; 4j+2, 4j+3: h1).  Values: lane = dim.
+        // Group g = warps 4g .. 4g+3 takes the CTA's tiles d with d % 2 = g (so S and
+        // P buffer g), warp w of it TMEM lane quarter w.  Logits (16x256b loads):
+        // thread t holds heads h0 = 16w + t/4 and h1 = h0 + 8 for tile rows 8j +
+        // 2(t%4) + {0,1}, j = 0..5 (registers 4j, 4j+1: h0; 4j+2, 4j+3: h1).  Values:
+        // lane = dim.  What must go tile by tile is the heads' running max: a warp
+        // takes it from the warp of the other group that had the tile before, and
+        // hands it on before its exponentials.  (One group for all tiles was the
+        // pipeline's slowest stage: 1.3 us of the 1.5 us per tile.)
+        // A row of P uses 96 of its 128 bytes; its other 16-byte chunks hold
+        //   chunk 6  the head's running max after the tile,
+        //   chunk 7  at the end of item i, at i % 2: the group's sum and the max that
+        //            the sum is relative to.
         constexpr int J = TR / 8;
-        const int q4 = warp;
+        const int b = warp >> 2;                        // group; its S and P buffer
+        const int q4 = warp & 3;
         const int t4 = lane & 3;
         const int h0 = 16 * q4 + (lane >> 2), h1 = h0 + 8;
-        const int e = threadIdx.x;                      // 0..127 inside the softmax group
+        const int e = threadIdx.x & 127;                // thread of the group
         const uint32_t lane_off = static_cast<uint32_t>(q4 * 32) << 16;
         const float sl2 = a.scale * 1.4426950408889634f;
-        uint32_t qph = 0, gph = 0, sfph = 0;
-        int b = 0, xb = 0;                              // buffers of this tile: S, P and flags; rows
-        uint32_t xph = 0, vph = 0;                      // parity bits per row buffer: x_full of this tile, x_empty
+        uint32_t qph = 0, gph = 0, aph = 0;
+        uint32_t d = 0;                                 // the CTA's tiles so far
         bool ok = true;
-        // The values GEMM of the tile `back` tiles ago (its buffer's latest use).
-        auto wait_values = [&](int back) -> bool {
-            const int pb = xb >= back ? xb - back : xb + kBufs - back;
-            return __all_sync(0xffffffffu, mbar_wait(&x_empty[pb], ((vph >> pb) & 1) ^ 1, abort_flag));
+        auto head_info = [&](int buf, int h, int ch) -> float * {
+            return reinterpret_cast<float *>(sP + buf * kPBuf + h * 128 + ((ch ^ (h & 7)) << 4));
         };
-        // Barrier of the softmax warps on an mbarrier, so that a wait that gives
-        // up (abort) cannot leave the other warps stuck.
-        auto group_sync = [&]() -> bool {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(grp);
-            const bool r = __all_sync(0xffffffffu, mbar_wait(grp, gph, abort_flag));
-            gph ^= 1;
-            return r;
+        // The values GEMM of tile x (its row buffer's latest use).
+        auto wait_values = [&](uint32_t x) -> bool {
+            return __all_sync(0xffffffffu, mbar_wait_hint(&x_empty[x % kBufs], (x / kBufs) & 1, abort_flag));
         };
         auto convert_q = [&]() {
             // q -> fp16 in place for the fp16 raw tier (no logit GEMM reads q now).
             uint4 *qv = reinterpret_cast<uint4 *>(sQ);
-            for (int k = e; k < 8 * kQBlk / 16; k += kSoftmaxWarps * 32) {
+            for (int k = e; k < 8 * kQBlk / 16; k += kGroupWarps * 32) {
                 uint4 v = qv[k];
                 uint32_t *w = reinterpret_cast<uint32_t *>(&v);
 #pragma unroll
@@ -707,44 +717,35 @@ __global__ void __launch_bounds__(threads_of(GW), 1) paged_attn_kernel(const __g
             __syncwarp();
             if (lane == 0) mbar_arrive(q16_ready);
         };
-        uint32_t done = 0;                              // tiles of this CTA so far
         for (int i = 0; ok && i < sc.n_pieces; ++i) {
             const Item m = make_piece(a, sc, i);
             const long long unit = static_cast<long long>(m.u) * a.hsplit + half;
             const long long slot = 2LL * blockIdx.x + (i == 0 ? 0 : 1);   // a partial's slot: first piece 0, last piece 1
-            float *ml = static_cast<float *>(a.ws) + n_slots * kNHead * kHeadDim;
             if (m.t0 >= m.t1) {
                 // No row at all: out = 0, lse = -inf (such a unit is never split).
                 uint32_t *o = reinterpret_cast<uint32_t *>(a.out + unit * kNHead * kHeadDim);
-                for (int k = e; k < kNHead * kHeadDim / 2; k += kSoftmaxWarps * 32) o[k] = 0u;
-                if (a.lse && e < kNHead) a.lse[unit * kNHead + e] = NEG_INF;
+                for (int k = threadIdx.x; k < kNHead * kHeadDim / 2; k += kSoftmaxWarps * 32) o[k] = 0u;
+                if (a.lse && threadIdx.x < kNHead) a.lse[unit * kNHead + threadIdx.x] = NEG_INF;
                 continue;
             }
-            ok = __all_sync(0xffffffffu, mbar_wait(q_full, qph, abort_flag));
+            ok = __all_sync(0xffffffffu, mbar_wait_hint(q_full, qph, abort_flag));
             if (!ok) break;
             qph ^= 1;
-            float M0 = NEG_INF, M1 = NEG_INF, l0 = 0.f, l1 = 0.f;   // running max (log2 units) and partial sums
-            bool q16 = false;
-            if (m.t0 >= m.ct) {                          // the item starts with a raw tile
-                convert_q();
-                q16 = true;
-            }
+            if (m.t0 >= m.ct && (d & 1) == static_cast<uint32_t>(b)) convert_q();   // the item starts with a raw tile
             // The next item's q may overwrite this one only after every softmax
             // warp has seen this one land: q_full must never run two phases
             // ahead of a warp's wait (its parity could not tell them apart).
             __syncwarp();
             if (lane == 0) mbar_arrive(q_free);
-            for (int t = m.t0; ok && t < m.t1; ++t) {
+            float M0 = NEG_INF, M1 = NEG_INF, l0 = 0.f, l1 = 0.f;   // sums of this thread, relative to M (log2 units)
+            for (int t = m.t0; t < m.t1; ++t, ++d) {
+                if ((d & 1) != static_cast<uint32_t>(b)) continue;
                 const bool raw = t >= m.ct;
-                ok = __all_sync(0xffffffffu, mbar_wait(&s_full[b], (sfph >> b) & 1, abort_flag));
+                ok = __all_sync(0xffffffffu, mbar_wait_hint(&s_full[b], (d >> 1) & 1, abort_flag));
                 if (!ok) break;
-                sfph ^= 1u << b;
                 // The next tile is the first raw one: its logits need q in fp16,
                 // and every compressed logit GEMM has completed (this one too).
-                if (!q16 && t + 1 < m.t1 && t + 1 >= m.ct) {
-                    convert_q();
-                    q16 = true;
-                }
+                if (t + 1 < m.t1 && t + 1 == m.ct) convert_q();
                 tc_fence_after();
                 uint32_t r[4 * J];
                 tmem_ld_s(tmem + lane_off + kTmemS + b * 64, r);
@@ -752,10 +753,9 @@ __global__ void __launch_bounds__(threads_of(GW), 1) paged_attn_kernel(const __g
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s_empty[b]);
                 // Row validity of this tile (written by the gather before x_full).
-                ok = __all_sync(0xffffffffu, mbar_wait(&x_full[xb], (xph >> xb) & 1, abort_flag));
+                ok = __all_sync(0xffffffffu, mbar_wait_hint(&x_full[d % kBufs], (d / kBufs) & 1, abort_flag));
                 if (!ok) break;
-                xph ^= 1u << xb;
-                const uint2 vm = sValid[xb];
+                const uint2 vm = sValid[d % kBufs];
                 // A tile whose rows are all listed, with a positive scale, keeps the
                 // raw logits: the max is taken before scaling and p = 2^(s*c - M)
                 // is one FMA and one ex2.  Otherwise masked rows are -inf and the
@@ -789,31 +789,50 @@ __global__ void __launch_bounds__(threads_of(GW), 1) paged_attn_kernel(const __g
                 mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2));
                 mx0 *= mul;
                 mx1 *= mul;
-                // The running max is raised only when the tile exceeds it by more than 2^8.
-                float al0 = 1.f, al1 = 1.f;
-                if (M0 == NEG_INF) {
-                    M0 = mx0;                            // first finite max: O and sums are still 0
-                } else if (mx0 > M0 + kRescaleThreshold) {
-                    al0 = ex2(M0 - mx0);
-                    M0 = mx0;
+                // The running max after the tile before, from the other group.
+                float P0 = NEG_INF, P1 = NEG_INF;
+                if (t > m.t0) {
+                    ok = __all_sync(0xffffffffu, mbar_wait_hint(&tok[4 * (b ^ 1) + q4], ((d - 1) >> 1) & 1, abort_flag));
+                    if (!ok) break;
+                    P0 = *head_info(b ^ 1, h0, 6);
+                    P1 = *head_info(b ^ 1, h1, 6);
                 }
-                if (M1 == NEG_INF) {
-                    M1 = mx1;
-                } else if (mx1 > M1 + kRescaleThreshold) {
-                    al1 = ex2(M1 - mx1);
-                    M1 = mx1;
+                // It is raised only when the tile exceeds it by more than 2^8, so
+                // p <= 256 always; al: the factor for what O^T holds.
+                float al0 = 1.f, al1 = 1.f, N0 = P0, N1 = P1;
+                if (P0 == NEG_INF) {
+                    N0 = mx0;                            // first finite max: O is still 0
+                } else if (mx0 > P0 + kRescaleThreshold) {
+                    al0 = ex2(P0 - mx0);
+                    N0 = mx0;
+                }
+                if (P1 == NEG_INF) {
+                    N1 = mx1;
+                } else if (mx1 > P1 + kRescaleThreshold) {
+                    al1 = ex2(P1 - mx1);
+                    N1 = mx1;
                 }
                 // Any head raised in any warp: every warp rescales its O^T lanes.
                 const bool wresc = __any_sync(0xffffffffu, (al0 != 1.f) | (al1 != 1.f));
                 if (t4 == 0) {
+                    *head_info(b, h0, 6) = N0;
+                    *head_info(b, h1, 6) = N1;
                     sAlpha[b * kNHead + h0] = al0;
                     sAlpha[b * kNHead + h1] = al1;
                 }
-                if (lane == 0) sFlag[b * kSoftmaxWarps + q4] = wresc ? 1u : 0u;
+                if (lane == 0) sFlag[b * kGroupWarps + q4] = wresc ? 1u : 0u;
                 // Arrive now, wait after the exponentials: the exchange of the
                 // rescale flags overlaps this warp's own work.
                 __syncwarp();
-                if (lane == 0) mbar_arrive(grp);
+                if (lane == 0) {
+                    mbar_arrive(&tok[warp]);
+                    mbar_arrive(&grp[b]);
+                }
+                // This thread's sums, relative to the max of the group's last tile.
+                if (N0 != M0) l0 *= M0 == NEG_INF ? 0.f : ex2(M0 - N0);
+                if (N1 != M1) l1 *= M1 == NEG_INF ? 0.f : ex2(M1 - N1);
+                M0 = N0;
+                M1 = N1;
                 const float nr0 = M0 == NEG_INF ? 0.f : -M0, nr1 = M1 == NEG_INF ? 0.f : -M1;
                 float s0 = 0.f, s1 = 0.f;
                 uint32_t pk0[J], pk1[J];
@@ -827,10 +846,10 @@ __global__ void __launch_bounds__(threads_of(GW), 1) paged_attn_kernel(const __g
                     pk0[j] = raw ? pack2<true>(pa, pb) : pack2<false>(pa, pb);
                     pk1[j] = raw ? pack2<true>(pc, pd) : pack2<false>(pc, pd);
                 }
-                l0 = l0 * al0 + s0;
-                l1 = l1 * al1 + s1;
+                l0 += s0;
+                l1 += s1;
                 // This P buffer was read by the values GEMM two tiles back.
-                if (done >= 2 && !(ok = wait_values(2))) break;
+                if (d >= 2 && !(ok = wait_values(d - 2))) break;
                 // P[h][row]: rows 8j + 2(t%4) + {0,1} are bytes 16j + 4(t%4) of the
                 // 128-byte row of head h, 16-byte chunk j swizzled with h & 7.
                 uint8_t *pbuf = sP + b * kPBuf;
@@ -841,18 +860,16 @@ __global__ void __launch_bounds__(threads_of(GW), 1) paged_attn_kernel(const __g
                     *reinterpret_cast<uint32_t *>(pbuf + h1 * 128 + ((j ^ sw) << 4) + 4 * t4) = pk1[j];
                 }
                 fence_proxy_async();
-                {
-                    ok = __all_sync(0xffffffffu, mbar_wait(grp, gph, abort_flag));
-                    gph ^= 1;
-                    if (!ok) break;
-                }
-                const uint4 fl = *reinterpret_cast<const uint4 *>(sFlag + b * kSoftmaxWarps);
-                const bool any_resc = (fl.x | fl.y | fl.z | fl.w) != 0u;
-                if (any_resc && t > m.t0) {
+                ok = __all_sync(0xffffffffu, mbar_wait_hint(&grp[b], gph, abort_flag));
+                gph ^= 1;
+                if (!ok) break;
+                const uint4 fl = *reinterpret_cast<const uint4 *>(sFlag + b * kGroupWarps);
+                if ((fl.x | fl.y | fl.z | fl.w) != 0u && t > m.t0) {
                     // O^T holds the sum up to the previous values GEMM: wait for it.
-                    if (!(ok = wait_values(1))) break;
+                    if (!(ok = wait_values(d - 1))) break;
                     tc_fence_after();
-                    for (int cc = 0; cc < 8; ++cc) {
+#pragma unroll 1
+                    for (int cc = 0; cc < 8; ++cc) {              // rare: not worth unrolling (spills)
                         uint32_t v[32];
                         const uint32_t ta = tmem + lane_off + kTmemO + cc * 32;
                         tmem_ld32(ta, v);
@@ -867,55 +884,68 @@ __global__ void __launch_bounds__(threads_of(GW), 1) paged_attn_kernel(const __g
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_full[b]);
-                ++done;
-                b ^= 1;
-                vph ^= 1u << xb;                         // x_empty's phase that this tile's values GEMM completes
-                xb = xb == kBufs - 1 ? 0 : xb + 1;
             }
             if (!ok) break;
-            // ---- epilogue: row sums over the four threads of a head, then O^T out
+            // ---- epilogue, both groups: the heads' sums, then O^T out
             l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
             l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
             l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
             l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
             if (t4 == 0) {
+                reinterpret_cast<float2 *>(head_info(b, h0, 7))[i & 1] = make_float2(l0, M0);
+                reinterpret_cast<float2 *>(head_info(b, h1, 7))[i & 1] = make_float2(l1, M1);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(all);
+            ok = __all_sync(0xffffffffu, mbar_wait_hint(all, aph, abort_flag));
+            aph ^= 1;
+            if (!ok) break;
+            float inv[2];                                // 1 / l of heads lane and lane + 32 (a partial: 1)
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const int h = k ? h1 : h0;
-                    const float L = k ? l1 : l0, M = k ? M1 : M0;
-                    if (!m.split) {
-                        sInvL[h] = L > 0.f ? 1.f / L : 0.f;
-                        if (a.lse) a.lse[unit * kNHead + h] = merged_lse(M, L);
-                    } else {
-                        sInvL[h] = 1.f;
-                        ml[(slot * kNHead + h) * 2] = L > 0.f ? M : NEG_INF;
-                        ml[(slot * kNHead + h) * 2 + 1] = L;
+            for (int k = 0; k < 2; ++k) {
+                const int h = lane + 32 * k;
+                const float M = *head_info((d - 1) & 1, h, 6);
+                float L = 0.f;
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    const float2 lm = reinterpret_cast<const float2 *>(head_info(g, h, 7))[i & 1];
+                    L += lm.y == NEG_INF ? 0.f : lm.y == M ? lm.x : lm.x * ex2(lm.y - M);
+                }
+                inv[k] = m.split ? 1.f : L > 0.f ? 1.f / L : 0.f;
+                if (warp == 0) {
+                    if (m.split) {
+                        float *ml = static_cast<float *>(a.ws) + n_slots * kNHead * kHeadDim + (slot * kNHead + h) * 2;
+                        ml[0] = L > 0.f ? M : NEG_INF;
+                        ml[1] = L;
+                    } else if (a.lse) {
+                        a.lse[unit * kNHead + h] = merged_lse(M, L);
                     }
                 }
             }
-            if (!(ok = group_sync())) break;
-            if (!(ok = wait_values(1))) break;           // the item's last values GEMM
+            if (!(ok = wait_values(d - 1))) break;       // the item's last values GEMM
             tc_fence_after();
-            for (int cc = 0; cc < 8; ++cc) {
+            // group g: dims 256 g .. 256 g + 255
+#pragma unroll 1
+            for (int cc = 4 * b; cc < 4 * b + 4; ++cc) {
                 uint32_t v[32];
                 tmem_ld32(tmem + lane_off + kTmemO + cc * 32, v);
                 tmem_wait_ld(v);
-                const int d = (cc >> 1) * 128 + q4 * 32 + lane, hb = (cc & 1) * 32;
+                const int dim = (cc >> 1) * 128 + q4 * 32 + lane, hb = (cc & 1) * 32;
                 if (m.split) {
-                    float *o = static_cast<float *>(a.ws) + (slot * kNHead + hb) * kHeadDim + d;
+                    float *o = static_cast<float *>(a.ws) + (slot * kNHead + hb) * kHeadDim + dim;
 #pragma unroll
                     for (int k = 0; k < 32; ++k) o[k * kHeadDim] = __uint_as_float(v[k]);
                 } else {
                     // bf16, two dims a store: of each pair of heads an even lane takes
                     // the first and an odd lane the second, with its neighbour's dim
-                    uint16_t *o = a.out + (unit * kNHead + hb + (lane & 1)) * kHeadDim + (d & ~1);
+                    uint16_t *o = a.out + (unit * kNHead + hb + (lane & 1)) * kHeadDim + (dim & ~1);
 #pragma unroll
                     for (int k = 0; k < 32; k += 2) {
-                        const float2 il = *reinterpret_cast<const float2 *>(sInvL + hb + k);
-                        const float x0 = __uint_as_float(v[k]) * il.x, x1 = __uint_as_float(v[k + 1]) * il.y;
-                        const float other = __shfl_xor_sync(0xffffffffu, (lane & 1) ? x0 : x1, 1);
+                        const float il = __shfl_sync(0xffffffffu, (cc & 1) ? inv[1] : inv[0], k + (lane & 1));
+                        const float mine = __uint_as_float((lane & 1) ? v[k + 1] : v[k]);
+                        const float other = __shfl_xor_sync(0xffffffffu, __uint_as_float((lane & 1) ? v[k] : v[k + 1]), 1);
                         *reinterpret_cast<uint32_t *>(o + k * kHeadDim) =
-                            (lane & 1) ? pack2<false>(other, x1) : pack2<false>(x0, other);
+                            (lane & 1) ? pack2<false>(other * il, mine * il) : pack2<false>(mine * il, other * il);
                     }
                 }
             }
