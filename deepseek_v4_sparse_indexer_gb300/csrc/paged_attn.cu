@@ -62,9 +62,9 @@ constexpr int kLookWarp = 10;                 // warp 10: row lookup
 constexpr int kFirstGatherWarp = 11;
 constexpr int kRowGroups = TR / 4;            // 4-row groups of a tile, dealt round-robin to the gather warps
 // Gather warps: five copy bf16 rows (two tiles in flight); the expansion of FP8
-// codes is arithmetic, so nine.
+// codes is arithmetic, so six (two groups each).
 constexpr int kGatherWarpsBf16 = 5;
-constexpr int kGatherWarpsFp8 = 9;
+constexpr int kGatherWarpsFp8 = 6;
 constexpr int threads_of(int gw) { return (kFirstGatherWarp + gw) * 32; }
 constexpr int kQBlk = kNHead * 128;           // 64 heads x 64 dims: 8 KB
 constexpr int kXBlk = 1024;                   // 8 rows x 64 dims
