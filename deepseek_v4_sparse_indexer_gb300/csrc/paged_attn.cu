@@ -121,6 +121,15 @@ DS4A_DEV void mbar_expect_tx(uint64_t *bar, uint32_t bytes) {
     asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
 }
 
+// 2^x by the MUFU approximation (relative error ~2^-22), results below 2^-126 as
+// 0: keeping them costs three more instructions each, and a weight that small
+// adds nothing.
+DS4A_DEV float ex2z(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // S of this warp's 16 heads and 48 rows: 32 columns, then 16.
 DS4A_DEV void tmem_ld_s(uint32_t taddr, uint32_t (&r)[24]) {
     asm volatile(
@@ -835,19 +844,32 @@ __global__ void __launch_bounds__(threads_of(GW), 1) paged_attn_kernel(const __g
                 M1 = N1;
                 const float nr0 = M0 == NEG_INF ? 0.f : -M0, nr1 = M1 == NEG_INF ? 0.f : -M1;
                 float s0 = 0.f, s1 = 0.f;
-                uint32_t pk0[J], pk1[J];
 #pragma unroll
                 for (int j = 0; j < J; ++j) {
-                    const float pa = ex2(fmaf(x[4 * j], mul, nr0)), pb = ex2(fmaf(x[4 * j + 1], mul, nr0));
-                    const float pc = ex2(fmaf(x[4 * j + 2], mul, nr1)), pd = ex2(fmaf(x[4 * j + 3], mul, nr1));
-                    s0 += pa + pb;
-                    s1 += pc + pd;
-                    // p in the rows' 16-bit type: the operand of the values GEMM
-                    pk0[j] = raw ? pack2<true>(pa, pb) : pack2<false>(pa, pb);
-                    pk1[j] = raw ? pack2<true>(pc, pd) : pack2<false>(pc, pd);
+                    x[4 * j] = ex2z(fmaf(x[4 * j], mul, nr0));
+                    x[4 * j + 1] = ex2z(fmaf(x[4 * j + 1], mul, nr0));
+                    x[4 * j + 2] = ex2z(fmaf(x[4 * j + 2], mul, nr1));
+                    x[4 * j + 3] = ex2z(fmaf(x[4 * j + 3], mul, nr1));
+                    s0 += x[4 * j] + x[4 * j + 1];
+                    s1 += x[4 * j + 2] + x[4 * j + 3];
                 }
                 l0 += s0;
                 l1 += s1;
+                // p in the rows' 16-bit type: the operand of the values GEMM
+                uint32_t pk0[J], pk1[J];
+                if (raw) {
+#pragma unroll
+                    for (int j = 0; j < J; ++j) {
+                        pk0[j] = pack2<true>(x[4 * j], x[4 * j + 1]);
+                        pk1[j] = pack2<true>(x[4 * j + 2], x[4 * j + 3]);
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < J; ++j) {
+                        pk0[j] = pack2<false>(x[4 * j], x[4 * j + 1]);
+                        pk1[j] = pack2<false>(x[4 * j + 2], x[4 * j + 3]);
+                    }
+                }
                 // This P buffer was read by the values GEMM two tiles back.
                 if (d >= 2 && !(ok = wait_values(d - 2))) break;
                 // P[h][row]: rows 8j + 2(t%4) + {0,1} are bytes 16j + 4(t%4) of the
