@@ -1027,10 +1027,19 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const __g
     const long long row0 = (static_cast<long long>(unit.x) * a.hsplit + half) * kNHead;
     // This warp's share of head h's pieces, w0, w0 + step, ... (at most 32 of them):
     // the sums relative to their own largest m; lane l holds dims 4l + 128j + 0..3.
+    // The first two pieces' rows load together with the (m, l) pairs.
     float M, L;
     float4 acc[4];
+    auto piece = [&](int i, int h) -> const float * { return wo + (slot(i) * kNHead + h) * kHeadDim + 4 * lane; };
     auto join = [&](int h, int w0, int step) {
         const int mine = w0 < np ? (np - w0 + step - 1) / step : 0;
+        float4 two[2][4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                two[i][j] = i < mine ? *reinterpret_cast<const float4 *>(piece(w0 + i * step, h) + 128 * j) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
         float m = NEG_INF, l = 0.f;
         if (lane < mine) {
             const float2 p = *reinterpret_cast<const float2 *>(ml + (slot(w0 + lane * step) * kNHead + h) * 2);
@@ -1043,20 +1052,26 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const __g
         L = e * l;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+        auto add = [&](int j, float wk, const float4 &v) {
+            acc[j].x = fmaf(wk, v.x, acc[j].x);
+            acc[j].y = fmaf(wk, v.y, acc[j].y);
+            acc[j].z = fmaf(wk, v.z, acc[j].z);
+            acc[j].w = fmaf(wk, v.w, acc[j].w);
+        };
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-        for (int i = 0; i < mine; ++i) {
-            const float wk = __shfl_sync(0xffffffffu, e, i);
-            const float *o = wo + (slot(w0 + i * step) * kNHead + h) * kHeadDim + 4 * lane;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float4 v = *reinterpret_cast<const float4 *>(o + 128 * j);
-                acc[j].x = fmaf(wk, v.x, acc[j].x);
-                acc[j].y = fmaf(wk, v.y, acc[j].y);
-                acc[j].z = fmaf(wk, v.z, acc[j].z);
-                acc[j].w = fmaf(wk, v.w, acc[j].w);
-            }
+        for (int i = 0; i < 2; ++i) {
+            const float wk = __shfl_sync(0xffffffffu, e, i);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) add(j, wk, two[i][j]);
+        }
+#pragma unroll 2
+        for (int i = 2; i < mine; ++i) {
+            const float wk = __shfl_sync(0xffffffffu, e, i);
+            const float *o = piece(w0 + i * step, h);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) add(j, wk, *reinterpret_cast<const float4 *>(o + 128 * j));
         }
     };
     if (np <= kMergeFew) {
