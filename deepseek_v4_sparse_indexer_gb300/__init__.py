@@ -4,7 +4,9 @@ hand-written CUDA behind the C ABI of include/ds4a.h.
 
 The Python surface is the ctypes binding (same names as the C entry points)
 and DecodeStep / PrefillStep, which chain the three ops on one stream, plus
-DenseStep for the ratio-128 layers (attention over all rows, no indexer).
+DenseStep for the ratio-128 layers (attention over all rows, no indexer) and
+PagedDecodeStep, a decode step over caches in pages (lengths -> block tables and
+slots -> norm and rotation -> score -> select -> attention).
 """
 from ._binding import (Ds4aError, load, ds4a_version, ds4a_workspace_bytes, ds4a_get_device_status,
                        ds4a_debug_inject_error, ds4a_debug_wait_timeout, ds4a_indexer_score, ds4a_topk_select,
@@ -15,7 +17,7 @@ from ._binding import (Ds4aError, load, ds4a_version, ds4a_workspace_bytes, ds4a
                        ds4a_paged_plan, ds4a_qk_norm_rope, ds4a_paged_indexer_score, ds4a_paged_attn_decode,
                        DS4A_OP_PAGED_ATTN_DECODE,
                        DS4A_OP_FLAG_128_HEADS, DS4A_ROPE_NEIGHBOURS, DS4A_ROPE_HALVES)
-from .step import DecodeStep, PrefillStep, DenseStep, ProducerStep, DEFAULT_SCALE
+from .step import DecodeStep, PrefillStep, DenseStep, ProducerStep, PagedDecodeStep, DEFAULT_SCALE
 
 __all__ = ["Ds4aError", "load", "ds4a_version", "ds4a_workspace_bytes", "ds4a_get_device_status",
            "ds4a_debug_inject_error", "ds4a_debug_wait_timeout", "ds4a_indexer_score", "ds4a_topk_select", "ds4a_sparse_attn_decode",
@@ -25,5 +27,5 @@ __all__ = ["Ds4aError", "load", "ds4a_version", "ds4a_workspace_bytes", "ds4a_ge
            "ds4a_paged_plan", "ds4a_qk_norm_rope", "ds4a_paged_indexer_score", "ds4a_paged_attn_decode",
            "DS4A_OP_PAGED_ATTN_DECODE",
            "DS4A_OP_FLAG_128_HEADS", "DS4A_ROPE_NEIGHBOURS", "DS4A_ROPE_HALVES",
-           "DecodeStep", "PrefillStep", "DenseStep", "ProducerStep",
+           "DecodeStep", "PrefillStep", "DenseStep", "ProducerStep", "PagedDecodeStep",
            "DEFAULT_SCALE"]

@@ -8,6 +8,10 @@ ProducerStep: the cache producer at a ratio boundary: the raw-window push of
 the new token, the compressor pooling of the frontier and (fp8=True) the FP8
 store of the pooled row.
 
+PagedDecodeStep: one decode step of a layer whose rows and keys lie in pages of a
+shared pool, from the sequences' lengths and the layer's projections to the
+attention output.
+
 DecodeStep and PrefillStep with fp8=True read the compressed rows from the FP8
 row store (x["rows8"] E4M3 codes, x["row_scale"] per-row scales) instead of
 the bf16 rows; with fused=True they score and select in one call
@@ -164,4 +168,92 @@ class ProducerStep:
         self.pool(x, stream)
         if self.fp8:
             self.store_fp8(stream)
+        return self.out
+
+
+class PagedDecodeStep:
+    """One new token for each of up to U sequences, over paged caches.
+
+    x holds, per step: past, add (i32 [U]: tokens in the cache and new ones, 1 or
+    0; sequences without a new token come last), q [U,H,512] and kv [U,512], the
+    projections before norm and rotation (bf16, fp16 or fp32); with top_k also iq
+    [U,64,128] and w f32 [U,64].  And, kept by the program: table i32
+    [U,max_pages], free_pages and free_head (updated in place), ring i32 [U] or
+    None, raw fp16 [n_ring,128,512], rows bf16 [n_pages,P,512] (fp8: uint8 codes
+    and row_scale f32 [n_pages,P]), ik bf16 [n_pages,P,128] with top_k, inv_freq f64
+    [n_rot / 2] and the norm weights q_norm, kv_norm, iq_norm, ik_norm (f32 or
+    None).  A layer of `ratio` tokens per row finishes a row every ratio tokens:
+    pooled [U,512] (and pooled_ik [U,128]) hold the rows finished in this step,
+    new row i of the batch in row i (cu_row says whose).
+
+    plan -> rotate -> store -> score -> select -> attend, each one call of the
+    library (two for the indexer's part); outputs and workspaces are kept, so the
+    step can be captured in a CUDA graph and replayed on other lengths.  top_k = 0:
+    every row is attended to (the ratio-128 layers).
+    """
+
+    def __init__(self, U, max_pages, page_size, top_k=512, ratio=4, device="cuda", n_head=B.N_HEAD, fp8=False, eps=1e-6,
+                 style=B.DS4A_ROPE_NEIGHBOURS):
+        self.U, self.page_size, self.top_k, self.ratio, self.n_head = U, page_size, top_k, ratio, n_head
+        self.fp8, self.eps, self.style = fp8, eps, style
+        dev = torch.device(device)
+        N_cap = max_pages * page_size
+        flag = B.DS4A_OP_FLAG_128_HEADS if n_head == 128 else 0
+        self.n_rows, self.n_raw, self.tok_pos, self.raw_slot, self.row_pos, self.row_slot = (
+            torch.empty(U, dtype=torch.int32, device=dev) for _ in range(6))
+        self.cu_tok, self.cu_row = (torch.empty(U + 1, dtype=torch.int32, device=dev) for _ in range(2))
+        # rows of q without a token are left as they were, so they start as zeros
+        self.q = torch.zeros(U, n_head, B.HEAD_DIM, dtype=torch.bfloat16, device=dev)
+        self.out = torch.empty(U, n_head, B.HEAD_DIM, dtype=torch.bfloat16, device=dev)
+        self.lse = torch.empty(U, n_head, dtype=torch.float32, device=dev)
+        self.ws_attn = _ws(B.ds4a_workspace_bytes(B.DS4A_OP_PAGED_ATTN_DECODE | flag, U, 1, N_cap, top_k), dev)
+        self.idx = self.count = None
+        if top_k:
+            self.iq = torch.zeros(U, B.N_IDX_HEAD, B.IDX_DIM, dtype=torch.bfloat16, device=dev)
+            self.scores = torch.empty(U, 1, N_cap, dtype=torch.float32, device=dev)
+            self.idx = torch.empty(U, 1, top_k, dtype=torch.int32, device=dev)
+            self.count = torch.empty(U, 1, dtype=torch.int32, device=dev)
+            self.ws_topk = _ws(B.ds4a_workspace_bytes(B.DS4A_OP_TOPK_SELECT, U, 1, N_cap, top_k), dev)
+
+    def plan(self, x, stream=None):
+        B.ds4a_paged_plan(x["past"], x["add"], self.ratio, self.page_size, x["free_pages"], x["free_head"], x["table"],
+                          self.n_rows, self.n_raw, self.cu_tok, self.cu_row, self.tok_pos, self.raw_slot, self.row_pos,
+                          self.row_slot, x["free_head"], ring=x.get("ring"), stream=stream)
+
+    def rotate(self, x, stream=None):
+        B.ds4a_qk_norm_rope(x["q"], x["kv"], self.tok_pos, x["inv_freq"], self.eps, x.get("q_norm"), x.get("kv_norm"), self.q,
+                            x["raw"].view(-1, B.HEAD_DIM), k_slot=self.raw_slot, style=self.style, stream=stream)
+        if self.top_k:
+            B.ds4a_qk_norm_rope(x["iq"], None, self.tok_pos, x["inv_freq"], self.eps, x.get("iq_norm"), None, self.iq, None,
+                                style=self.style, stream=stream)
+
+    def store(self, x, stream=None):
+        B.ds4a_qk_norm_rope(None, x["pooled"], self.row_pos, x["inv_freq"], self.eps, None, x.get("kv_norm"), None,
+                            x["rows"].view(-1, B.HEAD_DIM), k_slot=self.row_slot,
+                            k_scale=x["row_scale"].view(-1) if self.fp8 else None, style=self.style, stream=stream)
+        if self.top_k:
+            B.ds4a_qk_norm_rope(None, x["pooled_ik"], self.row_pos, x["inv_freq"], self.eps, None, x.get("ik_norm"), None,
+                                x["ik"].view(-1, B.IDX_DIM), k_slot=self.row_slot, style=self.style, stream=stream)
+
+    def score(self, x, stream=None):
+        B.ds4a_paged_indexer_score(self.iq.view(self.U, 1, B.N_IDX_HEAD, B.IDX_DIM), x["w"].view(self.U, 1, B.N_IDX_HEAD),
+                                   x["ik"], x["table"], self.n_rows, self.scores, stream=stream)
+
+    def select(self, x, stream=None):
+        B.ds4a_topk_select(self.scores, self.n_rows, self.top_k, self.idx, self.count, self.ws_topk, stream=stream)
+
+    def attend(self, x, scale=DEFAULT_SCALE, stream=None):
+        idx, count = (self.idx.view(self.U, self.top_k), self.count.view(self.U)) if self.top_k else (None, None)
+        B.ds4a_paged_attn_decode(self.q, x["rows"], x["table"], self.n_rows, x["raw"], self.n_raw, scale, self.out, self.lse,
+                                 self.ws_attn, idx=idx, count=count, row_scale=x["row_scale"] if self.fp8 else None,
+                                 ring=x.get("ring"), stream=stream)
+
+    def __call__(self, x, scale=DEFAULT_SCALE, stream=None):
+        self.plan(x, stream)
+        self.rotate(x, stream)
+        self.store(x, stream)
+        if self.top_k:
+            self.score(x, stream)
+            self.select(x, stream)
+        self.attend(x, scale, stream)
         return self.out
