@@ -716,7 +716,7 @@ ds4a_status ds4a_paged_indexer_score(const uint16_t *iq, const float *w, const u
         return DS4A_EINVAL;
     if (!aligned(iq, 16) || !aligned(ik, 16) || !aligned(w, 4) || !aligned(scores, 4)) return DS4A_EINVAL;
     const long long cap = static_cast<long long>(max_pages) << shift, pool = static_cast<long long>(n_pages) << shift;
-    if (cap >= (1LL << 31) || pool >= (1LL << 31)) return DS4A_EINVAL;
+    if (cap >= (1LL << 30) || pool >= (1LL << 31)) return DS4A_EINVAL;
     IndexerArgs a{};
     a.row_lim = static_cast<int>(cap < N_cap ? cap : N_cap);
     // the tiles of a batch are counted in 32 bits
@@ -762,7 +762,7 @@ ds4a_status ds4a_paged_attn_decode(int n_head, const uint16_t *q, const void *ro
     if (!(scale == scale)) return DS4A_EINVAL;
     const long long cap = static_cast<long long>(max_pages) << shift, pool = static_cast<long long>(n_pages) << shift;
     const long long raws = static_cast<long long>(n_ring) * kNSwa;
-    if (cap >= (1LL << 31) || pool >= (1LL << 31) || raws >= (1LL << 31)) return DS4A_EINVAL;
+    if (cap >= (1LL << 30) || pool >= (1LL << 31) || raws >= (1LL << 31)) return DS4A_EINVAL;
     const int list_cap = top_k ? top_k : static_cast<int>(cap);
     if (!paged_attn_sizes_ok(static_cast<long long>(U) * hsplit, list_cap)) return DS4A_EINVAL;
     const size_t need = paged_attn_ws_bytes(U, hsplit, list_cap);

@@ -10,12 +10,21 @@
 // result in bf16 for the projection behind it.
 //
 // What bounds it: 128 flop per byte of rows at 64 heads, so HBM, through two
-// 64-head UMMA streams (logits M=64 at half rate) that keep the tensor pipe about
-// three quarters busy at that rate.  A tile's chain (copy 0.8 us, logits 0.9,
-// softmax 0.8, values 0.8) is several times the 1.1 us in which an SM's share of
-// HBM delivers 48 rows, so the row buffers in flight decide: three tiles of 48
-// rows fit beside q (64 KB) and P where two of 64 rows did, and a gathered tile's
-// copies are issued before the previous one's have landed.
+// 64-head UMMA streams (logits M=64 at half rate) and about 240 KB of shared-
+// memory traffic a tile (q is read again for every tile), which are about two
+// thirds busy at that rate.  A tile's chain (copy 0.9 us, logits 0.8, softmax 1.2,
+// values 0.5) is several times the 1.1 us in which an SM's share of HBM delivers
+// 48 rows, so the row buffers in flight decide: three tiles of 48 rows fit beside
+// q (64 KB) and P where two of 64 rows did, a gathered tile's copies are issued
+// before the previous one's have landed, and two softmax groups overlap.
+// Measured (GB300): 640 units x 8,192 rows 934 us = 5.9 TB/s, 88 % of the copy
+// bandwidth, 640 ragged units of up to 8,192 rows 528 us; 1,368 units x 512 listed
+// rows 233-241 us = 4.5 TB/s, random 1 KB rows arriving by cp.async at 29 GB/s per
+// SM of the 34-40 that such a gather alone reaches; 128 heads: 128 units x 1,024
+// listed rows 92 us, each half at its own copy of the rows from L2; FP8 rows 48
+// units of up to 4,096 63 us, bound by the expansion of the codes (2.5 us a tile
+// through the conversion pipe).  A few units are latency: 1 x 1,024 rows 13.4 us
+// with its merge.
 //
 // Roles (one CTA per SM, persistent over its share of the batch's tiles):
 //   lookup   warp 10: turns a tile's rows (listed ones: row number, then page; dense
@@ -440,7 +449,7 @@ __global__ void __launch_bounds__(threads_of(GW), 1) paged_attn_kernel(const __g
         const int gw = warp - kFirstGatherWarp;
         const int chunk = lane & 7, rsub = lane >> 3;
         auto row_of = [&](int k) -> int { return 4 * (gw + k * GW) + rsub; };
-        uint32_t rph = 0, xph = 0;                         // parity bits per buffer
+        uint32_t rph = 0, xph = 0, used = 0;               // parity bits per buffer; buffers filled so far
         int xb = 0, ordinal = -1;                          // ordinal: items started
         bool ok = true;
         int pend = -1;                                     // buffer whose cp.async copies are in flight
@@ -507,6 +516,7 @@ __global__ void __launch_bounds__(threads_of(GW), 1) paged_attn_kernel(const __g
             }
             if (!(ok = wait_for(&x_empty[xb], ((xph >> xb) & 1) ^ 1))) break;
             xph ^= 1u << xb;
+            used |= 1u << xb;
             uint8_t *dst = sX + xb * kXBuf;
             if (gw == 0) {
                 if (lane == 0) sValid[xb] = mask;          // published by this warp's arrival
@@ -582,7 +592,16 @@ __global__ void __launch_bounds__(threads_of(GW), 1) paged_attn_kernel(const __g
         settle(false);                                     // also when a wait gave up: copies in flight have landed
         if (!ok) {
             *abort_flag = 1;
-            if (lane == 0) report(a.status, DS4A_DEV_TIMEOUT);
+            if (lane == 0) {
+                report(a.status, DS4A_DEV_TIMEOUT);
+                // TMA copies of q and of row tiles may still be in flight
+                if (gw == 0) {
+                    if (ordinal >= 0) wait_drain(q_full, ordinal & 1);
+                    for (int b = 0; b < kBufs; ++b)
+                        if ((used >> b) & 1) wait_drain(&x_full[b], ((xph >> b) & 1) ^ 1);
+                }
+            }
+            __syncwarp();
         }
     } else if (warp == kMmaWarp) {
         // ------------------------------------------------------------ logits issuer
@@ -1029,7 +1048,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const __g
     // the sums relative to their own largest m; lane l holds dims 4l + 128j + 0..3.
     // The first two pieces' rows load together with the (m, l) pairs.
     float M, L;
-    float4 acc[4];
+    float4 acc[4] = {};
     auto piece = [&](int i, int h) -> const float * { return wo + (slot(i) * kNHead + h) * kHeadDim + 4 * lane; };
     auto join = [&](int h, int w0, int step) {
         const int mine = w0 < np ? (np - w0 + step - 1) / step : 0;
@@ -1052,14 +1071,14 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const __g
         L = e * l;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
         auto add = [&](int j, float wk, const float4 &v) {
             acc[j].x = fmaf(wk, v.x, acc[j].x);
             acc[j].y = fmaf(wk, v.y, acc[j].y);
             acc[j].z = fmaf(wk, v.z, acc[j].z);
             acc[j].w = fmaf(wk, v.w, acc[j].w);
         };
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const float wk = __shfl_sync(0xffffffffu, e, i);

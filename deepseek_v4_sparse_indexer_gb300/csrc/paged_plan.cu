@@ -269,8 +269,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_plan_kernel(const __grid_co
 
 cudaError_t launch_paged_plan(PagedPlanArgs a, int num_sms, cudaStream_t s) {
     const size_t smem = (5 * static_cast<size_t>(a.B) + 3) * sizeof(int);
-    cudaError_t e = cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(smem));
+    cudaError_t e = cudaSuccess;
+    if (smem > 40960)
+        e = cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
     // One CTA covers a few thousand tokens and rows; more take every SM, or sixteen
     // CTAs as a cluster (a non-portable size) when the head is updated in place

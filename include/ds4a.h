@@ -607,7 +607,7 @@ ds4a_status ds4a_qk_norm_rope(const void *q, int q_type, int64_t q_tok_stride, c
  *    scores   fp32 [U][N_cap] (device), written for r < n_rows[u], the others
  *             left as they were.  A row whose page is not one of the pool's gets
  *             -inf and sets DS4A_DEV_BOUNDS.
- *    max_pages * page_size and n_pages * page_size are below 2^31.
+ *    max_pages * page_size is below 2^30, n_pages * page_size below 2^31.
  */
 ds4a_status ds4a_paged_indexer_score(const uint16_t *iq, const float *w, const uint16_t *ik,
                                      int n_pages, int page_size, const int32_t *table,
@@ -618,9 +618,10 @@ ds4a_status ds4a_paged_indexer_score(const uint16_t *iq, const float *w, const u
  * 5d. Attention of one new token per sequence over paged rows: 3a and 3c (one
  *    joint softmax over compressed rows and the raw window, fp32 softmax and
  *    accumulation) with the rows read through a block table, ragged lengths
- *    and bf16 output.  The batch is cut into equal shares of 64-row tiles by
- *    the lengths found on the device, a unit cut by a share boundary is
- *    computed in pieces, and a second kernel joins them.
+ *    and bf16 output.  The batch is cut into equal shares of row tiles by the
+ *    lengths found on the device, a unit cut by a share boundary is computed in
+ *    pieces, and a second kernel joins them.  Bit-identical from call to call on
+ *    the same batch.
  *
  *    n_head   64 or 128 (else DS4A_EUNSUPPORTED).
  *    q        bf16 [U][n_head][512] (device).
@@ -643,9 +644,10 @@ ds4a_status ds4a_paged_indexer_score(const uint16_t *iq, const float *w, const u
  *             bytes, 256-byte aligned (device).
  *    A length outside its range is clamped, a ring outside [0, n_ring) gives no
  *    raw rows, and a listed row that is not one of the unit's rows or whose
- *    page is not one of the pool's is masked; each sets DS4A_DEV_BOUNDS.
- *    q, rows, raw and out are 16-byte aligned.  max_pages * page_size and
- *    n_pages * page_size are below 2^31.
+ *    page is not one of the pool's is masked; each sets DS4A_DEV_BOUNDS.  A row
+ *    listed twice counts twice.
+ *    q, rows, raw and out are 16-byte aligned.  max_pages * page_size is below
+ *    2^30, n_pages * page_size and n_ring * 128 below 2^31.
  */
 ds4a_status ds4a_paged_attn_decode(int n_head, const uint16_t *q, const void *rows, int rows_type,
                                    const float *row_scale, int n_pages, int page_size,
