@@ -27,8 +27,8 @@
 // A large step that updates *free_head in place runs as one cluster instead, whose
 // barrier lies between the reads of the old head and its update.
 //
-// The kernel never lets its dependents launch early: the top-k kernels read the
-// row counts it writes before their own dependency wait.
+// The kernel never lets its dependents launch early, and fences the row counts it
+// writes: the top-k kernels read them before their own dependency wait.
 #include "common.cuh"
 #include "internal.h"
 
@@ -257,6 +257,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_plan_kernel(const __grid_co
                 a.n_raw[b] = len < kNSwa ? len : kNSwa;
             }
         }
+        __threadfence();
     }
     if (!ok) report(a.status, DS4A_DEV_BOUNDS);
     // ---- the free list's new head, once every CTA has read the old one
