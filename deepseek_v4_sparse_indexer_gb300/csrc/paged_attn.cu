@@ -17,14 +17,15 @@
 // 48 rows, so the row buffers in flight decide: three tiles of 48 rows fit beside
 // q (64 KB) and P where two of 64 rows did, a gathered tile's copies are issued
 // before the previous one's have landed, and two softmax groups overlap.
-// Measured (GB300): 640 units x 8,192 rows 934 us = 5.9 TB/s, 88 % of the copy
-// bandwidth, 640 ragged units of up to 8,192 rows 528 us; 1,368 units x 512 listed
-// rows 233-241 us = 4.5 TB/s, random 1 KB rows arriving by cp.async at 29 GB/s per
-// SM of the 34-40 that such a gather alone reaches; 128 heads: 128 units x 1,024
-// listed rows 92 us, each half at its own copy of the rows from L2; FP8 rows 48
-// units of up to 4,096 63 us, bound by the expansion of the codes (2.5 us a tile
-// through the conversion pipe).  A few units are latency: 1 x 1,024 rows 13.4 us
-// with its merge.
+// Measured (GB300): 640 units x 8,192 rows 965 us = 5.7 TB/s, 85 % of the copy
+// bandwidth, 640 ragged units of up to 8,192 rows 545 us; 1,368 units x 512 listed
+// rows 233 us = 4.6 TB/s, random 1 KB rows arriving by cp.async at 30 GB/s per SM
+// of the 34-40 that such a gather alone reaches; 128 heads: 128 units x 1,024
+// listed rows 92 us, each half at its own copy of the rows from L2.  FP8 rows, 48
+// units of up to 4,096: 60 us, 2.3 us a tile, bound by the pass that writes the
+// codes out as fp16: its instructions, and its 72 KB more a tile through shared
+// memory (the conversion itself is not: shifts and a multiplication in its place
+// took 73 us).  A few units are latency: 1 x 1,024 rows 13.4 us with its merge.
 //
 // Roles (one CTA per SM, persistent over its share of the batch's tiles):
 //   lookup   warp 10: turns a tile's rows (listed ones: row number, then page; dense
@@ -36,7 +37,7 @@
 //            groups dealt to the warps.  Dense lists and the raw window: TMA, one box
 //            per 16 rows of a page (8 with pages of 8 rows), boxes past the list's end
 //            or outside the pool read past the end of the tensor map, which fills
-//            zeros.  FP8 rows: codes to registers, written out as exact bf16.
+//            zeros.  FP8 rows: codes by cp.async, then written out as fp16.
 //   logits   warp 8: S[64 heads x 48 rows] = q . X^T into one of two TMEM buffers;
 //   softmax  warps 0-3 and 4-7, tiles in turn: S out of TMEM, running max (raised
 //            only past 2^8), P;
@@ -70,8 +71,8 @@ constexpr int kPvWarp = 9;                    // warp 9: values UMMA issuer
 constexpr int kLookWarp = 10;                 // warp 10: row lookup
 constexpr int kFirstGatherWarp = 11;
 constexpr int kRowGroups = TR / 4;            // 4-row groups of a tile, dealt round-robin to the gather warps
-// Gather warps: five copy bf16 rows (two tiles in flight); the expansion of FP8
-// codes is arithmetic, so six (two groups each).
+// Gather warps: five, so that the block has 16 warps of 128 registers.  FP8 rows:
+// six, two groups each (48 units of up to 4,096 rows 60 us; five 64, nine 62).
 constexpr int kGatherWarpsBf16 = 5;
 constexpr int kGatherWarpsFp8 = 6;
 constexpr int threads_of(int gw) { return (kFirstGatherWarp + gw) * 32; }
@@ -117,6 +118,22 @@ DS4A_DEV void tma_load_q(void *dst, const void *map, uint64_t *bar, int row) {
         "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(smem_u32(bar))
         : "memory");
 }
+// 4-byte async copy; src_bytes = 0 writes 4 zero bytes (src still valid).
+DS4A_DEV void cp_async4(uint32_t dst, const void *src, uint32_t src_bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
+}
+DS4A_DEV void ld_shared_v4(uint32_t addr, uint32_t (&v)[4]) {
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                 : "r"(addr)
+                 : "memory");
+}
+// Eight E4M3 codes (two words) as eight fp16 (four words, dims in order): exact.
+DS4A_DEV void e4m3x8_to_f16(uint32_t w0, uint32_t w1, uint32_t (&o)[4]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(o[j]) : "h"(static_cast<uint16_t>((j < 2 ? w0 : w1) >> (16 * (j & 1)))));
+}
 // One box of whole 8-row groups (map: (64 dims, 8 rows, 8 blocks, groups)).
 DS4A_DEV void tma_load_groups(void *dst, const void *map, uint64_t *bar, int group) {
     asm volatile(
@@ -136,6 +153,12 @@ DS4A_DEV void mbar_expect_tx(uint64_t *bar, uint32_t bytes) {
 DS4A_DEV float ex2z(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+DS4A_DEV float lg2(float x) {
+    float y;
+    asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 
@@ -322,6 +345,7 @@ __global__ void __launch_bounds__(threads_of(GW), 1) paged_attn_kernel(const __g
     uint64_t *tok = all + 1;                                           // [8] a softmax warp has set its heads' running max
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + kOffMisc);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kOffMisc + 4);
+    uint32_t *drain_ph = tmem_slot + 2;                                // phases begun: bit 0 q_full, bit 1 + b x_full[b]
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -346,6 +370,7 @@ __global__ void __launch_bounds__(threads_of(GW), 1) paged_attn_kernel(const __g
         mbar_init(all, kSoftmaxWarps);
         for (int w = 0; w < kSoftmaxWarps; ++w) mbar_init(&tok[w], 1);
         *abort_flag = 0;
+        *drain_ph = 0;
         mbar_fence_init();
         tma_prefetch_desc(&a.tm_q);
         if (a.tma_rows) tma_prefetch_desc(&a.tm_rows);
@@ -362,6 +387,16 @@ __global__ void __launch_bounds__(threads_of(GW), 1) paged_attn_kernel(const __g
     const int half = static_cast<int>(blockIdx.x) % a.hsplit;
     const long long n_slots = 2LL * gridDim.x;
 
+    // 16-byte chunk ch of row h of a P buffer.  A row uses 96 of its 128 bytes; the
+    // other two chunks hold
+    //   chunk 6  word 0: head h's running max after the tile; FP8: buffer 0, word 1 +
+    //            row buffer: the scale of tile row h; buffer 1, words 1 and 2: see the
+    //            softmax;
+    //   chunk 7  at the end of item i, at i % 2: the group's sum for head h and the
+    //            max that the sum is relative to.
+    auto head_info = [&](int buf, int h, int ch) -> float * {
+        return reinterpret_cast<float *>(sP + buf * kPBuf + h * 128 + ((ch ^ (h & 7)) << 4));
+    };
     const int box_shift = min(a.page_shift, 4), box = 1 << box_shift;   // rows of a TMA box of the pool
 
     if (warp == kLookWarp) {
@@ -426,9 +461,9 @@ __global__ void __launch_bounds__(threads_of(GW), 1) paged_attn_kernel(const __g
                 s.mask_hi = hi;
             }
             last_i = c.i;
-            if (tma && !raw) {
-                if ((lane & (box - 1)) == 0 && y0 >= 0) prefetch_l2(a.rows + static_cast<long long>(y0) * kHeadDim, box * kHeadDim * 2);
-                if ((lane & (box - 1)) == 0 && y1 >= 0) prefetch_l2(a.rows + static_cast<long long>(y1) * kHeadDim, box * kHeadDim * 2);
+            if (tma && !raw && (lane & (box - 1)) == 0) {
+                if (y0 >= 0) prefetch_l2(a.rows + static_cast<long long>(y0) * kHeadDim, box * kHeadDim * 2);
+                if (y1 >= 0) prefetch_l2(a.rows + static_cast<long long>(y1) * kHeadDim, box * kHeadDim * 2);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&r_full[sl]);
@@ -449,14 +484,54 @@ __global__ void __launch_bounds__(threads_of(GW), 1) paged_attn_kernel(const __g
         const int gw = warp - kFirstGatherWarp;
         const int chunk = lane & 7, rsub = lane >> 3;
         auto row_of = [&](int k) -> int { return 4 * (gw + k * GW) + rsub; };
-        uint32_t rph = 0, xph = 0, used = 0;               // parity bits per buffer; buffers filled so far
+        uint32_t rph = 0, xph = 0;
         int xb = 0, ordinal = -1;                          // ordinal: items started
         bool ok = true;
         int pend = -1;                                     // buffer whose cp.async copies are in flight
+        bool pend_fp8 = false;                             // they are FP8 codes
+        // FP8 rows: a row's 512 codes land in the upper half of the row's own 1 KB
+        // (column blocks 4-7, unswizzled), and the warp that copied them writes the
+        // row over them as fp16.  Lane l: codes 16l .. 16l+15, which become 16-byte
+        // chunks 2(l%4) and 2(l%4)+1 of column block l/4.  Lanes of odd blocks write
+        // their second chunk first, so the eight lanes of a store phase hit eight
+        // different 16-byte bank groups.
+        auto expand = [&](uint32_t buf) {
+            __syncwarp();                                  // the other lanes' copies have landed too
+            const int blk = lane >> 2, c0 = 2 * (lane & 3), odd = blk & 1;
+#pragma unroll
+            for (int k = 0; k < kGroups; ++k) {
+                const int g = gw + k * GW;
+                if (g >= kRowGroups) continue;             // warp-uniform
+                uint32_t code[4][4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = 4 * g + i;
+                    ld_shared_v4(buf + (r >> 3) * kXGroup + (r & 7) * 128 + (4 + (lane >> 3)) * kXBlk + (lane & 7) * 16, code[i]);
+                }
+                __syncwarp();                              // every lane has read the rows that are written now
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = 4 * g + i;
+                    uint32_t lo[4], hi[4];
+                    e4m3x8_to_f16(code[i][0], code[i][1], lo);
+                    e4m3x8_to_f16(code[i][2], code[i][3], hi);
+                    const uint32_t rowa = buf + (r >> 3) * kXGroup + (r & 7) * 128 + blk * kXBlk;
+                    const uint32_t a0 = rowa + ((c0 ^ (r & 7)) << 4), a1 = rowa + (((c0 + 1) ^ (r & 7)) << 4);
+                    if (odd) {
+                        st_shared_v4(a1, hi);
+                        st_shared_v4(a0, lo);
+                    } else {
+                        st_shared_v4(a0, lo);
+                        st_shared_v4(a1, hi);
+                    }
+                }
+            }
+        };
         auto settle = [&](bool one_newer) {
             if (pend < 0) return;
             if (one_newer) cp_async_wait<1>();
             else cp_async_wait<0>();
+            if (FP8 && pend_fp8) expand(smem_u32(sX) + pend * kXBuf);
             fence_proxy_async();
             __syncwarp();
             if (lane == 0) mbar_arrive(&x_full[pend]);
@@ -493,30 +568,8 @@ __global__ void __launch_bounds__(threads_of(GW), 1) paged_attn_kernel(const __g
                     tma_load_q(sQ, &a.tm_q, q_full, (unit * a.hsplit + half) * kNHead);
                 }
             }
-            // FP8 rows go to registers before their buffer is free.  Lane l: codes
-            // 16l .. 16l+15 of each row of its groups, and the rows' scales.
-            const bool fp8_tile = FP8 && !raw_tile;
-            uint4 rg[kGroups][4];
-            float s8[kGroups][4];
-            if (fp8_tile) {
-#pragma unroll
-                for (int k = 0; k < kGroups; ++k) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int sr = __shfl_sync(0xffffffffu, src[k], 8 * i);   // row i of the group (lanes 8i.. hold it)
-                        if (sr >= 0) {
-                            rg[k][i] = ld_nc_v4(reinterpret_cast<const uint4 *>(a.rows8 + static_cast<long long>(sr) * kHeadDim) + lane);
-                            s8[k][i] = __ldg(a.row_scale + sr);
-                        } else {
-                            rg[k][i] = make_uint4(0u, 0u, 0u, 0u);
-                            s8[k][i] = 0.f;
-                        }
-                    }
-                }
-            }
             if (!(ok = wait_for(&x_empty[xb], ((xph >> xb) & 1) ^ 1))) break;
             xph ^= 1u << xb;
-            used |= 1u << xb;
             uint8_t *dst = sX + xb * kXBuf;
             if (gw == 0) {
                 if (lane == 0) sValid[xb] = mask;          // published by this warp's arrival
@@ -534,7 +587,26 @@ __global__ void __launch_bounds__(threads_of(GW), 1) paged_attn_kernel(const __g
                 }
             }
             const uint32_t buf = smem_u32(dst);
-            if (!tma_tile && !fp8_tile) {
+            const bool fp8_tile = FP8 && !raw_tile;
+            if (fp8_tile) {
+#pragma unroll
+                for (int k = 0; k < kGroups; ++k) {
+                    const int g = gw + k * GW;
+                    if (g >= kRowGroups) continue;         // warp-uniform
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = 4 * g + i, sr = __shfl_sync(0xffffffffu, src[k], 8 * i);   // lanes 8i.. hold row i
+                        cp_async16(buf + (r >> 3) * kXGroup + (4 + (lane >> 3)) * kXBlk + (r & 7) * 128 + (lane & 7) * 16,
+                                   a.rows8 + static_cast<long long>(max(sr, 0)) * kHeadDim + lane * 16, sr >= 0 ? 16u : 0u);
+                    }
+                    if (chunk == 0)
+                        cp_async4(smem_u32(head_info(0, row_of(k), 6) + 1 + xb), a.row_scale + max(src[k], 0), src[k] >= 0 ? 4u : 0u);
+                }
+                cp_async_commit();
+                settle(true);
+                pend = xb;
+                pend_fp8 = true;
+            } else if (!tma_tile) {
                 // One pair of addresses per row, the blocks at constant steps from it
                 // (a masked row copies no bytes; its address is q's).
                 const uint16_t *from[kGroups];
@@ -554,36 +626,9 @@ __global__ void __launch_bounds__(threads_of(GW), 1) paged_attn_kernel(const __g
                 cp_async_commit();
                 settle(true);
                 pend = xb;
+                pend_fp8 = false;
             } else {
                 settle(false);
-                if (fp8_tile) {
-                    // dims 16l .. 16l+15 are 16-byte chunks 2(l%4) and 2(l%4)+1 of the
-                    // 64-column block l/4.  Lanes of odd blocks write their second
-                    // chunk first, so the eight lanes of a store phase hit eight
-                    // different 16-byte bank groups.
-                    const int blk = lane >> 2, c0 = 2 * (lane & 3), odd = blk & 1;
-#pragma unroll
-                    for (int k = 0; k < kGroups; ++k) {
-                        if (gw + k * GW >= kRowGroups) continue;       // warp-uniform
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int r = 4 * (gw + k * GW) + i;
-                            uint32_t lo[4], hi[4];
-                            e4m3x8_to_bf16(rg[k][i].x, rg[k][i].y, s8[k][i], lo);
-                            e4m3x8_to_bf16(rg[k][i].z, rg[k][i].w, s8[k][i], hi);
-                            const uint32_t rowa = buf + (r >> 3) * kXGroup + blk * kXBlk + (r & 7) * 128;
-                            const uint32_t a0 = rowa + ((c0 ^ (r & 7)) << 4), a1 = rowa + (((c0 + 1) ^ (r & 7)) << 4);
-                            if (odd) {
-                                st_shared_v4(a1, hi);
-                                st_shared_v4(a0, lo);
-                            } else {
-                                st_shared_v4(a0, lo);
-                                st_shared_v4(a1, hi);
-                            }
-                        }
-                    }
-                    fence_proxy_async();
-                }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&x_full[xb]);
             }
@@ -594,12 +639,7 @@ __global__ void __launch_bounds__(threads_of(GW), 1) paged_attn_kernel(const __g
             *abort_flag = 1;
             if (lane == 0) {
                 report(a.status, DS4A_DEV_TIMEOUT);
-                // TMA copies of q and of row tiles may still be in flight
-                if (gw == 0) {
-                    if (ordinal >= 0) wait_drain(q_full, ordinal & 1);
-                    for (int b = 0; b < kBufs; ++b)
-                        if ((used >> b) & 1) wait_drain(&x_full[b], ((xph >> b) & 1) ^ 1);
-                }
+                if (gw == 0) *drain_ph = (xph << 1) | static_cast<uint32_t>((ordinal + 1) & 1);
             }
             __syncwarp();
         }
@@ -620,7 +660,7 @@ __global__ void __launch_bounds__(threads_of(GW), 1) paged_attn_kernel(const __g
             bool q16 = false;
             for (int t = m.t0; t < m.t1; ++t) {
                 const bool raw = t >= m.ct;
-                if (raw && !q16) {
+                if ((FP8 || raw) && !q16) {
                     if (!(ok = warp_wait(q16_ready, q16ph, abort_flag))) break;
                     q16ph ^= 1;
                     q16 = true;
@@ -636,7 +676,7 @@ __global__ void __launch_bounds__(threads_of(GW), 1) paged_attn_kernel(const __g
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
                         umma_elect(tmem + kTmemS + b * 64, dq + static_cast<uint64_t>(blk * (kQBlk >> 4) + 2 * kk),
-                                   dx + static_cast<uint64_t>(blk * (kXBlk >> 4) + 2 * kk), raw ? id_f16 : id_bf,
+                                   dx + static_cast<uint64_t>(blk * (kXBlk >> 4) + 2 * kk), FP8 || raw ? id_f16 : id_bf,
                                    (blk | kk) ? 1u : 0u);
                 }
                 commit_elect(&s_full[b]);
@@ -681,7 +721,7 @@ __global__ void __launch_bounds__(threads_of(GW), 1) paged_attn_kernel(const __g
                     for (int ks = 0; ks < TR / 16; ++ks)
                         umma_elect(tmem + kTmemO + cd * kNHead,
                                    dxv + static_cast<uint64_t>((xb * kXBuf + 2 * cd * kXBlk + ks * 2 * kXGroup) >> 4),
-                                   dp + static_cast<uint64_t>((b * kPBuf + ks * 32) >> 4), raw ? id_f16 : id_bf,
+                                   dp + static_cast<uint64_t>((b * kPBuf + ks * 32) >> 4), FP8 || raw ? id_f16 : id_bf,
                                    (t == m.t0 && ks == 0) ? 0u : 1u);
                 }
                 commit_elect(&x_empty[xb]);              // row tile and P buffer free
@@ -708,10 +748,11 @@ __global__ void __launch_bounds__(threads_of(GW), 1) paged_attn_kernel(const __g
         // takes it from the warp of the other group that had the tile before, and
         // hands it on before its exponentials.  (One group for all tiles was the
         // pipeline's slowest stage: 1.3 us of the 1.5 us per tile.)
-        // A row of P uses 96 of its 128 bytes; its other 16-byte chunks hold
-        //   chunk 6  the head's running max after the tile,
-        //   chunk 7  at the end of item i, at i % 2: the group's sum and the max that
-        //            the sum is relative to.
+        // FP8: a row's elements are code * s_r; the tile holds the codes as fp16 and
+        // q is in fp16 for all tiles.  The logits take s_r from shared memory, and P
+        // the weight that multiplies the codes, 2^(l + log2 s_r - W), with a running
+        // max W of its own (of l + log2 s_r, kept like M: the one that O^T is relative
+        // to), so that every weight lies in fp16's range relative to the largest.  The sums stay relative to M; out = O^T 2^(W - M) / l.
         constexpr int J = TR / 8;
         const int b = warp >> 2;                        // group; its S and P buffer
         const int q4 = warp & 3;
@@ -723,9 +764,6 @@ __global__ void __launch_bounds__(threads_of(GW), 1) paged_attn_kernel(const __g
         uint32_t qph = 0, gph = 0, aph = 0;
         uint32_t d = 0;                                 // the CTA's tiles so far
         bool ok = true;
-        auto head_info = [&](int buf, int h, int ch) -> float * {
-            return reinterpret_cast<float *>(sP + buf * kPBuf + h * 128 + ((ch ^ (h & 7)) << 4));
-        };
         // The values GEMM of tile x (its row buffer's latest use).
         auto wait_values = [&](uint32_t x) -> bool {
             return __all_sync(0xffffffffu, mbar_wait_hint(&x_empty[x % kBufs], (x / kBufs) & 1, abort_flag));
@@ -759,7 +797,8 @@ __global__ void __launch_bounds__(threads_of(GW), 1) paged_attn_kernel(const __g
             ok = __all_sync(0xffffffffu, mbar_wait_hint(q_full, qph, abort_flag));
             if (!ok) break;
             qph ^= 1;
-            if (m.t0 >= m.ct && (d & 1) == static_cast<uint32_t>(b)) convert_q();   // the item starts with a raw tile
+            // fp16 from the first tile on
+            if ((FP8 || m.t0 >= m.ct) && (d & 1) == static_cast<uint32_t>(b)) convert_q();
             // The next item's q may overwrite this one only after every softmax
             // warp has seen this one land: q_full must never run two phases
             // ahead of a warp's wait (its parity could not tell them apart).
@@ -773,7 +812,7 @@ __global__ void __launch_bounds__(threads_of(GW), 1) paged_attn_kernel(const __g
                 if (!ok) break;
                 // The next tile is the first raw one: its logits need q in fp16,
                 // and every compressed logit GEMM has completed (this one too).
-                if (t + 1 < m.t1 && t + 1 == m.ct) convert_q();
+                if (!FP8 && t + 1 < m.t1 && t + 1 == m.ct) convert_q();
                 tc_fence_after();
                 uint32_t r[4 * J];
                 tmem_ld_s(tmem + lane_off + kTmemS + b * 64, r);
@@ -788,10 +827,21 @@ __global__ void __launch_bounds__(threads_of(GW), 1) paged_attn_kernel(const __g
                 // raw logits: the max is taken before scaling and p = 2^(s*c - M)
                 // is one FMA and one ex2.  Otherwise masked rows are -inf and the
                 // logits are scaled first (c = 1 below).
-                const bool full = vm.x == 0xffffffffu && vm.y == 0xffffu && sl2 > 0.f;
+                const bool full = !FP8 && vm.x == 0xffffffffu && vm.y == 0xffffu && sl2 > 0.f;
                 const float mul = full ? sl2 : 1.f;
                 float x[4 * J];
-                if (full) {
+                float e8[2 * J];                         // FP8: log2 of the rows' scales
+                if constexpr (FP8) {
+#pragma unroll
+                    for (int j = 0; j < 2 * J; ++j) {
+                        const int row = 8 * (j >> 1) + 2 * t4 + (j & 1);
+                        const float s = raw ? 1.f : head_info(0, row, 6)[1 + d % kBufs];
+                        e8[j] = lg2(fmaxf(s, 1.17549435e-38f));   // a scale of 0 adds to the sum, and below 1e-35 to the result
+                        const bool v = ((row < 32 ? vm.x : vm.y) >> (row & 31)) & 1u;
+                        x[4 * (j >> 1) + (j & 1)] = v ? __uint_as_float(r[4 * (j >> 1) + (j & 1)]) * (sl2 * s) : NEG_INF;
+                        x[4 * (j >> 1) + 2 + (j & 1)] = v ? __uint_as_float(r[4 * (j >> 1) + 2 + (j & 1)]) * (sl2 * s) : NEG_INF;
+                    }
+                } else if (full) {
 #pragma unroll
                     for (int j = 0; j < 4 * J; ++j) x[j] = __uint_as_float(r[j]);
                 } else {
@@ -817,34 +867,61 @@ __global__ void __launch_bounds__(threads_of(GW), 1) paged_attn_kernel(const __g
                 mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2));
                 mx0 *= mul;
                 mx1 *= mul;
+                float wx0 = NEG_INF, wx1 = NEG_INF;      // FP8: max of the codes' weights
+                if constexpr (FP8) {
+#pragma unroll
+                    for (int j = 0; j < J; ++j) {
+                        wx0 = fmaxf(wx0, fmaxf(x[4 * j] + e8[2 * j], x[4 * j + 1] + e8[2 * j + 1]));
+                        wx1 = fmaxf(wx1, fmaxf(x[4 * j + 2] + e8[2 * j], x[4 * j + 3] + e8[2 * j + 1]));
+                    }
+                    wx0 = fmaxf(wx0, __shfl_xor_sync(0xffffffffu, wx0, 1));
+                    wx0 = fmaxf(wx0, __shfl_xor_sync(0xffffffffu, wx0, 2));
+                    wx1 = fmaxf(wx1, __shfl_xor_sync(0xffffffffu, wx1, 1));
+                    wx1 = fmaxf(wx1, __shfl_xor_sync(0xffffffffu, wx1, 2));
+                }
                 // The running max after the tile before, from the other group.
-                float P0 = NEG_INF, P1 = NEG_INF;
+                float P0 = NEG_INF, P1 = NEG_INF, Q0 = NEG_INF, Q1 = NEG_INF;
                 if (t > m.t0) {
                     ok = __all_sync(0xffffffffu, mbar_wait_hint(&tok[4 * (b ^ 1) + q4], ((d - 1) >> 1) & 1, abort_flag));
                     if (!ok) break;
                     P0 = *head_info(b ^ 1, h0, 6);
                     P1 = *head_info(b ^ 1, h1, 6);
+                    if constexpr (FP8) {
+                        Q0 = head_info(1, h0, 6)[1 + (b ^ 1)];
+                        Q1 = head_info(1, h1, 6)[1 + (b ^ 1)];
+                    }
                 }
                 // It is raised only when the tile exceeds it by more than 2^8, so
-                // p <= 256 always; al: the factor for what O^T holds.
-                float al0 = 1.f, al1 = 1.f, N0 = P0, N1 = P1;
-                if (P0 == NEG_INF) {
-                    N0 = mx0;                            // first finite max: O is still 0
-                } else if (mx0 > P0 + kRescaleThreshold) {
-                    al0 = ex2(P0 - mx0);
-                    N0 = mx0;
-                }
-                if (P1 == NEG_INF) {
-                    N1 = mx1;
-                } else if (mx1 > P1 + kRescaleThreshold) {
-                    al1 = ex2(P1 - mx1);
-                    N1 = mx1;
+                // p <= 256 always.  (M: running max of the logits; W: of what O^T is
+                // relative to, M itself unless FP8; al: the factor for what O^T holds.)
+                float al0 = 1.f, al1 = 1.f, N0 = P0, N1 = P1, W0 = Q0, W1 = Q1;
+                auto raise = [&](float &top, float mx, float &al) {
+                    if (top == NEG_INF) {
+                        top = mx;                        // first finite max: nothing is summed yet
+                    } else if (mx > top + kRescaleThreshold) {
+                        al = ex2(top - mx);
+                        top = mx;
+                    }
+                };
+                if constexpr (FP8) {
+                    float unused = 1.f;
+                    raise(N0, mx0, unused);
+                    raise(N1, mx1, unused);
+                    raise(W0, wx0, al0);
+                    raise(W1, wx1, al1);
+                } else {
+                    raise(N0, mx0, al0);
+                    raise(N1, mx1, al1);
                 }
                 // Any head raised in any warp: every warp rescales its O^T lanes.
                 const bool wresc = __any_sync(0xffffffffu, (al0 != 1.f) | (al1 != 1.f));
                 if (t4 == 0) {
                     *head_info(b, h0, 6) = N0;
                     *head_info(b, h1, 6) = N1;
+                    if constexpr (FP8) {
+                        head_info(1, h0, 6)[1 + b] = W0;
+                        head_info(1, h1, 6)[1 + b] = W1;
+                    }
                     sAlpha[b * kNHead + h0] = al0;
                     sAlpha[b * kNHead + h1] = al1;
                 }
@@ -863,20 +940,33 @@ __global__ void __launch_bounds__(threads_of(GW), 1) paged_attn_kernel(const __g
                 M1 = N1;
                 const float nr0 = M0 == NEG_INF ? 0.f : -M0, nr1 = M1 == NEG_INF ? 0.f : -M1;
                 float s0 = 0.f, s1 = 0.f;
+                if constexpr (FP8) {
+                    const float nw0 = W0 == NEG_INF ? 0.f : -W0, nw1 = W1 == NEG_INF ? 0.f : -W1;
 #pragma unroll
-                for (int j = 0; j < J; ++j) {
-                    x[4 * j] = ex2z(fmaf(x[4 * j], mul, nr0));
-                    x[4 * j + 1] = ex2z(fmaf(x[4 * j + 1], mul, nr0));
-                    x[4 * j + 2] = ex2z(fmaf(x[4 * j + 2], mul, nr1));
-                    x[4 * j + 3] = ex2z(fmaf(x[4 * j + 3], mul, nr1));
-                    s0 += x[4 * j] + x[4 * j + 1];
-                    s1 += x[4 * j + 2] + x[4 * j + 3];
+                    for (int j = 0; j < J; ++j) {
+                        s0 += ex2z(x[4 * j] + nr0) + ex2z(x[4 * j + 1] + nr0);
+                        s1 += ex2z(x[4 * j + 2] + nr1) + ex2z(x[4 * j + 3] + nr1);
+                        x[4 * j] = ex2z(x[4 * j] + (e8[2 * j] + nw0));
+                        x[4 * j + 1] = ex2z(x[4 * j + 1] + (e8[2 * j + 1] + nw0));
+                        x[4 * j + 2] = ex2z(x[4 * j + 2] + (e8[2 * j] + nw1));
+                        x[4 * j + 3] = ex2z(x[4 * j + 3] + (e8[2 * j + 1] + nw1));
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < J; ++j) {
+                        x[4 * j] = ex2z(fmaf(x[4 * j], mul, nr0));
+                        x[4 * j + 1] = ex2z(fmaf(x[4 * j + 1], mul, nr0));
+                        x[4 * j + 2] = ex2z(fmaf(x[4 * j + 2], mul, nr1));
+                        x[4 * j + 3] = ex2z(fmaf(x[4 * j + 3], mul, nr1));
+                        s0 += x[4 * j] + x[4 * j + 1];
+                        s1 += x[4 * j + 2] + x[4 * j + 3];
+                    }
                 }
                 l0 += s0;
                 l1 += s1;
                 // p in the rows' 16-bit type: the operand of the values GEMM
                 uint32_t pk0[J], pk1[J];
-                if (raw) {
+                if (FP8 || raw) {
 #pragma unroll
                     for (int j = 0; j < J; ++j) {
                         pk0[j] = pack2<true>(x[4 * j], x[4 * j + 1]);
@@ -953,6 +1043,10 @@ __global__ void __launch_bounds__(threads_of(GW), 1) paged_attn_kernel(const __g
                     L += lm.y == NEG_INF ? 0.f : lm.y == M ? lm.x : lm.x * ex2(lm.y - M);
                 }
                 inv[k] = m.split ? 1.f : L > 0.f ? 1.f / L : 0.f;
+                if constexpr (FP8) {
+                    const float W = head_info(1, h, 6)[1 + ((d - 1) & 1)];
+                    inv[k] *= L > 0.f ? ex2(W - M) : 0.f;
+                }
                 if (warp == 0) {
                     if (m.split) {
                         float *ml = static_cast<float *>(a.ws) + n_slots * kNHead * kHeadDim + (slot * kNHead + h) * 2;
@@ -975,7 +1069,11 @@ __global__ void __launch_bounds__(threads_of(GW), 1) paged_attn_kernel(const __g
                 if (m.split) {
                     float *o = static_cast<float *>(a.ws) + (slot * kNHead + hb) * kHeadDim + dim;
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) o[k * kHeadDim] = __uint_as_float(v[k]);
+                    for (int k = 0; k < 32; ++k) {
+                        float y = __uint_as_float(v[k]);
+                        if constexpr (FP8) y *= __shfl_sync(0xffffffffu, (cc & 1) ? inv[1] : inv[0], k);
+                        o[k * kHeadDim] = y;
+                    }
                 } else {
                     // bf16, two dims a store: of each pair of heads an even lane takes
                     // the first and an odd lane the second, with its neighbour's dim
@@ -1002,6 +1100,12 @@ __global__ void __launch_bounds__(threads_of(GW), 1) paged_attn_kernel(const __g
 
     tc_fence_before();
     __syncthreads();
+    if (*abort_flag && threadIdx.x == 0) {
+        // A wait gave up: let the TMA copies of q and of row tiles that may be in
+        // flight land, the last phase of each barrier (one never used passes at once).
+        wait_drain(q_full, (*drain_ph & 1) ^ 1);
+        for (int k = 0; k < kBufs; ++k) wait_drain(&x_full[k], ((*drain_ph >> (k + 1)) & 1) ^ 1);
+    }
     if (warp == kMmaWarp) {
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);

@@ -105,6 +105,18 @@ def test_all_rows_fp8(cuda_lib, H, P):
     b.check()
 
 
+@pytest.mark.parametrize("H,P", [(64, 16), (128, 64)])
+def test_fp8_scales_of_any_size(cuda_lib, H, P):
+    """Scales that are no powers of two, and rows of scale 0: logit 0, nothing added but their weight."""
+    b = Batch(EDGES, P, H, fp8=True, n_raw=[128, 0, 65] * 5, seed=2)
+    b.row_scale *= torch.rand(b.row_scale.shape, generator=gen(5), device=DEV) + 1
+    b.row_scale.view(-1)[::7] = 0
+    b.exact = e4m3_rows(b.rows.view(-1, 512), b.row_scale.view(-1))
+    b(cuda_lib)
+    assert cuda_lib.ds4a_get_device_status() == (0, 0)
+    b.check()
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("top_k", [1, 63, 64, 100, 512, 2048])
 @pytest.mark.parametrize("H,P", [(64, 64), (128, 8)])
