@@ -24,6 +24,7 @@
 // items are 128 further on, mostly in the same sequence, whose lengths it still
 // holds.  Bound: a small step the latency of launch -> load -> scan -> search ->
 // load -> store, on one CTA; a large one the instructions per item, on every SM.
+// (8 sequences: 4.7 us; 256 with 262k tokens and 66k rows 6.8 us.)
 // A large step that updates *free_head in place runs as one cluster instead, whose
 // barrier lies between the reads of the old head and its update.
 //

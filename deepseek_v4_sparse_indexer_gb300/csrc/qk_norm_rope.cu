@@ -26,7 +26,11 @@
 // within the last chunk's last lanes (its pairs inside a lane, or n_rot / 16
 // lanes apart).  The token's angles are computed once per warp, one pair a lane,
 // and dealt out by shuffles; the next row's loads are in flight while a row is
-// reduced.  Bound: HBM (4 flop per byte).
+// reduced.  Bound: HBM (4 flop per byte).  Measured (GB300): 2,048 tokens x 64
+// heads of 512 bf16 46.2 us = 5.8 TB/s, 86 % of the copy bandwidth; of 128 14.9 us =
+// 4.6 TB/s (a token's angles, in fp64, weigh more on its smaller heads); 16,384 fp32
+// rows into the FP8 store 11.5 us = 3.7 TB/s (a row a warp and its angles); one
+// token 2.2 us.
 #include <cuda_fp16.h>
 
 #include "common.cuh"
