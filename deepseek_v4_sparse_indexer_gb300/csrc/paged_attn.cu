@@ -17,15 +17,15 @@
 // 48 rows, so the row buffers in flight decide: three tiles of 48 rows fit beside
 // q (64 KB) and P where two of 64 rows did, a gathered tile's copies are issued
 // before the previous one's have landed, and two softmax groups overlap.
-// Measured (GB300): 640 units x 8,192 rows 965 us = 5.7 TB/s, 85 % of the copy
-// bandwidth, 640 ragged units of up to 8,192 rows 545 us; 1,368 units x 512 listed
-// rows 233 us = 4.6 TB/s, random 1 KB rows arriving by cp.async at 30 GB/s per SM
+// Measured (GB300): 640 units x 8,192 rows 929 us = 5.9 TB/s, 88 % of the copy
+// bandwidth, 640 ragged units of up to 8,192 rows 524 us; 1,368 units x 512 listed
+// rows 232 us = 4.6 TB/s, random 1 KB rows arriving by cp.async at 30 GB/s per SM
 // of the 34-40 that such a gather alone reaches; 128 heads: 128 units x 1,024
-// listed rows 92 us, each half at its own copy of the rows from L2.  FP8 rows, 48
-// units of up to 4,096: 60 us, 2.3 us a tile, bound by the pass that writes the
+// listed rows 91 us, each half at its own copy of the rows from L2.  FP8 rows, 48
+// units of up to 4,096: 61 us, 2.3 us a tile, bound by the pass that writes the
 // codes out as fp16: its instructions, and its 72 KB more a tile through shared
 // memory (the conversion itself is not: shifts and a multiplication in its place
-// took 73 us).  A few units are latency: 1 x 1,024 rows 13.4 us with its merge.
+// took 73 us).  A few units are latency: 1 x 1,024 rows 13.1 us with its merge.
 //
 // Roles (one CTA per SM, persistent over its share of the batch's tiles):
 //   lookup   warp 10: turns a tile's rows (listed ones: row number, then page; dense
@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(threads_of(GW), 1) paged_attn_kernel(const __g
     uint64_t *tok = all + 1;                                           // [8] a softmax warp has set its heads' running max
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + kOffMisc);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kOffMisc + 4);
-    uint32_t *drain_ph = tmem_slot + 2;                                // phases begun: bit 0 q_full, bit 1 + b x_full[b]
+    uint32_t *drain_ph = tmem_slot + 2;                                // phases begun, odd: bit 0 q_full, bit 1 + b x_full[b]
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -572,7 +572,11 @@ __global__ void __launch_bounds__(threads_of(GW), 1) paged_attn_kernel(const __g
             xph ^= 1u << xb;
             uint8_t *dst = sX + xb * kXBuf;
             if (gw == 0) {
-                if (lane == 0) sValid[xb] = mask;          // published by this warp's arrival
+                if (lane == 0) {
+                    sValid[xb] = mask;                     // published by this warp's arrival
+                    // (kept here tile by tile: one store at the end is 6 % slower)
+                    *drain_ph = (xph << 1) | static_cast<uint32_t>((ordinal + 1) & 1);
+                }
                 if (tma_tile) {
                     if (lane == 0) mbar_expect_tx(&x_full[xb], kXBuf);
                     __syncwarp();
@@ -637,11 +641,7 @@ __global__ void __launch_bounds__(threads_of(GW), 1) paged_attn_kernel(const __g
         settle(false);                                     // also when a wait gave up: copies in flight have landed
         if (!ok) {
             *abort_flag = 1;
-            if (lane == 0) {
-                report(a.status, DS4A_DEV_TIMEOUT);
-                if (gw == 0) *drain_ph = (xph << 1) | static_cast<uint32_t>((ordinal + 1) & 1);
-            }
-            __syncwarp();
+            if (lane == 0) report(a.status, DS4A_DEV_TIMEOUT);
         }
     } else if (warp == kMmaWarp) {
         // ------------------------------------------------------------ logits issuer
@@ -1101,10 +1101,13 @@ __global__ void __launch_bounds__(threads_of(GW), 1) paged_attn_kernel(const __g
     tc_fence_before();
     __syncthreads();
     if (*abort_flag && threadIdx.x == 0) {
-        // A wait gave up: let the TMA copies of q and of row tiles that may be in
-        // flight land, the last phase of each barrier (one never used passes at once).
-        wait_drain(q_full, (*drain_ph & 1) ^ 1);
-        for (int k = 0; k < kBufs; ++k) wait_drain(&x_full[k], ((*drain_ph >> (k + 1)) & 1) ^ 1);
+        // A wait gave up: let the TMA copies of row tiles and of q that may be in
+        // flight land, the last phase begun of each barrier (one never used passes at
+        // once).  q may be one phase further: if not, that wait gives up in turn.
+        const uint32_t ph = *drain_ph;
+        for (int k = 0; k < kBufs; ++k) wait_drain(&x_full[k], ((ph >> (k + 1)) & 1) ^ 1);
+        wait_drain(q_full, (ph & 1) ^ 1);
+        wait_drain(q_full, ph & 1);
     }
     if (warp == kMmaWarp) {
         tc_fence_after();

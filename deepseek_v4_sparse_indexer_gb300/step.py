@@ -175,7 +175,8 @@ class PagedDecodeStep:
     """One new token for each of up to U sequences, over paged caches.
 
     x holds, per step: past, add (i32 [U]: tokens in the cache and new ones, 1 or
-    0; sequences without a new token come last), q [U,H,512] and kv [U,512], the
+    0; sequences without a new token come last, and what out holds for them is
+    of no use unless they are empty: zeros), q [U,H,512] and kv [U,512], the
     projections before norm and rotation (bf16, fp16 or fp32); with top_k also iq
     [U,64,128] and w f32 [U,64].  And, kept by the program: table i32
     [U,max_pages], free_pages and free_head (updated in place), ring i32 [U] or
@@ -240,7 +241,8 @@ class PagedDecodeStep:
                                    x["ik"], x["table"], self.n_rows, self.scores, stream=stream)
 
     def select(self, x, stream=None):
-        B.ds4a_topk_select(self.scores, self.n_rows, self.top_k, self.idx, self.count, self.ws_topk, stream=stream)
+        with torch.cuda.device(self.scores.device):        # the paged calls see to it themselves
+            B.ds4a_topk_select(self.scores, self.n_rows, self.top_k, self.idx, self.count, self.ws_topk, stream=stream)
 
     def attend(self, x, scale=DEFAULT_SCALE, stream=None):
         idx, count = (self.idx.view(self.U, self.top_k), self.count.view(self.U)) if self.top_k else (None, None)
