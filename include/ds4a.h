@@ -21,7 +21,9 @@
  *  - Pointers named as device buffers are CUDA device pointers owned by the
  *    caller; the library never frees, keeps or allocates memory.  Scratch
  *    memory, where an op needs it, is a caller-provided workspace `ws` of at
- *    least ds4a_workspace_bytes(...) bytes (NULL/0 when that returns 0).
+ *    least ds4a_workspace_bytes(...) bytes (NULL/0 when that returns 0).  It
+ *    belongs to one call at a time: calls (or replayed graphs) that may overlap
+ *    on the GPU need one each.
  *  - bf16 and fp16 tensors are passed as uint16_t storage words.
  *  - `stream` is a cudaStream_t passed as void* (NULL = legacy default
  *    stream).  Every op only enqueues kernels on it and returns; nothing
