@@ -17,15 +17,18 @@
 // 48 rows, so the row buffers in flight decide: three tiles of 48 rows fit beside
 // q (64 KB) and P where two of 64 rows did, a gathered tile's copies are issued
 // before the previous one's have landed, and two softmax groups overlap.
-// Measured (GB300): 640 units x 8,192 rows 929 us = 5.9 TB/s, 88 % of the copy
-// bandwidth, 640 ragged units of up to 8,192 rows 524 us; 1,368 units x 512 listed
-// rows 232 us = 4.6 TB/s, random 1 KB rows arriving by cp.async at 30 GB/s per SM
+// Five roles' code in turn on one SM also fills its instruction cache: loops are
+// unrolled only as far as it pays (all of them unrolled: 640 ragged units 524-560 us,
+// by where the code happened to lie, now 495).
+// Measured (GB300): 640 units x 8,192 rows 902 us = 6.1 TB/s, 91 % of the copy
+// bandwidth, 640 ragged units of up to 8,192 rows 495 us; 1,368 units x 512 listed
+// rows 228 us = 4.7 TB/s, random 1 KB rows arriving by cp.async at 31 GB/s per SM
 // of the 34-40 that such a gather alone reaches; 128 heads: 128 units x 1,024
-// listed rows 91 us, each half at its own copy of the rows from L2.  FP8 rows, 48
-// units of up to 4,096: 61 us, 2.3 us a tile, bound by the pass that writes the
-// codes out as fp16: its instructions, and its 72 KB more a tile through shared
-// memory (the conversion itself is not: shifts and a multiplication in its place
-// took 73 us).  A few units are latency: 1 x 1,024 rows 13.1 us with its merge.
+// listed rows 87 us, each half at its own copy of the rows from L2.  FP8 rows, 48
+// units of up to 4,096: 55 us, 2.1 us a tile, the cycle being longer by the pass that
+// writes the codes out as fp16 (its conversions are not the limit: shifts and a
+// multiplication in their place took longer).  A few units are latency: 1 x 1,024 rows
+// 13.4 us with its merge.
 //
 // Roles (one CTA per SM, persistent over its share of the batch's tiles):
 //   lookup   warp 10: turns a tile's rows (listed ones: row number, then page; dense
@@ -71,11 +74,13 @@ constexpr int kPvWarp = 9;                    // warp 9: values UMMA issuer
 constexpr int kLookWarp = 10;                 // warp 10: row lookup
 constexpr int kFirstGatherWarp = 11;
 constexpr int kRowGroups = TR / 4;            // 4-row groups of a tile, dealt round-robin to the gather warps
-// Gather warps: five, so that the block has 16 warps of 128 registers.  FP8 rows:
-// six, two groups each (48 units of up to 4,096 rows 60 us; five 64, nine 62).
-constexpr int kGatherWarpsBf16 = 5;
-constexpr int kGatherWarpsFp8 = 6;
-constexpr int threads_of(int gw) { return (kFirstGatherWarp + gw) * 32; }
+// Gather warps: four, three groups each (1,368 x 512 listed rows 228 us, with three
+// 229, five and six 230; 48 units of up to 4,096 FP8 rows 55 us, with three 56, five
+// 57, six 59).
+constexpr int kGatherWarps = 4;
+constexpr int kGroups = kRowGroups / kGatherWarps;
+static_assert(kRowGroups % kGatherWarps == 0, "whole 4-row groups for every gather warp");
+constexpr int kThreads = (kFirstGatherWarp + kGatherWarps) * 32;
 constexpr int kQBlk = kNHead * 128;           // 64 heads x 64 dims: 8 KB
 constexpr int kXBlk = 1024;                   // 8 rows x 64 dims
 constexpr int kXGroup = 8 * kXBlk;            // 8 rows
@@ -173,6 +178,18 @@ DS4A_DEV void tmem_ld_s(uint32_t taddr, uint32_t (&r)[24]) {
           "=&r"(r[9]), "=&r"(r[10]), "=&r"(r[11]), "=&r"(r[12]), "=&r"(r[13]), "=&r"(r[14]), "=&r"(r[15]), "=&r"(r[16]),
           "=&r"(r[17]), "=&r"(r[18]), "=&r"(r[19]), "=&r"(r[20]), "=&r"(r[21]), "=&r"(r[22]), "=&r"(r[23])
         : "r"(taddr), "r"(taddr + 32)
+        : "memory");
+}
+
+// 16 columns of this warp's 32 TMEM lanes.
+DS4A_DEV void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=&r"(r[0]), "=&r"(r[1]), "=&r"(r[2]), "=&r"(r[3]), "=&r"(r[4]), "=&r"(r[5]), "=&r"(r[6]), "=&r"(r[7]),
+          "=&r"(r[8]), "=&r"(r[9]), "=&r"(r[10]), "=&r"(r[11]), "=&r"(r[12]), "=&r"(r[13]), "=&r"(r[14]), "=&r"(r[15])
+        : "r"(taddr)
         : "memory");
 }
 
@@ -314,9 +331,8 @@ DS4A_DEV void advance(const PagedAttnArgs &a, const Sched &sc, Tile &x) {
     first_from(a, sc, x);
 }
 
-template <int GW, bool FP8>
-__global__ void __launch_bounds__(threads_of(GW), 1) paged_attn_kernel(const __grid_constant__ PagedAttnArgs a) {
-    constexpr int kGroups = (kRowGroups + GW - 1) / GW;   // 4-row groups per gather warp
+template <bool FP8>
+__global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_constant__ PagedAttnArgs a) {
     pdl_launch_dependents();
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -350,10 +366,10 @@ __global__ void __launch_bounds__(threads_of(GW), 1) paged_attn_kernel(const __g
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int b = 0; b < kBufs; ++b) {
-            mbar_init(&x_full[b], GW);
+            mbar_init(&x_full[b], kGatherWarps);
             mbar_init(&x_empty[b], 1);
             mbar_init(&r_full[b], 1);
-            mbar_init(&r_empty[b], GW);
+            mbar_init(&r_empty[b], kGatherWarps);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&s_full[b], 1);
@@ -414,8 +430,10 @@ __global__ void __launch_bounds__(threads_of(GW), 1) paged_attn_kernel(const __g
         int sl = 0, last_i = -1;
         bool ok = true;
         Tile c;
-        c.i = 0;
-        first_from(a, sc, c);
+        c.i = -1;
+        c.t = 0;
+        c.m.t1 = 0;                                        // advance goes to the first piece with tiles
+        advance(a, sc, c);
         int v0 = row_number(c, lane), v1 = row_number(c, lane + 32);
         for (;;) {
             const bool end = c.i >= sc.n_pieces;
@@ -478,12 +496,12 @@ __global__ void __launch_bounds__(threads_of(GW), 1) paged_attn_kernel(const __g
         }
     } else if (warp >= kFirstGatherWarp) {
         // ------------------------------------------------------------ row gather
-        // Warp g of GW brings the 4-row groups g, g + GW, ... of every tile.  Lane l
+        // Warp g of the four brings the 4-row groups g, g + 4, g + 8 of every tile.  Lane l
         // copies 16-byte chunk (l & 7) of row 4k + (l >> 3) of group k in every
         // 64-column block: a warp instruction moves four whole 128-byte segments.
         const int gw = warp - kFirstGatherWarp;
         const int chunk = lane & 7, rsub = lane >> 3;
-        auto row_of = [&](int k) -> int { return 4 * (gw + k * GW) + rsub; };
+        auto row_of = [&](int k) -> int { return 4 * (gw + k * kGatherWarps) + rsub; };
         uint32_t rph = 0, xph = 0;
         int xb = 0, ordinal = -1;                          // ordinal: items started
         bool ok = true;
@@ -498,10 +516,9 @@ __global__ void __launch_bounds__(threads_of(GW), 1) paged_attn_kernel(const __g
         auto expand = [&](uint32_t buf) {
             __syncwarp();                                  // the other lanes' copies have landed too
             const int blk = lane >> 2, c0 = 2 * (lane & 3), odd = blk & 1;
-#pragma unroll
+#pragma unroll 1
             for (int k = 0; k < kGroups; ++k) {
-                const int g = gw + k * GW;
-                if (g >= kRowGroups) continue;             // warp-uniform
+                const int g = gw + k * kGatherWarps;
                 uint32_t code[4][4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -551,7 +568,7 @@ __global__ void __launch_bounds__(threads_of(GW), 1) paged_attn_kernel(const __g
             const uint2 mask = make_uint2(s.mask_lo, s.mask_hi);
             int src[kGroups];
 #pragma unroll
-            for (int k = 0; k < kGroups; ++k) src[k] = row_of(k) < TR ? s.row[row_of(k)] : -1;
+            for (int k = 0; k < kGroups; ++k) src[k] = s.row[row_of(k)];
             const int bx = flags & kTileRaw ? 16 : box;
             const int y = lane * bx < TR ? s.row[lane * bx] : -1;   // lane i: box i
             __syncwarp();
@@ -574,7 +591,6 @@ __global__ void __launch_bounds__(threads_of(GW), 1) paged_attn_kernel(const __g
             if (gw == 0) {
                 if (lane == 0) {
                     sValid[xb] = mask;                     // published by this warp's arrival
-                    // (kept here tile by tile: one store at the end is 6 % slower)
                     *drain_ph = (xph << 1) | static_cast<uint32_t>((ordinal + 1) & 1);
                 }
                 if (tma_tile) {
@@ -595,8 +611,7 @@ __global__ void __launch_bounds__(threads_of(GW), 1) paged_attn_kernel(const __g
             if (fp8_tile) {
 #pragma unroll
                 for (int k = 0; k < kGroups; ++k) {
-                    const int g = gw + k * GW;
-                    if (g >= kRowGroups) continue;         // warp-uniform
+                    const int g = gw + k * kGatherWarps;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int r = 4 * g + i, sr = __shfl_sync(0xffffffffu, src[k], 8 * i);   // lanes 8i.. hold row i
@@ -621,11 +636,11 @@ __global__ void __launch_bounds__(threads_of(GW), 1) paged_attn_kernel(const __g
                     from[k] = (src[k] < 0 ? a.q : (raw_tile ? a.raw : a.rows) + static_cast<long long>(src[k]) * kHeadDim) + chunk * 8;
                     to[k] = buf + (r >> 3) * kXGroup + (r & 7) * 128 + ((chunk ^ (r & 7)) << 4);
                 }
-#pragma unroll
+#pragma unroll 2
                 for (int b = 0; b < 8; ++b) {
 #pragma unroll
                     for (int k = 0; k < kGroups; ++k)
-                        if (gw + k * GW < kRowGroups) cp_async16(to[k] + b * kXBlk, from[k] + b * 64, src[k] >= 0 ? 16u : 0u);
+                        cp_async16(to[k] + b * kXBlk, from[k] + b * 64, src[k] >= 0 ? 16u : 0u);
                 }
                 cp_async_commit();
                 settle(true);
@@ -671,7 +686,7 @@ __global__ void __launch_bounds__(threads_of(GW), 1) paged_attn_kernel(const __g
                 xph ^= 1u << xb;
                 tc_fence_after();
                 const uint64_t dx = dx0 + static_cast<uint64_t>(xb * (kXBuf >> 4));
-#pragma unroll
+#pragma unroll 1                                                    // 32 in a row: see the note on code size above
                 for (int blk = 0; blk < 8; ++blk) {
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
@@ -715,7 +730,7 @@ __global__ void __launch_bounds__(threads_of(GW), 1) paged_attn_kernel(const __g
                 }
                 tc_fence_after();
                 const bool raw = t >= m.ct;
-#pragma unroll
+#pragma unroll 1
                 for (int cd = 0; cd < 4; ++cd) {
 #pragma unroll
                     for (int ks = 0; ks < TR / 16; ++ks)
@@ -763,6 +778,7 @@ __global__ void __launch_bounds__(threads_of(GW), 1) paged_attn_kernel(const __g
         const float sl2 = a.scale * 1.4426950408889634f;
         uint32_t qph = 0, gph = 0, aph = 0;
         uint32_t d = 0;                                 // the CTA's tiles so far
+        uint32_t items = 0;                             // and its pieces with tiles
         bool ok = true;
         // The values GEMM of tile x (its row buffer's latest use).
         auto wait_values = [&](uint32_t x) -> bool {
@@ -771,6 +787,7 @@ __global__ void __launch_bounds__(threads_of(GW), 1) paged_attn_kernel(const __g
         auto convert_q = [&]() {
             // q -> fp16 in place for the fp16 raw tier (no logit GEMM reads q now).
             uint4 *qv = reinterpret_cast<uint4 *>(sQ);
+#pragma unroll 2
             for (int k = e; k < 8 * kQBlk / 16; k += kGroupWarps * 32) {
                 uint4 v = qv[k];
                 uint32_t *w = reinterpret_cast<uint32_t *>(&v);
@@ -915,6 +932,9 @@ __global__ void __launch_bounds__(threads_of(GW), 1) paged_attn_kernel(const __g
                 }
                 // Any head raised in any warp: every warp rescales its O^T lanes.
                 const bool wresc = __any_sync(0xffffffffu, (al0 != 1.f) | (al1 != 1.f));
+                // FP8: the epilogue of the item before has read W in every warp
+                if (FP8 && t == m.t0 && items > 0 &&
+                    !(ok = __all_sync(0xffffffffu, mbar_wait_hint(o_free, (items - 1) & 1, abort_flag)))) break;
                 if (t4 == 0) {
                     *head_info(b, h0, 6) = N0;
                     *head_info(b, h1, 6) = N1;
@@ -1035,13 +1055,12 @@ __global__ void __launch_bounds__(threads_of(GW), 1) paged_attn_kernel(const __g
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const int h = lane + 32 * k;
-                const float M = *head_info((d - 1) & 1, h, 6);
+                const float2 lm0 = reinterpret_cast<const float2 *>(head_info(0, h, 7))[i & 1];
+                const float2 lm1 = reinterpret_cast<const float2 *>(head_info(1, h, 7))[i & 1];
+                const float M = fmaxf(lm0.y, lm1.y);     // it only grows: the last tile's
                 float L = 0.f;
-#pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    const float2 lm = reinterpret_cast<const float2 *>(head_info(g, h, 7))[i & 1];
-                    L += lm.y == NEG_INF ? 0.f : lm.y == M ? lm.x : lm.x * ex2(lm.y - M);
-                }
+                if (lm0.y != NEG_INF) L += lm0.x * ex2(lm0.y - M);
+                if (lm1.y != NEG_INF) L += lm1.x * ex2(lm1.y - M);
                 inv[k] = m.split ? 1.f : L > 0.f ? 1.f / L : 0.f;
                 if constexpr (FP8) {
                     const float W = head_info(1, h, 6)[1 + ((d - 1) & 1)];
@@ -1061,17 +1080,17 @@ __global__ void __launch_bounds__(threads_of(GW), 1) paged_attn_kernel(const __g
             tc_fence_after();
             // group g: dims 256 g .. 256 g + 255
 #pragma unroll 1
-            for (int cc = 4 * b; cc < 4 * b + 4; ++cc) {
-                uint32_t v[32];
-                tmem_ld32(tmem + lane_off + kTmemO + cc * 32, v);
-                tmem_wait_ld(v);
-                const int dim = (cc >> 1) * 128 + q4 * 32 + lane, hb = (cc & 1) * 32;
+            for (int cc = 8 * b; cc < 8 * b + 8; ++cc) {
+                uint32_t v[16];
+                tmem_ld16(tmem + lane_off + kTmemO + cc * 16, v);
+                const int dim = (cc >> 2) * 128 + q4 * 32 + lane, hb = (cc & 3) * 16;   // heads hb .. hb + 15
+                const float iv = (cc & 2) ? inv[1] : inv[0];
                 if (m.split) {
                     float *o = static_cast<float *>(a.ws) + (slot * kNHead + hb) * kHeadDim + dim;
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) {
+                    for (int k = 0; k < 16; ++k) {
                         float y = __uint_as_float(v[k]);
-                        if constexpr (FP8) y *= __shfl_sync(0xffffffffu, (cc & 1) ? inv[1] : inv[0], k);
+                        if constexpr (FP8) y *= __shfl_sync(0xffffffffu, iv, (hb & 16) + k);
                         o[k * kHeadDim] = y;
                     }
                 } else {
@@ -1079,8 +1098,8 @@ __global__ void __launch_bounds__(threads_of(GW), 1) paged_attn_kernel(const __g
                     // the first and an odd lane the second, with its neighbour's dim
                     uint16_t *o = a.out + (unit * kNHead + hb + (lane & 1)) * kHeadDim + (dim & ~1);
 #pragma unroll
-                    for (int k = 0; k < 32; k += 2) {
-                        const float il = __shfl_sync(0xffffffffu, (cc & 1) ? inv[1] : inv[0], k + (lane & 1));
+                    for (int k = 0; k < 16; k += 2) {
+                        const float il = __shfl_sync(0xffffffffu, iv, (hb & 16) + k + (lane & 1));
                         const float mine = __uint_as_float((lane & 1) ? v[k + 1] : v[k]);
                         const float other = __shfl_xor_sync(0xffffffffu, __uint_as_float((lane & 1) ? v[k] : v[k + 1]), 1);
                         *reinterpret_cast<uint32_t *>(o + k * kHeadDim) =
@@ -1091,6 +1110,7 @@ __global__ void __launch_bounds__(threads_of(GW), 1) paged_attn_kernel(const __g
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(o_free);
+            ++items;
         }
         if (!ok) {
             *abort_flag = 1;
@@ -1260,13 +1280,11 @@ size_t paged_attn_ws_bytes(int U, int hsplit, int list_cap) {
 }
 
 cudaError_t launch_paged_attn(const PagedAttnArgs &a, int num_sms, cudaStream_t s) {
-    const int gw = a.rows8 ? kGatherWarpsFp8 : kGatherWarpsBf16;
-    void (*kern)(PagedAttnArgs) =
-        a.rows8 ? paged_attn_kernel<kGatherWarpsFp8, true> : paged_attn_kernel<kGatherWarpsBf16, false>;
+    void (*kern)(PagedAttnArgs) = a.rows8 ? paged_attn_kernel<true> : paged_attn_kernel<false>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     if (e != cudaSuccess) return e;
     const int shares = static_cast<int>(shares_of(a.U, a.hsplit, a.list_cap, num_sms < kMaxCtas ? num_sms : kMaxCtas));
-    e = launch_k(kern, dim3(static_cast<unsigned>(shares * a.hsplit)), dim3(threads_of(gw)), kSmemBytes, s, a);
+    e = launch_k(kern, dim3(static_cast<unsigned>(shares * a.hsplit)), dim3(kThreads), kSmemBytes, s, a);
     if (e != cudaSuccess || shares <= 1) return e;
     return launch_k(paged_merge_kernel, dim3(static_cast<unsigned>((shares - 1) * a.hsplit * kMergeBlocks)),
                     dim3(32 * kMergeWarps), 0, s, a, shares);
