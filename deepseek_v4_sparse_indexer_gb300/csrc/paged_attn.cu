@@ -181,6 +181,9 @@ DS4A_DEV void tmem_ld_s(uint32_t taddr, uint32_t (&r)[24]) {
         : "memory");
 }
 
+// Natural log of the sum L 2^M; -inf without rows, NaN when a logit was.
+DS4A_DEV float lse_of(float M, float L) { return L == 0.f || L > 0.f ? merged_lse(M, L) : L; }
+
 // 16 columns of this warp's 32 TMEM lanes.
 DS4A_DEV void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
@@ -1059,20 +1062,21 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                 const float2 lm1 = reinterpret_cast<const float2 *>(head_info(1, h, 7))[i & 1];
                 const float M = fmaxf(lm0.y, lm1.y);     // it only grows: the last tile's
                 float L = 0.f;
-                if (lm0.y != NEG_INF) L += lm0.x * ex2(lm0.y - M);
-                if (lm1.y != NEG_INF) L += lm1.x * ex2(lm1.y - M);
-                inv[k] = m.split ? 1.f : L > 0.f ? 1.f / L : 0.f;
+                // (a group without a finite logit: its sum is 0, or NaN)
+                L += lm0.y == NEG_INF ? lm0.x : lm0.x * ex2(lm0.y - M);
+                L += lm1.y == NEG_INF ? lm1.x : lm1.x * ex2(lm1.y - M);
+                inv[k] = m.split ? 1.f : L == 0.f ? 0.f : 1.f / L;   // a NaN stays one
                 if constexpr (FP8) {
                     const float W = head_info(1, h, 6)[1 + ((d - 1) & 1)];
-                    inv[k] *= L > 0.f ? ex2(W - M) : 0.f;
+                    inv[k] *= L == 0.f ? 0.f : ex2(W - M);
                 }
                 if (warp == 0) {
                     if (m.split) {
                         float *ml = static_cast<float *>(a.ws) + n_slots * kNHead * kHeadDim + (slot * kNHead + h) * 2;
-                        ml[0] = L > 0.f ? M : NEG_INF;
+                        ml[0] = L == 0.f ? NEG_INF : M;
                         ml[1] = L;
                     } else if (a.lse) {
-                        a.lse[unit * kNHead + h] = merged_lse(M, L);
+                        a.lse[unit * kNHead + h] = lse_of(M, L);
                     }
                 }
             }
@@ -1189,7 +1193,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const __g
         float m = NEG_INF, l = 0.f;
         if (lane < mine) {
             const float2 p = *reinterpret_cast<const float2 *>(ml + (slot(w0 + lane * step) * kNHead + h) * 2);
-            if (p.y > 0.f) m = p.x, l = p.y;
+            if (p.y != 0.f) m = p.x, l = p.y;               // also a NaN: it goes on into the sums
         }
         M = m;
 #pragma unroll
@@ -1223,12 +1227,12 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const __g
     if (np <= kMergeFew) {
         for (int h = h_lo + blk * kMergeWarps + warp; h < h_hi; h += kMergeBlocks * kMergeWarps) {
             join(h, 0, 1);
-            const float inv = L > 0.f ? 1.f / L : 0.f;
+            const float inv = L == 0.f ? 0.f : 1.f / L;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 *reinterpret_cast<uint2 *>(a.out + (row0 + h) * kHeadDim + 128 * j + 4 * lane) =
                     make_uint2(pack2<false>(acc[j].x * inv, acc[j].y * inv), pack2<false>(acc[j].z * inv, acc[j].w * inv));
-            if (a.lse && lane == 0) a.lse[row0 + h] = merged_lse(M, L);
+            if (a.lse && lane == 0) a.lse[row0 + h] = lse_of(M, L);
         }
         return;
     }
@@ -1251,9 +1255,9 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const __g
             x = fmaf(e, s_acc[w][2 * threadIdx.x], x);
             y = fmaf(e, s_acc[w][2 * threadIdx.x + 1], y);
         }
-        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
         *reinterpret_cast<uint32_t *>(a.out + (row0 + h) * kHeadDim + 2 * threadIdx.x) = pack2<false>(x * inv, y * inv);
-        if (a.lse && threadIdx.x == 0) a.lse[row0 + h] = merged_lse(top, sum);
+        if (a.lse && threadIdx.x == 0) a.lse[row0 + h] = lse_of(top, sum);
         __syncthreads();
     }
 }

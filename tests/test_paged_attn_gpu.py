@@ -201,6 +201,28 @@ def test_listed_rows_that_do_not_exist(cuda_lib):
     b.check(listed=listed)
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("lengths", [[700, 700, 700], [16384], [5, 60] * 100])
+def test_nan_in_a_row_or_a_head_stays(cuda_lib, lengths, fp8):
+    """A NaN in a row that counts makes its unit NaN, in one piece or in many, and a NaN in a head's query that head."""
+    b = Batch(lengths, 64, fp8=fp8, seed=4)
+    row = int(pool_rows(b.table, 0, torch.tensor([lengths[0] // 2], device=DEV), 64)[0])
+    keep = b.rows.view(-1, 512)[row].clone()
+    b.rows.view(-1, 512)[row, 7] = 0x7F if fp8 else float("nan")
+    b(cuda_lib)
+    assert torch.isnan(b.out[1].float()).all() and torch.isnan(b.lse[1]).all()
+    b.check(units=range(1, min(b.U, 20)))
+    b.rows.view(-1, 512)[row] = keep
+    b.q[0, 9, 100] = float("nan")
+    b(cuda_lib)
+    nan = torch.zeros(64, dtype=torch.bool, device=DEV)
+    nan[9] = True
+    assert torch.equal(torch.isnan(b.out[1].float()).all(-1), nan) and torch.equal(torch.isnan(b.out[1].float()).any(-1), nan)
+    assert torch.equal(torch.isnan(b.lse[1]), nan)
+    b.check(units=range(1, min(b.U, 20)))
+    assert cuda_lib.ds4a_get_device_status() == (0, 0)
+
+
 def test_lengths_out_of_range(cuda_lib):
     """Clamped and flagged: no length reads outside its table, list or ring."""
     b = Batch([128, 128, 128, 128], 64, top_k=32)
