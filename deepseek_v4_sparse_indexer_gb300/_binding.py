@@ -519,6 +519,7 @@ def ds4a_sparse_attn_prefill_fp8(q, q_pos, rows8, row_scale, idx, count, raw, ra
 # Paged caches
 # ----------------------------------------------------------------------------
 
+_I32, _F32, _F64, _BF16, _U8 = torch.int32, torch.float32, torch.float64, torch.bfloat16, torch.uint8
 _TYPES = {torch.bfloat16: DS4A_BF16, torch.float16: DS4A_F16, torch.float32: DS4A_F32, torch.uint8: DS4A_E4M3}
 
 
@@ -529,12 +530,12 @@ _TYPES = {torch.bfloat16: DS4A_BF16, torch.float16: DS4A_F16, torch.float32: DS4
 def _req_ints(dev, *tensors):
     """Each (name, tensor, n) is contiguous int32 on device index `dev` with n elements."""
     for name, t, n in tensors:
-        if t.dtype is not torch.int32 or t.get_device() != dev or t.numel() != n or not t.is_contiguous():
+        if t.dtype is not _I32 or t.get_device() != dev or t.numel() != n or not t.is_contiguous():
             raise ValueError(f"{name}: must be contiguous int32 on cuda:{dev} with {n} elements")
 
 
 def _table_stride(table, U, dev):
-    if table.dtype is not torch.int32 or table.get_device() != dev or table.dim() != 2:
+    if table.dtype is not _I32 or table.get_device() != dev or table.dim() != 2:
         raise ValueError(f"table: int32 [{U}, max_pages] on cuda:{dev}")
     n, cols = table.shape
     rows, one = table.stride()
@@ -559,7 +560,7 @@ def _launch(dev, stream, name, *args):
     f = getattr(_lib or load(), name)
     # torch.cuda.current_stream() builds a Stream object: 2.8 us of a 4 us call
     raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-    if dev == torch.cuda.current_device():
+    if dev == torch._C._cuda_getDevice():
         st = f(*args, raw)
     else:
         with torch.cuda.device(dev):
@@ -605,10 +606,10 @@ def ds4a_qk_norm_rope(q, k, pos, inv_freq, eps, q_weight, k_weight, q_out, k_out
     T, D = pos.numel(), x.shape[-1]
     H = q_type = k_type = k_out_type = q_stride = k_stride = k_rows = 0
     _req_ints(dev, ("pos", pos, T))
-    if inv_freq.dtype is not torch.float64 or inv_freq.get_device() != dev or not inv_freq.is_contiguous():
+    if inv_freq.dtype is not _F64 or inv_freq.get_device() != dev or not inv_freq.is_contiguous():
         raise ValueError("inv_freq: contiguous float64 [n_rot / 2]")
     for w in (q_weight, k_weight):
-        if w is not None and (w.dtype is not torch.float32 or w.get_device() != dev or w.numel() != D
+        if w is not None and (w.dtype is not _F32 or w.get_device() != dev or w.numel() != D
                               or not w.is_contiguous()):
             raise ValueError(f"q_weight, k_weight: contiguous float32 [{D}]")
     if q is not None:
@@ -621,7 +622,7 @@ def ds4a_qk_norm_rope(q, k, pos, inv_freq, eps, q_weight, k_weight, q_out, k_out
             raise ValueError("q: [T, H, D] with contiguous heads")
         if T <= 1:
             q_stride = H * D
-        if q_out is None or q_out.dtype is not torch.bfloat16 or q_out.get_device() != dev \
+        if q_out is None or q_out.dtype is not _BF16 or q_out.get_device() != dev \
                 or q_out.numel() != T * H * D or not q_out.is_contiguous():
             raise ValueError("q_out: contiguous bf16 [T, H, D]")
     if k is not None:
@@ -638,7 +639,7 @@ def ds4a_qk_norm_rope(q, k, pos, inv_freq, eps, q_weight, k_weight, q_out, k_out
                 or k_out.shape[1] != D or not k_out.is_contiguous():
             raise ValueError("k_out: contiguous bf16, fp16 or uint8 [rows, D]")
         k_rows = k_out.shape[0]
-        if k_out_type == DS4A_E4M3 and (k_scale is None or k_scale.dtype is not torch.float32
+        if k_out_type == DS4A_E4M3 and (k_scale is None or k_scale.dtype is not _F32
                                         or k_scale.get_device() != dev or k_scale.numel() != k_rows
                                         or not k_scale.is_contiguous()):
             raise ValueError("k_scale: contiguous float32 [rows]")
@@ -658,13 +659,13 @@ def ds4a_paged_indexer_score(iq, w, ik, table, n_rows, scores, stream=None):
     if scores.dim() != 3:
         raise ValueError("scores: [U, 1, N_cap]")
     U, one, N_cap = scores.shape
-    if one != 1 or scores.dtype is not torch.float32 or scores.get_device() != dev or not scores.is_contiguous():
+    if one != 1 or scores.dtype is not _F32 or scores.get_device() != dev or not scores.is_contiguous():
         raise ValueError("scores: contiguous float32 [U, 1, N_cap]")
-    if iq.dtype is not torch.bfloat16 or iq.numel() != U * N_IDX_HEAD * IDX_DIM or not iq.is_contiguous():
+    if iq.dtype is not _BF16 or iq.numel() != U * N_IDX_HEAD * IDX_DIM or not iq.is_contiguous():
         raise ValueError("iq: contiguous bf16 [U, 1, 64, 128]")
-    if w.dtype is not torch.float32 or w.get_device() != dev or w.numel() != U * N_IDX_HEAD or not w.is_contiguous():
+    if w.dtype is not _F32 or w.get_device() != dev or w.numel() != U * N_IDX_HEAD or not w.is_contiguous():
         raise ValueError("w: contiguous float32 [U, 1, 64]")
-    if ik.dtype is not torch.bfloat16 or ik.get_device() != dev or ik.dim() != 3 or not ik.is_contiguous():
+    if ik.dtype is not _BF16 or ik.get_device() != dev or ik.dim() != 3 or not ik.is_contiguous():
         raise ValueError("ik: contiguous bf16 [n_pages, page_size, 128]")
     n_pages, page_size, width = ik.shape
     if width != IDX_DIM:
@@ -685,22 +686,22 @@ def ds4a_paged_attn_decode(q, rows, table, n_rows, raw, n_raw, scale, out, lse=N
     out bf16 [U,H,512]; lse f32 [U,H] or None; ws uint8 workspace of
     ds4a_workspace_bytes(DS4A_OP_PAGED_ATTN_DECODE, U, 1, max_pages * P, top_k)."""
     dev = _device_index(q, "q")
-    if q.dtype is not torch.bfloat16 or q.dim() != 3 or not q.is_contiguous():
+    if q.dtype is not _BF16 or q.dim() != 3 or not q.is_contiguous():
         raise ValueError("q: contiguous bf16 [U, H, 512]")
     U, H, width = q.shape
     if width != HEAD_DIM:
         raise ValueError("q: contiguous bf16 [U, H, 512]")
-    if out.dtype is not torch.bfloat16 or out.get_device() != dev or out.numel() != U * H * HEAD_DIM \
+    if out.dtype is not _BF16 or out.get_device() != dev or out.numel() != U * H * HEAD_DIM \
             or not out.is_contiguous():
         raise ValueError("out: contiguous bf16 [U, H, 512]")
-    fp8 = rows.dtype is torch.uint8
-    if not (fp8 or rows.dtype is torch.bfloat16) or rows.get_device() != dev or rows.dim() != 3 \
+    fp8 = rows.dtype is _U8
+    if not (fp8 or rows.dtype is _BF16) or rows.get_device() != dev or rows.dim() != 3 \
             or not rows.is_contiguous():
         raise ValueError("rows: contiguous bf16 or uint8 [n_pages, page_size, 512]")
     n_pages, page_size, width = rows.shape
     if width != HEAD_DIM:
         raise ValueError("rows: contiguous bf16 or uint8 [n_pages, page_size, 512]")
-    if fp8 and (row_scale is None or row_scale.dtype is not torch.float32 or row_scale.get_device() != dev
+    if fp8 and (row_scale is None or row_scale.dtype is not _F32 or row_scale.get_device() != dev
                 or row_scale.numel() != n_pages * page_size or not row_scale.is_contiguous()):
         raise ValueError("row_scale: contiguous float32 [n_pages, page_size]")
     if raw.dtype is not torch.float16 or raw.get_device() != dev or raw.dim() != 3 or raw.shape[1:] != (N_SWA, HEAD_DIM) \
@@ -719,7 +720,7 @@ def ds4a_paged_attn_decode(q, rows, table, n_rows, raw, n_raw, scale, out, lse=N
     if idx is not None:
         top_k = idx.shape[-1]
         _req_ints(dev, ("idx", idx, U * top_k), ("count", count, U))
-    if lse is not None and (lse.dtype is not torch.float32 or lse.get_device() != dev or lse.numel() != U * H
+    if lse is not None and (lse.dtype is not _F32 or lse.get_device() != dev or lse.numel() != U * H
                             or not lse.is_contiguous()):
         raise ValueError("lse: contiguous float32 [U, H]")
     ws_ptr, ws_bytes = None, 0
