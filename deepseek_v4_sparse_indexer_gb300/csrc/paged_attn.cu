@@ -411,8 +411,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
     //   chunk 6  word 0: head h's running max after the tile; FP8: buffer 0, word 1 +
     //            row buffer: the scale of tile row h; buffer 1, words 1 and 2: see the
     //            softmax;
-    //   chunk 7  at the end of item i, at i % 2: the group's sum for head h and the
-    //            max that the sum is relative to.
+    //   chunk 7  at the end of item i (of those with tiles), at i % 2: the group's sum
+    //            for head h and the max that the sum is relative to.
     auto head_info = [&](int buf, int h, int ch) -> float * {
         return reinterpret_cast<float *>(sP + buf * kPBuf + h * 128 + ((ch ^ (h & 7)) << 4));
     };
@@ -1046,8 +1046,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
             l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
             l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
             if (t4 == 0) {
-                reinterpret_cast<float2 *>(head_info(b, h0, 7))[i & 1] = make_float2(l0, M0);
-                reinterpret_cast<float2 *>(head_info(b, h1, 7))[i & 1] = make_float2(l1, M1);
+                reinterpret_cast<float2 *>(head_info(b, h0, 7))[items & 1] = make_float2(l0, M0);
+                reinterpret_cast<float2 *>(head_info(b, h1, 7))[items & 1] = make_float2(l1, M1);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(all);
@@ -1058,8 +1058,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const int h = lane + 32 * k;
-                const float2 lm0 = reinterpret_cast<const float2 *>(head_info(0, h, 7))[i & 1];
-                const float2 lm1 = reinterpret_cast<const float2 *>(head_info(1, h, 7))[i & 1];
+                const float2 lm0 = reinterpret_cast<const float2 *>(head_info(0, h, 7))[items & 1];
+                const float2 lm1 = reinterpret_cast<const float2 *>(head_info(1, h, 7))[items & 1];
                 const float M = fmaxf(lm0.y, lm1.y);     // it only grows: the last tile's
                 float L = 0.f;
                 // (a group without a finite logit: its sum is 0, or NaN)
