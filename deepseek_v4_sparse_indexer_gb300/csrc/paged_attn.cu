@@ -935,7 +935,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                 }
                 // Any head raised in any warp: every warp rescales its O^T lanes.
                 const bool wresc = __any_sync(0xffffffffu, (al0 != 1.f) | (al1 != 1.f));
-                // FP8: the epilogue of the item before has read W in every warp
+                // FP8: the epilogue of the item before has read W in every warp (the other
+                // group's first tile waits for this one's token)
                 if (FP8 && t == m.t0 && items > 0 &&
                     !(ok = __all_sync(0xffffffffu, mbar_wait_hint(o_free, (items - 1) & 1, abort_flag)))) break;
                 if (t4 == 0) {
@@ -945,17 +946,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                         head_info(1, h0, 6)[1 + b] = W0;
                         head_info(1, h1, 6)[1 + b] = W1;
                     }
-                    sAlpha[b * kNHead + h0] = al0;
-                    sAlpha[b * kNHead + h1] = al1;
                 }
-                if (lane == 0) sFlag[b * kGroupWarps + q4] = wresc ? 1u : 0u;
-                // Arrive now, wait after the exponentials: the exchange of the
-                // rescale flags overlaps this warp's own work.
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&tok[warp]);
-                    mbar_arrive(&grp[b]);
-                }
+                if (lane == 0) mbar_arrive(&tok[warp]);
                 // This thread's sums, relative to the max of the group's last tile.
                 if (N0 != M0) l0 *= M0 == NEG_INF ? 0.f : ex2(M0 - N0);
                 if (N1 != M1) l1 *= M1 == NEG_INF ? 0.f : ex2(M1 - N1);
@@ -1004,6 +997,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                 }
                 // This P buffer was read by the values GEMM two tiles back.
                 if (d >= 2 && !(ok = wait_values(d - 2))) break;
+                // (So every warp of the group is past that tile's flags and factors too.)
+                // Arrive now, wait after P is written.
+                if (t4 == 0) {
+                    sAlpha[b * kNHead + h0] = al0;
+                    sAlpha[b * kNHead + h1] = al1;
+                }
+                if (lane == 0) sFlag[b * kGroupWarps + q4] = wresc ? 1u : 0u;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&grp[b]);
                 // P[h][row]: rows 8j + 2(t%4) + {0,1} are bytes 16j + 4(t%4) of the
                 // 128-byte row of head h, 16-byte chunk j swizzled with h & 7.
                 uint8_t *pbuf = sP + b * kPBuf;
