@@ -25,9 +25,9 @@
 // rows 228 us = 4.7 TB/s, random 1 KB rows arriving by cp.async at 31 GB/s per SM
 // of the 34-40 that such a gather alone reaches; 128 heads: 128 units x 1,024
 // listed rows 87 us, each half at its own copy of the rows from L2.  FP8 rows, 48
-// units of up to 4,096: 55 us, 2.1 us a tile, the cycle being longer by the pass that
-// writes the codes out as fp16 (its conversions are not the limit: shifts and a
-// multiplication in their place took longer).  A few units are latency: 1 x 1,024 rows
+// units of up to 4,096: 58 us, 2.2 us a tile, the cycle being longer by the pass that
+// writes the codes out as bf16 (as fp16, one conversion a pair instead of four, 57
+// us: the latency of the pass counts, not its conversions).  A few units are latency: 1 x 1,024 rows
 // 13.4 us with its merge.
 //
 // Roles (one CTA per SM, persistent over its share of the batch's tiles):
@@ -40,7 +40,7 @@
 //            groups dealt to the warps.  Dense lists and the raw window: TMA, one box
 //            per 16 rows of a page (8 with pages of 8 rows), boxes past the list's end
 //            or outside the pool read past the end of the tensor map, which fills
-//            zeros.  FP8 rows: codes by cp.async, then written out as fp16.
+//            zeros.  FP8 rows: codes by cp.async, then written out as bf16.
 //   logits   warp 8: S[64 heads x 48 rows] = q . X^T into one of two TMEM buffers;
 //   softmax  warps 0-3 and 4-7, tiles in turn: S out of TMEM, running max (raised
 //            only past 2^8), P;
@@ -132,12 +132,6 @@ DS4A_DEV void ld_shared_v4(uint32_t addr, uint32_t (&v)[4]) {
                  : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
                  : "r"(addr)
                  : "memory");
-}
-// Eight E4M3 codes (two words) as eight fp16 (four words, dims in order): exact.
-DS4A_DEV void e4m3x8_to_f16(uint32_t w0, uint32_t w1, uint32_t (&o)[4]) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(o[j]) : "h"(static_cast<uint16_t>((j < 2 ? w0 : w1) >> (16 * (j & 1)))));
 }
 // One box of whole 8-row groups (map: (64 dims, 8 rows, 8 blocks, groups)).
 DS4A_DEV void tma_load_groups(void *dst, const void *map, uint64_t *bar, int group) {
@@ -512,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
         bool pend_fp8 = false;                             // they are FP8 codes
         // FP8 rows: a row's 512 codes land in the upper half of the row's own 1 KB
         // (column blocks 4-7, unswizzled), and the warp that copied them writes the
-        // row over them as fp16.  Lane l: codes 16l .. 16l+15, which become 16-byte
+        // row over them as bf16.  Lane l: codes 16l .. 16l+15, which become 16-byte
         // chunks 2(l%4) and 2(l%4)+1 of column block l/4.  Lanes of odd blocks write
         // their second chunk first, so the eight lanes of a store phase hit eight
         // different 16-byte bank groups.
@@ -533,8 +527,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                 for (int i = 0; i < 4; ++i) {
                     const int r = 4 * g + i;
                     uint32_t lo[4], hi[4];
-                    e4m3x8_to_f16(code[i][0], code[i][1], lo);
-                    e4m3x8_to_f16(code[i][2], code[i][3], hi);
+                    e4m3x8_to_bf16(code[i][0], code[i][1], 1.f, lo);
+                    e4m3x8_to_bf16(code[i][2], code[i][3], 1.f, hi);
                     const uint32_t rowa = buf + (r >> 3) * kXGroup + (r & 7) * 128 + blk * kXBlk;
                     const uint32_t a0 = rowa + ((c0 ^ (r & 7)) << 4), a1 = rowa + (((c0 + 1) ^ (r & 7)) << 4);
                     if (odd) {
@@ -678,7 +672,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
             bool q16 = false;
             for (int t = m.t0; t < m.t1; ++t) {
                 const bool raw = t >= m.ct;
-                if ((FP8 || raw) && !q16) {
+                if (raw && !q16) {
                     if (!(ok = warp_wait(q16_ready, q16ph, abort_flag))) break;
                     q16ph ^= 1;
                     q16 = true;
@@ -694,7 +688,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
                         umma_elect(tmem + kTmemS + b * 64, dq + static_cast<uint64_t>(blk * (kQBlk >> 4) + 2 * kk),
-                                   dx + static_cast<uint64_t>(blk * (kXBlk >> 4) + 2 * kk), FP8 || raw ? id_f16 : id_bf,
+                                   dx + static_cast<uint64_t>(blk * (kXBlk >> 4) + 2 * kk), raw ? id_f16 : id_bf,
                                    (blk | kk) ? 1u : 0u);
                 }
                 commit_elect(&s_full[b]);
@@ -739,7 +733,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                     for (int ks = 0; ks < TR / 16; ++ks)
                         umma_elect(tmem + kTmemO + cd * kNHead,
                                    dxv + static_cast<uint64_t>((xb * kXBuf + 2 * cd * kXBlk + ks * 2 * kXGroup) >> 4),
-                                   dp + static_cast<uint64_t>((b * kPBuf + ks * 32) >> 4), FP8 || raw ? id_f16 : id_bf,
+                                   dp + static_cast<uint64_t>((b * kPBuf + ks * 32) >> 4), raw ? id_f16 : id_bf,
                                    (t == m.t0 && ks == 0) ? 0u : 1u);
                 }
                 commit_elect(&x_empty[xb]);              // row tile and P buffer free
@@ -766,11 +760,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
         // takes it from the warp of the other group that had the tile before, and
         // hands it on before its exponentials.  (One group for all tiles was the
         // pipeline's slowest stage: 1.3 us of the 1.5 us per tile.)
-        // FP8: a row's elements are code * s_r; the tile holds the codes as fp16 and
-        // q is in fp16 for all tiles.  The logits take s_r from shared memory, and P
-        // the weight that multiplies the codes, 2^(l + log2 s_r - W), with a running
-        // max W of its own (of l + log2 s_r, kept like M: the one that O^T is relative
-        // to), so that every weight lies in fp16's range relative to the largest.  The sums stay relative to M; out = O^T 2^(W - M) / l.
+        // FP8: a row's elements are code * s_r; the tile holds the codes as bf16 (exact).
+        // The logits take s_r from shared memory, and P the weight that multiplies
+        // the codes, 2^(l + log2 s_r - W), with a running max W of its own (of l +
+        // log2 s_r, kept like M: the one that O^T is relative to), so that scales of
+        // any size neither overflow nor vanish.  The sums stay relative to M; out =
+        // O^T 2^(W - M) / l.  P is bf16: a long list's weights may each lie 2^-25 and
+        // more below the largest and still carry much of the sum together, and bf16
+        // keeps every weight to half a step of itself where fp16 (once used here) lost
+        // those below 2^-25 and rounded those below 2^-14 to ever fewer bits.
         constexpr int J = TR / 8;
         const int b = warp >> 2;                        // group; its S and P buffer
         const int q4 = warp & 3;
@@ -817,8 +815,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
             ok = __all_sync(0xffffffffu, mbar_wait_hint(q_full, qph, abort_flag));
             if (!ok) break;
             qph ^= 1;
-            // fp16 from the first tile on
-            if ((FP8 || m.t0 >= m.ct) && (d & 1) == static_cast<uint32_t>(b)) convert_q();
+            // the item starts with a raw tile
+            if (m.t0 >= m.ct && (d & 1) == static_cast<uint32_t>(b)) convert_q();
             // The next item's q may overwrite this one only after every softmax
             // warp has seen this one land: q_full must never run two phases
             // ahead of a warp's wait (its parity could not tell them apart).
@@ -832,7 +830,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                 if (!ok) break;
                 // The next tile is the first raw one: its logits need q in fp16,
                 // and every compressed logit GEMM has completed (this one too).
-                if (!FP8 && t + 1 < m.t1 && t + 1 == m.ct) convert_q();
+                if (t + 1 < m.t1 && t + 1 == m.ct) convert_q();
                 tc_fence_after();
                 uint32_t r[4 * J];
                 tmem_ld_s(tmem + lane_off + kTmemS + b * 64, r);
@@ -980,9 +978,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                 }
                 l0 += s0;
                 l1 += s1;
-                // p in the rows' 16-bit type: the operand of the values GEMM
+                // p in the rows' 16-bit type: the operand of the values GEMM (its two
+                // operands have one type).  bf16 is off by up to 2^-8 of each weight; fp16,
+                // for the window's rows, by 2^-11, and loses weights below 2^-25 of the
+                // largest (all 128 together: 2^-18 of it).
                 uint32_t pk0[J], pk1[J];
-                if (FP8 || raw) {
+                if (raw) {
 #pragma unroll
                     for (int j = 0; j < J; ++j) {
                         pk0[j] = pack2<true>(x[4 * j], x[4 * j + 1]);

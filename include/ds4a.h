@@ -630,8 +630,10 @@ ds4a_status ds4a_paged_indexer_score(const uint16_t *iq, const float *w, const u
  *    rows     rows_type DS4A_BF16: bf16 [n_pages][page_size][512].  DS4A_E4M3:
  *             uint8 codes of that shape, and row_scale fp32
  *             [n_pages][page_size], >= 0 (device), as 4c writes them.  Rows
- *             multiply as code * scale, with q rounded to fp16 (so |q| < 65,520)
- *             and the weights in fp16, as for raw rows.
+ *             multiply as code * scale, in bf16 as bf16 rows do (the codes are
+ *             exact in bf16, the scale goes into the logits and the weights in
+ *             fp32), so that the error does not depend on the list's length or
+ *             on how the scales differ.
  *    table    int32 [U] rows of max_pages entries, table_stride apart (device).
  *    n_rows   int32 [U] (device): rows of unit u, 0 .. max_pages * page_size.
  *    idx, count, top_k   both NULL and 0: the unit attends to all its rows
