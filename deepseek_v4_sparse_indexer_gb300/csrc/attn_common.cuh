@@ -139,9 +139,10 @@ DS4A_DEV void tmem_ld16x256_x8(uint32_t taddr, uint32_t (&r)[32]) {
         : "r"(taddr));
 }
 
-// log sum exp of a head joined from pieces: M in log2 units, L = 0 for no row.
-DS4A_DEV float merged_lse(float M, float L) {
-    return L > 0.f ? (M + log2f(L)) * 0.6931471805599453f : -__int_as_float(0x7f800000);
+// Natural log of the sum L 2^M of a head's exponentials: L = 0 for no row, NaN when
+// a logit was.
+DS4A_DEV float lse_of(float M, float L) {
+    return L == 0.f ? -__int_as_float(0x7f800000) : (M + log2f(L)) * 0.6931471805599453f;
 }
 
 }  // namespace ds4a

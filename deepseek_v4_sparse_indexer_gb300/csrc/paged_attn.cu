@@ -175,9 +175,6 @@ DS4A_DEV void tmem_ld_s(uint32_t taddr, uint32_t (&r)[24]) {
         : "memory");
 }
 
-// Natural log of the sum L 2^M; -inf without rows, NaN when a logit was.
-DS4A_DEV float lse_of(float M, float L) { return L == 0.f || L > 0.f ? merged_lse(M, L) : L; }
-
 // 16 columns of this warp's 32 TMEM lanes.
 DS4A_DEV void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(

@@ -804,16 +804,14 @@ __global__ void __launch_bounds__(attn_threads(GW), 1) sparse_attn_kernel(const 
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     const int h = k ? h1 : h0;
-                    const float L = k ? l1 : l0, M = k ? M1 : M0;
+                    const float L = k ? l1 : l0, M = k ? M1 : M0;   // L: 0 without rows, NaN when a logit was
                     if (!m.split) {
-                        sInvL[h] = L > 0.f ? 1.f / L : 0.f;
-                        if (a.lse)
-                            a.lse[static_cast<long long>(m.unit) * kNHead + h] =
-                                L > 0.f ? (M + log2f(L)) * 0.6931471805599453f : NEG_INF;
+                        sInvL[h] = L == 0.f ? 0.f : 1.f / L;
+                        if (a.lse) a.lse[static_cast<long long>(m.unit) * kNHead + h] = lse_of(M, L);
                     } else {
                         sInvL[h] = 1.f;
                         float *ml = static_cast<float *>(a.ws) + n_slots * kNHead * kHeadDim;
-                        ml[(slot * kNHead + h) * 2] = L > 0.f ? M : NEG_INF;
+                        ml[(slot * kNHead + h) * 2] = L == 0.f ? NEG_INF : M;
                         ml[(slot * kNHead + h) * 2 + 1] = L;
                     }
                 }
@@ -883,8 +881,8 @@ DS4A_DEV float4 merge_pieces(const float *wo, const float *ml, int h, int np, Sl
     float m = NEG_INF;
     for (int i = threadIdx.x; i < np; i += kMergeThreads) {
         const float2 p = *reinterpret_cast<const float2 *>(ml + (slot(i) * kNHead + h) * 2);
-        s_w[i] = p.y > 0.f ? p.x : NEG_INF;
-        s_l[i] = p.y > 0.f ? p.y : 0.f;
+        s_w[i] = p.y == 0.f ? NEG_INF : p.x;
+        s_l[i] = p.y;                                       // also a NaN: it goes on into the sum
         m = fmaxf(m, s_w[i]);
     }
 #pragma unroll
@@ -925,7 +923,7 @@ DS4A_DEV float4 merge_pieces(const float *wo, const float *ml, int h, int np, Sl
             acc.w += wk * o[j].w;
         }
     }
-    const float inv = L > 0.f ? 1.f / L : 0.f;
+    const float inv = L == 0.f ? 0.f : 1.f / L;
     acc.x *= inv;
     acc.y *= inv;
     acc.z *= inv;
@@ -960,7 +958,7 @@ __global__ void __launch_bounds__(kMergeThreads) attn_merge_kernel(const __grid_
     const float4 acc = merge_pieces(wo, ml, h, c1 - c0 + 1, piece_slot, M, L);
     const long long u = u_rem0 + v;
     *reinterpret_cast<float4 *>(a.out + (u * kNHead + h) * kHeadDim + threadIdx.x * 4) = acc;
-    if (a.lse && threadIdx.x == 0) a.lse[u * kNHead + h] = merged_lse(M, L);
+    if (a.lse && threadIdx.x == 0) a.lse[u * kNHead + h] = lse_of(M, L);
 }
 
 // Tiles per unit in the tile space: the top_k compressed rows and the raw window.

@@ -278,7 +278,7 @@ ds4a_status ds4a_topk_select_noalloc(const float *scores, const int32_t *n_rows,
  *    fp32 softmax and accumulation on the tensor cores.  Compressed rows
  *    multiply in bf16; raw rows (kept rounded to f16, §3-1) multiply in fp16
  *    with q rounded to fp16 and the probabilities in fp16.  An empty row set
- *    gives out = 0, lse = -inf.
+ *    gives out = 0, lse = -inf; a NaN logit makes its head's out and lse NaN.
  *
  *    q       bf16 [U][64][512] (device).
  *    rows    bf16 [U][N_cap][512]; unit u at rows + u*rows_unit_stride (device).
