@@ -33,6 +33,7 @@ DS4A_OP_FLAG_128_HEADS = 0x100
 DS4A_BF16, DS4A_F16, DS4A_F32, DS4A_E4M3 = 0, 1, 2, 3
 DS4A_ROPE_NEIGHBOURS, DS4A_ROPE_HALVES = 0, 1
 DS4A_MIN_PAGE, DS4A_MAX_PAGE, DS4A_MAX_PLAN_SEQS = 8, 4096, 8192
+DS4A_PLAN_TOKENS_BY_SEQ, DS4A_PLAN_ROWS_BY_SEQ = 1, 2
 
 N_HEAD, HEAD_DIM, N_IDX_HEAD, IDX_DIM, N_SWA = 64, 512, 64, 128, 128
 
@@ -43,7 +44,8 @@ EXPORTS = ("ds4a_strerror", "ds4a_version", "ds4a_workspace_bytes", "ds4a_get_de
            "ds4a_dense_attn_decode", "ds4a_kv_push_raw", "ds4a_compressor_pool",
            "ds4a_sparse_attn_decode_heads", "ds4a_sparse_attn_prefill_heads", "ds4a_dense_attn_decode_heads",
            "ds4a_rows_to_fp8", "ds4a_sparse_attn_decode_fp8", "ds4a_sparse_attn_prefill_fp8", "ds4a_indexer_topk",
-           "ds4a_paged_plan", "ds4a_qk_norm_rope", "ds4a_paged_indexer_score", "ds4a_paged_attn_decode")
+           "ds4a_paged_plan", "ds4a_paged_plan_form", "ds4a_qk_norm_rope", "ds4a_paged_indexer_score",
+           "ds4a_paged_attn_decode")
 DS4A_TOPK_NOALLOC_SCRATCH_BYTES = 8 << 20
 DS4A_MAX_TOP_K = 2048
 
@@ -123,6 +125,8 @@ def load(build_if_missing: bool = True):
     L.ds4a_paged_plan.argtypes = [_vp, _vp, _i32, _i32, _i32, _vp, _i32, _vp, _vp, _vp, _i64, _i32, _vp, _vp, _vp, _vp,
                                   _vp, _vp, _vp, _i32, _vp, _vp, _i32, _vp]
     L.ds4a_paged_plan.restype = _i32
+    L.ds4a_paged_plan_form.argtypes = [_i32] + L.ds4a_paged_plan.argtypes
+    L.ds4a_paged_plan_form.restype = _i32
     L.ds4a_qk_norm_rope.argtypes = [_vp, _i32, _i64, _vp, _i32, _i64, _vp, _vp, _i32, _i32, _f32, _vp, _vp, _vp, _vp,
                                     _i32, _vp, _vp, _i64, _i32, _i32, _i32, _vp]
     L.ds4a_qk_norm_rope.restype = _i32
@@ -570,12 +574,13 @@ def _launch(dev, stream, name, *args):
 
 
 def ds4a_paged_plan(past, add, ratio, page_size, free_pages, free_head, table, n_rows, n_raw, cu_tok, cu_row, tok_pos,
-                    raw_slot, row_pos, row_slot, free_head_out, ring=None, stream=None):
+                    raw_slot, row_pos, row_slot, free_head_out, ring=None, stream=None, form=0):
     """Block tables and slot maps of one step from the request lengths, all int32:
     past, add [B]; free_pages [n_free], free_head [1]; table [B, max_pages]
     (updated); n_rows, n_raw [B], cu_tok, cu_row [B + 1], tok_pos, raw_slot
     [T_cap], row_pos, row_slot [R_cap] and free_head_out [1] (written; may be
-    free_head); ring [B] or None."""
+    free_head); ring [B] or None.  form: DS4A_PLAN_TOKENS_BY_SEQ and / or
+    DS4A_PLAN_ROWS_BY_SEQ lay the token / row maps out by sequence (add 0 or 1)."""
     dev = _device_index(past, "past")
     B, T, R, n_free = past.numel(), tok_pos.numel(), row_pos.numel(), free_pages.numel()
     _req_ints(dev, ("past", past, B), ("add", add, B), ("free_pages", free_pages, n_free), ("free_head", free_head, 1),
@@ -585,8 +590,9 @@ def ds4a_paged_plan(past, add, ratio, page_size, free_pages, free_head, table, n
     if ring is not None:
         _req_ints(dev, ("ring", ring, B))
     stride, max_pages = _table_stride(table, B, dev)
-    _launch(dev, stream, "ds4a_paged_plan", past.data_ptr(), add.data_ptr(), B, ratio, page_size, free_pages.data_ptr(),
-            n_free, free_head.data_ptr(), free_head_out.data_ptr(), table.data_ptr(), stride, max_pages,
+    name, lead = ("ds4a_paged_plan_form", (form,)) if form else ("ds4a_paged_plan", ())
+    _launch(dev, stream, name, *lead, past.data_ptr(), add.data_ptr(), B, ratio, page_size, free_pages.data_ptr(), n_free,
+            free_head.data_ptr(), free_head_out.data_ptr(), table.data_ptr(), stride, max_pages,
             _opt(ring), n_rows.data_ptr(), n_raw.data_ptr(), cu_tok.data_ptr(),
             cu_row.data_ptr(), tok_pos.data_ptr(), raw_slot.data_ptr(), T, row_pos.data_ptr(), row_slot.data_ptr(), R)
 

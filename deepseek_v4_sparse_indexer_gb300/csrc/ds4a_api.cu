@@ -604,14 +604,28 @@ ds4a_status ds4a_paged_plan(const int32_t *past, const int32_t *add, int B, int 
                             int32_t *table, int64_t table_stride, int max_pages, const int32_t *ring, int32_t *n_rows,
                             int32_t *n_raw, int32_t *cu_tok, int32_t *cu_row, int32_t *tok_pos, int32_t *raw_slot,
                             int T_cap, int32_t *row_pos, int32_t *row_slot, int R_cap, void *stream) {
-    const NvtxRange nvtx_range("ds4a_paged_plan");
+    return ds4a_paged_plan_form(0, past, add, B, ratio, page_size, free_pages, n_free, free_head, free_head_out, table,
+                                table_stride, max_pages, ring, n_rows, n_raw, cu_tok, cu_row, tok_pos, raw_slot, T_cap,
+                                row_pos, row_slot, R_cap, stream);
+}
+
+ds4a_status ds4a_paged_plan_form(int form, const int32_t *past, const int32_t *add, int B, int ratio, int page_size,
+                                 const int32_t *free_pages, int n_free, const int32_t *free_head,
+                                 int32_t *free_head_out, int32_t *table, int64_t table_stride, int max_pages,
+                                 const int32_t *ring, int32_t *n_rows, int32_t *n_raw, int32_t *cu_tok,
+                                 int32_t *cu_row, int32_t *tok_pos, int32_t *raw_slot, int T_cap, int32_t *row_pos,
+                                 int32_t *row_slot, int R_cap, void *stream) {
+    const NvtxRange nvtx_range(form ? "ds4a_paged_plan_form" : "ds4a_paged_plan");
     if (ds4a_status inj = take_injected()) return inj;
+    if (form & ~(DS4A_PLAN_TOKENS_BY_SEQ | DS4A_PLAN_ROWS_BY_SEQ)) return DS4A_EINVAL;
     if (!past || !add || !free_head || !free_head_out || !table || !n_rows || !n_raw || !cu_tok || !cu_row ||
         !tok_pos || !raw_slot || !row_pos || !row_slot || n_free < 0 || (n_free > 0 && !free_pages))
         return DS4A_EINVAL;
     const int shift = page_shift(page_size);
     if (B < 1 || B > DS4A_MAX_PLAN_SEQS || ratio < 1 || shift < 0 || max_pages < 1 || table_stride < max_pages ||
         T_cap < 1 || R_cap < 1)
+        return DS4A_EINVAL;
+    if (((form & DS4A_PLAN_TOKENS_BY_SEQ) && T_cap < B) || ((form & DS4A_PLAN_ROWS_BY_SEQ) && R_cap < B))
         return DS4A_EINVAL;
     DevInfo *di = nullptr;
     if (ds4a_status st = current_device(&di)) return st;
@@ -639,6 +653,7 @@ ds4a_status ds4a_paged_plan(const int32_t *past, const int32_t *add, int B, int 
     a.row_pos = row_pos;
     a.row_slot = row_slot;
     a.R_cap = R_cap;
+    a.form = form;
     a.status = di->status;
     return launch_paged_plan(a, di->sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? DS4A_OK : DS4A_ECUDA;
 }

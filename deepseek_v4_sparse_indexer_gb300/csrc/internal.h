@@ -146,6 +146,7 @@ struct PagedPlanArgs {
     int T_cap;
     int32_t *row_pos, *row_slot;
     int R_cap;
+    int form;                    // DS4A_PLAN_* bits
     uint32_t *status;
     int cluster;                 // set by the launcher: the CTAs are one cluster
 };

@@ -14,7 +14,8 @@
 //                          (j + 1) * ratio - 1, slot table[b][j / P] * P + j % P
 //     page   page[b] + i   table[b][old pages + i] = free_pages[head + page[b] + i]
 // A row in a page that this step allocates takes the page from the free list,
-// not from the table another thread is writing.
+// not from the table another thread is writing.  By sequence (a decode step: at most
+// one token, so at most one row, each), the item of sequence b is entry b of its map.
 //
 // Every CTA scans all the lengths into shared memory (at most 8,192 sequences,
 // 160 KB) instead of waiting for one that does, so that a search is followed by
@@ -70,11 +71,12 @@ struct Seq {
     int past, add;
     bool ok;
 };
-// Lengths of sequence b: negative ones, and a sum past 2^31 - 1, count as 0.
+// Lengths of sequence b: negative ones, a sum past 2^31 - 1 and, by sequence, an add
+// above 1 count as 0.
 DS4A_DEV Seq seq_of(const PagedPlanArgs &a, int b) {
     Seq s = {a.past[b], a.add[b], true};
     if (s.past < 0) s.past = 0, s.ok = false;
-    if (s.add < 0 || s.past > 0x7fffffff - s.add) s.add = 0, s.ok = false;
+    if (s.add < 0 || s.past > 0x7fffffff - s.add || (a.form && s.add > 1)) s.add = 0, s.ok = false;
     return s;
 }
 
@@ -161,6 +163,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_plan_kernel(const __grid_co
         const long long at = static_cast<long long>(head) + g;
         return at < a.n_free ? a.free_pages[at] : -1;
     };
+    // The item of map entry x is item `at` of its kind in sequence b; false: no item.
+    const bool tok_by_seq = a.form & DS4A_PLAN_TOKENS_BY_SEQ, row_by_seq = a.form & DS4A_PLAN_ROWS_BY_SEQ;
+    auto item_at = [&](long long x, bool by_seq, const int *cu, int n, int &at) -> bool {
+        at = by_seq ? (x < B ? cu[x] : 0) : static_cast<int>(x);
+        return by_seq ? x < B && cu[x + 1] > at : x < n;
+    };
     // ---- each kind in blocks of equal runs, at most one per warp; the warps of
     // all CTAs take the blocks in turn
     const int n_warps = gridDim.x * kWarps;
@@ -184,15 +192,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_plan_kernel(const __grid_co
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     pos[q] = slot[q] = -1;
-                    if (x + q >= T) continue;
-                    if (x + q >= seq_end) {
-                        const int b = find_seq(cu_tok, B, static_cast<int>(x) + q);
+                    int at;
+                    if (!item_at(x + q, tok_by_seq, cu_tok, T, at)) continue;
+                    if (at >= seq_end) {
+                        const int b = tok_by_seq ? static_cast<int>(x) + q : find_seq(cu_tok, B, at);
                         seq_end = cu_tok[b + 1];
                         first = s_past[b] - cu_tok[b];
                         kept = first + seq_end - kNSwa;
                         ring = s_ring[b];
                     }
-                    pos[q] = first + static_cast<int>(x) + q;
+                    pos[q] = first + at;
                     if (pos[q] >= kept && ring >= 0) slot[q] = ring * kNSwa + (pos[q] & (kNSwa - 1));
                 }
                 store4(a.tok_pos, x, a.T_cap, pos, vec_tok);
@@ -210,9 +219,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_plan_kernel(const __grid_co
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     pos[q] = slot[q] = -1;
-                    if (x + q >= R) continue;
-                    if (x + q >= seq_end) {
-                        const int b = find_seq(cu_row, B, static_cast<int>(x) + q);
+                    int item;
+                    if (!item_at(x + q, row_by_seq, cu_row, R, item)) continue;
+                    if (item >= seq_end) {
+                        const int b = row_by_seq ? static_cast<int>(x) + q : find_seq(cu_row, B, item);
                         const int old = s_past[b] / a.ratio;
                         seq_end = cu_row[b + 1];
                         first = old - cu_row[b];
@@ -221,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_plan_kernel(const __grid_co
                         table = a.table + b * a.table_stride;
                         last_i = -1;
                     }
-                    const int j = first + static_cast<int>(x) + q, i = j >> a.shift;
+                    const int j = first + item, i = j >> a.shift;
                     if (i != last_i) {
                         last_i = i;
                         page = i >= a.max_pages ? -1 : i >= held ? free_page(taken + i) : table[i];

@@ -175,8 +175,8 @@ class PagedDecodeStep:
     """One new token for each of up to U sequences, over paged caches.
 
     x holds, per step: past, add (i32 [U]: tokens in the cache and new ones, 1 or
-    0; sequences without a new token come last, and what out holds for them is
-    of no use unless they are empty: zeros), q [U,H,512] and kv [U,512], the
+    0, in any order; what out holds for a sequence without a new token is of no
+    use unless it is empty: zeros), q [U,H,512] and kv [U,512], the
     projections before norm and rotation (bf16, fp16 or fp32); with top_k also iq
     [U,64,128] and w f32 [U,64].  And, kept by the program: table i32
     [U,max_pages], free_pages and free_head (updated in place), ring i32 [U] or
@@ -185,7 +185,9 @@ class PagedDecodeStep:
     [n_rot / 2] and the norm weights q_norm, kv_norm, iq_norm, ik_norm (f32 or
     None).  A layer of `ratio` tokens per row finishes a row every ratio tokens:
     pooled [U,512] (and pooled_ik [U,128]) hold the rows finished in this step,
-    new row i of the batch in row i (cu_row says whose).
+    new row i of the batch in row i (cu_row says whose) or, with
+    pooled_by_sequence, sequence u's in row u, as ds4a_compressor_pool writes
+    them (a sequence that finishes none: its row is not read).
 
     plan -> rotate -> store -> score -> select -> attend, each one call of the
     library (two for the indexer's part); outputs and workspaces are kept, so the
@@ -194,9 +196,11 @@ class PagedDecodeStep:
     """
 
     def __init__(self, U, max_pages, page_size, top_k=512, ratio=4, device="cuda", n_head=B.N_HEAD, fp8=False, eps=1e-6,
-                 style=B.DS4A_ROPE_NEIGHBOURS):
+                 style=B.DS4A_ROPE_NEIGHBOURS, pooled_by_sequence=False):
         self.U, self.page_size, self.top_k, self.ratio, self.n_head = U, page_size, top_k, ratio, n_head
         self.fp8, self.eps, self.style = fp8, eps, style
+        # q, kv and out are kept by sequence, so the tokens' positions and slots are too
+        self.form = B.DS4A_PLAN_TOKENS_BY_SEQ | (B.DS4A_PLAN_ROWS_BY_SEQ if pooled_by_sequence else 0)
         dev = torch.device(device)
         N_cap = max_pages * page_size
         flag = B.DS4A_OP_FLAG_128_HEADS if n_head == 128 else 0
@@ -219,7 +223,7 @@ class PagedDecodeStep:
     def plan(self, x, stream=None):
         B.ds4a_paged_plan(x["past"], x["add"], self.ratio, self.page_size, x["free_pages"], x["free_head"], x["table"],
                           self.n_rows, self.n_raw, self.cu_tok, self.cu_row, self.tok_pos, self.raw_slot, self.row_pos,
-                          self.row_slot, x["free_head"], ring=x.get("ring"), stream=stream)
+                          self.row_slot, x["free_head"], ring=x.get("ring"), stream=stream, form=self.form)
 
     def rotate(self, x, stream=None):
         B.ds4a_qk_norm_rope(x["q"], x["kv"], self.tok_pos, x["inv_freq"], self.eps, x.get("q_norm"), x.get("kv_norm"), self.q,

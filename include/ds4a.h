@@ -104,6 +104,10 @@ typedef int ds4a_status;
 #define DS4A_MAX_PAGE 4096
 #define DS4A_MAX_PLAN_SEQS 8192 /* sequences of one ds4a_paged_plan call        */
 
+/* What the maps of ds4a_paged_plan_form look like; OR-ed, 0: ds4a_paged_plan's. */
+#define DS4A_PLAN_TOKENS_BY_SEQ 1  /* entry b of the token maps: sequence b's token */
+#define DS4A_PLAN_ROWS_BY_SEQ 2    /* entry b of the row maps: sequence b's new row */
+
 /* Human-readable text of a status code (static storage). */
 const char *ds4a_strerror(ds4a_status status);
 
@@ -546,6 +550,24 @@ ds4a_status ds4a_paged_plan(const int32_t *past, const int32_t *add, int B, int 
                             int32_t *n_rows, int32_t *n_raw, int32_t *cu_tok, int32_t *cu_row,
                             int32_t *tok_pos, int32_t *raw_slot, int T_cap, int32_t *row_pos,
                             int32_t *row_slot, int R_cap, void *stream);
+
+/*
+ *    The same with the maps laid out for a decode step, where a sequence has at
+ *    most one new token, and so at most one new row, and a program keeps its
+ *    buffers by sequence: with DS4A_PLAN_TOKENS_BY_SEQ entry b of tok_pos and
+ *    raw_slot is sequence b's token, with DS4A_PLAN_ROWS_BY_SEQ entry b of row_pos
+ *    and row_slot its new row; -1 for a sequence without one and behind the last
+ *    sequence.  Sequences with and without a token may then lie in any order.
+ *    With either form an add above 1 sets DS4A_DEV_BOUNDS and counts as 0, and
+ *    the capacity of its maps is at least B.  Every other output is the same.
+ */
+ds4a_status ds4a_paged_plan_form(int form, const int32_t *past, const int32_t *add, int B,
+                                 int ratio, int page_size, const int32_t *free_pages, int n_free,
+                                 const int32_t *free_head, int32_t *free_head_out, int32_t *table,
+                                 int64_t table_stride, int max_pages, const int32_t *ring,
+                                 int32_t *n_rows, int32_t *n_raw, int32_t *cu_tok,
+                                 int32_t *cu_row, int32_t *tok_pos, int32_t *raw_slot, int T_cap,
+                                 int32_t *row_pos, int32_t *row_slot, int R_cap, void *stream);
 
 /*
  * 5b. Norm and rotation of queries and keys (§2: RoPE on the last n_rot dims
