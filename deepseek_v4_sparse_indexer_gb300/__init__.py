@@ -15,7 +15,7 @@ from ._binding import (Ds4aError, load, ds4a_version, ds4a_workspace_bytes, ds4a
                        ds4a_sparse_attn_prefill_heads, ds4a_dense_attn_decode_heads, ds4a_rows_to_fp8,
                        ds4a_sparse_attn_decode_fp8, ds4a_sparse_attn_prefill_fp8, ds4a_indexer_topk,
                        ds4a_paged_plan, ds4a_qk_norm_rope, ds4a_paged_indexer_score, ds4a_paged_attn_decode,
-                       DS4A_OP_PAGED_ATTN_DECODE, DS4A_PLAN_TOKENS_BY_SEQ, DS4A_PLAN_ROWS_BY_SEQ,
+                       DS4A_OP_PAGED_ATTN_DECODE, DS4A_PLAN_TOKENS_BY_SEQ, DS4A_PLAN_ROWS_BY_SEQ, DS4A_PLAN_FIRST_POS,
                        DS4A_OP_FLAG_128_HEADS, DS4A_ROPE_NEIGHBOURS, DS4A_ROPE_HALVES)
 from .step import DecodeStep, PrefillStep, DenseStep, ProducerStep, PagedDecodeStep, DEFAULT_SCALE
 
@@ -25,7 +25,7 @@ __all__ = ["Ds4aError", "load", "ds4a_version", "ds4a_workspace_bytes", "ds4a_ge
            "ds4a_sparse_attn_decode_heads", "ds4a_sparse_attn_prefill_heads", "ds4a_dense_attn_decode_heads",
            "ds4a_rows_to_fp8", "ds4a_sparse_attn_decode_fp8", "ds4a_sparse_attn_prefill_fp8", "ds4a_indexer_topk",
            "ds4a_paged_plan", "ds4a_qk_norm_rope", "ds4a_paged_indexer_score", "ds4a_paged_attn_decode",
-           "DS4A_OP_PAGED_ATTN_DECODE", "DS4A_PLAN_TOKENS_BY_SEQ", "DS4A_PLAN_ROWS_BY_SEQ",
+           "DS4A_OP_PAGED_ATTN_DECODE", "DS4A_PLAN_TOKENS_BY_SEQ", "DS4A_PLAN_ROWS_BY_SEQ", "DS4A_PLAN_FIRST_POS",
            "DS4A_OP_FLAG_128_HEADS", "DS4A_ROPE_NEIGHBOURS", "DS4A_ROPE_HALVES",
            "DecodeStep", "PrefillStep", "DenseStep", "ProducerStep", "PagedDecodeStep",
            "DEFAULT_SCALE"]

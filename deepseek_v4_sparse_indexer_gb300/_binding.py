@@ -33,7 +33,7 @@ DS4A_OP_FLAG_128_HEADS = 0x100
 DS4A_BF16, DS4A_F16, DS4A_F32, DS4A_E4M3 = 0, 1, 2, 3
 DS4A_ROPE_NEIGHBOURS, DS4A_ROPE_HALVES = 0, 1
 DS4A_MIN_PAGE, DS4A_MAX_PAGE, DS4A_MAX_PLAN_SEQS = 8, 4096, 8192
-DS4A_PLAN_TOKENS_BY_SEQ, DS4A_PLAN_ROWS_BY_SEQ = 1, 2
+DS4A_PLAN_TOKENS_BY_SEQ, DS4A_PLAN_ROWS_BY_SEQ, DS4A_PLAN_FIRST_POS = 1, 2, 4
 
 N_HEAD, HEAD_DIM, N_IDX_HEAD, IDX_DIM, N_SWA = 64, 512, 64, 128, 128
 
@@ -580,7 +580,8 @@ def ds4a_paged_plan(past, add, ratio, page_size, free_pages, free_head, table, n
     (updated); n_rows, n_raw [B], cu_tok, cu_row [B + 1], tok_pos, raw_slot
     [T_cap], row_pos, row_slot [R_cap] and free_head_out [1] (written; may be
     free_head); ring [B] or None.  form: DS4A_PLAN_TOKENS_BY_SEQ and / or
-    DS4A_PLAN_ROWS_BY_SEQ lay the token / row maps out by sequence (add 0 or 1)."""
+    DS4A_PLAN_ROWS_BY_SEQ lay the token / row maps out by sequence (add 0 or 1),
+    DS4A_PLAN_FIRST_POS makes row_pos the position of a row's first token."""
     dev = _device_index(past, "past")
     B, T, R, n_free = past.numel(), tok_pos.numel(), row_pos.numel(), free_pages.numel()
     _req_ints(dev, ("past", past, B), ("add", add, B), ("free_pages", free_pages, n_free), ("free_head", free_head, 1),

@@ -617,7 +617,7 @@ ds4a_status ds4a_paged_plan_form(int form, const int32_t *past, const int32_t *a
                                  int32_t *row_slot, int R_cap, void *stream) {
     const NvtxRange nvtx_range(form ? "ds4a_paged_plan_form" : "ds4a_paged_plan");
     if (ds4a_status inj = take_injected()) return inj;
-    if (form & ~(DS4A_PLAN_TOKENS_BY_SEQ | DS4A_PLAN_ROWS_BY_SEQ)) return DS4A_EINVAL;
+    if (form & ~(DS4A_PLAN_TOKENS_BY_SEQ | DS4A_PLAN_ROWS_BY_SEQ | DS4A_PLAN_FIRST_POS)) return DS4A_EINVAL;
     if (!past || !add || !free_head || !free_head_out || !table || !n_rows || !n_raw || !cu_tok || !cu_row ||
         !tok_pos || !raw_slot || !row_pos || !row_slot || n_free < 0 || (n_free > 0 && !free_pages))
         return DS4A_EINVAL;

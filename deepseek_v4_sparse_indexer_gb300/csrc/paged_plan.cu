@@ -11,7 +11,7 @@
 //                          (the chunk's last 128 tokens only: earlier ones would
 //                          be overwritten within the step)
 //     row    row[b] + i    row j = old rows + i of the sequence: position
-//                          (j + 1) * ratio - 1, slot table[b][j / P] * P + j % P
+//                          (j + 1) * ratio - 1 (or j * ratio), slot table[b][j / P] * P + j % P
 //     page   page[b] + i   table[b][old pages + i] = free_pages[head + page[b] + i]
 // A row in a page that this step allocates takes the page from the free list,
 // not from the table another thread is writing.  By sequence (a decode step: at most
@@ -76,7 +76,7 @@ struct Seq {
 DS4A_DEV Seq seq_of(const PagedPlanArgs &a, int b) {
     Seq s = {a.past[b], a.add[b], true};
     if (s.past < 0) s.past = 0, s.ok = false;
-    if (s.add < 0 || s.past > 0x7fffffff - s.add || (a.form && s.add > 1)) s.add = 0, s.ok = false;
+    if (s.add < 0 || s.past > 0x7fffffff - s.add || (s.add > 1 && (a.form & (DS4A_PLAN_TOKENS_BY_SEQ | DS4A_PLAN_ROWS_BY_SEQ)))) s.add = 0, s.ok = false;
     return s;
 }
 
@@ -169,6 +169,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_plan_kernel(const __grid_co
         at = by_seq ? (x < B ? cu[x] : 0) : static_cast<int>(x);
         return by_seq ? x < B && cu[x + 1] > at : x < n;
     };
+    const int pos_in_row = a.form & DS4A_PLAN_FIRST_POS ? 0 : a.ratio - 1;
     // ---- each kind in blocks of equal runs, at most one per warp; the warps of
     // all CTAs take the blocks in turn
     const int n_warps = gridDim.x * kWarps;
@@ -236,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_plan_kernel(const __grid_co
                         last_i = i;
                         page = i >= a.max_pages ? -1 : i >= held ? free_page(taken + i) : table[i];
                     }
-                    pos[q] = static_cast<int>((static_cast<long long>(j) + 1) * a.ratio - 1);
+                    pos[q] = static_cast<int>(static_cast<long long>(j) * a.ratio + pos_in_row);
                     const long long at = (static_cast<long long>(page) << a.shift) + (j & ((1 << a.shift) - 1));
                     if (page < 0 || at > 0x7fffffffLL) ok = false;
                     else slot[q] = static_cast<int>(at);

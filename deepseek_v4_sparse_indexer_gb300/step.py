@@ -187,7 +187,9 @@ class PagedDecodeStep:
     pooled [U,512] (and pooled_ik [U,128]) hold the rows finished in this step,
     new row i of the batch in row i (cu_row says whose) or, with
     pooled_by_sequence, sequence u's in row u, as ds4a_compressor_pool writes
-    them (a sequence that finishes none: its row is not read).
+    them (a sequence that finishes none: its row is not read).  row_position:
+    "last" or "first", the token of a row whose position its tail (and its key's)
+    is turned by.
 
     plan -> rotate -> store -> score -> select -> attend, each one call of the
     library (two for the indexer's part); outputs and workspaces are kept, so the
@@ -196,11 +198,14 @@ class PagedDecodeStep:
     """
 
     def __init__(self, U, max_pages, page_size, top_k=512, ratio=4, device="cuda", n_head=B.N_HEAD, fp8=False, eps=1e-6,
-                 style=B.DS4A_ROPE_NEIGHBOURS, pooled_by_sequence=False):
+                 style=B.DS4A_ROPE_NEIGHBOURS, pooled_by_sequence=False, row_position="last"):
         self.U, self.page_size, self.top_k, self.ratio, self.n_head = U, page_size, top_k, ratio, n_head
         self.fp8, self.eps, self.style = fp8, eps, style
         # q, kv and out are kept by sequence, so the tokens' positions and slots are too
-        self.form = B.DS4A_PLAN_TOKENS_BY_SEQ | (B.DS4A_PLAN_ROWS_BY_SEQ if pooled_by_sequence else 0)
+        if row_position not in ("last", "first"):
+            raise ValueError("row_position: \"last\" or \"first\"")
+        self.form = B.DS4A_PLAN_TOKENS_BY_SEQ | (B.DS4A_PLAN_ROWS_BY_SEQ if pooled_by_sequence else 0) \
+            | (B.DS4A_PLAN_FIRST_POS if row_position == "first" else 0)
         dev = torch.device(device)
         N_cap = max_pages * page_size
         flag = B.DS4A_OP_FLAG_128_HEADS if n_head == 128 else 0

@@ -107,6 +107,7 @@ typedef int ds4a_status;
 /* What the maps of ds4a_paged_plan_form look like; OR-ed, 0: ds4a_paged_plan's. */
 #define DS4A_PLAN_TOKENS_BY_SEQ 1  /* entry b of the token maps: sequence b's token */
 #define DS4A_PLAN_ROWS_BY_SEQ 2    /* entry b of the row maps: sequence b's new row */
+#define DS4A_PLAN_FIRST_POS 4      /* row_pos: that of the row's first token        */
 
 /* Human-readable text of a status code (static storage). */
 const char *ds4a_strerror(ds4a_status status);
@@ -558,8 +559,11 @@ ds4a_status ds4a_paged_plan(const int32_t *past, const int32_t *add, int B, int 
  *    raw_slot is sequence b's token, with DS4A_PLAN_ROWS_BY_SEQ entry b of row_pos
  *    and row_slot its new row; -1 for a sequence without one and behind the last
  *    sequence.  Sequences with and without a token may then lie in any order.
- *    With either form an add above 1 sets DS4A_DEV_BOUNDS and counts as 0, and
- *    the capacity of its maps is at least B.  Every other output is the same.
+ *    With either of the two an add above 1 sets DS4A_DEV_BOUNDS and counts as 0,
+ *    and the capacity of its maps is at least B.  With DS4A_PLAN_FIRST_POS
+ *    (any step) a row's position is that of its first token, row * ratio: the
+ *    pages say that a pooled row's tail is rotated, not by which position, so the
+ *    program says it for its model.  Every other output is the same.
  */
 ds4a_status ds4a_paged_plan_form(int form, const int32_t *past, const int32_t *add, int B,
                                  int ratio, int page_size, const int32_t *free_pages, int n_free,

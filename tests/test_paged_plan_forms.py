@@ -10,11 +10,11 @@ from paged_util import WINDOW, plan_reference
 from test_paged_abi import PLAN, call
 from test_paged_plan_gpu import KEYS, Plan, status
 
-TOKENS, ROWS = B.DS4A_PLAN_TOKENS_BY_SEQ, B.DS4A_PLAN_ROWS_BY_SEQ
+TOKENS, ROWS, FIRST = B.DS4A_PLAN_TOKENS_BY_SEQ, B.DS4A_PLAN_ROWS_BY_SEQ, B.DS4A_PLAN_FIRST_POS
 
 
 @pytest.mark.parametrize("form,change", [
-    (4, {}), (-1, {}), (8 | TOKENS, {}), (TOKENS, dict(T_cap=1)), (ROWS, dict(R_cap=1)), (TOKENS | ROWS, dict(R_cap=1)),
+    (16, {}), (-1, {}), (8 | TOKENS, {}), (TOKENS, dict(T_cap=1)), (ROWS, dict(R_cap=1)), (TOKENS | ROWS, dict(R_cap=1)),
     (TOKENS, dict(past=None)), (ROWS, dict(page_size=48)), (TOKENS, dict(B=B.DS4A_MAX_PLAN_SEQS + 1)), (0, dict(T_cap=0))])
 def test_form_rejects(form, change):
     assert call(B.load().ds4a_paged_plan_form, dict(form=form, **PLAN), **change) == B.DS4A_EINVAL
@@ -28,6 +28,8 @@ def test_injected_error():
 def by_sequence(p, form):
     """The walk's arrays, the maps of `form` laid out by sequence."""
     want, table, head = plan_reference(p.past, p.add, p.ratio, p.P, p.free, p.head, p.table, p.ring, p.T_cap, p.R_cap)
+    if form & FIRST:
+        want["row_pos"] = [x if x < 0 else x - (p.ratio - 1) for x in want["row_pos"]]
     for bit, cu, keys, cap in ((TOKENS, "cu_tok", ("tok_pos", "raw_slot"), p.T_cap),
                                (ROWS, "cu_row", ("row_pos", "row_slot"), p.R_cap)):
         if form & bit:
@@ -53,7 +55,7 @@ def check(p, form):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("form", [TOKENS, ROWS, TOKENS | ROWS])
+@pytest.mark.parametrize("form", [TOKENS, ROWS, TOKENS | ROWS, TOKENS | ROWS | FIRST])
 @pytest.mark.parametrize("B_,ratio,P,off", [(1, 4, 64, 0), (3, 1, 8, 1), (130, 4, 8, 0), (130, 2, 4096, 1), (1500, 128, 16, 0),
                                             (8192, 3, 64, 0)])
 def test_decode_steps(cuda_lib, B_, ratio, P, off, form):
@@ -117,3 +119,14 @@ def test_a_ring_or_page_that_is_not_there(cuda_lib):
     assert p.out["raw_slot"].tolist() == [p.ring[0] * WINDOW + 31, p.ring[1] * WINDOW + 31, -1]
     assert p.out["row_slot"].tolist() == [-1, p.table[1][0] * 8 + 7, 50 * 8]
     assert p.out["tok_pos"].tolist() == [31, 31, 3] and p.out["row_pos"].tolist() == [31, 31, 3]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("ratio,P", [(1, 8), (4, 64), (128, 8)])
+def test_first_position_of_a_chunk(cuda_lib, ratio, P):
+    rng = random.Random(ratio)
+    past = [rng.randint(0, 3000) for _ in range(40)]
+    p = Plan(past, [rng.choice((0, 1, 129, rng.randint(0, 2048))) for _ in past], ratio, P)
+    go(cuda_lib, p, FIRST)
+    assert status(cuda_lib) == (0, 0)
+    assert p.d_head_out.item() == check(p, FIRST)

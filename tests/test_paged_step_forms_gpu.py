@@ -167,3 +167,17 @@ def test_fed_by_the_compressor(cuda_lib):
         assert ((x["pooled"].double() - pooled).abs() <= 2.0 ** -14 * frontier["kv"].abs().amax(1)).all()
         run.check(past, add)
         past = [p + a for p, a in zip(past, add)]
+
+
+class First(Run):
+    def row_pos(self, j):
+        return j * self.ratio
+
+
+@pytest.mark.parametrize("by_seq", [False, True])
+@pytest.mark.parametrize("ratio", [1, 4])
+def test_rows_turned_by_their_first_token(cuda_lib, ratio, by_seq):
+    import deepseek_v4_sparse_indexer_gb300 as pkg
+    First(pkg, ratio=ratio, by_seq=by_seq, row_position="first").steps(cuda_lib, 20)
+    with pytest.raises(ValueError):
+        pkg.PagedDecodeStep(U, MAX_PAGES, P, row_position="middle")
