@@ -183,7 +183,8 @@ class PagedDecodeStep:
     None, raw fp16 [n_ring,128,512], rows bf16 [n_pages,P,512] (fp8: uint8 codes
     and row_scale f32 [n_pages,P]), ik bf16 [n_pages,P,128] with top_k, inv_freq f64
     [n_rot / 2] and the norm weights q_norm, kv_norm, iq_norm, ik_norm (f32 or
-    None).  A layer of `ratio` tokens per row finishes a row every ratio tokens:
+    None).  style and idx_style (style unless given) say which dims pair in the
+    layer's heads and rows and in the indexer's queries and keys.  A layer of `ratio` tokens per row finishes a row every ratio tokens:
     pooled [U,512] (and pooled_ik [U,128]) hold the rows finished in this step,
     new row i of the batch in row i (cu_row says whose) or, with
     pooled_by_sequence, sequence u's in row u, as ds4a_compressor_pool writes
@@ -198,9 +199,11 @@ class PagedDecodeStep:
     """
 
     def __init__(self, U, max_pages, page_size, top_k=512, ratio=4, device="cuda", n_head=B.N_HEAD, fp8=False, eps=1e-6,
-                 style=B.DS4A_ROPE_NEIGHBOURS, pooled_by_sequence=False, row_position="last"):
+                 style=B.DS4A_ROPE_NEIGHBOURS, pooled_by_sequence=False, row_position="last",
+                 idx_style=None):
         self.U, self.page_size, self.top_k, self.ratio, self.n_head = U, page_size, top_k, ratio, n_head
         self.fp8, self.eps, self.style = fp8, eps, style
+        self.idx_style = style if idx_style is None else idx_style
         # q, kv and out are kept by sequence, so the tokens' positions and slots are too
         if row_position not in ("last", "first"):
             raise ValueError("row_position: \"last\" or \"first\"")
@@ -235,7 +238,7 @@ class PagedDecodeStep:
                             x["raw"].view(-1, B.HEAD_DIM), k_slot=self.raw_slot, style=self.style, stream=stream)
         if self.top_k:
             B.ds4a_qk_norm_rope(x["iq"], None, self.tok_pos, x["inv_freq"], self.eps, x.get("iq_norm"), None, self.iq, None,
-                                style=self.style, stream=stream)
+                                style=self.idx_style, stream=stream)
 
     def store(self, x, stream=None):
         B.ds4a_qk_norm_rope(None, x["pooled"], self.row_pos, x["inv_freq"], self.eps, None, x.get("kv_norm"), None,
@@ -243,7 +246,7 @@ class PagedDecodeStep:
                             k_scale=x["row_scale"].view(-1) if self.fp8 else None, style=self.style, stream=stream)
         if self.top_k:
             B.ds4a_qk_norm_rope(None, x["pooled_ik"], self.row_pos, x["inv_freq"], self.eps, None, x.get("ik_norm"), None,
-                                x["ik"].view(-1, B.IDX_DIM), k_slot=self.row_slot, style=self.style, stream=stream)
+                                x["ik"].view(-1, B.IDX_DIM), k_slot=self.row_slot, style=self.idx_style, stream=stream)
 
     def score(self, x, stream=None):
         B.ds4a_paged_indexer_score(self.iq.view(self.U, 1, B.N_IDX_HEAD, B.IDX_DIM), x["w"].view(self.U, 1, B.N_IDX_HEAD),

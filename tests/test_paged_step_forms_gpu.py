@@ -181,3 +181,11 @@ def test_rows_turned_by_their_first_token(cuda_lib, ratio, by_seq):
     First(pkg, ratio=ratio, by_seq=by_seq, row_position="first").steps(cuda_lib, 20)
     with pytest.raises(ValueError):
         pkg.PagedDecodeStep(U, MAX_PAGES, P, row_position="middle")
+
+
+@pytest.mark.parametrize("style,idx_style", [(0, 1), (1, 0), (1, None)])
+def test_pairs_of_the_heads_and_of_the_indexer(cuda_lib, style, idx_style):
+    import deepseek_v4_sparse_indexer_gb300 as pkg
+    run = Run(pkg, style=style, idx_style=idx_style)
+    run.style, run.idx_style = style, style if idx_style is None else idx_style
+    run.steps(cuda_lib, 12)
