@@ -183,7 +183,8 @@ class PagedDecodeStep:
     None, raw fp16 [n_ring,128,512], rows bf16 [n_pages,P,512] (fp8: uint8 codes
     and row_scale f32 [n_pages,P]), ik bf16 [n_pages,P,128] with top_k, inv_freq f64
     [n_rot / 2] and the norm weights q_norm, kv_norm, iq_norm, ik_norm (f32 or
-    None).  style and idx_style (style unless given) say which dims pair in the
+    None) and, where the pooled rows have a norm of their own, row_norm (else they
+    take kv_norm).  style and idx_style (style unless given) say which dims pair in the
     layer's heads and rows and in the indexer's queries and keys.  A layer of `ratio` tokens per row finishes a row every ratio tokens:
     pooled [U,512] (and pooled_ik [U,128]) hold the rows finished in this step,
     new row i of the batch in row i (cu_row says whose) or, with
@@ -241,7 +242,8 @@ class PagedDecodeStep:
                                 style=self.idx_style, stream=stream)
 
     def store(self, x, stream=None):
-        B.ds4a_qk_norm_rope(None, x["pooled"], self.row_pos, x["inv_freq"], self.eps, None, x.get("kv_norm"), None,
+        row_norm = x["row_norm"] if "row_norm" in x else x.get("kv_norm")
+        B.ds4a_qk_norm_rope(None, x["pooled"], self.row_pos, x["inv_freq"], self.eps, None, row_norm, None,
                             x["rows"].view(-1, B.HEAD_DIM), k_slot=self.row_slot,
                             k_scale=x["row_scale"].view(-1) if self.fp8 else None, style=self.style, stream=stream)
         if self.top_k:

@@ -189,3 +189,13 @@ def test_pairs_of_the_heads_and_of_the_indexer(cuda_lib, style, idx_style):
     run = Run(pkg, style=style, idx_style=idx_style)
     run.style, run.idx_style = style, style if idx_style is None else idx_style
     run.steps(cuda_lib, 12)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("ones", [False, True])
+def test_pooled_rows_with_a_norm_of_their_own(cuda_lib, fp8, ones):
+    import deepseek_v4_sparse_indexer_gb300 as pkg
+    run = Run(pkg, fp8=fp8)
+    run.x["row_norm"] = None if ones else 1 + 0.3 * run.normal(512)      # None: all ones
+    run.pooled_norm = "row_norm"
+    run.steps(cuda_lib, 12)
