@@ -178,7 +178,9 @@ class PagedDecodeStep:
     0, in any order; what out holds for a sequence without a new token is of no
     use unless it is empty: zeros), q [U,H,512] and kv [U,512], the
     projections before norm and rotation (bf16, fp16 or fp32); with top_k also iq
-    [U,64,128] and w f32 [U,64].  And, kept by the program: table i32
+    [U,64,128] (with rotate_iq=False the indexer's queries as they are scored, bf16
+    and contiguous: a model that does not normalise them turns them itself) and w
+    f32 [U,64].  And, kept by the program: table i32
     [U,max_pages], free_pages and free_head (updated in place), ring i32 [U] or
     None, raw fp16 [n_ring,128,512], rows bf16 [n_pages,P,512] (fp8: uint8 codes
     and row_scale f32 [n_pages,P]), ik bf16 [n_pages,P,128] with top_k, inv_freq f64
@@ -201,10 +203,11 @@ class PagedDecodeStep:
 
     def __init__(self, U, max_pages, page_size, top_k=512, ratio=4, device="cuda", n_head=B.N_HEAD, fp8=False, eps=1e-6,
                  style=B.DS4A_ROPE_NEIGHBOURS, pooled_by_sequence=False, row_position="last",
-                 idx_style=None):
+                 idx_style=None, rotate_iq=True):
         self.U, self.page_size, self.top_k, self.ratio, self.n_head = U, page_size, top_k, ratio, n_head
         self.fp8, self.eps, self.style = fp8, eps, style
         self.idx_style = style if idx_style is None else idx_style
+        self.rotate_iq = rotate_iq
         # q, kv and out are kept by sequence, so the tokens' positions and slots are too
         if row_position not in ("last", "first"):
             raise ValueError("row_position: \"last\" or \"first\"")
@@ -223,7 +226,8 @@ class PagedDecodeStep:
         self.ws_attn = _ws(B.ds4a_workspace_bytes(B.DS4A_OP_PAGED_ATTN_DECODE | flag, U, 1, N_cap, top_k), dev)
         self.idx = self.count = None
         if top_k:
-            self.iq = torch.zeros(U, B.N_IDX_HEAD, B.IDX_DIM, dtype=torch.bfloat16, device=dev)
+            if rotate_iq:
+                self.iq = torch.zeros(U, B.N_IDX_HEAD, B.IDX_DIM, dtype=torch.bfloat16, device=dev)
             self.scores = torch.empty(U, 1, N_cap, dtype=torch.float32, device=dev)
             self.idx = torch.empty(U, 1, top_k, dtype=torch.int32, device=dev)
             self.count = torch.empty(U, 1, dtype=torch.int32, device=dev)
@@ -237,7 +241,7 @@ class PagedDecodeStep:
     def rotate(self, x, stream=None):
         B.ds4a_qk_norm_rope(x["q"], x["kv"], self.tok_pos, x["inv_freq"], self.eps, x.get("q_norm"), x.get("kv_norm"), self.q,
                             x["raw"].view(-1, B.HEAD_DIM), k_slot=self.raw_slot, style=self.style, stream=stream)
-        if self.top_k:
+        if self.top_k and self.rotate_iq:
             B.ds4a_qk_norm_rope(x["iq"], None, self.tok_pos, x["inv_freq"], self.eps, x.get("iq_norm"), None, self.iq, None,
                                 style=self.idx_style, stream=stream)
 
@@ -251,7 +255,8 @@ class PagedDecodeStep:
                                 x["ik"].view(-1, B.IDX_DIM), k_slot=self.row_slot, style=self.idx_style, stream=stream)
 
     def score(self, x, stream=None):
-        B.ds4a_paged_indexer_score(self.iq.view(self.U, 1, B.N_IDX_HEAD, B.IDX_DIM), x["w"].view(self.U, 1, B.N_IDX_HEAD),
+        iq = self.iq if self.rotate_iq else x["iq"]
+        B.ds4a_paged_indexer_score(iq.view(self.U, 1, B.N_IDX_HEAD, B.IDX_DIM), x["w"].view(self.U, 1, B.N_IDX_HEAD),
                                    x["ik"], x["table"], self.n_rows, self.scores, stream=stream)
 
     def select(self, x, stream=None):

@@ -199,3 +199,18 @@ def test_pooled_rows_with_a_norm_of_their_own(cuda_lib, fp8, ones):
     run.x["row_norm"] = None if ones else 1 + 0.3 * run.normal(512)      # None: all ones
     run.pooled_norm = "row_norm"
     run.steps(cuda_lib, 12)
+
+
+class GivenQueries(Run):
+    def check_index_queries(self, live, pos):
+        self.step.iq = self.x["iq"]              # what the scores are checked with; the step has no buffer of its own
+
+
+def test_indexer_queries_as_given(cuda_lib):
+    import deepseek_v4_sparse_indexer_gb300 as pkg
+    run = GivenQueries(pkg, rotate_iq=False)
+    assert not hasattr(run.step, "iq")
+    run.steps(cuda_lib, 12)
+    run.x["iq"] = run.x["iq"].float()
+    with pytest.raises(ValueError):
+        run.step(run.x, SCALE)
