@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_plan_kernel(const __grid_co
     if (tid == 0) cu_tok[0] = cu_row[0] = cu_page[0] = 0;
     __syncthreads();
     const int T = cu_tok[B], R = cu_row[B], G = cu_page[B];
-    const int head = head_in < 0 ? 0 : head_in;
+    const int head = head_in < 0 ? a.n_free : head_in;     // negative: as a list that is used up
     const long long head_end = static_cast<long long>(head) + G;
     if (head_in < 0 || T > a.T_cap || R > a.R_cap || head_end > a.n_free) ok = false;
 
@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_plan_kernel(const __grid_co
     // ---- the free list's new head, once every CTA has read the old one
     if (a.cluster) cluster_sync_all();
     if (blockIdx.x == 0 && tid == 0)
-        a.free_head_out[0] = static_cast<int>(min(head_end, static_cast<long long>(max(a.n_free, head))));
+        a.free_head_out[0] = head_in < 0 ? head_in : static_cast<int>(min(head_end, static_cast<long long>(max(a.n_free, head))));
 }
 
 }  // namespace

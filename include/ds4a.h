@@ -518,7 +518,8 @@ ds4a_status ds4a_sparse_attn_prefill_fp8(const uint16_t *q, const int32_t *q_pos
  *                 free_pages[*free_head] on.  n_free may be 0 (NULL).
  *    free_head    int32 [1] (device).   free_head_out  int32 [1] (device,
  *                 written): *free_head plus the pages taken; may be free_head
- *                 itself.
+ *                 itself.  A negative head sets DS4A_DEV_BOUNDS, takes no page and
+ *                 stays as it is.
  *    table        int32 [B] rows of max_pages entries, table_stride apart
  *                 (device, updated): the entries of the step's new pages are
  *                 written, the others left as they were.

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from deepseek_v4_sparse_indexer_gb300 import _binding as B
-from paged_util import WINDOW, plan_reference
+from paged_util import WINDOW, pages_of, plan_reference
 from test_paged_abi import PLAN, call
 from test_paged_plan_gpu import KEYS, Plan, status
 
@@ -130,3 +130,24 @@ def test_first_position_of_a_chunk(cuda_lib, ratio, P):
     go(cuda_lib, p, FIRST)
     assert status(cuda_lib) == (0, 0)
     assert p.d_head_out.item() == check(p, FIRST)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("add", [40, 4000])       # one CTA, and every SM
+def test_negative_head_takes_no_page(cuda_lib, add):
+    """A head that was never set: flagged, and no page that another sequence may hold is handed out."""
+    p = Plan([8, 0, 12], [add] * 3, 4, 8)
+    p.d_head.fill_(-2)
+    go(cuda_lib, p, 0)
+    assert status(cuda_lib) == (cuda_lib.DS4A_EDEVICE, cuda_lib.DS4A_DEV_BOUNDS)
+    assert p.d_head_out.item() == -2
+    want, _, _ = by_sequence(p, 0)
+    for k in ("n_rows", "n_raw", "cu_tok", "cu_row", "tok_pos", "raw_slot", "row_pos"):
+        assert p.out[k].tolist() == want[k], k
+    held = [1, 0, 1]
+    slots = [p.table[b][j // 8] * 8 + j % 8 if j // 8 < held[b] else -1
+             for b in range(3) for j in range(p.past[b] // 4, (p.past[b] + add) // 4)]
+    assert p.out["row_slot"].tolist() == slots + [-1] * (p.R_cap - len(slots))
+    new = [pages_of((p.past[b] + add) // 4, 8) for b in range(3)]
+    assert p.d_table[:, :p.max_pages].tolist() == [p.table[b][:held[b]] + [-1] * (new[b] - held[b]) + p.table[b][new[b]:]
+                                                   for b in range(3)]
