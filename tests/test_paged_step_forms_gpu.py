@@ -214,3 +214,9 @@ def test_indexer_queries_as_given(cuda_lib):
     run.x["iq"] = run.x["iq"].float()
     with pytest.raises(ValueError):
         run.step(run.x, SCALE)
+
+
+def test_more_wanted_than_the_table_holds(cuda_lib):
+    """top_k above max_pages * page_size: every row is selected."""
+    import deepseek_v4_sparse_indexer_gb300 as pkg
+    Run(pkg, top_k=512, ratio=1).steps(cuda_lib, 12)
