@@ -770,7 +770,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) topk_row_kernel(const float *__
     pdl_launch_dependents();
     const long long row = blockIdx.x;
     const int u = static_cast<int>(row / Q);
-    const int n_given = n_rows[u];                      // no kernel of this library writes n_rows
+    const int n_given = n_rows[u];                      // ahead of the wait: see pdl_wait on who writes row counts
     const int n = clamp_rows(n_given, N_cap);
     pdl_wait();
     extern __shared__ __align__(16) uint8_t row_smem[];
@@ -903,7 +903,7 @@ __global__ void __launch_bounds__(kSplitThreads) topk_split_kernel(const __grid_
     const long long row = blockIdx.x / a.C;
     const int c = static_cast<int>(blockIdx.x - row * a.C);
     const int u = static_cast<int>(row / a.Q);
-    const int n_given = a.n_rows[u];                    // no kernel of this library writes n_rows
+    const int n_given = a.n_rows[u];                    // ahead of the wait: see pdl_wait on who writes row counts
     const int n = clamp_rows(n_given, a.N_cap);
     pdl_wait();
     __shared__ SelSmem S;
@@ -1173,7 +1173,7 @@ __global__ void __launch_bounds__(kClusterThreads) topk_cluster_kernel(const __g
     const uint32_t q = cluster_rank();
     const long long row = blockIdx.x / C;
     const int u = static_cast<int>(row / a.Q);
-    const int n_given = a.n_rows[u];                    // no kernel of this library writes n_rows
+    const int n_given = a.n_rows[u];                    // ahead of the wait: see pdl_wait on who writes row counts
     const int n = clamp_rows(n_given, a.N_cap);
     pdl_wait();
     if (q == 0 && threadIdx.x == 0 && row % a.Q == 0 && n != n_given)
