@@ -55,8 +55,8 @@ DS4A_DEV void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
 }
 DS4A_DEV void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// Eight E4M3 codes (two words) times a power-of-two scale as eight bf16
-// (four words, dims in order).  E4M3 -> f16 is exact, and so are the scaling
+// Eight E4M3 codes (two words) times a power-of-two scale (1: the codes themselves)
+// as eight bf16 (four words, dims in order).  E4M3 -> f16 is exact, and so are the scaling
 // in fp32 and the rounding to bf16 of a value with at most four significant
 // bits (down to 2^-133, the smallest bf16 subnormal).
 DS4A_DEV void e4m3x8_to_bf16(uint32_t w0, uint32_t w1, float s, uint32_t (&o)[4]) {
@@ -69,15 +69,6 @@ DS4A_DEV void e4m3x8_to_bf16(uint32_t w0, uint32_t w1, float s, uint32_t (&o)[4]
         const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h2));
         o[j] = pack2<false>(f.x * s, f.y * s);
     }
-}
-// 16-byte read-only load that bypasses L1 (rows are read once).  Volatile, so
-// that it stays ahead of the buffer wait that follows it.
-DS4A_DEV uint4 ld_nc_v4(const uint4 *p) {
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
 }
 DS4A_DEV void st_shared_v4(uint32_t addr, const uint32_t (&v)[4]) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
@@ -124,19 +115,6 @@ DS4A_DEV bool wait_drain(uint64_t *bar, uint32_t parity) {
     while (!mbar_try_wait(bar, parity))
         if (globaltimer_ns() - t0 > kWaitLimitNs) return false;
     return true;
-}
-
-DS4A_DEV void tmem_ld16x256_x8(uint32_t taddr, uint32_t (&r)[32]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
-          "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
-          "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
-          "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr));
 }
 
 // Natural log of the sum L 2^M of a head's exponentials: L = 0 for no row, NaN when
