@@ -73,10 +73,11 @@ struct Seq {
 };
 // Lengths of sequence b: negative ones, a sum past 2^31 - 1 and, by sequence, an add
 // above 1 count as 0.
+template <bool BY_SEQ>
 DS4A_DEV Seq seq_of(const PagedPlanArgs &a, int b) {
     Seq s = {a.past[b], a.add[b], true};
     if (s.past < 0) s.past = 0, s.ok = false;
-    if (s.add < 0 || s.past > 0x7fffffff - s.add || (s.add > 1 && (a.form & (DS4A_PLAN_TOKENS_BY_SEQ | DS4A_PLAN_ROWS_BY_SEQ)))) s.add = 0, s.ok = false;
+    if (s.add < 0 || s.past > 0x7fffffff - s.add || (BY_SEQ && s.add > 1)) s.add = 0, s.ok = false;
     return s;
 }
 
@@ -102,6 +103,10 @@ DS4A_DEV void store4(int32_t *p, long long i, int n, const int (&v)[4], bool vec
         if (i + q < n) p[i + q] = v[q];
 }
 
+// BY_SEQ: the token or the row maps are laid out by sequence (a kernel of its own: as
+// a flag of one kernel it cost the other form 0.3 us of 4.8).
+constexpr int kBySeq = DS4A_PLAN_TOKENS_BY_SEQ | DS4A_PLAN_ROWS_BY_SEQ;
+template <bool BY_SEQ>
 __global__ void __launch_bounds__(kThreads, 1) paged_plan_kernel(const __grid_constant__ PagedPlanArgs a) {
     extern __shared__ int smem[];
     const int B = a.B;
@@ -118,7 +123,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_plan_kernel(const __grid_co
     Sums mine = {0, 0, 0};
     bool ok = true;
     for (int b = b0; b < b1; ++b) {
-        const Seq s = seq_of(a, b);
+        const Seq s = seq_of<BY_SEQ>(a, b);
         const int ring = a.ring ? a.ring[b] : b;
         const bool ring_ok = ring >= 0 && ring <= (0x7fffffff >> 7);
         ok = ok && s.ok && (ring_ok || s.add == 0);
@@ -164,7 +169,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_plan_kernel(const __grid_co
         return at < a.n_free ? a.free_pages[at] : -1;
     };
     // The item of map entry x is item `at` of its kind in sequence b; false: no item.
-    const bool tok_by_seq = a.form & DS4A_PLAN_TOKENS_BY_SEQ, row_by_seq = a.form & DS4A_PLAN_ROWS_BY_SEQ;
+    const bool tok_by_seq = BY_SEQ && (a.form & DS4A_PLAN_TOKENS_BY_SEQ), row_by_seq = BY_SEQ && (a.form & DS4A_PLAN_ROWS_BY_SEQ);
     auto item_at = [&](long long x, bool by_seq, const int *cu, int n, int &at) -> bool {
         at = by_seq ? (x < B ? cu[x] : 0) : static_cast<int>(x);
         return by_seq ? x < B && cu[x + 1] > at : x < n;
@@ -283,8 +288,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_plan_kernel(const __grid_co
 cudaError_t launch_paged_plan(PagedPlanArgs a, int num_sms, cudaStream_t s) {
     const size_t smem = (5 * static_cast<size_t>(a.B) + 3) * sizeof(int);
     cudaError_t e = cudaSuccess;
+    void (*kern)(PagedPlanArgs) = a.form & kBySeq ? paged_plan_kernel<true> : paged_plan_kernel<false>;
     if (smem > 40960)
-        e = cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
     // One CTA covers a few thousand tokens and rows; more take every SM, or sixteen
     // CTAs as a cluster (a non-portable size) when the head is updated in place
@@ -294,11 +300,11 @@ cudaError_t launch_paged_plan(PagedPlanArgs a, int num_sms, cudaStream_t s) {
     if (!a.cluster) {
         const long long want = items <= 8LL * kThreads ? 1 : (items + 4 * kThreads - 1) / (4 * kThreads);
         const unsigned grid = static_cast<unsigned>(want < num_sms ? want : num_sms);
-        return launch_k(paged_plan_kernel, dim3(grid), dim3(kThreads), smem, s, a);
+        return launch_k(kern, dim3(grid), dim3(kThreads), smem, s, a);
     }
-    e = cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
-    return launch_k_cluster(paged_plan_kernel, dim3(16), dim3(kThreads), smem, 16, s, a);
+    return launch_k_cluster(kern, dim3(16), dim3(kThreads), smem, 16, s, a);
 }
 
 }  // namespace ds4a
