@@ -176,24 +176,25 @@ class PagedDecodeStep:
 
     x holds, per step: past, add (i32 [U]: tokens in the cache and new ones, 1 or
     0, in any order; what out holds for a sequence without a new token is of no
-    use unless it is empty: zeros), q [U,H,512] and kv [U,512], the
-    projections before norm and rotation (bf16, fp16 or fp32); with top_k also iq
-    [U,64,128] (with rotate_iq=False the indexer's queries as they are scored, bf16
-    and contiguous: a model that does not normalise them turns them itself) and w
-    f32 [U,64].  And, kept by the program: table i32
-    [U,max_pages], free_pages and free_head (updated in place), ring i32 [U] or
-    None, raw fp16 [n_ring,128,512], rows bf16 [n_pages,P,512] (fp8: uint8 codes
-    and row_scale f32 [n_pages,P]), ik bf16 [n_pages,P,128] with top_k, inv_freq f64
-    [n_rot / 2] and the norm weights q_norm, kv_norm, iq_norm, ik_norm (f32 or
-    None) and, where the pooled rows have a norm of their own, row_norm (else they
-    take kv_norm).  style and idx_style (style unless given) say which dims pair in the
-    layer's heads and rows and in the indexer's queries and keys.  A layer of `ratio` tokens per row finishes a row every ratio tokens:
-    pooled [U,512] (and pooled_ik [U,128]) hold the rows finished in this step,
-    new row i of the batch in row i (cu_row says whose) or, with
-    pooled_by_sequence, sequence u's in row u, as ds4a_compressor_pool writes
-    them (a sequence that finishes none: its row is not read).  row_position:
-    "last" or "first", the token of a row whose position its tail (and its key's)
-    is turned by.
+    use unless it is empty: zeros), q [U,H,512] and kv [U,512], the projections
+    before norm and rotation (bf16, fp16 or fp32); with top_k also iq [U,64,128]
+    (with rotate_iq=False the indexer's queries as they are scored, bf16 and
+    contiguous: for a model that does not normalise them) and w f32 [U,64].  And,
+    kept by the program: table i32 [U,max_pages], free_pages and free_head
+    (updated in place), ring i32 [U] or None, raw fp16 [n_ring,128,512], rows bf16
+    [n_pages,P,512] (fp8: uint8 codes and row_scale f32 [n_pages,P]), ik bf16
+    [n_pages,P,128] with top_k, inv_freq f64 [n_rot / 2], the norm weights q_norm,
+    kv_norm, iq_norm, ik_norm (f32 or None) and, where the pooled rows have a norm
+    of their own, row_norm (else they take kv_norm).
+
+    style and idx_style (style unless given) say which dims pair in the layer's
+    heads and rows and in the indexer's queries and keys.  A layer of `ratio`
+    tokens per row finishes a row every ratio tokens: pooled [U,512] (and
+    pooled_ik [U,128]) hold the rows finished in this step, new row i of the batch
+    in row i (cu_row says whose) or, with pooled_by_sequence, sequence u's in row
+    u, as ds4a_compressor_pool writes them (a sequence that finishes none: its row
+    is not read).  row_position: "last" or "first", the token of a row whose
+    position its tail (and its key's) is turned by.
 
     plan -> rotate -> store -> score -> select -> attend, each one call of the
     library (two for the indexer's part); outputs and workspaces are kept, so the
@@ -202,8 +203,8 @@ class PagedDecodeStep:
     """
 
     def __init__(self, U, max_pages, page_size, top_k=512, ratio=4, device="cuda", n_head=B.N_HEAD, fp8=False, eps=1e-6,
-                 style=B.DS4A_ROPE_NEIGHBOURS, pooled_by_sequence=False, row_position="last",
-                 idx_style=None, rotate_iq=True):
+                 style=B.DS4A_ROPE_NEIGHBOURS, pooled_by_sequence=False, row_position="last", idx_style=None,
+                 rotate_iq=True):
         self.U, self.page_size, self.top_k, self.ratio, self.n_head = U, page_size, top_k, ratio, n_head
         self.fp8, self.eps, self.style = fp8, eps, style
         self.idx_style = style if idx_style is None else idx_style

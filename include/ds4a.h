@@ -418,9 +418,9 @@ ds4a_status ds4a_kv_push_raw(const float *kv, uint16_t *raw, int64_t raw_unit_st
  *      out[u,j] = sum_r e^(score[u,r,j] - m) kv[u,r,j] / sum_r e^(score[u,r,j] - m)
  *
  *    and out[u,j] = 0 when no score of the column is finite.  fp32 throughout.
- *    The projections that produce kv and score, the positional bias added to
- *    the scores and the normalisation and RoPE after pooling need trained
- *    weights and are not part of this library; the FP8 round trip is 4c.
+ *    The projections that produce kv and score and the positional bias added
+ *    to the scores need trained weights and are not part of this library; the
+ *    normalisation and RoPE after pooling are 5b, the FP8 round trip is 4c.
  *
  *    kv, score  fp32 [U][ratio][width] (device).    out  fp32 [U][width] (device).
  *    ratio >= 1; width a positive multiple of 4; pointers 16-byte aligned.
@@ -446,8 +446,8 @@ ds4a_status ds4a_compressor_pool(const float *kv, const float *score, int ratio,
  *                    even), saturating at +-448; NaN stays NaN (code 0x7F)
  *
  *    The stored value of element (r,d) is e4m3(rows8[r,d]) * row_scale[r].
- *    The normalisation and RoPE before it need trained weights and are not
- *    part of this library.
+ *    The normalisation and RoPE before it are 5b, which can store the row in
+ *    the same pass.
  *
  *    x          fp32 [n_rows][512] (device), 16-byte aligned.
  *    rows8      uint8 [n_rows][512] (device, written), 16-byte aligned.
@@ -636,7 +636,8 @@ ds4a_status ds4a_qk_norm_rope(const void *q, int q_type, int64_t q_tok_stride, c
  *    scores   fp32 [U][N_cap] (device), written for r < n_rows[u], the others
  *             left as they were.  A row whose page is not one of the pool's gets
  *             -inf and sets DS4A_DEV_BOUNDS.
- *    max_pages * page_size is below 2^30, n_pages * page_size below 2^31.
+ *    max_pages * page_size is below 2^30, n_pages * page_size and the batch's
+ *    128-row tiles, U * ceil(min(N_cap, max_pages * page_size) / 128), below 2^31.
  */
 ds4a_status ds4a_paged_indexer_score(const uint16_t *iq, const float *w, const uint16_t *ik,
                                      int n_pages, int page_size, const int32_t *table,
@@ -680,7 +681,9 @@ ds4a_status ds4a_paged_indexer_score(const uint16_t *iq, const float *w, const u
  *    page is not one of the pool's is masked; each sets DS4A_DEV_BOUNDS.  A row
  *    listed twice counts twice.
  *    q, rows, raw and out are 16-byte aligned.  max_pages * page_size is below
- *    2^30, n_pages * page_size and n_ring * 128 below 2^31.
+ *    2^30, n_pages * page_size and n_ring * 128 below 2^31, as are U * n_head and
+ *    the batch's 48-row tiles (U times the most that a unit can have, times 2 with
+ *    128 heads).
  */
 ds4a_status ds4a_paged_attn_decode(int n_head, const uint16_t *q, const void *rows, int rows_type,
                                    const float *row_scale, int n_pages, int page_size,
