@@ -18,17 +18,17 @@
 // q (64 KB) and P where two of 64 rows did, a gathered tile's copies are issued
 // before the previous one's have landed, and two softmax groups overlap.
 // Five roles' code in turn on one SM also fills its instruction cache: loops are
-// unrolled only as far as it pays (all of them unrolled: 640 ragged units 524-560 us,
-// by where the code happened to lie, now 495).
+// unrolled only as far as it pays (all of them unrolled, 640 ragged units took 6 to
+// 13 % longer, by where the code happened to lie).
 // Measured (GB300): 640 units x 8,192 rows 902 us = 6.1 TB/s, 91 % of the copy
-// bandwidth, 640 ragged units of up to 8,192 rows 495 us; 1,368 units x 512 listed
-// rows 228 us = 4.7 TB/s, random 1 KB rows arriving by cp.async at 31 GB/s per SM
+// bandwidth, 640 ragged units of up to 8,192 rows 500 us; 1,368 units x 512 listed
+// rows 229 us = 4.7 TB/s, random 1 KB rows arriving by cp.async at 31 GB/s per SM
 // of the 34-40 that such a gather alone reaches; 128 heads: 128 units x 1,024
-// listed rows 87 us, each half at its own copy of the rows from L2.  FP8 rows, 48
-// units of up to 4,096: 58 us, 2.2 us a tile, the cycle being longer by the pass that
-// writes the codes out as bf16 (as fp16, one conversion a pair instead of four, 57
-// us: the latency of the pass counts, not its conversions).  A few units are latency: 1 x 1,024 rows
-// 13.4 us with its merge.
+// listed rows 89 us, each half at its own copy of the rows from L2.  FP8 rows, 48
+// units of up to 4,096: 59 us, 152 x 4,096 207 us = 2.3 us a tile, the cycle being
+// longer by the pass that writes the codes out as bf16 (as fp16, one conversion a
+// pair instead of four, 197 us).  A few units are latency: 1 x 1,024 rows 13.2 us
+// with its merge.
 //
 // Roles (one CTA per SM, persistent over its share of the batch's tiles):
 //   lookup   warp 10: turns a tile's rows (listed ones: row number, then page; dense
@@ -74,9 +74,8 @@ constexpr int kPvWarp = 9;                    // warp 9: values UMMA issuer
 constexpr int kLookWarp = 10;                 // warp 10: row lookup
 constexpr int kFirstGatherWarp = 11;
 constexpr int kRowGroups = TR / 4;            // 4-row groups of a tile, dealt round-robin to the gather warps
-// Gather warps: four, three groups each (1,368 x 512 listed rows 228 us, with three
-// 229, five and six 230; 48 units of up to 4,096 FP8 rows 55 us, with three 56, five
-// 57, six 59).
+// Gather warps: four, three groups each (1,368 x 512 listed rows 229 us, with three
+// to six 229-231; 152 x 4,096 FP8 rows 207 us, with six 224).
 constexpr int kGatherWarps = 4;
 constexpr int kGroups = kRowGroups / kGatherWarps;
 static_assert(kRowGroups % kGatherWarps == 0, "whole 4-row groups for every gather warp");

@@ -23,9 +23,10 @@
 // into blocks of consecutive items that the warps of all CTAs take in turn, so
 // that a small step's loads of all four are in flight at once; a lane's next four
 // items are 128 further on, mostly in the same sequence, whose lengths it still
-// holds.  Bound: a small step the latency of launch -> load -> scan -> search ->
-// load -> store, on one CTA; a large one the instructions per item, on every SM.
-// (8 sequences: 4.7 us; 256 with 262k tokens and 66k rows 6.8 us.)
+// holds.  Bound: the latency of launch -> load -> scan -> search -> load -> store; a
+// large step repeats the last three in each warp, on every SM (its items' instructions
+// are a few percent of its time).  (8 sequences: 4.8 us; 256 with 262k tokens and 66k
+// rows 6.9 us.)
 // A large step that updates *free_head in place runs as one cluster instead, whose
 // barrier lies between the reads of the old head and its update.
 //
@@ -294,7 +295,7 @@ cudaError_t launch_paged_plan(PagedPlanArgs a, int num_sms, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     // One CTA covers a few thousand tokens and rows; more take every SM, or sixteen
     // CTAs as a cluster (a non-portable size) when the head is updated in place
-    // (262k tokens and 66k rows: 6.8 us, 13.6 us in place).
+    // (262k tokens and 66k rows: 6.9 us, 13.6 us in place).
     const long long items = static_cast<long long>(a.T_cap) + a.R_cap;
     a.cluster = items > 8LL * kThreads && a.free_head == a.free_head_out;
     if (!a.cluster) {
