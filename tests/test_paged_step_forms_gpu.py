@@ -220,3 +220,25 @@ def test_more_wanted_than_the_table_holds(cuda_lib):
     """top_k above max_pages * page_size: every row is selected."""
     import deepseek_v4_sparse_indexer_gb300 as pkg
     Run(pkg, top_k=512, ratio=1).steps(cuda_lib, 12)
+
+
+def test_on_a_stream_of_its_own(cuda_lib):
+    """Every part of the step runs on the given stream: the results of the default one."""
+    import deepseek_v4_sparse_indexer_gb300 as pkg
+    runs = [Run(pkg, by_seq=True, seed=3) for _ in range(2)]
+    side = torch.cuda.Stream()
+    past = [0] * U
+    for i in range(9):
+        add = [(u + i) % 3 > 0 for u in range(U)]
+        for run in runs:
+            run.draw()
+            run.x["past"].copy_(ints(past)), run.x["add"].copy_(ints([int(a) for a in add]))
+        torch.cuda.synchronize()
+        runs[0].step(runs[0].x, SCALE)
+        runs[1].step(runs[1].x, SCALE, stream=side)
+        torch.cuda.synchronize()
+        live = [u for u in range(U) if add[u]]
+        assert torch.equal(runs[0].step.out[live], runs[1].step.out[live])
+        assert torch.equal(runs[0].step.idx[live], runs[1].step.idx[live])
+        past = [p + int(a) for p, a in zip(past, add)]
+    assert cuda_lib.ds4a_get_device_status() == (0, 0)
