@@ -15,6 +15,9 @@ from ._binding import (Ds4aError, load, ds4a_version, ds4a_workspace_bytes, ds4a
                        ds4a_sparse_attn_prefill_heads, ds4a_dense_attn_decode_heads, ds4a_rows_to_fp8,
                        ds4a_sparse_attn_decode_fp8, ds4a_sparse_attn_prefill_fp8, ds4a_indexer_topk,
                        ds4a_paged_plan, ds4a_qk_norm_rope, ds4a_paged_indexer_score, ds4a_paged_attn_decode,
+                       ds4a_paged_block_keys, ds4a_paged_block_score, ds4a_paged_attn_blocks, ds4a_paged_attn_mass,
+                       ds4a_paged_evict, ds4a_add_rms_norm, DS4A_OP_PAGED_ATTN_BLOCKS, DS4A_OP_PAGED_EVICT,
+                       DS4A_SCALE_POW2, DS4A_SCALE_MAX,
                        DS4A_OP_PAGED_ATTN_DECODE, DS4A_PLAN_TOKENS_BY_SEQ, DS4A_PLAN_ROWS_BY_SEQ, DS4A_PLAN_FIRST_POS,
                        DS4A_OP_FLAG_128_HEADS, DS4A_ROPE_NEIGHBOURS, DS4A_ROPE_HALVES)
 from .step import DecodeStep, PrefillStep, DenseStep, ProducerStep, PagedDecodeStep, DEFAULT_SCALE
@@ -25,6 +28,9 @@ __all__ = ["Ds4aError", "load", "ds4a_version", "ds4a_workspace_bytes", "ds4a_ge
            "ds4a_sparse_attn_decode_heads", "ds4a_sparse_attn_prefill_heads", "ds4a_dense_attn_decode_heads",
            "ds4a_rows_to_fp8", "ds4a_sparse_attn_decode_fp8", "ds4a_sparse_attn_prefill_fp8", "ds4a_indexer_topk",
            "ds4a_paged_plan", "ds4a_qk_norm_rope", "ds4a_paged_indexer_score", "ds4a_paged_attn_decode",
+           "ds4a_paged_block_keys", "ds4a_paged_block_score", "ds4a_paged_attn_blocks", "ds4a_paged_attn_mass",
+           "ds4a_paged_evict", "ds4a_add_rms_norm", "DS4A_OP_PAGED_ATTN_BLOCKS", "DS4A_OP_PAGED_EVICT",
+           "DS4A_SCALE_POW2", "DS4A_SCALE_MAX",
            "DS4A_OP_PAGED_ATTN_DECODE", "DS4A_PLAN_TOKENS_BY_SEQ", "DS4A_PLAN_ROWS_BY_SEQ", "DS4A_PLAN_FIRST_POS",
            "DS4A_OP_FLAG_128_HEADS", "DS4A_ROPE_NEIGHBOURS", "DS4A_ROPE_HALVES",
            "DecodeStep", "PrefillStep", "DenseStep", "ProducerStep", "PagedDecodeStep",

@@ -29,9 +29,14 @@ DS4A_OP_SPARSE_ATTN_PREFILL = 3
 DS4A_OP_DENSE_ATTN_DECODE = 4
 DS4A_OP_INDEXER_TOPK = 5
 DS4A_OP_PAGED_ATTN_DECODE = 6
+DS4A_OP_PAGED_ATTN_BLOCKS = 7
+DS4A_OP_PAGED_EVICT = 8
 DS4A_OP_FLAG_128_HEADS = 0x100
 DS4A_BF16, DS4A_F16, DS4A_F32, DS4A_E4M3 = 0, 1, 2, 3
 DS4A_ROPE_NEIGHBOURS, DS4A_ROPE_HALVES = 0, 1
+DS4A_LIST_ROWS, DS4A_LIST_BLOCKS = 0, 1
+DS4A_SCALE_POW2, DS4A_SCALE_MAX = 0, 1
+DS4A_MAX_NORM_DIM = 16384
 DS4A_MIN_PAGE, DS4A_MAX_PAGE, DS4A_MAX_PLAN_SEQS = 8, 4096, 8192
 DS4A_PLAN_TOKENS_BY_SEQ, DS4A_PLAN_ROWS_BY_SEQ, DS4A_PLAN_FIRST_POS = 1, 2, 4
 
@@ -45,7 +50,8 @@ EXPORTS = ("ds4a_strerror", "ds4a_version", "ds4a_workspace_bytes", "ds4a_get_de
            "ds4a_sparse_attn_decode_heads", "ds4a_sparse_attn_prefill_heads", "ds4a_dense_attn_decode_heads",
            "ds4a_rows_to_fp8", "ds4a_sparse_attn_decode_fp8", "ds4a_sparse_attn_prefill_fp8", "ds4a_indexer_topk",
            "ds4a_paged_plan", "ds4a_paged_plan_form", "ds4a_qk_norm_rope", "ds4a_paged_indexer_score",
-           "ds4a_paged_attn_decode")
+           "ds4a_paged_attn_decode", "ds4a_paged_block_keys", "ds4a_paged_block_score", "ds4a_paged_attn_blocks",
+           "ds4a_paged_attn_mass", "ds4a_paged_evict", "ds4a_add_rms_norm")
 DS4A_TOPK_NOALLOC_SCRATCH_BYTES = 8 << 20
 DS4A_MAX_TOP_K = 2048
 
@@ -135,6 +141,22 @@ def load(build_if_missing: bool = True):
     L.ds4a_paged_attn_decode.argtypes = [_i32, _vp, _vp, _i32, _vp, _i32, _i32, _vp, _i64, _i32, _vp, _vp, _vp, _i32,
                                          _vp, _i32, _vp, _vp, _f32, _vp, _vp, _i32, _vp, _sz, _vp]
     L.ds4a_paged_attn_decode.restype = _i32
+    L.ds4a_paged_block_keys.argtypes = [_vp, _i32, _i32, _vp, _i64, _i32, _vp, _vp, _vp, _vp, _vp, _i32, _vp]
+    L.ds4a_paged_block_keys.restype = _i32
+    L.ds4a_paged_block_score.argtypes = [_vp, _vp, _vp, _i32, _vp, _i64, _i32, _vp, _i32, _i32, _vp, _i32, _i32, _vp]
+    L.ds4a_paged_block_score.restype = _i32
+    L.ds4a_paged_attn_blocks.argtypes = L.ds4a_paged_attn_decode.argtypes
+    L.ds4a_paged_attn_blocks.restype = _i32
+    L.ds4a_paged_attn_mass.argtypes = [_i32, _vp, _vp, _i32, _vp, _i32, _i32, _vp, _i64, _i32, _vp, _i32, _vp, _vp, _i32,
+                                       _f32, _vp, _vp, _i64, _i32, _vp]
+    L.ds4a_paged_attn_mass.restype = _i32
+    L.ds4a_paged_evict.argtypes = [_vp, _i32, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _i32, _i32, _i32,
+                                   _i32, _i32, _vp, _i32, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                   _sz, _vp]
+    L.ds4a_paged_evict.restype = _i32
+    L.ds4a_add_rms_norm.argtypes = [_vp, _i32, _i64, _vp, _i32, _i64, _vp, _i64, _vp, _f32, _vp, _i32, _vp, _vp, _i32,
+                                    _i32, _vp, _i32, _i32, _vp]
+    L.ds4a_add_rms_norm.restype = _i32
     _lib = L
     return L
 
@@ -683,24 +705,15 @@ def ds4a_paged_indexer_score(iq, w, ik, table, n_rows, scores, stream=None):
             table.data_ptr(), stride, max_pages, n_rows.data_ptr(), scores.data_ptr(), U, N_cap)
 
 
-def ds4a_paged_attn_decode(q, rows, table, n_rows, raw, n_raw, scale, out, lse=None, ws=None, idx=None, count=None,
-                           row_scale=None, ring=None, stream=None):
-    """Attention of one new token per unit over paged rows and the raw window: q
-    bf16 [U,H,512] (H = 64 or 128); rows bf16 [n_pages,P,512], or uint8 E4M3
-    codes with row_scale f32 [n_pages,P]; table i32 [U,max_pages]; n_rows i32
-    [U]; raw fp16 [n_ring,128,512]; n_raw i32 [U]; ring i32 [U] or None (ring u);
-    idx i32 [U,top_k] and count i32 [U]: the listed rows only, None: all rows;
-    out bf16 [U,H,512]; lse f32 [U,H] or None; ws uint8 workspace of
-    ds4a_workspace_bytes(DS4A_OP_PAGED_ATTN_DECODE, U, 1, max_pages * P, top_k)."""
+def _paged_rows(q, rows, row_scale, table, n_rows, idx, count):
+    """What the attention calls over paged rows share: (device, U, H, the arguments
+    from n_head to n_rows, those of the list)."""
     dev = _device_index(q, "q")
     if q.dtype is not _BF16 or q.dim() != 3 or not q.is_contiguous():
         raise ValueError("q: contiguous bf16 [U, H, 512]")
     U, H, width = q.shape
     if width != HEAD_DIM:
         raise ValueError("q: contiguous bf16 [U, H, 512]")
-    if out.dtype is not _BF16 or out.get_device() != dev or out.numel() != U * H * HEAD_DIM \
-            or not out.is_contiguous():
-        raise ValueError("out: contiguous bf16 [U, H, 512]")
     fp8 = rows.dtype is _U8
     if not (fp8 or rows.dtype is _BF16) or rows.get_device() != dev or rows.dim() != 3 \
             or not rows.is_contiguous():
@@ -711,31 +724,234 @@ def ds4a_paged_attn_decode(q, rows, table, n_rows, raw, n_raw, scale, out, lse=N
     if fp8 and (row_scale is None or row_scale.dtype is not _F32 or row_scale.get_device() != dev
                 or row_scale.numel() != n_pages * page_size or not row_scale.is_contiguous()):
         raise ValueError("row_scale: contiguous float32 [n_pages, page_size]")
-    if raw.dtype is not torch.float16 or raw.get_device() != dev or raw.dim() != 3 or raw.shape[1:] != (N_SWA, HEAD_DIM) \
-            or not raw.is_contiguous():
-        raise ValueError("raw: contiguous fp16 [n_ring, 128, 512]")
-    n_ring = raw.shape[0]
     stride, max_pages = _table_stride(table, U, dev)
-    _req_ints(dev, ("n_rows", n_rows, U), ("n_raw", n_raw, U))
-    if ring is not None:
-        _req_ints(dev, ("ring", ring, U))
-    elif n_ring < U:
-        raise ValueError("raw: a ring per unit, or give ring")
+    _req_ints(dev, ("n_rows", n_rows, U))
     top_k = 0
     if (idx is None) != (count is None):
         raise ValueError("idx and count go together")
     if idx is not None:
         top_k = idx.shape[-1]
         _req_ints(dev, ("idx", idx, U * top_k), ("count", count, U))
+    return dev, U, H, (H, q.data_ptr(), rows.data_ptr(), DS4A_E4M3 if fp8 else DS4A_BF16, row_scale.data_ptr() if fp8 else None,
+                       n_pages, page_size, table.data_ptr(), stride, max_pages, n_rows.data_ptr()), \
+        (_opt(idx), _opt(count), top_k)
+
+
+def _workspace(ws, dev):
+    if ws is None:
+        return None, 0
+    if ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError("ws: a contiguous tensor on the same device")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def _paged_attn(name, q, rows, table, n_rows, raw, n_raw, scale, out, lse, ws, idx, count, row_scale, ring, stream):
+    dev, U, H, lead, lists = _paged_rows(q, rows, row_scale, table, n_rows, idx, count)
+    if out.dtype is not _BF16 or out.get_device() != dev or out.numel() != U * H * HEAD_DIM \
+            or not out.is_contiguous():
+        raise ValueError("out: contiguous bf16 [U, H, 512]")
+    if raw.dtype is not torch.float16 or raw.get_device() != dev or raw.dim() != 3 or raw.shape[1:] != (N_SWA, HEAD_DIM) \
+            or not raw.is_contiguous():
+        raise ValueError("raw: contiguous fp16 [n_ring, 128, 512]")
+    n_ring = raw.shape[0]
+    _req_ints(dev, ("n_raw", n_raw, U))
+    if ring is not None:
+        _req_ints(dev, ("ring", ring, U))
+    elif n_ring < U:
+        raise ValueError("raw: a ring per unit, or give ring")
     if lse is not None and (lse.dtype is not _F32 or lse.get_device() != dev or lse.numel() != U * H
                             or not lse.is_contiguous()):
         raise ValueError("lse: contiguous float32 [U, H]")
-    ws_ptr, ws_bytes = None, 0
-    if ws is not None:
-        if ws.get_device() != dev or not ws.is_contiguous():
-            raise ValueError("ws: a contiguous tensor on the same device")
-        ws_ptr, ws_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
-    _launch(dev, stream, "ds4a_paged_attn_decode", H, q.data_ptr(), rows.data_ptr(), DS4A_E4M3 if fp8 else DS4A_BF16,
-            row_scale.data_ptr() if fp8 else None, n_pages, page_size, table.data_ptr(), stride, max_pages,
-            n_rows.data_ptr(), _opt(idx), _opt(count), top_k, raw.data_ptr(), n_ring, _opt(ring), n_raw.data_ptr(), scale,
+    ws_ptr, ws_bytes = _workspace(ws, dev)
+    _launch(dev, stream, name, *lead, *lists, raw.data_ptr(), n_ring, _opt(ring), n_raw.data_ptr(), scale,
             out.data_ptr(), _opt(lse), U, ws_ptr, ws_bytes)
+
+
+def ds4a_paged_attn_decode(q, rows, table, n_rows, raw, n_raw, scale, out, lse=None, ws=None, idx=None, count=None,
+                           row_scale=None, ring=None, stream=None):
+    """Attention of one new token per unit over paged rows and the raw window: q
+    bf16 [U,H,512] (H = 64 or 128); rows bf16 [n_pages,P,512], or uint8 E4M3
+    codes with row_scale f32 [n_pages,P]; table i32 [U,max_pages]; n_rows i32
+    [U]; raw fp16 [n_ring,128,512]; n_raw i32 [U]; ring i32 [U] or None (ring u);
+    idx i32 [U,top_k] and count i32 [U]: the listed rows only, None: all rows;
+    out bf16 [U,H,512]; lse f32 [U,H] or None; ws uint8 workspace of
+    ds4a_workspace_bytes(DS4A_OP_PAGED_ATTN_DECODE, U, 1, max_pages * P, top_k)."""
+    _paged_attn("ds4a_paged_attn_decode", q, rows, table, n_rows, raw, n_raw, scale, out, lse, ws, idx, count, row_scale,
+                ring, stream)
+
+
+def ds4a_paged_attn_blocks(q, rows, table, n_rows, block_idx, block_count, raw, n_raw, scale, out, lse=None, ws=None,
+                           row_scale=None, ring=None, stream=None):
+    """ds4a_paged_attn_decode over the rows of listed blocks (pages of the unit's
+    table): block_idx i32 [U,top_k], block_count i32 [U]; ws uint8 workspace of
+    ds4a_workspace_bytes(DS4A_OP_PAGED_ATTN_BLOCKS, U, 1, top_k * P, 0)."""
+    if block_idx is None or block_count is None:
+        raise ValueError("block_idx and block_count: a list of blocks per unit")
+    _paged_attn("ds4a_paged_attn_blocks", q, rows, table, n_rows, raw, n_raw, scale, out, lse, ws, block_idx, block_count,
+                row_scale, ring, stream)
+
+
+def ds4a_paged_attn_mass(q, rows, table, n_rows, scale, lse, mass, idx=None, count=None, blocks=False, row_scale=None,
+                         stream=None):
+    """Adds the weights that an attention gave each row, exp(scale q.x - lse) summed
+    over the plane's 64 heads, to mass f32 [H/64,U,>= max_pages * P] (updated).
+    lse f32 [U,H] from that attention; the other arguments are its own, idx and
+    count naming blocks with blocks=True."""
+    dev, U, H, lead, lists = _paged_rows(q, rows, row_scale, table, n_rows, idx, count)
+    if lse.dtype is not _F32 or lse.get_device() != dev or lse.numel() != U * H or not lse.is_contiguous():
+        raise ValueError("lse: contiguous float32 [U, H]")
+    if mass.dtype is not _F32 or mass.get_device() != dev or mass.dim() != 3 or not mass.is_contiguous() \
+            or mass.shape[0] * N_HEAD != H or mass.shape[1] != U:
+        raise ValueError("mass: contiguous float32 [H / 64, U, rows]")
+    _launch(dev, stream, "ds4a_paged_attn_mass", *lead, DS4A_LIST_BLOCKS if blocks else DS4A_LIST_ROWS, *lists, scale,
+            lse.data_ptr(), mass.data_ptr(), mass.shape[2], U)
+
+
+def _block_keys(block_keys, n_pages, dev):
+    if block_keys.dtype is not _BF16 or block_keys.get_device() != dev or block_keys.dim() != 2 \
+            or block_keys.shape[1] != IDX_DIM or not block_keys.is_contiguous() \
+            or (n_pages is not None and block_keys.shape[0] != n_pages):
+        raise ValueError("block_keys: contiguous bf16 [n_pages, 128]")
+
+
+def ds4a_paged_block_keys(ik, table, n_rows, block_keys, n_blocks, first_row=None, cu_row=None, stream=None):
+    """Mean indexer key of each block (page) that got rows: ik bf16 [n_pages,P,128];
+    table i32 [B,max_pages]; n_rows i32 [B]; block_keys bf16 [n_pages,128]
+    (updated); n_blocks i32 [B] (written).  The rows from first_row i32 [B] on, or
+    the last cu_row[b+1] - cu_row[b] (cu_row i32 [B+1], the plan's), or all."""
+    dev = _device_index(ik, "ik")
+    if ik.dtype is not _BF16 or ik.dim() != 3 or ik.shape[2] != IDX_DIM or not ik.is_contiguous():
+        raise ValueError("ik: contiguous bf16 [n_pages, page_size, 128]")
+    n_pages, page_size, _ = ik.shape
+    _block_keys(block_keys, n_pages, dev)
+    B = n_rows.numel()
+    stride, max_pages = _table_stride(table, B, dev)
+    _req_ints(dev, ("n_rows", n_rows, B), ("n_blocks", n_blocks, B))
+    if first_row is not None:
+        _req_ints(dev, ("first_row", first_row, B))
+    if cu_row is not None:
+        _req_ints(dev, ("cu_row", cu_row, B + 1))
+    _launch(dev, stream, "ds4a_paged_block_keys", ik.data_ptr(), n_pages, page_size, table.data_ptr(), stride, max_pages,
+            n_rows.data_ptr(), _opt(first_row), _opt(cu_row), block_keys.data_ptr(), n_blocks.data_ptr(), B)
+
+
+def ds4a_paged_block_score(iq, w, block_keys, table, n_blocks, scores, n_first=0, n_last=0, stream=None):
+    """Indexer scores of one query per unit over its blocks' mean keys: iq bf16
+    [U,1,64,128]; w f32 [U,1,64]; block_keys bf16 [n_pages,128]; table i32
+    [U,max_pages]; n_blocks i32 [U]; scores f32 [U,1,NB_cap] (written for b <
+    n_blocks[u]; +inf for the first n_first and last n_last blocks)."""
+    dev = _device_index(iq, "iq")
+    if scores.dim() != 3:
+        raise ValueError("scores: [U, 1, NB_cap]")
+    U, one, NB_cap = scores.shape
+    if one != 1 or scores.dtype is not _F32 or scores.get_device() != dev or not scores.is_contiguous():
+        raise ValueError("scores: contiguous float32 [U, 1, NB_cap]")
+    if iq.dtype is not _BF16 or iq.numel() != U * N_IDX_HEAD * IDX_DIM or not iq.is_contiguous():
+        raise ValueError("iq: contiguous bf16 [U, 1, 64, 128]")
+    if w.dtype is not _F32 or w.get_device() != dev or w.numel() != U * N_IDX_HEAD or not w.is_contiguous():
+        raise ValueError("w: contiguous float32 [U, 1, 64]")
+    _block_keys(block_keys, None, dev)
+    _req_ints(dev, ("n_blocks", n_blocks, U))
+    stride, max_pages = _table_stride(table, U, dev)
+    _launch(dev, stream, "ds4a_paged_block_score", iq.data_ptr(), w.data_ptr(), block_keys.data_ptr(), block_keys.shape[0],
+            table.data_ptr(), stride, max_pages, n_blocks.data_ptr(), n_first, n_last, scores.data_ptr(), U, NB_cap)
+
+
+def ds4a_paged_evict(mass, n_rows, table, rows, free_pages, free_head, keep, limit, mass_out, n_rows_out, table_out,
+                     free_pages_out, free_head_out, ws, first=0, recent=0, row_scale=None, ik=None, n_shared=None,
+                     gone=None, gone_out=None, first_row=None, stream=None):
+    """Cuts every sequence of more than `limit` rows to `keep`: its first `first`, its
+    last `recent` and those of the greatest mass, copied to pages of the free list;
+    the old pages go back to it.  mass f32 [planes,B,>= max_pages * P]; n_rows i32
+    [B]; table i32 [B,max_pages]; rows bf16 or uint8 [n_pages,P,512] with row_scale
+    f32 [n_pages,P], ik bf16 [n_pages,P,128] or None (all updated); free_pages i32
+    [n_free], free_head i32 [1]; each *_out may be its input; n_shared, gone,
+    gone_out, first_row i32 [B] or None; ws uint8 workspace of
+    ds4a_workspace_bytes(DS4A_OP_PAGED_EVICT, B, 1, max_pages * P, keep)."""
+    dev = _device_index(mass, "mass")
+    B, n_free = n_rows.numel(), free_pages.numel()
+    for t in (mass, mass_out):
+        if t.dtype is not _F32 or t.get_device() != dev or t.dim() != 3 or t.shape != mass.shape or t.shape[1] != B \
+                or not t.is_contiguous():
+            raise ValueError("mass, mass_out: contiguous float32 [planes, B, rows]")
+    fp8 = rows.dtype is _U8
+    if not (fp8 or rows.dtype is _BF16) or rows.get_device() != dev or rows.dim() != 3 or rows.shape[2] != HEAD_DIM \
+            or not rows.is_contiguous():
+        raise ValueError("rows: contiguous bf16 or uint8 [n_pages, page_size, 512]")
+    n_pages, page_size, _ = rows.shape
+    if fp8 and (row_scale is None or row_scale.dtype is not _F32 or row_scale.get_device() != dev
+                or row_scale.numel() != n_pages * page_size or not row_scale.is_contiguous()):
+        raise ValueError("row_scale: contiguous float32 [n_pages, page_size]")
+    if ik is not None and (ik.dtype is not _BF16 or ik.get_device() != dev or ik.shape != (n_pages, page_size, IDX_DIM)
+                           or not ik.is_contiguous()):
+        raise ValueError("ik: contiguous bf16 [n_pages, page_size, 128]")
+    stride, max_pages = _table_stride(table, B, dev)
+    if _table_stride(table_out, B, dev) != (stride, max_pages):
+        raise ValueError("table_out: laid out as table")
+    _req_ints(dev, ("n_rows", n_rows, B), ("n_rows_out", n_rows_out, B), ("free_pages", free_pages, n_free),
+              ("free_pages_out", free_pages_out, n_free), ("free_head", free_head, 1), ("free_head_out", free_head_out, 1))
+    for name, t in (("n_shared", n_shared), ("gone", gone), ("gone_out", gone_out), ("first_row", first_row)):
+        if t is not None:
+            _req_ints(dev, (name, t, B))
+    ws_ptr, ws_bytes = _workspace(ws, dev)
+    _launch(dev, stream, "ds4a_paged_evict", mass.data_ptr(), mass.shape[0], mass.shape[2], mass_out.data_ptr(),
+            n_rows.data_ptr(), n_rows_out.data_ptr(), table.data_ptr(), table_out.data_ptr(), stride, max_pages, page_size,
+            n_pages, B, keep, limit, first, recent, rows.data_ptr(), DS4A_E4M3 if fp8 else DS4A_BF16,
+            row_scale.data_ptr() if fp8 else None, _opt(ik), free_pages.data_ptr(), free_pages_out.data_ptr(), n_free,
+            free_head.data_ptr(), free_head_out.data_ptr(), _opt(n_shared), _opt(gone), _opt(gone_out), _opt(first_row),
+            ws_ptr, ws_bytes)
+
+
+# ----------------------------------------------------------------------------
+# Between layers
+# ----------------------------------------------------------------------------
+
+def _norm_rows(t, name, dev, shape):
+    """(address, type, row stride) of [T, D] rows in 16 or 32 bits; nothing for None."""
+    if t is None:
+        return None, 0, 0
+    kind = _TYPES.get(t.dtype, -1)
+    if not DS4A_BF16 <= kind <= DS4A_F32 or t.get_device() != dev or t.shape != shape:
+        raise ValueError(f"{name}: bf16, fp16 or fp32 [T, D] on cuda:{dev}")
+    stride, one = t.stride()
+    if one != 1 and shape[1] > 1:
+        raise ValueError(f"{name}: contiguous rows")
+    return t.data_ptr(), kind, stride if shape[0] > 1 else shape[1]
+
+
+def ds4a_add_rms_norm(x, weight, eps, out=None, residual=None, res_out=None, codes=None, scales=None, group=128,
+                      scale_style=DS4A_SCALE_POW2, n_live=None, stream=None):
+    """h = x + residual; y = h * weight / sqrt(mean h^2 + eps): x [T,D], residual
+    [T,D] or None and res_out [T,D] (h; may be residual) in bf16, fp16 or fp32, rows
+    any stride apart; weight f32 [D] or None; out [T,D] in 16 or 32 bits and / or
+    codes uint8 [T,D] E4M3 with scales f32 [T,ceil(D / group)] (written), a scale
+    for every 32, 64 or 128 elements or (group = 0) for a row; n_live i32 [1] or
+    None: rows from there on are left as they were."""
+    dev = _device_index(x, "x")
+    if x.dim() != 2:
+        raise ValueError("x: [T, D]")
+    T, D = shape = x.shape
+    x_ptr, x_type, x_stride = _norm_rows(x, "x", dev, shape)
+    res_ptr, res_type, res_stride = _norm_rows(residual, "residual", dev, shape)
+    out_ptr, out_type, out_stride = _norm_rows(out, "out", dev, shape)
+    ro_ptr, ro_type, ro_stride = _norm_rows(res_out, "res_out", dev, shape)
+    if out is not None and out_stride != D:
+        raise ValueError("out: contiguous [T, D]")
+    if res_out is not None and (residual is None or ro_type != res_type):
+        raise ValueError("res_out: with a residual, in its type")
+    if weight is not None and (weight.dtype is not _F32 or weight.get_device() != dev or weight.numel() != D
+                               or not weight.is_contiguous()):
+        raise ValueError(f"weight: contiguous float32 [{D}]")
+    if (codes is None) != (scales is None):
+        raise ValueError("codes and scales go together")
+    if codes is not None:
+        if codes.dtype is not _U8 or codes.get_device() != dev or codes.numel() != T * D or not codes.is_contiguous():
+            raise ValueError("codes: contiguous uint8 [T, D]")
+        groups = -(-D // group) if group > 0 else 1
+        if scales.dtype is not _F32 or scales.get_device() != dev or scales.numel() != T * groups \
+                or not scales.is_contiguous():
+            raise ValueError(f"scales: contiguous float32 [T, {groups}]")
+    if n_live is not None:
+        _req_ints(dev, ("n_live", n_live, 1))
+    _launch(dev, stream, "ds4a_add_rms_norm", x_ptr, x_type, x_stride, res_ptr, res_type, res_stride, ro_ptr, ro_stride,
+            _opt(weight), eps, out_ptr, out_type, _opt(codes), _opt(scales), group, scale_style, _opt(n_live), T, D)

@@ -183,7 +183,7 @@ size_t ds4a_workspace_bytes(int op, int U, int Q, int N_cap, int top_k) {
     const int h = (op & DS4A_OP_FLAG_128_HEADS) ? 2 : 1;
     op &= ~DS4A_OP_FLAG_128_HEADS;
     if (h == 2 && op != DS4A_OP_SPARSE_ATTN_DECODE && op != DS4A_OP_SPARSE_ATTN_PREFILL &&
-        op != DS4A_OP_DENSE_ATTN_DECODE && op != DS4A_OP_PAGED_ATTN_DECODE)
+        op != DS4A_OP_DENSE_ATTN_DECODE && op != DS4A_OP_PAGED_ATTN_DECODE && op != DS4A_OP_PAGED_ATTN_BLOCKS)
         return static_cast<size_t>(-1);
     if (static_cast<long long>(U) * h > 0x7fffffffLL) return static_cast<size_t>(-1);
     U *= h;
@@ -209,6 +209,12 @@ size_t ds4a_workspace_bytes(int op, int U, int Q, int N_cap, int top_k) {
         if (top_k < 0 || top_k > DS4A_MAX_TOP_K || !paged_attn_sizes_ok(U, top_k ? top_k : N_cap))
             return static_cast<size_t>(-1);
         return paged_attn_ws_bytes(U / h, h, top_k ? top_k : N_cap);
+    case DS4A_OP_PAGED_ATTN_BLOCKS:
+        if (top_k != 0 || !paged_attn_sizes_ok(U, N_cap)) return static_cast<size_t>(-1);
+        return paged_attn_ws_bytes(U / h, h, N_cap);
+    case DS4A_OP_PAGED_EVICT:
+        if (U > DS4A_MAX_PLAN_SEQS || top_k < 1 || top_k > N_cap || N_cap >= (1 << 30)) return static_cast<size_t>(-1);
+        return evict_ws_bytes(U, top_k, page_shift(DS4A_MIN_PAGE));
     default: return static_cast<size_t>(-1);
     }
 }
@@ -757,34 +763,27 @@ ds4a_status ds4a_paged_indexer_score(const uint16_t *iq, const float *w, const u
     return launch_indexer_score(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? DS4A_OK : DS4A_ECUDA;
 }
 
-ds4a_status ds4a_paged_attn_decode(int n_head, const uint16_t *q, const void *rows, int rows_type,
-                                   const float *row_scale, int n_pages, int page_size, const int32_t *table,
-                                   int64_t table_stride, int max_pages, const int32_t *n_rows, const int32_t *idx,
-                                   const int32_t *count, int top_k, const uint16_t *raw, int n_ring,
-                                   const int32_t *ring, const int32_t *n_raw, float scale, uint16_t *out, float *lse,
-                                   int U, void *ws, size_t ws_bytes, void *stream) {
-    const NvtxRange nvtx_range("ds4a_paged_attn_decode");
-    if (ds4a_status inj = take_injected()) return inj;
+namespace {
+// What the attention calls over paged rows share: the checks and the arguments of the
+// rows and their lists.  list: 0 none (all rows), 1 rows, 2 blocks.
+ds4a_status paged_rows(PagedAttnArgs &a, int n_head, const uint16_t *q, const void *rows, int rows_type,
+                       const float *row_scale, int n_pages, int page_size, const int32_t *table, int64_t table_stride,
+                       int max_pages, const int32_t *n_rows, int list, const int32_t *idx, const int32_t *count,
+                       int top_k, float scale, int U) {
     if (n_head != 64 && n_head != 128) return DS4A_EUNSUPPORTED;
     if (rows_type != DS4A_BF16 && rows_type != DS4A_E4M3) return DS4A_EUNSUPPORTED;
     const int hsplit = n_head / kNHead, shift = page_shift(page_size);
-    if (!q || !rows || !table || !n_rows || !raw || !n_raw || !out || U < 1 || shift < 0) return DS4A_EINVAL;
-    if ((idx == nullptr) != (count == nullptr) || (idx == nullptr) != (top_k == 0)) return DS4A_EINVAL;
-    if (top_k < 0 || top_k > DS4A_MAX_TOP_K || n_pages < 1 || n_ring < 1 || max_pages < 1 || table_stride < max_pages)
+    if (!q || !rows || !table || !n_rows || U < 1 || shift < 0) return DS4A_EINVAL;
+    if ((idx == nullptr) != (list == 0) || (count == nullptr) != (list == 0) || (top_k == 0) != (list == 0)) return DS4A_EINVAL;
+    if (top_k < 0 || top_k > DS4A_MAX_TOP_K || n_pages < 1 || max_pages < 1 || table_stride < max_pages)
         return DS4A_EINVAL;
-    if (!aligned(q, 16) || !aligned(rows, 16) || !aligned(raw, 16) || !aligned(out, 16)) return DS4A_EINVAL;
+    if (!aligned(q, 16) || !aligned(rows, 16)) return DS4A_EINVAL;
     if (rows_type == DS4A_E4M3 && (!row_scale || !aligned(row_scale, 4))) return DS4A_EINVAL;
     if (!(scale == scale)) return DS4A_EINVAL;
     const long long cap = static_cast<long long>(max_pages) << shift, pool = static_cast<long long>(n_pages) << shift;
-    const long long raws = static_cast<long long>(n_ring) * kNSwa;
-    if (cap >= (1LL << 30) || pool >= (1LL << 31) || raws >= (1LL << 31)) return DS4A_EINVAL;
-    const int list_cap = top_k ? top_k : static_cast<int>(cap);
+    if (cap >= (1LL << 30) || pool >= (1LL << 31)) return DS4A_EINVAL;
+    const int list_cap = list == 0 ? static_cast<int>(cap) : list == 1 ? top_k : top_k << shift;
     if (!paged_attn_sizes_ok(static_cast<long long>(U) * hsplit, list_cap)) return DS4A_EINVAL;
-    const size_t need = paged_attn_ws_bytes(U, hsplit, list_cap);
-    if (need && (!ws || ws_bytes < need || !aligned(ws, 256))) return DS4A_EWORKSPACE;
-    DevInfo *di = nullptr;
-    if (ds4a_status st = current_device(&di)) return st;
-    PagedAttnArgs a{};
     a.q = q;
     a.rows = static_cast<const uint16_t *>(rows);
     a.rows8 = rows_type == DS4A_E4M3 ? static_cast<const uint8_t *>(rows) : nullptr;
@@ -798,24 +797,275 @@ ds4a_status ds4a_paged_attn_decode(int n_head, const uint16_t *q, const void *ro
     a.idx = idx;
     a.count = count;
     a.list_cap = list_cap;
+    a.block_lists = list == 2;
+    a.idx_stride = top_k;
+    a.scale = scale;
+    a.U = U;
+    a.hsplit = hsplit;
+    a.tma_rows = !a.rows8 && list != 1;
+    return DS4A_OK;
+}
+bool encode_paged_rows(PagedAttnArgs &a) {
+    const int page_size = 1 << a.page_shift;
+    return encode_row_blocks(&a.tm_q, false, a.q, static_cast<unsigned long long>(a.U) * a.hsplit * kNHead, kNHead) &&
+           (!a.tma_rows || encode_row_groups(&a.tm_rows, false, a.rows, static_cast<unsigned long long>(a.n_pages) << a.page_shift,
+                                             page_size < 16 ? static_cast<unsigned>(page_size) : 16u));
+}
+ds4a_status paged_attn(PagedAttnArgs &a, const uint16_t *raw, int n_ring, const int32_t *ring, const int32_t *n_raw,
+                       uint16_t *out, float *lse, void *ws, size_t ws_bytes, void *stream) {
+    if (!raw || !n_raw || !out || n_ring < 1 || !aligned(raw, 16) || !aligned(out, 16)) return DS4A_EINVAL;
+    const long long raws = static_cast<long long>(n_ring) * kNSwa;
+    if (raws >= (1LL << 31)) return DS4A_EINVAL;
+    const size_t need = paged_attn_ws_bytes(a.U, a.hsplit, a.list_cap);
+    if (need && (!ws || ws_bytes < need || !aligned(ws, 256))) return DS4A_EWORKSPACE;
+    DevInfo *di = nullptr;
+    if (ds4a_status st = current_device(&di)) return st;
     a.raw = raw;
     a.ring = ring;
     a.n_ring = n_ring;
     a.n_raw = n_raw;
-    a.scale = scale;
     a.out = out;
     a.lse = lse;
-    a.U = U;
-    a.hsplit = hsplit;
     a.ws = need ? ws : nullptr;
     a.status = di->status;
-    a.tma_rows = !a.rows8 && !idx;
-    if (!encode_row_blocks(&a.tm_q, false, q, static_cast<unsigned long long>(U) * n_head, kNHead) ||
-        !encode_row_groups(&a.tm_raw, true, raw, static_cast<unsigned long long>(raws), 16) ||
-        (a.tma_rows && !encode_row_groups(&a.tm_rows, false, rows, static_cast<unsigned long long>(pool),
-                                          page_size < 16 ? static_cast<unsigned>(page_size) : 16u)))
+    if (!encode_paged_rows(a) || !encode_row_groups(&a.tm_raw, true, raw, static_cast<unsigned long long>(raws), 16))
         return DS4A_EINVAL;
     return launch_paged_attn(a, di->sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? DS4A_OK : DS4A_ECUDA;
+}
+}  // namespace
+
+ds4a_status ds4a_paged_attn_decode(int n_head, const uint16_t *q, const void *rows, int rows_type,
+                                   const float *row_scale, int n_pages, int page_size, const int32_t *table,
+                                   int64_t table_stride, int max_pages, const int32_t *n_rows, const int32_t *idx,
+                                   const int32_t *count, int top_k, const uint16_t *raw, int n_ring,
+                                   const int32_t *ring, const int32_t *n_raw, float scale, uint16_t *out, float *lse,
+                                   int U, void *ws, size_t ws_bytes, void *stream) {
+    const NvtxRange nvtx_range("ds4a_paged_attn_decode");
+    if (ds4a_status inj = take_injected()) return inj;
+    PagedAttnArgs a{};
+    if (ds4a_status st = paged_rows(a, n_head, q, rows, rows_type, row_scale, n_pages, page_size, table, table_stride,
+                                    max_pages, n_rows, idx || count || top_k ? 1 : 0, idx, count, top_k, scale, U))
+        return st;
+    return paged_attn(a, raw, n_ring, ring, n_raw, out, lse, ws, ws_bytes, stream);
+}
+
+ds4a_status ds4a_paged_attn_blocks(int n_head, const uint16_t *q, const void *rows, int rows_type,
+                                   const float *row_scale, int n_pages, int page_size, const int32_t *table,
+                                   int64_t table_stride, int max_pages, const int32_t *n_rows,
+                                   const int32_t *block_idx, const int32_t *block_count, int top_k,
+                                   const uint16_t *raw, int n_ring, const int32_t *ring, const int32_t *n_raw,
+                                   float scale, uint16_t *out, float *lse, int U, void *ws, size_t ws_bytes,
+                                   void *stream) {
+    const NvtxRange nvtx_range("ds4a_paged_attn_blocks");
+    if (ds4a_status inj = take_injected()) return inj;
+    PagedAttnArgs a{};
+    if (ds4a_status st = paged_rows(a, n_head, q, rows, rows_type, row_scale, n_pages, page_size, table, table_stride,
+                                    max_pages, n_rows, 2, block_idx, block_count, top_k, scale, U))
+        return st;
+    return paged_attn(a, raw, n_ring, ring, n_raw, out, lse, ws, ws_bytes, stream);
+}
+
+ds4a_status ds4a_paged_attn_mass(int n_head, const uint16_t *q, const void *rows, int rows_type,
+                                 const float *row_scale, int n_pages, int page_size, const int32_t *table,
+                                 int64_t table_stride, int max_pages, const int32_t *n_rows, int list_kind,
+                                 const int32_t *idx, const int32_t *count, int top_k, float scale, const float *lse,
+                                 float *mass, int64_t mass_stride, int U, void *stream) {
+    const NvtxRange nvtx_range("ds4a_paged_attn_mass");
+    if (ds4a_status inj = take_injected()) return inj;
+    if (list_kind != DS4A_LIST_ROWS && list_kind != DS4A_LIST_BLOCKS) return DS4A_EINVAL;
+    const int list = !(idx || count || top_k) ? 0 : list_kind == DS4A_LIST_BLOCKS ? 2 : 1;
+    PagedAttnArgs a{};
+    if (ds4a_status st = paged_rows(a, n_head, q, rows, rows_type, row_scale, n_pages, page_size, table, table_stride,
+                                    max_pages, n_rows, list, idx, count, top_k, scale, U))
+        return st;
+    if (!lse || !mass || !aligned(lse, 4) || !aligned(mass, 4) || mass_stride < a.N_cap || mass_stride >= (1LL << 40))
+        return DS4A_EINVAL;
+    DevInfo *di = nullptr;
+    if (ds4a_status st = current_device(&di)) return st;
+    a.lse = const_cast<float *>(lse);                      // read only
+    a.mass = mass;
+    a.mass_stride = mass_stride;
+    a.status = di->status;
+    if (!encode_paged_rows(a)) return DS4A_EINVAL;
+    return launch_paged_attn_mass(a, di->sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? DS4A_OK : DS4A_ECUDA;
+}
+
+ds4a_status ds4a_paged_block_keys(const uint16_t *ik, int n_pages, int page_size, const int32_t *table,
+                                  int64_t table_stride, int max_pages, const int32_t *n_rows,
+                                  const int32_t *first_row, const int32_t *cu_row, uint16_t *block_keys,
+                                  int32_t *n_blocks, int B, void *stream) {
+    const NvtxRange nvtx_range("ds4a_paged_block_keys");
+    if (ds4a_status inj = take_injected()) return inj;
+    const int shift = page_shift(page_size);
+    if (!ik || !table || !n_rows || !block_keys || !n_blocks || shift < 0 || (first_row && cu_row)) return DS4A_EINVAL;
+    if (B < 1 || B > DS4A_MAX_PLAN_SEQS || n_pages < 1 || max_pages < 1 || table_stride < max_pages) return DS4A_EINVAL;
+    if (!aligned(ik, 16) || !aligned(block_keys, 16)) return DS4A_EINVAL;
+    if (static_cast<long long>(max_pages) << shift >= (1LL << 30) || static_cast<long long>(n_pages) << shift >= (1LL << 31))
+        return DS4A_EINVAL;
+    DevInfo *di = nullptr;
+    if (ds4a_status st = current_device(&di)) return st;
+    BlockKeysArgs a{};
+    a.ik = ik;
+    a.n_pages = n_pages;
+    a.shift = shift;
+    a.table = table;
+    a.table_stride = table_stride;
+    a.max_pages = max_pages;
+    a.n_rows = n_rows;
+    a.first_row = first_row;
+    a.cu_row = cu_row;
+    a.block_keys = block_keys;
+    a.n_blocks = n_blocks;
+    a.B = B;
+    a.status = di->status;
+    return launch_block_keys(a, di->sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? DS4A_OK : DS4A_ECUDA;
+}
+
+ds4a_status ds4a_paged_block_score(const uint16_t *iq, const float *w, const uint16_t *block_keys, int n_pages,
+                                   const int32_t *table, int64_t table_stride, int max_pages, const int32_t *n_blocks,
+                                   int n_first, int n_last, float *scores, int U, int NB_cap, void *stream) {
+    const NvtxRange nvtx_range("ds4a_paged_block_score");
+    if (ds4a_status inj = take_injected()) return inj;
+    if (!iq || !w || !block_keys || !table || !n_blocks || !scores) return DS4A_EINVAL;
+    if (U < 1 || U > (1 << 24) || NB_cap < 1 || n_pages < 1 || max_pages < 1 || table_stride < max_pages || n_first < 0 ||
+        n_last < 0)
+        return DS4A_EINVAL;
+    if (!aligned(iq, 16) || !aligned(block_keys, 16) || !aligned(w, 4) || !aligned(scores, 4)) return DS4A_EINVAL;
+    const int lim = max_pages < NB_cap ? max_pages : NB_cap;
+    if (lim >= (1 << 30) || U * block_score_tiles(lim) >= (1LL << 31)) return DS4A_EINVAL;
+    DevInfo *di = nullptr;
+    if (ds4a_status st = current_device(&di)) return st;
+    BlockScoreArgs a{};
+    a.iq = iq;
+    a.w = w;
+    a.block_keys = block_keys;
+    a.n_pages = n_pages;
+    a.table = table;
+    a.table_stride = table_stride;
+    a.n_blocks = n_blocks;
+    a.scores = scores;
+    a.U = U;
+    a.NB_cap = NB_cap;
+    a.lim = lim;
+    a.n_first = n_first;
+    a.n_last = n_last;
+    a.status = di->status;
+    return launch_block_score(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? DS4A_OK : DS4A_ECUDA;
+}
+
+ds4a_status ds4a_paged_evict(const float *mass, int n_planes, int64_t mass_stride, float *mass_out,
+                             const int32_t *n_rows, int32_t *n_rows_out, const int32_t *table, int32_t *table_out,
+                             int64_t table_stride, int max_pages, int page_size, int n_pages, int B, int keep,
+                             int limit, int first, int recent, void *rows, int rows_type, float *row_scale,
+                             uint16_t *ik, const int32_t *free_pages, int32_t *free_pages_out, int n_free,
+                             const int32_t *free_head, int32_t *free_head_out, const int32_t *n_shared,
+                             const int32_t *gone, int32_t *gone_out, int32_t *first_row, void *ws, size_t ws_bytes,
+                             void *stream) {
+    const NvtxRange nvtx_range("ds4a_paged_evict");
+    if (ds4a_status inj = take_injected()) return inj;
+    if (rows_type != DS4A_BF16 && rows_type != DS4A_E4M3) return DS4A_EUNSUPPORTED;
+    const int shift = page_shift(page_size);
+    if (!mass || !mass_out || !n_rows || !n_rows_out || !table || !table_out || !rows || !free_head || !free_head_out ||
+        shift < 0 || n_free < 0 || (n_free > 0 && (!free_pages || !free_pages_out)) || (gone && !gone_out))
+        return DS4A_EINVAL;
+    if (n_planes < 1 || n_planes > 16 || B < 1 || B > DS4A_MAX_PLAN_SEQS || n_pages < 1 || max_pages < 1 ||
+        table_stride < max_pages)
+        return DS4A_EINVAL;
+    const long long cap = static_cast<long long>(max_pages) << shift, pool = static_cast<long long>(n_pages) << shift;
+    if (cap >= (1LL << 30) || pool >= (1LL << 31) || mass_stride < cap || mass_stride >= (1LL << 40)) return DS4A_EINVAL;
+    if (keep < 1 || keep > cap || limit < keep || first < 0 || recent < 0 || static_cast<long long>(first) + recent > keep)
+        return DS4A_EINVAL;
+    if (!aligned(rows, 16) || (ik && !aligned(ik, 16)) || !aligned(mass, 4) || !aligned(mass_out, 4)) return DS4A_EINVAL;
+    if (rows_type == DS4A_E4M3 && (!row_scale || !aligned(row_scale, 4))) return DS4A_EINVAL;
+    if (!ws || ws_bytes < evict_ws_bytes(B, keep, shift) || !aligned(ws, 256)) return DS4A_EWORKSPACE;
+    DevInfo *di = nullptr;
+    if (ds4a_status st = current_device(&di)) return st;
+    EvictArgs a{};
+    a.mass = mass;
+    a.mass_out = mass_out;
+    a.n_planes = n_planes;
+    a.mass_stride = mass_stride;
+    a.n_rows = n_rows;
+    a.n_rows_out = n_rows_out;
+    a.table = table;
+    a.table_out = table_out;
+    a.table_stride = table_stride;
+    a.max_pages = max_pages;
+    a.shift = shift;
+    a.n_pages = n_pages;
+    a.B = B;
+    a.keep = keep;
+    a.limit = limit;
+    a.first = first;
+    a.recent = recent;
+    a.rows = rows;
+    a.fp8 = rows_type == DS4A_E4M3;
+    a.row_scale = row_scale;
+    a.ik = ik;
+    a.free_pages = free_pages;
+    a.free_out = free_pages_out;
+    a.n_free = n_free;
+    a.free_head = free_head;
+    a.head_out = free_head_out;
+    a.n_shared = n_shared;
+    a.gone = gone;
+    a.gone_out = gone_out;
+    a.first_row = first_row;
+    a.ws = ws;
+    a.status = di->status;
+    return launch_evict(a, di->sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? DS4A_OK : DS4A_ECUDA;
+}
+
+ds4a_status ds4a_add_rms_norm(const void *x, int x_type, int64_t x_stride, const void *res, int res_type,
+                              int64_t res_stride, void *res_out, int64_t res_out_stride, const float *weight, float eps,
+                              void *out, int out_type, uint8_t *codes, float *scales, int group, int scale_style,
+                              const int32_t *n_live, int T, int D, void *stream) {
+    const NvtxRange nvtx_range("ds4a_add_rms_norm");
+    if (ds4a_status inj = take_injected()) return inj;
+    if (T < 0) return DS4A_EINVAL;
+    if (T == 0) return DS4A_OK;                            // an empty tensor may have no address
+    if (!x || (!out && !codes) || (res_out && !res) || (codes && !scales)) return DS4A_EINVAL;
+    if (D < 8 || D % 8 || D > DS4A_MAX_NORM_DIM) return DS4A_EUNSUPPORTED;
+    auto known = [](int type) { return type == DS4A_BF16 || type == DS4A_F16 || type == DS4A_F32; };
+    auto stride_ok = [&](int64_t stride, int type) {
+        return T == 1 || (stride >= D && stride % (type == DS4A_F32 ? 4 : 8) == 0 && stride < (1LL << 32));
+    };
+    if (!known(x_type) || (res && !known(res_type)) || (out && !known(out_type))) return DS4A_EUNSUPPORTED;
+    if (codes && group != 0 && group != 32 && group != 64 && group != 128) return DS4A_EUNSUPPORTED;
+    if (codes && scale_style != DS4A_SCALE_POW2 && scale_style != DS4A_SCALE_MAX) return DS4A_EINVAL;
+    if (!(eps > 0.f) || eps > 3e38f) return DS4A_EINVAL;
+    if (!aligned(x, 16) || !aligned(res, 16) || !aligned(res_out, 16) || !aligned(weight, 16) || !aligned(out, 16) ||
+        !aligned(codes, 16) || !aligned(scales, 4) || !aligned(n_live, 4))
+        return DS4A_EINVAL;
+    if (!stride_ok(x_stride, x_type) || (res && !stride_ok(res_stride, res_type)) ||
+        (res_out && !stride_ok(res_out_stride, res_type)))
+        return DS4A_EINVAL;
+    if (res_out == res && res && T > 1 && res_out_stride != res_stride) return DS4A_EINVAL;
+    DevInfo *di = nullptr;
+    if (ds4a_status st = current_device(&di)) return st;
+    AddNormArgs a{};
+    a.x = x;
+    a.x_type = x_type;
+    a.x_stride = T > 1 ? x_stride : 0;
+    a.res = res;
+    a.res_type = res_type;
+    a.res_stride = T > 1 ? res_stride : 0;
+    a.res_out = res_out;
+    a.res_out_stride = T > 1 ? res_out_stride : 0;
+    a.weight = weight;
+    a.eps = eps;
+    a.out = out;
+    a.out_type = out_type;
+    a.codes = codes;
+    a.scales = scales;
+    a.group = group;
+    a.n_groups = codes && group ? (D + group - 1) / group : 1;
+    a.scale_style = scale_style;
+    a.n_live = n_live;
+    a.T = T;
+    a.D = D;
+    a.status = di->status;
+    return launch_add_rms_norm(a, di->sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? DS4A_OK : DS4A_ECUDA;
 }
 
 }  // extern "C"

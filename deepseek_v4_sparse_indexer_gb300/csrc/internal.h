@@ -168,14 +168,18 @@ struct PagedAttnArgs {
     const int32_t *n_rows;       // [U]: rows that exist
     int N_cap;                   // the most a unit's table can name
     const int32_t *idx, *count;  // [U][list_cap], [U]; null: all rows
-    int list_cap;                // the most a unit's list can hold (dense: N_cap)
+    int list_cap;                // the most rows a unit's list can hold (dense: N_cap)
+    int block_lists;             // idx lists blocks (pages of the unit's table), count counts them
+    int idx_stride;              // entries of a unit's list (block lists and masses)
     const uint16_t *raw;         // fp16 [n_ring][128][512]
     const int32_t *ring;         // [U] or null: unit u has ring u
     int n_ring;
     const int32_t *n_raw;        // [U]
     float scale;
     uint16_t *out;               // bf16 [U * hsplit][64][512]
-    float *lse;                  // [U * hsplit][64] or null
+    float *lse;                  // [U * hsplit][64] or null (a mass reads it)
+    float *mass;                 // mass only: [hsplit][U][mass_stride]
+    long long mass_stride;
     int U, hsplit;               // units; 1 (64 heads) or 2 (128)
     void *ws;
     uint32_t *status;
@@ -183,6 +187,98 @@ struct PagedAttnArgs {
 long long paged_attn_tiles(int list_cap);   // the most tiles a unit can have
 size_t paged_attn_ws_bytes(int U, int hsplit, int list_cap);
 cudaError_t launch_paged_attn(const PagedAttnArgs &a, int num_sms, cudaStream_t s);
+cudaError_t launch_paged_attn_mass(const PagedAttnArgs &a, int num_sms, cudaStream_t s);
+
+// ---- blocks of a paged cache (the rows of one page)
+struct BlockKeysArgs {
+    const uint16_t *ik;          // bf16 [n_pages][P][128]
+    int n_pages, shift;          // shift: log2 of the page size
+    const int32_t *table;
+    long long table_stride;
+    int max_pages;
+    const int32_t *n_rows;       // [B]
+    const int32_t *first_row;    // [B] or null
+    const int32_t *cu_row;       // [B + 1] or null
+    uint16_t *block_keys;        // bf16 [n_pages][128]
+    int32_t *n_blocks;           // [B]
+    int B;
+    int split;                   // set by the launcher: thread blocks per sequence
+    uint32_t *status;
+};
+cudaError_t launch_block_keys(BlockKeysArgs a, int num_sms, cudaStream_t s);
+
+struct BlockScoreArgs {
+    const uint16_t *iq;          // bf16 [U][64][128]
+    const float *w;              // [U][64]
+    const uint16_t *block_keys;  // bf16 [n_pages][128]
+    int n_pages;
+    const int32_t *table;
+    long long table_stride;
+    const int32_t *n_blocks;     // [U]
+    float *scores;               // [U][NB_cap]
+    int U, NB_cap, lim;          // lim: the most blocks a unit can have
+    int n_first, n_last;
+    int tiles;                   // set by the launcher
+    uint32_t *status;
+};
+long long block_score_tiles(int NB);
+cudaError_t launch_block_score(BlockScoreArgs a, cudaStream_t s);
+
+// ---- eviction
+struct EvictArgs {
+    const float *mass;           // [n_planes][B][mass_stride]
+    float *mass_out;
+    int n_planes;
+    long long mass_stride;
+    const int32_t *n_rows;       // [B]
+    int32_t *n_rows_out;
+    const int32_t *table;        // [B][table_stride]
+    int32_t *table_out;
+    long long table_stride;
+    int max_pages, shift, n_pages;
+    int B, keep, limit, first, recent;
+    void *rows;                  // bf16 or E4M3 pool
+    int fp8;
+    float *row_scale;            // E4M3: scale per pool row
+    uint16_t *ik;                // bf16 [n_pages][P][128] or null
+    const int32_t *free_pages;
+    int32_t *free_out;
+    int n_free;
+    const int32_t *free_head;
+    int32_t *head_out;
+    const int32_t *n_shared;     // [B] or null
+    const int32_t *gone;         // [B] or null
+    int32_t *gone_out;           // [B] or null
+    int32_t *first_row;          // [B] or null
+    void *ws;
+    int need, keys_in_smem;      // set by the launcher
+    uint32_t *status;
+};
+size_t evict_ws_bytes(int B, int keep, int shift);
+cudaError_t launch_evict(EvictArgs a, int num_sms, cudaStream_t s);
+
+// ---- residual, norm and 8-bit output
+struct AddNormArgs {
+    const void *x;               // [T][D]
+    int x_type;
+    long long x_stride;
+    const void *res;             // [T][D] or null
+    int res_type;
+    long long res_stride;
+    void *res_out;               // [T][D] (res_type) or null
+    long long res_out_stride;
+    const float *weight;         // [D] or null
+    float eps;
+    void *out;                   // [T][D] (out_type) or null
+    int out_type;
+    uint8_t *codes;              // [T][D] or null
+    float *scales;               // [T][n_groups]
+    int group, n_groups, scale_style;   // group 0: the whole row
+    const int32_t *n_live;       // [1] or null
+    int T, D;
+    uint32_t *status;
+};
+cudaError_t launch_add_rms_norm(const AddNormArgs &a, int num_sms, cudaStream_t s);
 
 struct NormRopeArgs {
     const void *q;               // [T][n_head][D] (token stride q_stride) or null

@@ -104,6 +104,15 @@ constexpr uint32_t kTmemO = 128;
 constexpr int kMaxCtas = 160;                 // grid cap (one persistent CTA per SM; 152 on GB300)
 constexpr float kRescaleThreshold = 8.0f;     // log2 units
 
+// What a kernel attends to, or adds up: all rows or a row list; a list of blocks (the
+// rows of one page each); the weights of any of the three, summed over heads.  Kernels
+// of their own, so that none carries the others' instructions.
+constexpr int kRowsKind = 0, kBlocksKind = 1, kMassKind = 2;
+template <int KIND>
+DS4A_DEV bool lists_blocks(const PagedAttnArgs &a) {
+    return KIND == kBlocksKind || (KIND == kMassKind && a.block_lists);
+}
+
 // Logits: M = 64 heads, N = 48 rows, both K-major; values: M = 128 dims, N = 64
 // heads, A (the row tile as dims x rows) MN-major, B (P) K-major.
 __host__ __device__ constexpr uint32_t idesc(bool f16_inputs, bool values) {
@@ -197,19 +206,40 @@ struct Lens {
     int cnt, lim, nrw, ring;   // listed rows, rows that exist, raw rows, raw ring
     bool ok;                   // every value lay in its range
 };
+template <int KIND>
 DS4A_DEV Lens lens_of(const PagedAttnArgs &a, int u) {
     Lens l;
-    const int n = a.n_rows[u], c = a.idx ? a.count[u] : n, r = a.n_raw[u];
-    l.ring = a.ring ? a.ring[u] : u;
+    const int n = a.n_rows[u], c = a.idx ? a.count[u] : n;
     l.lim = min(max(n, 0), a.N_cap);
-    l.cnt = min(max(c, 0), a.list_cap);
+    if (lists_blocks<KIND>(a)) {                   // the last block's rows counted whole
+        const int listed = min(max(c, 0), a.idx_stride);
+        l.cnt = listed << a.page_shift;
+        l.ok = l.lim == n && listed == c;
+    } else {
+        l.cnt = min(max(c, 0), a.list_cap);
+        l.ok = l.lim == n && l.cnt == c;
+    }
+    l.nrw = l.ring = 0;
+    if constexpr (KIND == kMassKind) return l;     // the window gets no mass
+    const int r = a.n_raw[u];
+    l.ring = a.ring ? a.ring[u] : u;
     l.nrw = min(max(r, 0), kNSwa);
-    l.ok = l.lim == n && l.cnt == c && l.nrw == r;
+    l.ok = l.ok && l.nrw == r;
     if (l.ring < 0 || l.ring >= a.n_ring) {
         l.ok = l.ok && l.nrw == 0;     // a unit without raw rows needs no ring
         l.nrw = l.ring = 0;
     }
     return l;
+}
+// Row j of unit u's list, as a row number within the unit (-1: no such block; the last
+// block's rows may lie behind the unit's end).
+template <int KIND>
+DS4A_DEV int listed_row(const PagedAttnArgs &a, int u, int j) {
+    if (!a.idx) return j;
+    const int32_t *list = a.idx + static_cast<long long>(u) * a.idx_stride;
+    if (!lists_blocks<KIND>(a)) return __ldg(list + j);
+    const int b = __ldg(list + (j >> a.page_shift));
+    return b < 0 || b >= a.N_cap >> a.page_shift ? -1 : (b << a.page_shift) + (j & ((1 << a.page_shift) - 1));
 }
 __host__ __device__ constexpr int tiles_of(int rows) { return (rows + TR - 1) / TR; }
 DS4A_DEV int tiles_of(const Lens &l) { return tiles_of(l.cnt) + tiles_of(l.nrw); }
@@ -223,6 +253,7 @@ struct Sched {
 // Share c of the batch's T tiles: [c T / g, (c + 1) T / g), g = min(shares, T).
 // The whole block calls it.  info[c] (for the merge): the share's first unit,
 // that unit's first tile and tile count in the batch, and T.
+template <int KIND>
 DS4A_DEV Sched make_sched(const PagedAttnArgs &a, int4 *info) {
     __shared__ int s_warp[32];
     __shared__ int s_out[4];
@@ -231,7 +262,7 @@ DS4A_DEV Sched make_sched(const PagedAttnArgs &a, int4 *info) {
     const int per = (a.U + n_thr - 1) / n_thr;
     const int u_lo = min(tid * per, a.U), u_hi = min(u_lo + per, a.U);
     int sum = 0;
-    for (int u = u_lo; u < u_hi; ++u) sum += max(tiles_of(lens_of(a, u)), 1);
+    for (int u = u_lo; u < u_hi; ++u) sum += max(tiles_of(lens_of<KIND>(a, u)), 1);
     int inc = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -251,7 +282,7 @@ DS4A_DEV Sched make_sched(const PagedAttnArgs &a, int4 *info) {
     const int hi = static_cast<int>(static_cast<long long>(c + 1) * T / g);
     if (c < g) {
         for (int u = u_lo; u < u_hi; ++u) {
-            const int w = max(tiles_of(lens_of(a, u)), 1);
+            const int w = max(tiles_of(lens_of<KIND>(a, u)), 1);
             if (start <= lo && lo < start + w) {
                 s_out[0] = u;
                 s_out[1] = lo - start;
@@ -288,10 +319,11 @@ struct Item {
     int t0, t1;          // tile range
     bool split;          // the unit's tiles are shared with another CTA: the piece is a partial
 };
+template <int KIND>
 DS4A_DEV Item make_piece(const PagedAttnArgs &a, const Sched &sc, int i) {
     Item m;
     m.u = sc.u0 + i;
-    const Lens l = lens_of(a, m.u);
+    const Lens l = lens_of<KIND>(a, m.u);
     const int tiles = tiles_of(l), w = max(tiles, 1);
     const int lt0 = i == 0 ? sc.off0 : 0, lt1 = i == sc.n_pieces - 1 ? sc.end_last : w;
     if (!l.ok && lt0 == 0 && threadIdx.x == 0) report(a.status, DS4A_DEV_BOUNDS);
@@ -311,20 +343,22 @@ struct Tile {
     Item m;
     int i, t;            // piece and tile; i == n_pieces: behind the last tile
 };
+template <int KIND>
 DS4A_DEV void first_from(const PagedAttnArgs &a, const Sched &sc, Tile &x) {
     for (; x.i < sc.n_pieces; ++x.i) {
-        x.m = make_piece(a, sc, x.i);
+        x.m = make_piece<KIND>(a, sc, x.i);
         x.t = x.m.t0;
         if (x.m.t0 < x.m.t1) return;
     }
 }
+template <int KIND>
 DS4A_DEV void advance(const PagedAttnArgs &a, const Sched &sc, Tile &x) {
     if (x.i >= sc.n_pieces || ++x.t < x.m.t1) return;
     ++x.i;
-    first_from(a, sc, x);
+    first_from<KIND>(a, sc, x);
 }
 
-template <bool FP8>
+template <bool FP8, int KIND>
 __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_constant__ PagedAttnArgs a) {
     pdl_launch_dependents();
     extern __shared__ uint8_t smem_raw[];
@@ -360,7 +394,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
     if (threadIdx.x == 0) {
         for (int b = 0; b < kBufs; ++b) {
             mbar_init(&x_full[b], kGatherWarps);
-            mbar_init(&x_empty[b], 1);
+            // the values GEMM; of a mass, the logits GEMM and the warps that read the tile's mask and scales
+            mbar_init(&x_empty[b], KIND == kMassKind ? 1 + kGroupWarps : 1);
             mbar_init(&r_full[b], 1);
             mbar_init(&r_empty[b], kGatherWarps);
         }
@@ -383,14 +418,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
         mbar_fence_init();
         tma_prefetch_desc(&a.tm_q);
         if (a.tma_rows) tma_prefetch_desc(&a.tm_rows);
-        tma_prefetch_desc(&a.tm_raw);
+        if (KIND != kMassKind) tma_prefetch_desc(&a.tm_raw);
     }
     if (warp == kMmaWarp) tmem_alloc(tmem_slot, kTmemCols);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     pdl_wait();                                  // the lengths may come from the kernel before
-    const Sched sc = make_sched(a, a.ws ? merge_info(a.ws, gridDim.x) : nullptr);
+    const Sched sc = make_sched<KIND>(a, a.ws ? merge_info(a.ws, gridDim.x) : nullptr);
     const uint32_t tmem = *tmem_slot;
     const float NEG_INF = -__int_as_float(0x7f800000);
     const int half = static_cast<int>(blockIdx.x) % a.hsplit;
@@ -417,6 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
         auto row_number = [&](const Tile &x, int r) -> int {   // row r of the tile within the unit
             if (x.i >= sc.n_pieces || x.t >= x.m.ct || r >= TR) return -1;
             const int j = x.t * TR + r;
+            if constexpr (KIND != kRowsKind) return j >= x.m.cnt ? -1 : listed_row<KIND>(a, x.m.u, j);
             return j >= x.m.cnt ? -1 : listed ? __ldg(a.idx + static_cast<long long>(x.m.u) * a.list_cap + j) : j;
         };
         uint32_t rph = 0;
@@ -426,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
         c.i = -1;
         c.t = 0;
         c.m.t1 = 0;                                        // advance goes to the first piece with tiles
-        advance(a, sc, c);
+        advance<KIND>(a, sc, c);
         int v0 = row_number(c, lane), v1 = row_number(c, lane + 32);
         for (;;) {
             const bool end = c.i >= sc.n_pieces;
@@ -436,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
             };
             const int p0 = page_of(v0), p1 = page_of(v1);
             Tile n = c;
-            advance(a, sc, n);
+            advance<KIND>(a, sc, n);
             const int n0 = row_number(n, lane), n1 = row_number(n, lane + 32);
             ok = __all_sync(0xffffffffu, mbar_wait_hint(&r_empty[sl], ((rph >> sl) & 1) ^ 1, abort_flag));
             if (!ok) break;
@@ -457,12 +493,25 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                 return page < 0 || page >= a.n_pages ? -1 : (page << shift) + (v & ((1 << shift) - 1));
             };
             const int y0 = pool_row(lane, v0, p0), y1 = pool_row(lane + 32, v1, p1);
-            // a listed row that is not one of the unit's rows, or outside the pool
-            if (__any_sync(0xffffffffu, (lane < valid && y0 < 0) || (lane + 32 < valid && y1 < 0)) && lane == 0)
+            // a listed row that is not one of the unit's rows, or outside the pool (of a
+            // block that exists the rows behind the unit's end are no fault)
+            auto fault = [&](int r, int v, int y) -> bool {
+                if (r >= valid || y >= 0) return false;
+                if constexpr (KIND != kRowsKind)
+                    if (lists_blocks<KIND>(a) && !raw && v >= c.m.lim && (v >> shift) << shift < c.m.lim) return false;
+                return true;
+            };
+            if (__any_sync(0xffffffffu, fault(lane, v0, y0) || fault(lane + 32, v1, y1)) && lane == 0)
                 report(a.status, DS4A_DEV_BOUNDS);
             const uint32_t lo = __ballot_sync(0xffffffffu, y0 >= 0), hi = __ballot_sync(0xffffffffu, y1 >= 0);
             // By TMA when the valid rows end with a box (the raw map's box: 16 rows).
-            const bool tma = raw ? (valid & 15) == 0 : a.tma_rows && (valid & (box - 1)) == 0;
+            bool tma = raw ? (valid & 15) == 0 : a.tma_rows && (valid & (box - 1)) == 0;
+            if constexpr (KIND != kRowsKind) {
+                // Blocks in any order: every box is there as a whole or not at all.
+                const int lead = lane & ~(box - 1);
+                const bool split = (((lo >> lane) ^ (lo >> lead)) & 1u) || (lane < TR - 32 && (((hi >> lane) ^ (hi >> lead)) & 1u));
+                if (!raw) tma = tma && !__any_sync(0xffffffffu, split);
+            }
             s.row[lane] = y0;
             if (lane < TR - 32) s.row[lane + 32] = y1;
             if (lane == 0) {
@@ -661,7 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
         const uint64_t dq = sw128_desc(smem_u32(sQ), 16, 1024), dx0 = sw128_desc(smem_u32(sX), 16, kXGroup);
         int b = 0, xb = 0;
         for (int i = 0; ok && i < sc.n_pieces; ++i) {
-            const Item m = make_piece(a, sc, i);
+            const Item m = make_piece<KIND>(a, sc, i);
             if (m.t0 >= m.t1) continue;
             if (!(ok = warp_wait(q_full, qph, abort_flag))) break;
             qph ^= 1;
@@ -688,6 +737,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                                    (blk | kk) ? 1u : 0u);
                 }
                 commit_elect(&s_full[b]);
+                if constexpr (KIND == kMassKind) commit_elect(&x_empty[xb]);   // the row tile is free
                 if (t == m.t1 - 1) commit_elect(q_free);
                 b ^= 1;
                 xb = xb == kBufs - 1 ? 0 : xb + 1;
@@ -700,6 +750,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
         commit_elect(drain);
         wait_drain(drain, 0);
         __syncwarp();
+    } else if (KIND == kMassKind && warp == kPvWarp) {
+        // a mass has no values GEMM
     } else if (warp == kPvWarp) {
         // ------------------------------------------------------------ values issuer
         // V(t) once the softmax has written P(t) (and rescaled O when a head's
@@ -712,7 +764,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
         const uint64_t dxv = sw128_desc(smem_u32(sX), kXBlk, kXGroup), dp = sw128_desc(smem_u32(sP), 16, 1024);
         int b = 0, xb = 0;
         for (int i = 0; ok && i < sc.n_pieces; ++i) {
-            const Item m = make_piece(a, sc, i);
+            const Item m = make_piece<KIND>(a, sc, i);
             if (m.t0 >= m.t1) continue;
             for (int t = m.t0; t < m.t1; ++t) {
                 if (!(ok = warp_wait(&p_full[b], (pfph >> b) & 1, abort_flag))) break;
@@ -746,6 +798,99 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
         commit_elect(drain_v);
         wait_drain(drain_v, 0);
         __syncwarp();
+    } else if constexpr (KIND == kMassKind) {
+        // ------------------------------------------------------------ weights and their sums
+        // As in the softmax below, group g = warps 4g .. 4g+3 takes the tiles d with d % 2
+        // = g, and thread t holds heads 16w + t/4 and 8 more for tile rows 8j + 2(t%4) +
+        // {0,1}.  A row's weights are summed over the thread's two heads, the warp's 16
+        // (a butterfly that halves the values it carries: 12 shuffles for 48 rows) and,
+        // through shared memory, the four warps, always in that order; warp w adds rows
+        // 12w .. 12w + 11 of the tile to the mass.  Atomics: a row listed twice gets the
+        // same weight twice, in whatever order.
+        constexpr int J = TR / 8, kShare = TR / kGroupWarps;
+        const int b = warp >> 2, q4 = warp & 3, t4 = lane & 3;
+        const int h0 = 16 * q4 + (lane >> 2), h1 = h0 + 8;
+        const uint32_t lane_off = static_cast<uint32_t>(q4 * 32) << 16;
+        const float sl2 = a.scale * 1.4426950408889634f;
+        float *sSum = reinterpret_cast<float *>(sP + kPBuf);    // [group][tile parity][warp][TR]
+        uint32_t qph = 0, d = 0;
+        bool ok = true;
+        for (int i = 0; ok && i < sc.n_pieces; ++i) {
+            const Item m = make_piece<KIND>(a, sc, i);
+            if (m.t0 >= m.t1) continue;
+            const long long unit = static_cast<long long>(m.u) * a.hsplit + half;
+            // -lse in log2 units; a head that attended to nothing gives no weight
+            auto offset = [&](int h) -> float {
+                const float l = a.lse[unit * kNHead + h];
+                return l == NEG_INF ? NEG_INF : -l * 1.4426950408889634f;
+            };
+            const float n0 = offset(h0), n1 = offset(h1);
+            float *mass = a.mass + (static_cast<long long>(half) * a.U + m.u) * a.mass_stride;
+            ok = __all_sync(0xffffffffu, mbar_wait_hint(q_full, qph, abort_flag));
+            if (!ok) break;
+            qph ^= 1;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_free);
+            for (int t = m.t0; t < m.t1; ++t, ++d) {
+                if ((d & 1) != static_cast<uint32_t>(b)) continue;
+                const int mine = kShare * q4 + lane, j0 = t * TR + mine;   // the row that this lane adds
+                const int row = lane < kShare && j0 < m.cnt ? listed_row<KIND>(a, m.u, j0) : -1;
+                ok = __all_sync(0xffffffffu, mbar_wait_hint(&s_full[b], (d >> 1) & 1, abort_flag));
+                if (!ok) break;
+                tc_fence_after();
+                uint32_t r[4 * J];
+                tmem_ld_s(tmem + lane_off + kTmemS + b * 64, r);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s_empty[b]);
+                ok = __all_sync(0xffffffffu, mbar_wait_hint(&x_full[d % kBufs], (d / kBufs) & 1, abort_flag));
+                if (!ok) break;
+                const uint2 vm = sValid[d % kBufs];
+                float y[2 * J];
+#pragma unroll
+                for (int j = 0; j < 2 * J; ++j) {
+                    float c = sl2;
+                    if constexpr (FP8) c *= head_info(0, 8 * (j >> 1) + 2 * t4 + (j & 1), 6)[1 + d % kBufs];
+                    y[j] = ex2z(fmaf(__uint_as_float(r[4 * (j >> 1) + (j & 1)]), c, n0)) +
+                           ex2z(fmaf(__uint_as_float(r[4 * (j >> 1) + 2 + (j & 1)]), c, n1));
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&x_empty[d % kBufs]);
+                // lanes with bit 4 take rows 24.., with bit 3 the odd ones
+                const bool b4 = lane & 16, b3 = lane & 8;
+                float z[J], w[J / 2];
+#pragma unroll
+                for (int j = 0; j < J; ++j) {
+                    const float other = __shfl_xor_sync(0xffffffffu, b4 ? y[j] : y[J + j], 16);
+                    z[j] = b4 ? other + y[J + j] : y[j] + other;
+                }
+#pragma unroll
+                for (int j = 0; j < J / 2; ++j) {
+                    const float other = __shfl_xor_sync(0xffffffffu, b3 ? z[2 * j] : z[2 * j + 1], 8);
+                    w[j] = b3 ? other + z[2 * j + 1] : z[2 * j] + other;
+                    w[j] += __shfl_xor_sync(0xffffffffu, w[j], 4);
+                }
+                // (two tiles of the group in turn: the sums of one are read before its warps
+                // meet at the next one's barrier)
+                const int par = (d >> 1) & 1;
+                float *sum = sSum + (b * 2 + par) * kGroupWarps * TR;
+                if (!(lane & 4)) {
+#pragma unroll
+                    for (int j = 0; j < J / 2; ++j) sum[q4 * TR + (b4 ? TR / 2 : 0) + 8 * j + 2 * t4 + (b3 ? 1 : 0)] = w[j];
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&grp[b]);
+                ok = __all_sync(0xffffffffu, mbar_wait_hint(&grp[b], par, abort_flag));
+                if (!ok) break;
+                const bool there = lane < kShare && (((mine < 32 ? vm.x : vm.y) >> (mine & 31)) & 1u);
+                if (there && row >= 0)
+                    atomicAdd(mass + row, ((sum[mine] + sum[TR + mine]) + sum[2 * TR + mine]) + sum[3 * TR + mine]);
+            }
+        }
+        if (!ok) {
+            *abort_flag = 1;
+            if (lane == 0) report(a.status, DS4A_DEV_TIMEOUT);
+        }
     } else {
         // ------------------------------------------------------------ softmax + epilogue
         // Group g = warps 4g .. 4g+3 takes the CTA's tiles d with d % 2 = g (so S and
@@ -798,7 +943,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
             if (lane == 0) mbar_arrive(q16_ready);
         };
         for (int i = 0; ok && i < sc.n_pieces; ++i) {
-            const Item m = make_piece(a, sc, i);
+            const Item m = make_piece<KIND>(a, sc, i);
             const long long unit = static_cast<long long>(m.u) * a.hsplit + half;
             const long long slot = 2LL * blockIdx.x + (i == 0 ? 0 : 1);   // a partial's slot: first piece 0, last piece 1
             if (m.t0 >= m.t1) {
@@ -1282,15 +1427,26 @@ size_t paged_attn_ws_bytes(int U, int hsplit, int list_cap) {
     return static_cast<size_t>(ctas) * (2 * kNHead * (kHeadDim + 2) * sizeof(float) + sizeof(int4));
 }
 
-cudaError_t launch_paged_attn(const PagedAttnArgs &a, int num_sms, cudaStream_t s) {
-    void (*kern)(PagedAttnArgs) = a.rows8 ? paged_attn_kernel<true> : paged_attn_kernel<false>;
+template <int KIND>
+cudaError_t launch_kind(const PagedAttnArgs &a, int num_sms, int *shares, cudaStream_t s) {
+    void (*kern)(PagedAttnArgs) = a.rows8 ? paged_attn_kernel<true, KIND> : paged_attn_kernel<false, KIND>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     if (e != cudaSuccess) return e;
-    const int shares = static_cast<int>(shares_of(a.U, a.hsplit, a.list_cap, num_sms < kMaxCtas ? num_sms : kMaxCtas));
-    e = launch_k(kern, dim3(static_cast<unsigned>(shares * a.hsplit)), dim3(kThreads), kSmemBytes, s, a);
+    *shares = static_cast<int>(shares_of(a.U, a.hsplit, a.list_cap, num_sms < kMaxCtas ? num_sms : kMaxCtas));
+    return launch_k(kern, dim3(static_cast<unsigned>(*shares * a.hsplit)), dim3(kThreads), kSmemBytes, s, a);
+}
+
+cudaError_t launch_paged_attn(const PagedAttnArgs &a, int num_sms, cudaStream_t s) {
+    int shares = 0;
+    const cudaError_t e = a.block_lists ? launch_kind<kBlocksKind>(a, num_sms, &shares, s) : launch_kind<kRowsKind>(a, num_sms, &shares, s);
     if (e != cudaSuccess || shares <= 1) return e;
     return launch_k(paged_merge_kernel, dim3(static_cast<unsigned>((shares - 1) * a.hsplit * kMergeBlocks)),
                     dim3(32 * kMergeWarps), 0, s, a, shares);
+}
+
+cudaError_t launch_paged_attn_mass(const PagedAttnArgs &a, int num_sms, cudaStream_t s) {
+    int shares = 0;                                        // every row lies in one piece: nothing to join
+    return launch_kind<kMassKind>(a, num_sms, &shares, s);
 }
 
 }  // namespace ds4a

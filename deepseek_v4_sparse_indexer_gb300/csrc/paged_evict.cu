@@ -1,0 +1,400 @@
+// Eviction from a paged cache by accumulated attention weight: a sequence with more
+// than `limit` rows keeps `keep` of them,
+//
+//     rows 0 .. first - 1 and its last `recent` rows, and of the others those with the
+//     greatest mass (the sum of its planes; of equal ones the lower row, NaN lowest),
+//
+// in their order, in pages from the free list; the old pages go back in front of the
+// list's head.  Rows are copied and not moved within their pages, so that every copy
+// is independent of the others and a page that another sequence reads stays whole.
+//
+// evict_select_kernel, a block of 1,024 threads per sequence: the kept rows' smallest
+// key by a radix select (11, 11 and 10 bits of an order-preserving key; keys in shared
+// memory where they fit), then the kept rows' numbers by a count and a fill over the
+// warps' runs of rows, and the masses in their new places.  evict_move_kernel: the
+// copies, eight rows a warp (all of their loads in flight), and the lists.
+// Bound: the copies HBM; a few sequences the select's chain of passes.
+#include "common.cuh"
+#include "internal.h"
+
+namespace ds4a {
+namespace {
+
+constexpr int kThreads = 1024, kWarps = kThreads / 32;
+constexpr int kBins = 2048;
+constexpr int kKeysMost = 49152;              // keys that fit into shared memory (192 KB)
+
+// ---- workspace (ints): [0] the list's head, then per sequence: rows before (0: left
+// alone, -1: refused behind its place in the list); new pages; the kept rows' slots
+struct EvictWs {
+    int32_t *head, *info, *pages, *src;
+};
+__host__ __device__ inline EvictWs evict_ws(void *ws, int B, int need) {
+    int32_t *p = static_cast<int32_t *>(ws);
+    EvictWs w;
+    w.head = p;
+    w.info = p + 64;
+    w.pages = w.info + B;
+    w.src = w.pages + static_cast<long long>(B) * need;
+    return w;
+}
+
+DS4A_DEV int warp_sum(int v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+__global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const __grid_constant__ EvictArgs a) {
+    pdl_launch_dependents();
+    extern __shared__ uint32_t s_keys[];                   // the rows' keys, or nothing
+    __shared__ uint32_t s_hist[kBins];
+    __shared__ int s_gt[kWarps], s_eq[kWarps];
+    __shared__ uint32_t s_bin, s_left;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, b = blockIdx.x;
+    const int P = 1 << a.shift;
+    const int cap = a.max_pages << a.shift;
+    const EvictWs ws = evict_ws(a.ws, a.B, a.need);
+    pdl_wait();
+    const int n_raw = a.n_rows[b], n = min(max(n_raw, 0), cap);
+    const int head = a.free_head[0];
+    if (tid == 0) {
+        if (n != n_raw || head < 0) report(a.status, DS4A_DEV_BOUNDS);
+        if (b == 0) ws.head[0] = head;
+    }
+    if (n <= a.limit || head < 0) {
+        if (tid == 0) ws.info[b] = 0;
+        return;
+    }
+    // ---- this sequence's place among those over the limit, and its new pages
+    int before = 0;
+    for (int k = tid; k < b; k += kThreads) before += min(max(a.n_rows[k], 0), cap) > a.limit;
+    before = warp_sum(before);
+    if (lane == 0) s_gt[warp] = before;
+    __syncthreads();
+    before = warp_sum(s_gt[lane]);
+    const long long at = head + static_cast<long long>(before) * a.need;
+    if (at + a.need > a.n_free) {
+        if (tid == 0) {
+            ws.info[b] = 0;
+            report(a.status, DS4A_DEV_BOUNDS);
+        }
+        return;
+    }
+    const int32_t *table = a.table + b * a.table_stride;
+    bool ok = true;
+    for (int i = tid; i < a.need; i += kThreads) {
+        const int page = a.free_pages[at + i];
+        ok = ok && page >= 0 && page < a.n_pages;
+        ws.pages[static_cast<long long>(b) * a.need + i] = page;
+    }
+    for (int i = tid; i < (n + P - 1) >> a.shift; i += kThreads) {
+        const int page = table[i];
+        ok = ok && page >= 0 && page < a.n_pages;
+    }
+    if (!__syncthreads_and(ok)) {
+        if (tid == 0) {
+            ws.info[b] = -1;
+            report(a.status, DS4A_DEV_BOUNDS);
+        }
+        return;
+    }
+    if (tid == 0) ws.info[b] = n;
+
+    // ---- the least key that is kept
+    const float *mass = a.mass + b * a.mass_stride;
+    const long long plane = a.B * a.mass_stride;
+    auto key_of = [&](int r) -> uint32_t {
+        float m = mass[r];
+        for (int p = 1; p < a.n_planes; ++p) m += mass[p * plane + r];
+        return m == m ? float_key(m) : 0u;
+    };
+    const int lo = a.first, hi = n - a.recent;             // the rows that compete
+    if (a.keys_in_smem) {
+        for (int r = lo + tid; r < hi; r += kThreads) s_keys[r] = key_of(r);
+    }
+    auto key_at = [&](int r) -> uint32_t { return a.keys_in_smem ? s_keys[r] : key_of(r); };
+    uint32_t left = static_cast<uint32_t>(a.keep - a.first - a.recent);   // of them are kept
+    uint32_t least = 0xffffffffu;                          // none: no key is above it, and none of its like is taken
+    if (left > 0) {
+        uint32_t prefix = 0;
+#pragma unroll 1
+        for (int pass = 0; pass < 3; ++pass) {
+            const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+            const int bits = pass == 2 ? 10 : 11;
+            const uint32_t above = pass == 0 ? 0u : 0xffffffffu << (shift + bits);
+            for (int i = tid; i < kBins; i += kThreads) s_hist[i] = 0u;
+            __syncthreads();
+            for (int r = lo + tid; r < hi; r += kThreads) {
+                const uint32_t k = key_at(r);
+                if ((k & above) == prefix) atomicAdd(&s_hist[(k >> shift) & ((1u << bits) - 1u)], 1u);
+            }
+            __syncthreads();
+            // thread t: bins 2t and 2t + 1, counted from the top
+            const int top = kBins - 1 - 2 * tid;
+            const uint32_t c1 = s_hist[top], c0 = s_hist[top - 1];
+            uint32_t inc = c1 + c0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t v = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += v;
+            }
+            if (lane == 31) s_gt[warp] = static_cast<int>(inc);
+            __syncthreads();
+            uint32_t base = 0;
+            for (int w = 0; w < warp; ++w) base += static_cast<uint32_t>(s_gt[w]);
+            const uint32_t ahead = base + inc - (c1 + c0);
+            if (ahead < left && left <= ahead + c1) {
+                s_bin = static_cast<uint32_t>(top);
+                s_left = left - ahead;
+            } else if (ahead + c1 < left && left <= ahead + c1 + c0) {
+                s_bin = static_cast<uint32_t>(top - 1);
+                s_left = left - ahead - c1;
+            }
+            __syncthreads();
+            prefix |= s_bin << shift;
+            left = s_left;
+            __syncthreads();                               // before the next pass writes them
+        }
+        least = prefix;                                    // `left` rows of this key are kept, the lowest
+    } else {
+        __syncthreads();
+    }
+
+    // ---- the kept rows' numbers, in order: warp w has rows [w run, (w + 1) run)
+    const int run = ((n + kWarps - 1) / kWarps + 31) & ~31;
+    const int r0 = min(warp * run, n), r1 = min(r0 + run, n);
+    auto is_gt = [&](int r) -> bool { return r < lo || r >= hi || key_at(r) > least; };
+    auto is_eq = [&](int r) -> bool { return r >= lo && r < hi && key_at(r) == least; };
+    int gt = 0, eq = 0;
+    for (int r = r0 + lane; r < r1; r += 32) {
+        gt += is_gt(r);
+        eq += is_eq(r);
+    }
+    gt = warp_sum(gt);
+    eq = warp_sum(eq);
+    __syncthreads();
+    if (lane == 0) {
+        s_gt[warp] = gt;
+        s_eq[warp] = eq;
+    }
+    __syncthreads();
+    int gt0 = 0, eq0 = 0;
+    for (int w = 0; w < warp; ++w) {
+        gt0 += s_gt[w];
+        eq0 += s_eq[w];
+    }
+    int32_t *src = ws.src + static_cast<long long>(b) * a.keep;
+    const int take = static_cast<int>(left);               // of the rows with the least key
+    const uint32_t below = (1u << lane) - 1u;
+    for (int r = r0; r < r1; r += 32) {                    // (whole warps: the ballots)
+        const bool in = r + lane < r1;
+        const bool g = in && is_gt(r + lane), e = in && is_eq(r + lane);
+        const uint32_t bg = __ballot_sync(0xffffffffu, g), be = __ballot_sync(0xffffffffu, e);
+        const int eq_at = eq0 + __popc(be & below);
+        // kept rows before this one: the greater ones and the taken ones of the least key
+        const int j = gt0 + __popc(bg & below) + min(eq_at, take);
+        if ((g || (e && eq_at < take)) && j < a.keep) src[j] = r + lane;
+        gt0 += __popc(bg);
+        eq0 += __popc(be);
+    }
+    __syncthreads();
+
+    // ---- masses in their new places and slots in place of row numbers.  mass_out may
+    // be mass: entry j comes from row r_j >= j, so a later part's sources lie behind an
+    // earlier part's places, and within a part all loads come before all stores.
+    float *mass_out = a.mass_out + b * a.mass_stride;
+    constexpr int kPart = 4;
+    for (int j0 = 0; j0 < a.keep; j0 += kPart * kThreads) {
+        int row[kPart];
+#pragma unroll
+        for (int i = 0; i < kPart; ++i) {
+            const int j = j0 + i * kThreads + tid;
+            row[i] = j < a.keep ? src[j] : 0;
+        }
+        for (int p = 0; p < a.n_planes; ++p) {
+            float m[kPart];
+#pragma unroll
+            for (int i = 0; i < kPart; ++i) m[i] = mass[p * plane + row[i]];
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < kPart; ++i) {
+                const int j = j0 + i * kThreads + tid;
+                if (j < a.keep) mass_out[p * plane + j] = m[i];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kPart; ++i) {
+            const int j = j0 + i * kThreads + tid;
+            if (j < a.keep) src[j] = (table[row[i] >> a.shift] << a.shift) + (row[i] & (P - 1));
+        }
+    }
+    __syncthreads();
+    for (int p = 0; p < a.n_planes; ++p)
+        for (int j = a.keep + tid; j < n; j += kThreads) mass_out[p * plane + j] = 0.f;
+}
+
+// ---- copies and lists
+constexpr int kMoveThreads = 256, kMoveWarps = kMoveThreads / 32;
+constexpr int kRows = 8;                      // rows a warp copies at a time
+
+template <bool FP8>
+__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_constant__ EvictArgs a) {
+    // It writes row counts that a top-k may read before its own wait: no
+    // pdl_launch_dependents here, and a fence before the end.
+    extern __shared__ int s_seq[];                         // [B] the evicted sequences, [B] old pages before each
+    __shared__ int s_ev[kMoveWarps], s_pg[kMoveWarps], s_tk[kMoveWarps];
+    int *s_ret = s_seq + a.B;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const EvictWs ws = evict_ws(a.ws, a.B, a.need);
+    pdl_wait();
+    auto returned = [&](int b, int n) -> int {             // old pages of sequence b that go to the list
+        const int pages = static_cast<int>((static_cast<long long>(n) + (1 << a.shift) - 1) >> a.shift);
+        return pages - (a.n_shared ? min(max(a.n_shared[b], 0), pages) : 0);
+    };
+    // every block scans the sequences: thread t has [t per, (t + 1) per)
+    const int per = (a.B + kMoveThreads - 1) / kMoveThreads, b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
+    int ev = 0, pg = 0, tk = 0;
+    for (int b = b0; b < b1; ++b) {
+        const int n = ws.info[b];
+        tk += n != 0;
+        if (n > 0) {
+            ++ev;
+            pg += returned(b, n);
+        }
+    }
+    int ev_inc = ev, pg_inc = pg;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, ev_inc, o), y = __shfl_up_sync(0xffffffffu, pg_inc, o);
+        if (lane >= o) ev_inc += x, pg_inc += y;
+    }
+    tk = warp_sum(tk);
+    if (lane == 31) {
+        s_ev[warp] = ev_inc;
+        s_pg[warp] = pg_inc;
+        s_tk[warp] = tk;
+    }
+    __syncthreads();
+    int e = ev_inc - ev, g = pg_inc - pg, E = 0, G = 0, taken = 0;
+    for (int w = 0; w < kMoveWarps; ++w) {
+        if (w < warp) e += s_ev[w], g += s_pg[w];
+        E += s_ev[w];
+        G += s_pg[w];
+        taken += s_tk[w];
+    }
+    for (int b = b0; b < b1; ++b) {
+        const int n = ws.info[b];
+        if (n > 0) {
+            s_seq[e] = b;
+            s_ret[e] = g;
+            ++e;
+            g += returned(b, n);
+        }
+    }
+    __syncthreads();
+    const int head = ws.head[0];
+    const long long head_out = head < 0 ? head : head + static_cast<long long>(taken) * a.need - G;
+
+    // ---- copies
+    const int n_warps = gridDim.x * kMoveWarps, me = blockIdx.x * kMoveWarps + warp;
+    const int parts = (a.keep + kRows - 1) / kRows;
+    for (long long x = me; x < static_cast<long long>(E) * parts; x += n_warps) {
+        const int q = static_cast<int>(x / parts), b = s_seq[q], j0 = static_cast<int>(x - static_cast<long long>(q) * parts) * kRows;
+        const int j = min(j0 + (lane & (kRows - 1)), a.keep - 1);   // (rows past the last repeat it)
+        const int from = ws.src[static_cast<long long>(b) * a.keep + j];
+        const int to = (ws.pages[static_cast<long long>(b) * a.need + (j >> a.shift)] << a.shift) + (j & ((1 << a.shift) - 1));
+        constexpr int kWide = FP8 ? 512 : 1024, kLoads = kWide / 512;
+        uint4 v[kRows][kLoads], k[kRows / 2];
+        float sc = 0.f;
+        const uint8_t *rows = static_cast<const uint8_t *>(a.rows);
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            const long long f = __shfl_sync(0xffffffffu, from, i);
+#pragma unroll
+            for (int c = 0; c < kLoads; ++c) v[i][c] = *reinterpret_cast<const uint4 *>(rows + f * kWide + c * 512 + lane * 16);
+        }
+        if (a.ik) {
+#pragma unroll
+            for (int i = 0; i < kRows / 2; ++i) {
+                const long long f = __shfl_sync(0xffffffffu, from, 2 * i + (lane >> 4));
+                k[i] = *reinterpret_cast<const uint4 *>(a.ik + f * kIdxDim + (lane & 15) * 8);
+            }
+        }
+        if (FP8 && lane < kRows) sc = a.row_scale[from];
+        uint8_t *out = static_cast<uint8_t *>(a.rows);
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            const long long t = __shfl_sync(0xffffffffu, to, i);
+#pragma unroll
+            for (int c = 0; c < kLoads; ++c) *reinterpret_cast<uint4 *>(out + t * kWide + c * 512 + lane * 16) = v[i][c];
+        }
+        if (a.ik) {
+#pragma unroll
+            for (int i = 0; i < kRows / 2; ++i) {
+                const long long t = __shfl_sync(0xffffffffu, to, 2 * i + (lane >> 4));
+                *reinterpret_cast<uint4 *>(a.ik + t * kIdxDim + (lane & 15) * 8) = k[i];
+            }
+        }
+        if (FP8 && lane < kRows) a.row_scale[to] = sc;
+    }
+
+    // ---- tables and the free list: a warp per evicted sequence, from the last warp on
+    // (the first ones have copies).  An entry is read before its place is written.
+    for (int q = n_warps - 1 - me; q < E; q += n_warps) {
+        const int b = s_seq[q], n = ws.info[b];
+        const int pages = static_cast<int>((static_cast<long long>(n) + (1 << a.shift) - 1) >> a.shift);
+        const int shared = pages - returned(b, n);
+        const int32_t *table = a.table + b * a.table_stride;
+        int32_t *table_out = a.table_out + b * a.table_stride;
+        for (int i = lane; i < pages; i += 32) {
+            const int old = table[i];
+            if (i < a.need) table_out[i] = ws.pages[static_cast<long long>(b) * a.need + i];
+            const long long at = head_out + s_ret[q] + (i - shared);
+            if (i >= shared) {
+                if (at >= 0) a.free_out[at] = old;
+                else report(a.status, DS4A_DEV_BOUNDS);
+            }
+        }
+    }
+    // ---- counts
+    if (blockIdx.x == gridDim.x - 1) {
+        for (int b = tid; b < a.B; b += kMoveThreads) {
+            const int n = ws.info[b], old = a.n_rows[b];
+            if (a.gone_out) a.gone_out[b] = (a.gone ? a.gone[b] : 0) + (n > 0 ? n - a.keep : 0);
+            if (a.first_row) a.first_row[b] = n > 0 ? 0 : max(old, 0);
+            a.n_rows_out[b] = n > 0 ? a.keep : old;
+        }
+        if (tid == 0) a.head_out[0] = head < 0 ? head : static_cast<int>(max(head_out, 0LL));
+        __threadfence();
+    }
+}
+
+}  // namespace
+
+size_t evict_ws_bytes(int B, int keep, int shift) {
+    const long long need = (static_cast<long long>(keep) + (1 << shift) - 1) >> shift;
+    return static_cast<size_t>(64 + B + B * need + static_cast<long long>(B) * keep) * sizeof(int32_t);
+}
+
+cudaError_t launch_evict(EvictArgs a, int num_sms, cudaStream_t s) {
+    const long long cap = static_cast<long long>(a.max_pages) << a.shift;
+    a.need = static_cast<int>((static_cast<long long>(a.keep) + (1 << a.shift) - 1) >> a.shift);
+    a.keys_in_smem = cap <= kKeysMost;
+    const size_t smem = a.keys_in_smem ? static_cast<size_t>(cap) * 4 : 0;
+    cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    e = launch_k(evict_select_kernel, dim3(static_cast<unsigned>(a.B)), dim3(kThreads), smem, s, a);
+    if (e != cudaSuccess) return e;
+    void (*kern)(EvictArgs) = a.fp8 ? evict_move_kernel<true> : evict_move_kernel<false>;
+    const size_t lists = 2 * static_cast<size_t>(a.B) * sizeof(int);
+    if (lists > 40960) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(lists));
+        if (e != cudaSuccess) return e;
+    }
+    // two blocks an SM: sixteen warps, 8 to 10 KB of loads each
+    const long long most = 2LL * num_sms, want = static_cast<long long>(a.B) * ((a.keep + kRows - 1) / kRows + kMoveWarps - 1) / kMoveWarps + 1;
+    return launch_k(kern, dim3(static_cast<unsigned>(want < most ? want : most)), dim3(kMoveThreads), lists, s, a);
+}
+
+}  // namespace ds4a

@@ -86,6 +86,8 @@ typedef int ds4a_status;
 #define DS4A_OP_DENSE_ATTN_DECODE 4
 #define DS4A_OP_INDEXER_TOPK 5
 #define DS4A_OP_PAGED_ATTN_DECODE 6
+#define DS4A_OP_PAGED_ATTN_BLOCKS 7
+#define DS4A_OP_PAGED_EVICT 8
 /* OR-ed into an attention op: the workspace of the 128-head (Pro shape) call. */
 #define DS4A_OP_FLAG_128_HEADS 0x100
 
@@ -98,6 +100,15 @@ typedef int ds4a_status;
 /* Which dims of a head's last n_rot rotate together (ds4a_qk_norm_rope). */
 #define DS4A_ROPE_NEIGHBOURS 0  /* dim 2i of the tail with dim 2i + 1          */
 #define DS4A_ROPE_HALVES 1      /* dim i of the tail with dim n_rot / 2 + i    */
+
+/* What a list names (ds4a_paged_attn_mass). */
+#define DS4A_LIST_ROWS 0        /* rows of the unit                            */
+#define DS4A_LIST_BLOCKS 1      /* blocks of the unit: all rows of a page      */
+
+/* Scale of a group of E4M3 codes whose largest magnitude is A (ds4a_add_rms_norm). */
+#define DS4A_SCALE_POW2 0       /* the smallest power of two with A <= 448 s   */
+#define DS4A_SCALE_MAX 1        /* A / 448                                     */
+#define DS4A_MAX_NORM_DIM 16384
 
 /* Page sizes of a paged cache: a power of two of rows in this range. */
 #define DS4A_MIN_PAGE 8
@@ -693,6 +704,205 @@ ds4a_status ds4a_paged_attn_decode(int n_head, const uint16_t *q, const void *ro
                                    int n_ring, const int32_t *ring, const int32_t *n_raw,
                                    float scale, uint16_t *out, float *lse, int U, void *ws,
                                    size_t ws_bytes, void *stream);
+
+/*
+ * 6. Blocks.  A block of a sequence is the rows of one page, block i those of page
+ *    table[u][i]; the last one may be part-filled.  Scoring one mean key per block
+ *    instead of every key reads 1 / page_size of the indexer's bytes, and whole
+ *    pages reach the attention as contiguous copies.  The pages of the engine know
+ *    no blocks: the selection is this library's, with the indexer's own score.
+ *
+ * 6a. Mean keys of the blocks that a step changed:
+ *
+ *      block_keys[page] = mean of the keys of the page's rows that exist
+ *
+ *    (fp32 sums in a fixed order, one rounding to bf16).  A program keeps
+ *    block_keys beside its key store and calls this once the step's keys are stored.
+ *
+ *    ik          bf16 [n_pages][page_size][128], contiguous, 16-byte aligned (device).
+ *    table       int32 [B] rows of max_pages entries, table_stride apart (device).
+ *    n_rows      int32 [B] (device): rows of each sequence now.
+ *    first_row   int32 [B] (device) or NULL: the first row that is new or has moved
+ *                (n_rows[b]: none), as ds4a_paged_evict writes it.
+ *    cu_row      int32 [B + 1] (device) or NULL: exclusive sums of the new rows, as
+ *                ds4a_paged_plan writes them: the last cu_row[b + 1] - cu_row[b] rows
+ *                are new.  At most one of the two; neither: every row is.
+ *    block_keys  bf16 [n_pages][128], 16-byte aligned (device, updated: the pages that
+ *                hold such a row; the others are left as they were).
+ *    n_blocks    int32 [B] (device, written): ceil(n_rows / page_size).
+ *    Lengths out of range are clamped and pages outside the pool left out; each sets
+ *    DS4A_DEV_BOUNDS.  1 <= B <= DS4A_MAX_PLAN_SEQS; max_pages * page_size is below
+ *    2^30, n_pages * page_size below 2^31.
+ */
+ds4a_status ds4a_paged_block_keys(const uint16_t *ik, int n_pages, int page_size,
+                                  const int32_t *table, int64_t table_stride, int max_pages,
+                                  const int32_t *n_rows, const int32_t *first_row,
+                                  const int32_t *cu_row, uint16_t *block_keys, int32_t *n_blocks,
+                                  int B, void *stream);
+
+/*
+ * 6b. Scores of the blocks, one query per unit: 1's formula on the mean keys,
+ *
+ *      scores[u,b] = sum_h w[u,h] * max(0, sum_d iq[u,h,d] * block_keys[table[u][b]][d])
+ *
+ *    and +inf for the first n_first and the last n_last blocks of a unit, which are
+ *    then selected whatever they score.  ds4a_topk_select over [U][1][NB_cap] with
+ *    n_blocks for its n_rows gives the lists that 6c reads.
+ *
+ *    iq, w, table  as in 5c.    block_keys  bf16 [n_pages][128], 16-byte aligned.
+ *    n_blocks  int32 [U] (device), 0 .. min(NB_cap, max_pages); a count outside sets
+ *              DS4A_DEV_BOUNDS and is clamped.
+ *    scores    fp32 [U][NB_cap] (device), written for b < n_blocks[u], the others left
+ *              as they were.  A block whose page is not one of the pool's gets -inf and
+ *              sets DS4A_DEV_BOUNDS.
+ */
+ds4a_status ds4a_paged_block_score(const uint16_t *iq, const float *w, const uint16_t *block_keys,
+                                   int n_pages, const int32_t *table, int64_t table_stride,
+                                   int max_pages, const int32_t *n_blocks, int n_first, int n_last,
+                                   float *scores, int U, int NB_cap, void *stream);
+
+/*
+ * 6c. Attention of one new token per sequence over the rows of listed blocks and
+ *    the raw window: 5d with block_idx int32 [U][top_k] block numbers of the unit, in
+ *    any order, and block_count int32 [U], 1 <= top_k <= DS4A_MAX_TOP_K.  Of the last,
+ *    part-filled block the rows that exist are attended to.  A block that no row of
+ *    the unit lies in, or whose page is not one of the pool's, is masked and sets
+ *    DS4A_DEV_BOUNDS; a block listed twice counts twice.  ws: ds4a_workspace_bytes(
+ *    DS4A_OP_PAGED_ATTN_BLOCKS [| DS4A_OP_FLAG_128_HEADS], U, 1, top_k * page_size, 0).
+ *    Everything else, the arithmetic and the limits included, is as in 5d.
+ */
+ds4a_status ds4a_paged_attn_blocks(int n_head, const uint16_t *q, const void *rows, int rows_type,
+                                   const float *row_scale, int n_pages, int page_size,
+                                   const int32_t *table, int64_t table_stride, int max_pages,
+                                   const int32_t *n_rows, const int32_t *block_idx,
+                                   const int32_t *block_count, int top_k, const uint16_t *raw,
+                                   int n_ring, const int32_t *ring, const int32_t *n_raw,
+                                   float scale, uint16_t *out, float *lse, int U, void *ws,
+                                   size_t ws_bytes, void *stream);
+
+/*
+ * 7. Eviction by accumulated attention weight.
+ *
+ * 7a. The weights that an attention gave the rows, summed over heads and added to
+ *    what earlier steps gave them.  For each unit u, plane p (heads 64 p .. 64 p + 63)
+ *    and attended row r of the compressed rows:
+ *
+ *      mass[p,u,r] += sum_{h of p} exp(scale * q[u,h,:] . x_r - lse[u,h])
+ *
+ *    in fp32, the rows and products as in 5d.  The raw window has a part in lse but
+ *    gets no mass.  Where lse is -inf a head adds nothing.  A row listed twice is
+ *    added to twice.  Bit-identical from call to call.
+ *
+ *    q, rows, rows_type, row_scale, table, n_rows, idx, count, top_k, scale   those
+ *             of the attention call: 5d, or with list_kind DS4A_LIST_BLOCKS 6c.
+ *             list_kind says nothing without a list.
+ *    lse      fp32 [U][n_head] (device), as the attention wrote it.
+ *    mass     fp32 [n_head / 64][U] rows of mass_stride elements (device, updated);
+ *             mass_stride >= max_pages * page_size.  A program keeps it beside its
+ *             tables and starts a sequence's row with zeros.
+ *    A masked row (5d, 6c) is not added to.  No workspace.
+ */
+ds4a_status ds4a_paged_attn_mass(int n_head, const uint16_t *q, const void *rows, int rows_type,
+                                 const float *row_scale, int n_pages, int page_size,
+                                 const int32_t *table, int64_t table_stride, int max_pages,
+                                 const int32_t *n_rows, int list_kind, const int32_t *idx,
+                                 const int32_t *count, int top_k, float scale, const float *lse,
+                                 float *mass, int64_t mass_stride, int U, void *stream);
+
+/*
+ * 7b. Eviction.  Every sequence with more than `limit` rows keeps `keep` of them:
+ *    its first `first` and last `recent` rows, and of the others those with the
+ *    greatest mass, the sum of its planes (equal ones: the lower row; NaN: below all
+ *    others).  They stay in order and are copied, with their indexer keys, scales and
+ *    masses, to ceil(keep / page_size) pages taken from the free list, in sequence
+ *    order; the sequence's old pages go back to the list, in front of its head, in
+ *    sequence and table order.  (A softmax over compressed rows does not depend on
+ *    their positions: each row's tail was rotated when it was stored.)  Other
+ *    sequences are left as they are.
+ *
+ *    mass        fp32 [n_planes][B] rows of mass_stride elements (device), 1 <=
+ *                n_planes <= 16, mass_stride >= max_pages * page_size.  mass_out the
+ *                same (device, updated; may be mass): of an evicted sequence entries
+ *                0 .. keep - 1 are the kept rows', those up to its old length zeros.
+ *    n_rows      int32 [B] (device).  n_rows_out int32 [B] (device, written; may be
+ *                n_rows): keep for an evicted sequence, n_rows for another.
+ *    table       int32 [B] rows of max_pages entries, table_stride apart (device).
+ *                table_out the same (device, updated; may be table): entries 0 ..
+ *                ceil(keep / page_size) - 1 of the evicted sequences.
+ *    rows        bf16 or E4M3 (rows_type) pool [n_pages][page_size][512], row_scale fp32
+ *                [n_pages][page_size] with E4M3, ik bf16 [n_pages][page_size][128] or
+ *                NULL (device, updated: the new pages).
+ *    free_pages, free_pages_out  int32 [n_free], free_head, free_head_out int32 [1]
+ *                (device; the second of each pair updated, may be the first): as in 5a.
+ *                The pages taken are free_pages[*free_head ..]; *free_head_out is
+ *                *free_head plus the pages taken minus those returned, which are
+ *                free_pages_out[*free_head_out ..].  A page returned past the list's
+ *                start is dropped and sets DS4A_DEV_BOUNDS.
+ *    n_shared    int32 [B] or NULL (device): leading pages of a sequence that other
+ *                sequences hold too; they are not returned (their rows are copied, so
+ *                the others read them as before).
+ *    gone        int32 [B] or NULL (device): rows evicted earlier (zeros when NULL).
+ *                gone_out int32 [B] or NULL (device, written; may be gone): with this
+ *                call's added, for ds4a_paged_plan_evicted.
+ *    first_row   int32 [B] or NULL (device, written): 0 for an evicted sequence, n_rows
+ *                for another, for 6a.
+ *    ws          workspace of ds4a_workspace_bytes(DS4A_OP_PAGED_EVICT, B, 1, max_pages
+ *                * page_size, keep) bytes, 256-byte aligned (device).
+ *    1 <= keep <= limit, first + recent <= keep <= max_pages * page_size, 1 <= B <=
+ *    DS4A_MAX_PLAN_SEQS.  A length out of range is clamped; a free list that runs out
+ *    leaves the sequences it does not reach as they are, a negative head all of them,
+ *    and a page, old or new, that is not one of the pool's its sequence (whose new
+ *    pages are lost to the list); each sets DS4A_DEV_BOUNDS.
+ */
+ds4a_status ds4a_paged_evict(const float *mass, int n_planes, int64_t mass_stride, float *mass_out,
+                             const int32_t *n_rows, int32_t *n_rows_out, const int32_t *table,
+                             int32_t *table_out, int64_t table_stride, int max_pages, int page_size,
+                             int n_pages, int B, int keep, int limit, int first, int recent,
+                             void *rows, int rows_type, float *row_scale, uint16_t *ik,
+                             const int32_t *free_pages, int32_t *free_pages_out, int n_free,
+                             const int32_t *free_head, int32_t *free_head_out,
+                             const int32_t *n_shared, const int32_t *gone, int32_t *gone_out,
+                             int32_t *first_row, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * 8. The residual's addition, RMS norm and 8-bit output, in one pass over T rows of
+ *    D elements:
+ *
+ *      h = x + res                                     (res_out: the new residual)
+ *      y[d] = h[d] * weight[d] / sqrt(mean_d h[d]^2 + eps)
+ *      codes[d] = E4M3 of y[d] / s, s the scale of d's group of `group` elements
+ *                 (to nearest, ties to even, saturating at +-448; NaN stays NaN)
+ *
+ *    fp32 sums and products from the unrounded h, one rounding to each output's type.
+ *    With A the largest |y| of the group (NaN elements do not count), s is the
+ *    smallest power of two with A <= 448 s, as in 4c (DS4A_SCALE_POW2), or A / 448
+ *    (DS4A_SCALE_MAX, at least 2^-126; codes are of y * (448 / A)); 1 where A is 0 or
+ *    infinite.  A row whose sum of squares passes the fp32 range gives y = 0.
+ *
+ *    x        bf16, fp16 or fp32 (x_type) [T] rows, x_stride elements apart (device).
+ *    res      bf16, fp16 or fp32 (res_type) [T] rows, res_stride apart, or NULL: h = x.
+ *    res_out  [T] rows of res_type, res_out_stride apart, or NULL (device, written; may
+ *             be res itself, with its stride).
+ *    weight   fp32 [D] or NULL: all ones (device).
+ *    out      bf16, fp16 or fp32 (out_type) [T][D], contiguous, or NULL (device, written).
+ *    codes    uint8 [T][D], contiguous, or NULL (device, written).  At least one of out
+ *             and codes.
+ *    scales   fp32 [T][ceil(D / group)] (device, written with codes).
+ *    group    32, 64 or 128 elements (the last group of a row may be shorter), or 0: a
+ *             scale for the whole row.
+ *    n_live   int32 [1] or NULL (device): rows from *n_live on are padding and left as
+ *             they were in every output; out of [0, T] sets DS4A_DEV_BOUNDS and is
+ *             clamped.
+ *    D a multiple of 8 up to DS4A_MAX_NORM_DIM (else DS4A_EUNSUPPORTED), T >= 0 (0:
+ *    nothing is launched), eps > 0.  Buffers 16-byte aligned (scales 4), strides
+ *    at least D and whole multiples of 16 bytes.  out, codes and scales overlap no
+ *    other buffer.
+ */
+ds4a_status ds4a_add_rms_norm(const void *x, int x_type, int64_t x_stride, const void *res,
+                              int res_type, int64_t res_stride, void *res_out,
+                              int64_t res_out_stride, const float *weight, float eps, void *out,
+                              int out_type, uint8_t *codes, float *scales, int group,
+                              int scale_style, const int32_t *n_live, int T, int D, void *stream);
 
 #ifdef __cplusplus
 }
