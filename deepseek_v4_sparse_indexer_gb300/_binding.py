@@ -51,7 +51,7 @@ EXPORTS = ("ds4a_strerror", "ds4a_version", "ds4a_workspace_bytes", "ds4a_get_de
            "ds4a_rows_to_fp8", "ds4a_sparse_attn_decode_fp8", "ds4a_sparse_attn_prefill_fp8", "ds4a_indexer_topk",
            "ds4a_paged_plan", "ds4a_paged_plan_form", "ds4a_qk_norm_rope", "ds4a_paged_indexer_score",
            "ds4a_paged_attn_decode", "ds4a_paged_block_keys", "ds4a_paged_block_score", "ds4a_paged_attn_blocks",
-           "ds4a_paged_attn_mass", "ds4a_paged_evict", "ds4a_add_rms_norm")
+           "ds4a_paged_attn_mass", "ds4a_paged_evict", "ds4a_add_rms_norm", "ds4a_paged_plan_evicted")
 DS4A_TOPK_NOALLOC_SCRATCH_BYTES = 8 << 20
 DS4A_MAX_TOP_K = 2048
 
@@ -133,6 +133,8 @@ def load(build_if_missing: bool = True):
     L.ds4a_paged_plan.restype = _i32
     L.ds4a_paged_plan_form.argtypes = [_i32] + L.ds4a_paged_plan.argtypes
     L.ds4a_paged_plan_form.restype = _i32
+    L.ds4a_paged_plan_evicted.argtypes = [_i32, _vp, _vp] + L.ds4a_paged_plan.argtypes[1:]
+    L.ds4a_paged_plan_evicted.restype = _i32
     L.ds4a_qk_norm_rope.argtypes = [_vp, _i32, _i64, _vp, _i32, _i64, _vp, _vp, _i32, _i32, _f32, _vp, _vp, _vp, _vp,
                                     _i32, _vp, _vp, _i64, _i32, _i32, _i32, _vp]
     L.ds4a_qk_norm_rope.restype = _i32
@@ -148,7 +150,7 @@ def load(build_if_missing: bool = True):
     L.ds4a_paged_attn_blocks.argtypes = L.ds4a_paged_attn_decode.argtypes
     L.ds4a_paged_attn_blocks.restype = _i32
     L.ds4a_paged_attn_mass.argtypes = [_i32, _vp, _vp, _i32, _vp, _i32, _i32, _vp, _i64, _i32, _vp, _i32, _vp, _vp, _i32,
-                                       _f32, _vp, _vp, _i64, _i32, _vp]
+                                       _f32, _vp, _vp, _vp, _i64, _i32, _vp]
     L.ds4a_paged_attn_mass.restype = _i32
     L.ds4a_paged_evict.argtypes = [_vp, _i32, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _i32, _i32, _i32,
                                    _i32, _i32, _vp, _i32, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
@@ -596,14 +598,15 @@ def _launch(dev, stream, name, *args):
 
 
 def ds4a_paged_plan(past, add, ratio, page_size, free_pages, free_head, table, n_rows, n_raw, cu_tok, cu_row, tok_pos,
-                    raw_slot, row_pos, row_slot, free_head_out, ring=None, stream=None, form=0):
+                    raw_slot, row_pos, row_slot, free_head_out, ring=None, stream=None, form=0, gone=None):
     """Block tables and slot maps of one step from the request lengths, all int32:
     past, add [B]; free_pages [n_free], free_head [1]; table [B, max_pages]
     (updated); n_rows, n_raw [B], cu_tok, cu_row [B + 1], tok_pos, raw_slot
     [T_cap], row_pos, row_slot [R_cap] and free_head_out [1] (written; may be
     free_head); ring [B] or None.  form: DS4A_PLAN_TOKENS_BY_SEQ and / or
     DS4A_PLAN_ROWS_BY_SEQ lay the token / row maps out by sequence (add 0 or 1),
-    DS4A_PLAN_FIRST_POS makes row_pos the position of a row's first token."""
+    DS4A_PLAN_FIRST_POS makes row_pos the position of a row's first token.  gone [B]
+    or None: each sequence's evicted rows (ds4a_paged_evict)."""
     dev = _device_index(past, "past")
     B, T, R, n_free = past.numel(), tok_pos.numel(), row_pos.numel(), free_pages.numel()
     _req_ints(dev, ("past", past, B), ("add", add, B), ("free_pages", free_pages, n_free), ("free_head", free_head, 1),
@@ -613,8 +616,11 @@ def ds4a_paged_plan(past, add, ratio, page_size, free_pages, free_head, table, n
     if ring is not None:
         _req_ints(dev, ("ring", ring, B))
     stride, max_pages = _table_stride(table, B, dev)
-    name, lead = ("ds4a_paged_plan_form", (form,)) if form else ("ds4a_paged_plan", ())
-    _launch(dev, stream, name, *lead, past.data_ptr(), add.data_ptr(), B, ratio, page_size, free_pages.data_ptr(), n_free,
+    name, lead, evicted = ("ds4a_paged_plan_form", (form,), ()) if form else ("ds4a_paged_plan", (), ())
+    if gone is not None:
+        _req_ints(dev, ("gone", gone, B))
+        name, lead, evicted = "ds4a_paged_plan_evicted", (form,), (gone.data_ptr(),)
+    _launch(dev, stream, name, *lead, past.data_ptr(), add.data_ptr(), *evicted, B, ratio, page_size, free_pages.data_ptr(), n_free,
             free_head.data_ptr(), free_head_out.data_ptr(), table.data_ptr(), stride, max_pages,
             _opt(ring), n_rows.data_ptr(), n_raw.data_ptr(), cu_tok.data_ptr(),
             cu_row.data_ptr(), tok_pos.data_ptr(), raw_slot.data_ptr(), T, row_pos.data_ptr(), row_slot.data_ptr(), R)
@@ -792,19 +798,22 @@ def ds4a_paged_attn_blocks(q, rows, table, n_rows, block_idx, block_count, raw, 
 
 
 def ds4a_paged_attn_mass(q, rows, table, n_rows, scale, lse, mass, idx=None, count=None, blocks=False, row_scale=None,
-                         stream=None):
+                         tok_pos=None, stream=None):
     """Adds the weights that an attention gave each row, exp(scale q.x - lse) summed
     over the plane's 64 heads, to mass f32 [H/64,U,>= max_pages * P] (updated).
     lse f32 [U,H] from that attention; the other arguments are its own, idx and
-    count naming blocks with blocks=True."""
+    count naming blocks with blocks=True.  tok_pos i32 [U] or None: units whose entry
+    is negative are left as they were."""
     dev, U, H, lead, lists = _paged_rows(q, rows, row_scale, table, n_rows, idx, count)
     if lse.dtype is not _F32 or lse.get_device() != dev or lse.numel() != U * H or not lse.is_contiguous():
         raise ValueError("lse: contiguous float32 [U, H]")
     if mass.dtype is not _F32 or mass.get_device() != dev or mass.dim() != 3 or not mass.is_contiguous() \
             or mass.shape[0] * N_HEAD != H or mass.shape[1] != U:
         raise ValueError("mass: contiguous float32 [H / 64, U, rows]")
+    if tok_pos is not None:
+        _req_ints(dev, ("tok_pos", tok_pos, U))
     _launch(dev, stream, "ds4a_paged_attn_mass", *lead, DS4A_LIST_BLOCKS if blocks else DS4A_LIST_ROWS, *lists, scale,
-            lse.data_ptr(), mass.data_ptr(), mass.shape[2], U)
+            lse.data_ptr(), _opt(tok_pos), mass.data_ptr(), mass.shape[2], U)
 
 
 def _block_keys(block_keys, n_pages, dev):

@@ -615,13 +615,14 @@ ds4a_status ds4a_paged_plan(const int32_t *past, const int32_t *add, int B, int 
                                 row_pos, row_slot, R_cap, stream);
 }
 
-ds4a_status ds4a_paged_plan_form(int form, const int32_t *past, const int32_t *add, int B, int ratio, int page_size,
+namespace {
+ds4a_status plan_call(const char *name, int form, const int32_t *gone, const int32_t *past, const int32_t *add, int B, int ratio, int page_size,
                                  const int32_t *free_pages, int n_free, const int32_t *free_head,
                                  int32_t *free_head_out, int32_t *table, int64_t table_stride, int max_pages,
                                  const int32_t *ring, int32_t *n_rows, int32_t *n_raw, int32_t *cu_tok,
                                  int32_t *cu_row, int32_t *tok_pos, int32_t *raw_slot, int T_cap, int32_t *row_pos,
                                  int32_t *row_slot, int R_cap, void *stream) {
-    const NvtxRange nvtx_range(form ? "ds4a_paged_plan_form" : "ds4a_paged_plan");
+    const NvtxRange nvtx_range(name);
     if (ds4a_status inj = take_injected()) return inj;
     if (form & ~(DS4A_PLAN_TOKENS_BY_SEQ | DS4A_PLAN_ROWS_BY_SEQ | DS4A_PLAN_FIRST_POS)) return DS4A_EINVAL;
     if (!past || !add || !free_head || !free_head_out || !table || !n_rows || !n_raw || !cu_tok || !cu_row ||
@@ -660,8 +661,33 @@ ds4a_status ds4a_paged_plan_form(int form, const int32_t *past, const int32_t *a
     a.row_slot = row_slot;
     a.R_cap = R_cap;
     a.form = form;
+    a.gone = gone;
     a.status = di->status;
     return launch_paged_plan(a, di->sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? DS4A_OK : DS4A_ECUDA;
+}
+}  // namespace
+
+ds4a_status ds4a_paged_plan_form(int form, const int32_t *past, const int32_t *add, int B, int ratio, int page_size,
+                                 const int32_t *free_pages, int n_free, const int32_t *free_head,
+                                 int32_t *free_head_out, int32_t *table, int64_t table_stride, int max_pages,
+                                 const int32_t *ring, int32_t *n_rows, int32_t *n_raw, int32_t *cu_tok,
+                                 int32_t *cu_row, int32_t *tok_pos, int32_t *raw_slot, int T_cap, int32_t *row_pos,
+                                 int32_t *row_slot, int R_cap, void *stream) {
+    return plan_call(form ? "ds4a_paged_plan_form" : "ds4a_paged_plan", form, nullptr, past, add, B, ratio, page_size, free_pages, n_free, free_head, free_head_out,
+                     table, table_stride, max_pages, ring, n_rows, n_raw, cu_tok, cu_row, tok_pos, raw_slot, T_cap,
+                     row_pos, row_slot, R_cap, stream);
+}
+
+ds4a_status ds4a_paged_plan_evicted(int form, const int32_t *past, const int32_t *add, const int32_t *gone, int B, int ratio, int page_size,
+                                 const int32_t *free_pages, int n_free, const int32_t *free_head,
+                                 int32_t *free_head_out, int32_t *table, int64_t table_stride, int max_pages,
+                                 const int32_t *ring, int32_t *n_rows, int32_t *n_raw, int32_t *cu_tok,
+                                 int32_t *cu_row, int32_t *tok_pos, int32_t *raw_slot, int T_cap, int32_t *row_pos,
+                                 int32_t *row_slot, int R_cap, void *stream) {
+    if (!gone) return DS4A_EINVAL;
+    return plan_call("ds4a_paged_plan_evicted", form, gone, past, add, B, ratio, page_size, free_pages, n_free, free_head, free_head_out,
+                     table, table_stride, max_pages, ring, n_rows, n_raw, cu_tok, cu_row, tok_pos, raw_slot, T_cap,
+                     row_pos, row_slot, R_cap, stream);
 }
 
 ds4a_status ds4a_qk_norm_rope(const void *q, int q_type, int64_t q_tok_stride, const void *k, int k_type,
@@ -869,7 +895,7 @@ ds4a_status ds4a_paged_attn_mass(int n_head, const uint16_t *q, const void *rows
                                  const float *row_scale, int n_pages, int page_size, const int32_t *table,
                                  int64_t table_stride, int max_pages, const int32_t *n_rows, int list_kind,
                                  const int32_t *idx, const int32_t *count, int top_k, float scale, const float *lse,
-                                 float *mass, int64_t mass_stride, int U, void *stream) {
+                                 const int32_t *tok_pos, float *mass, int64_t mass_stride, int U, void *stream) {
     const NvtxRange nvtx_range("ds4a_paged_attn_mass");
     if (ds4a_status inj = take_injected()) return inj;
     if (list_kind != DS4A_LIST_ROWS && list_kind != DS4A_LIST_BLOCKS) return DS4A_EINVAL;
@@ -885,6 +911,7 @@ ds4a_status ds4a_paged_attn_mass(int n_head, const uint16_t *q, const void *rows
     a.lse = const_cast<float *>(lse);                      // read only
     a.mass = mass;
     a.mass_stride = mass_stride;
+    a.tok_pos = tok_pos;
     a.status = di->status;
     if (!encode_paged_rows(a)) return DS4A_EINVAL;
     return launch_paged_attn_mass(a, di->sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? DS4A_OK : DS4A_ECUDA;

@@ -147,6 +147,7 @@ struct PagedPlanArgs {
     int32_t *row_pos, *row_slot;
     int R_cap;
     int form;                    // DS4A_PLAN_* bits
+    const int32_t *gone;         // [B] or null: evicted rows
     uint32_t *status;
     int cluster;                 // set by the launcher: the CTAs are one cluster
 };
@@ -180,6 +181,7 @@ struct PagedAttnArgs {
     float *lse;                  // [U * hsplit][64] or null (a mass reads it)
     float *mass;                 // mass only: [hsplit][U][mass_stride]
     long long mass_stride;
+    const int32_t *tok_pos;      // mass only: [U] or null; negative: no token
     int U, hsplit;               // units; 1 (64 heads) or 2 (128)
     void *ws;
     uint32_t *status;

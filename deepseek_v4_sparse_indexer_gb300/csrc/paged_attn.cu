@@ -220,7 +220,10 @@ DS4A_DEV Lens lens_of(const PagedAttnArgs &a, int u) {
         l.ok = l.lim == n && l.cnt == c;
     }
     l.nrw = l.ring = 0;
-    if constexpr (KIND == kMassKind) return l;     // the window gets no mass
+    if constexpr (KIND == kMassKind) {             // the window gets no mass, nor a unit without a token
+        if (a.tok_pos && a.tok_pos[u] < 0) l.cnt = 0;
+        return l;
+    }
     const int r = a.n_raw[u];
     l.ring = a.ring ? a.ring[u] : u;
     l.nrw = min(max(r, 0), kNSwa);

@@ -30,6 +30,9 @@
 // A large step that updates *free_head in place runs as one cluster instead, whose
 // barrier lies between the reads of the old head and its update.
 //
+// After evictions a sequence holds `gone` rows fewer than its tokens have made: row j
+// of the sequence lies in place j - gone of its table, its position is unchanged.
+//
 // The kernel never lets its dependents launch early, and fences the row counts it
 // writes: the top-k kernels read them before their own dependency wait.
 #include "common.cuh"
@@ -107,12 +110,14 @@ DS4A_DEV void store4(int32_t *p, long long i, int n, const int (&v)[4], bool vec
 // BY_SEQ: the token or the row maps are laid out by sequence (a kernel of its own: as
 // a flag of one kernel it cost the other form 0.3 us of 4.8).
 constexpr int kBySeq = DS4A_PLAN_TOKENS_BY_SEQ | DS4A_PLAN_ROWS_BY_SEQ;
-template <bool BY_SEQ>
+template <bool BY_SEQ, bool GONE>
 __global__ void __launch_bounds__(kThreads, 1) paged_plan_kernel(const __grid_constant__ PagedPlanArgs a) {
     extern __shared__ int smem[];
     const int B = a.B;
     int *cu_tok = smem, *cu_row = smem + (B + 1), *cu_page = smem + 2 * (B + 1), *s_past = smem + 3 * (B + 1);
     int *s_ring = s_past + B;                              // -1: no such ring
+    int *s_gone = s_ring + B;                              // (GONE only)
+    auto gone_of = [&](int b) -> int { return GONE ? s_gone[b] : 0; };
     __shared__ Sums s_warp[kWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_wait();
@@ -130,7 +135,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_plan_kernel(const __grid_co
         ok = ok && s.ok && (ring_ok || s.add == 0);
         s_past[b] = s.past;
         s_ring[b] = ring_ok ? ring : -1;
-        const int r0 = s.past / a.ratio, r1 = (s.past + s.add) / a.ratio;
+        int r0 = s.past / a.ratio, r1 = (s.past + s.add) / a.ratio;
+        if constexpr (GONE) {
+            int gone = a.gone[b];
+            if (gone < 0 || gone > r0) gone = 0, ok = false;
+            s_gone[b] = gone;
+            r0 -= gone;
+            r1 -= gone;
+        }
         const Sums one = {s.add, r1 - r0, pages_of(r1, a.shift) - pages_of(r0, a.shift)};
         cu_tok[b + 1] = one.tok;                 // summed below
         cu_row[b + 1] = one.row;
@@ -219,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_plan_kernel(const __grid_co
         k -= nb_tok;
         if (k < nb_row) {                                  // ---- rows, four in a row per lane: mostly one page
             const long long end = min((static_cast<long long>(k) + 1) * run_row, static_cast<long long>(a.R_cap));
-            int seq_end = 0, first = 0, held = 0, taken = 0, last_i = -1, page = -1;
+            int seq_end = 0, first = 0, gone = 0, held = 0, taken = 0, last_i = -1, page = -1;
             const int32_t *table = nullptr;
             for (long long x = static_cast<long long>(k) * run_row + 4 * lane; x < end; x += 4 * 32) {
                 int pos[4], slot[4];
@@ -230,7 +242,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_plan_kernel(const __grid_co
                     if (!item_at(x + q, row_by_seq, cu_row, R, item)) continue;
                     if (item >= seq_end) {
                         const int b = row_by_seq ? static_cast<int>(x) + q : find_seq(cu_row, B, item);
-                        const int old = s_past[b] / a.ratio;
+                        gone = gone_of(b);
+                        const int old = s_past[b] / a.ratio - gone;
                         seq_end = cu_row[b + 1];
                         first = old - cu_row[b];
                         held = pages_of(old, a.shift);
@@ -243,7 +256,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_plan_kernel(const __grid_co
                         last_i = i;
                         page = i >= a.max_pages ? -1 : i >= held ? free_page(taken + i) : table[i];
                     }
-                    pos[q] = static_cast<int>(static_cast<long long>(j) * a.ratio + pos_in_row);
+                    pos[q] = static_cast<int>(static_cast<long long>(j + gone) * a.ratio + pos_in_row);
                     const long long at = (static_cast<long long>(page) << a.shift) + (j & ((1 << a.shift) - 1));
                     if (page < 0 || at > 0x7fffffffLL) ok = false;
                     else slot[q] = static_cast<int>(at);
@@ -258,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_plan_kernel(const __grid_co
             const int end = static_cast<int>(min((static_cast<long long>(k) + 1) * run_page, static_cast<long long>(G)));
             for (long long x = static_cast<long long>(k) * run_page + lane; x < end; x += 32) {
                 const int g = static_cast<int>(x), b = find_seq(cu_page, B, g);
-                const long long i = static_cast<long long>(pages_of(s_past[b] / a.ratio, a.shift)) + (g - cu_page[b]);
+                const long long i = static_cast<long long>(pages_of(s_past[b] / a.ratio - gone_of(b), a.shift)) + (g - cu_page[b]);
                 if (i < a.max_pages) a.table[b * a.table_stride + i] = free_page(g);
                 else ok = false;
             }
@@ -271,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_plan_kernel(const __grid_co
             a.cu_row[b] = cu_row[b];
             if (b < B) {
                 const int old = s_past[b], len = old + (cu_tok[b + 1] - cu_tok[b]);
-                a.n_rows[b] = old / a.ratio + (cu_row[b + 1] - cu_row[b]);
+                a.n_rows[b] = old / a.ratio - gone_of(b) + (cu_row[b + 1] - cu_row[b]);
                 a.n_raw[b] = len < kNSwa ? len : kNSwa;
             }
         }
@@ -287,9 +300,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_plan_kernel(const __grid_co
 }  // namespace
 
 cudaError_t launch_paged_plan(PagedPlanArgs a, int num_sms, cudaStream_t s) {
-    const size_t smem = (5 * static_cast<size_t>(a.B) + 3) * sizeof(int);
+    const size_t smem = ((a.gone ? 6 : 5) * static_cast<size_t>(a.B) + 3) * sizeof(int);
     cudaError_t e = cudaSuccess;
-    void (*kern)(PagedPlanArgs) = a.form & kBySeq ? paged_plan_kernel<true> : paged_plan_kernel<false>;
+    void (*kern)(PagedPlanArgs) = a.gone ? (a.form & kBySeq ? paged_plan_kernel<true, true> : paged_plan_kernel<false, true>)
+                                         : (a.form & kBySeq ? paged_plan_kernel<true, false> : paged_plan_kernel<false, false>);
     if (smem > 40960)
         e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;

@@ -200,11 +200,27 @@ class PagedDecodeStep:
     library (two for the indexer's part); outputs and workspaces are kept, so the
     step can be captured in a CUDA graph and replayed on other lengths.  top_k = 0:
     every row is attended to (the ratio-128 layers).
+
+    blocks = k (with top_k = 0) selects k blocks, whole pages, instead of rows, by the
+    indexer's score of each block's mean key, keep_blocks = (first, last) of them
+    whatever they score; x also holds block_keys bf16 [n_pages,128], kept by the
+    program.
+
+    mass = True adds the weights of each step's attention to x["mass"] f32
+    [H/64,U,max_pages * P], kept by the program (zeros for a new sequence).  With
+    evict = (keep, limit, first, recent), evict(x) cuts the sequences that the last
+    step left with more than limit rows to keep of them (ds4a_paged_evict, in
+    place); x["gone"] i32 [U] (zeros for a new sequence) counts the rows evicted,
+    which later steps' plans go by.  x may hold n_shared i32 [U].
     """
 
     def __init__(self, U, max_pages, page_size, top_k=512, ratio=4, device="cuda", n_head=B.N_HEAD, fp8=False, eps=1e-6,
                  style=B.DS4A_ROPE_NEIGHBOURS, pooled_by_sequence=False, row_position="last", idx_style=None,
-                 rotate_iq=True):
+                 rotate_iq=True, blocks=0, keep_blocks=(0, 0), mass=False, evict=None):
+        if blocks and top_k:
+            raise ValueError("blocks: with top_k = 0")
+        if evict is not None and not mass:
+            raise ValueError("evict: with mass = True")
         self.U, self.page_size, self.top_k, self.ratio, self.n_head = U, page_size, top_k, ratio, n_head
         self.fp8, self.eps, self.style = fp8, eps, style
         self.idx_style = style if idx_style is None else idx_style
@@ -224,25 +240,34 @@ class PagedDecodeStep:
         self.q = torch.zeros(U, n_head, B.HEAD_DIM, dtype=torch.bfloat16, device=dev)
         self.out = torch.empty(U, n_head, B.HEAD_DIM, dtype=torch.bfloat16, device=dev)
         self.lse = torch.empty(U, n_head, dtype=torch.float32, device=dev)
-        self.ws_attn = _ws(B.ds4a_workspace_bytes(B.DS4A_OP_PAGED_ATTN_DECODE | flag, U, 1, N_cap, top_k), dev)
+        self.blocks, self.keep_blocks, self.mass, self.evict_sizes = blocks, keep_blocks, mass, evict
+        self.ws_attn = _ws(B.ds4a_workspace_bytes(B.DS4A_OP_PAGED_ATTN_BLOCKS | flag, U, 1, blocks * page_size, 0) if blocks else
+                           B.ds4a_workspace_bytes(B.DS4A_OP_PAGED_ATTN_DECODE | flag, U, 1, N_cap, top_k), dev)
         self.idx = self.count = None
-        if top_k:
+        self.listed = blocks or top_k                # entries of a sequence's list (0: no indexer)
+        if self.listed:
+            n_scores = max_pages if blocks else N_cap
             if rotate_iq:
                 self.iq = torch.zeros(U, B.N_IDX_HEAD, B.IDX_DIM, dtype=torch.bfloat16, device=dev)
-            self.scores = torch.empty(U, 1, N_cap, dtype=torch.float32, device=dev)
-            self.idx = torch.empty(U, 1, top_k, dtype=torch.int32, device=dev)
+            self.scores = torch.empty(U, 1, n_scores, dtype=torch.float32, device=dev)
+            self.idx = torch.empty(U, 1, self.listed, dtype=torch.int32, device=dev)
             self.count = torch.empty(U, 1, dtype=torch.int32, device=dev)
-            self.ws_topk = _ws(B.ds4a_workspace_bytes(B.DS4A_OP_TOPK_SELECT, U, 1, N_cap, top_k), dev)
+            self.ws_topk = _ws(B.ds4a_workspace_bytes(B.DS4A_OP_TOPK_SELECT, U, 1, n_scores, self.listed), dev)
+        if blocks:
+            self.n_blocks = torch.empty(U, dtype=torch.int32, device=dev)
+        if evict is not None:
+            self.first_row = torch.empty(U, dtype=torch.int32, device=dev)
+            self.ws_evict = _ws(B.ds4a_workspace_bytes(B.DS4A_OP_PAGED_EVICT, U, 1, N_cap, evict[0]), dev)
 
     def plan(self, x, stream=None):
         B.ds4a_paged_plan(x["past"], x["add"], self.ratio, self.page_size, x["free_pages"], x["free_head"], x["table"],
                           self.n_rows, self.n_raw, self.cu_tok, self.cu_row, self.tok_pos, self.raw_slot, self.row_pos,
-                          self.row_slot, x["free_head"], ring=x.get("ring"), stream=stream, form=self.form)
+                          self.row_slot, x["free_head"], ring=x.get("ring"), stream=stream, form=self.form, gone=x.get("gone"))
 
     def rotate(self, x, stream=None):
         B.ds4a_qk_norm_rope(x["q"], x["kv"], self.tok_pos, x["inv_freq"], self.eps, x.get("q_norm"), x.get("kv_norm"), self.q,
                             x["raw"].view(-1, B.HEAD_DIM), k_slot=self.raw_slot, style=self.style, stream=stream)
-        if self.top_k and self.rotate_iq:
+        if self.listed and self.rotate_iq:
             B.ds4a_qk_norm_rope(x["iq"], None, self.tok_pos, x["inv_freq"], self.eps, x.get("iq_norm"), None, self.iq, None,
                                 style=self.idx_style, stream=stream)
 
@@ -251,31 +276,64 @@ class PagedDecodeStep:
         B.ds4a_qk_norm_rope(None, x["pooled"], self.row_pos, x["inv_freq"], self.eps, None, row_norm, None,
                             x["rows"].view(-1, B.HEAD_DIM), k_slot=self.row_slot,
                             k_scale=x["row_scale"].view(-1) if self.fp8 else None, style=self.style, stream=stream)
-        if self.top_k:
+        if self.listed:
             B.ds4a_qk_norm_rope(None, x["pooled_ik"], self.row_pos, x["inv_freq"], self.eps, None, x.get("ik_norm"), None,
                                 x["ik"].view(-1, B.IDX_DIM), k_slot=self.row_slot, style=self.idx_style, stream=stream)
 
     def score(self, x, stream=None):
         iq = self.iq if self.rotate_iq else x["iq"]
+        if self.blocks:
+            B.ds4a_paged_block_keys(x["ik"], x["table"], self.n_rows, x["block_keys"], self.n_blocks, cu_row=self.cu_row,
+                                    stream=stream)
+            B.ds4a_paged_block_score(iq.view(self.U, 1, B.N_IDX_HEAD, B.IDX_DIM), x["w"].view(self.U, 1, B.N_IDX_HEAD),
+                                     x["block_keys"], x["table"], self.n_blocks, self.scores, *self.keep_blocks, stream=stream)
+            return
         B.ds4a_paged_indexer_score(iq.view(self.U, 1, B.N_IDX_HEAD, B.IDX_DIM), x["w"].view(self.U, 1, B.N_IDX_HEAD),
                                    x["ik"], x["table"], self.n_rows, self.scores, stream=stream)
 
     def select(self, x, stream=None):
         with torch.cuda.device(self.scores.device):        # the paged calls see to it themselves
-            B.ds4a_topk_select(self.scores, self.n_rows, self.top_k, self.idx, self.count, self.ws_topk, stream=stream)
+            B.ds4a_topk_select(self.scores, self.n_blocks if self.blocks else self.n_rows, self.listed, self.idx, self.count,
+                               self.ws_topk, stream=stream)
+
+    def _lists(self):
+        return (self.idx.view(self.U, self.listed), self.count.view(self.U)) if self.listed else (None, None)
 
     def attend(self, x, scale=DEFAULT_SCALE, stream=None):
-        idx, count = (self.idx.view(self.U, self.top_k), self.count.view(self.U)) if self.top_k else (None, None)
+        idx, count = self._lists()
+        row_scale = x["row_scale"] if self.fp8 else None
+        if self.blocks:
+            B.ds4a_paged_attn_blocks(self.q, x["rows"], x["table"], self.n_rows, idx, count, x["raw"], self.n_raw, scale,
+                                     self.out, self.lse, self.ws_attn, row_scale=row_scale, ring=x.get("ring"), stream=stream)
+            return
         B.ds4a_paged_attn_decode(self.q, x["rows"], x["table"], self.n_rows, x["raw"], self.n_raw, scale, self.out, self.lse,
-                                 self.ws_attn, idx=idx, count=count, row_scale=x["row_scale"] if self.fp8 else None,
-                                 ring=x.get("ring"), stream=stream)
+                                 self.ws_attn, idx=idx, count=count, row_scale=row_scale, ring=x.get("ring"), stream=stream)
+
+    def accumulate(self, x, scale=DEFAULT_SCALE, stream=None):
+        idx, count = self._lists()
+        B.ds4a_paged_attn_mass(self.q, x["rows"], x["table"], self.n_rows, scale, self.lse, x["mass"], idx=idx, count=count,
+                               blocks=bool(self.blocks), row_scale=x["row_scale"] if self.fp8 else None, tok_pos=self.tok_pos,
+                               stream=stream)
+
+    def evict(self, x, stream=None):
+        keep, limit, first, recent = self.evict_sizes
+        B.ds4a_paged_evict(x["mass"], self.n_rows, x["table"], x["rows"], x["free_pages"], x["free_head"], keep, limit,
+                           x["mass"], self.n_rows, x["table"], x["free_pages"], x["free_head"], self.ws_evict, first=first,
+                           recent=recent, row_scale=x["row_scale"] if self.fp8 else None,
+                           ik=x["ik"] if self.listed else None, n_shared=x.get("n_shared"), gone=x["gone"],
+                           gone_out=x["gone"], first_row=self.first_row, stream=stream)
+        if self.blocks:
+            B.ds4a_paged_block_keys(x["ik"], x["table"], self.n_rows, x["block_keys"], self.n_blocks,
+                                    first_row=self.first_row, stream=stream)
 
     def __call__(self, x, scale=DEFAULT_SCALE, stream=None):
         self.plan(x, stream)
         self.rotate(x, stream)
         self.store(x, stream)
-        if self.top_k:
+        if self.listed:
             self.score(x, stream)
             self.select(x, stream)
         self.attend(x, scale, stream)
+        if self.mass:
+            self.accumulate(x, scale, stream)
         return self.out

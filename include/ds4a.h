@@ -586,6 +586,23 @@ ds4a_status ds4a_paged_plan_form(int form, const int32_t *past, const int32_t *a
                                  int32_t *row_pos, int32_t *row_slot, int R_cap, void *stream);
 
 /*
+ *    The same for sequences that rows were evicted from (7b): gone int32 [B] (device)
+ *    says how many of sequence b's rows, so that it holds floor(past / ratio) - gone
+ *    of them before the step; n_rows, the pages and the new rows' slots go by the
+ *    rows held, positions by the tokens.  A value below 0 or above the rows made
+ *    sets DS4A_DEV_BOUNDS and counts as 0.
+ */
+ds4a_status ds4a_paged_plan_evicted(int form, const int32_t *past, const int32_t *add,
+                                    const int32_t *gone, int B, int ratio, int page_size,
+                                    const int32_t *free_pages, int n_free,
+                                    const int32_t *free_head, int32_t *free_head_out,
+                                    int32_t *table, int64_t table_stride, int max_pages,
+                                    const int32_t *ring, int32_t *n_rows, int32_t *n_raw,
+                                    int32_t *cu_tok, int32_t *cu_row, int32_t *tok_pos,
+                                    int32_t *raw_slot, int T_cap, int32_t *row_pos,
+                                    int32_t *row_slot, int R_cap, void *stream);
+
+/*
  * 5b. Norm and rotation of queries and keys (§2: RoPE on the last n_rot dims
  *    of a head; §3-2: a pooled row is RMS-normalised and its tail rotated
  *    before it is stored): what turns projections into the rotated q, raw
@@ -797,6 +814,8 @@ ds4a_status ds4a_paged_attn_blocks(int n_head, const uint16_t *q, const void *ro
  *             of the attention call: 5d, or with list_kind DS4A_LIST_BLOCKS 6c.
  *             list_kind says nothing without a list.
  *    lse      fp32 [U][n_head] (device), as the attention wrote it.
+ *    tok_pos  int32 [U] or NULL (device): a unit whose entry is negative had no token
+ *             in this step (5a's map by sequence) and is left as it was.
  *    mass     fp32 [n_head / 64][U] rows of mass_stride elements (device, updated);
  *             mass_stride >= max_pages * page_size.  A program keeps it beside its
  *             tables and starts a sequence's row with zeros.
@@ -807,7 +826,8 @@ ds4a_status ds4a_paged_attn_mass(int n_head, const uint16_t *q, const void *rows
                                  const int32_t *table, int64_t table_stride, int max_pages,
                                  const int32_t *n_rows, int list_kind, const int32_t *idx,
                                  const int32_t *count, int top_k, float scale, const float *lse,
-                                 float *mass, int64_t mass_stride, int U, void *stream);
+                                 const int32_t *tok_pos, float *mass, int64_t mass_stride, int U,
+                                 void *stream);
 
 /*
  * 7b. Eviction.  Every sequence with more than `limit` rows keeps `keep` of them:
