@@ -977,7 +977,7 @@ ds4a_status ds4a_paged_block_score(const uint16_t *iq, const float *w, const uin
     a.n_first = n_first;
     a.n_last = n_last;
     a.status = di->status;
-    return launch_block_score(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? DS4A_OK : DS4A_ECUDA;
+    return launch_block_score(a, di->sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? DS4A_OK : DS4A_ECUDA;
 }
 
 ds4a_status ds4a_paged_evict(const float *mass, int n_planes, int64_t mass_stride, float *mass_out,

@@ -204,10 +204,9 @@ struct BlockKeysArgs {
     uint16_t *block_keys;        // bf16 [n_pages][128]
     int32_t *n_blocks;           // [B]
     int B;
-    int split;                   // set by the launcher: thread blocks per sequence
     uint32_t *status;
 };
-cudaError_t launch_block_keys(BlockKeysArgs a, int num_sms, cudaStream_t s);
+cudaError_t launch_block_keys(const BlockKeysArgs &a, int num_sms, cudaStream_t s);
 
 struct BlockScoreArgs {
     const uint16_t *iq;          // bf16 [U][64][128]
@@ -224,7 +223,7 @@ struct BlockScoreArgs {
     uint32_t *status;
 };
 long long block_score_tiles(int NB);
-cudaError_t launch_block_score(BlockScoreArgs a, cudaStream_t s);
+cudaError_t launch_block_score(BlockScoreArgs a, int num_sms, cudaStream_t s);
 
 // ---- eviction
 struct EvictArgs {
@@ -276,11 +275,12 @@ struct AddNormArgs {
     uint8_t *codes;              // [T][D] or null
     float *scales;               // [T][n_groups]
     int group, n_groups, scale_style;   // group 0: the whole row
+    int group_shift;             // set by the launcher: log2 of group
     const int32_t *n_live;       // [1] or null
     int T, D;
     uint32_t *status;
 };
-cudaError_t launch_add_rms_norm(const AddNormArgs &a, int num_sms, cudaStream_t s);
+cudaError_t launch_add_rms_norm(AddNormArgs a, int num_sms, cudaStream_t s);
 
 struct NormRopeArgs {
     const void *q;               // [T][n_head][D] (token stride q_stride) or null

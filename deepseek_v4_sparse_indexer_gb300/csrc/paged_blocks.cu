@@ -15,8 +15,8 @@ namespace {
 // ---- mean keys
 // One block of threads per page: 16 threads a 256-byte key, eight keys a thread (all
 // of their loads in flight), summed in fp32 in a fixed order: the thread's own, then
-// the two halves of a warp, then the warps.  Sequence b's pages that got rows are
-// dealt to gridDim.x / B blocks; a decode step has one or two.
+// the two halves of a warp, then the warps.  Every block scans the sequences' lengths
+// and takes every gridDim.x-th of the pages that got rows, whosever they are.
 // Bound: HBM (the keys); a decode step latency.
 constexpr int kKeyThreadsMax = 512;
 
@@ -32,33 +32,74 @@ DS4A_DEV void add8(float (&s)[8], const uint4 &v) {
 __global__ void __launch_bounds__(kKeyThreadsMax) block_keys_kernel(const __grid_constant__ BlockKeysArgs a) {
     // It writes the block counts that a top-k may read before its own wait: no
     // pdl_launch_dependents here, and a fence before the end.
+    extern __shared__ int s_cu[];                          // [B + 1] pages to do before each sequence's
     __shared__ float s_part[kKeyThreadsMax / 32][16][8];
+    __shared__ int s_warp[kKeyThreadsMax / 32];
     pdl_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
-    const int b = blockIdx.x / a.split, first_of = blockIdx.x - b * a.split;
     const int P = 1 << a.shift;
     const long long cap = static_cast<long long>(a.max_pages) << a.shift;
-    int n = a.n_rows[b], from = 0;
-    bool ok = n >= 0 && n <= cap;
-    n = static_cast<int>(min(max(static_cast<long long>(n), 0LL), cap));
-    if (a.first_row) {
-        from = a.first_row[b];
+    // rows of sequence b, and the first of them that is new
+    auto lengths = [&](int b, int &from, bool &ok) -> int {
+        const int raw = a.n_rows[b];
+        const int n = static_cast<int>(min(max(static_cast<long long>(raw), 0LL), cap));
+        ok = raw == n;
+        from = 0;
+        if (a.first_row) {
+            from = a.first_row[b];
+        } else if (a.cu_row) {
+            const long long first = static_cast<long long>(n) - a.cu_row[b + 1] + a.cu_row[b];
+            from = static_cast<int>(min(max(first, -1LL), n + 1LL));
+        }
         ok = ok && from >= 0 && from <= n;
-    } else if (a.cu_row) {
-        const long long add = static_cast<long long>(a.cu_row[b + 1]) - a.cu_row[b];
-        ok = ok && add >= 0 && add <= n;
-        from = static_cast<int>(n - min(max(add, 0LL), static_cast<long long>(n)));
+        from = min(max(from, 0), n);
+        return n;
+    };
+    // exclusive sums: thread t has sequences [t per, (t + 1) per)
+    const int per = (a.B + blockDim.x - 1) / blockDim.x, b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
+    int sum = 0;
+    for (int b = b0; b < b1; ++b) {
+        int from;
+        bool ok;
+        const int n = lengths(b, from, ok);
+        const int blocks = static_cast<int>((static_cast<long long>(n) + P - 1) >> a.shift);
+        const int todo = from < n ? blocks - (from >> a.shift) : 0;
+        s_cu[b + 1] = todo;
+        sum += todo;
+        if (blockIdx.x == 0) {
+            a.n_blocks[b] = blocks;
+            if (!ok) report(a.status, DS4A_DEV_BOUNDS);
+        }
     }
-    from = min(max(from, 0), n);
-    if (!ok && first_of == 0 && tid == 0) report(a.status, DS4A_DEV_BOUNDS);
-    const int blocks = static_cast<int>((static_cast<long long>(n) + P - 1) >> a.shift);
-    if (first_of == 0 && tid == 0) {
-        a.n_blocks[b] = blocks;
-        __threadfence();
+    if (blockIdx.x == 0) __threadfence();
+    int inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += v;
     }
-    if (from >= n) return;                                 // no row is new
+    if (lane == 31) s_warp[warp] = inc;
+    if (tid == 0) s_cu[0] = 0;
+    __syncthreads();
+    int base = inc - sum;
+    for (int w = 0; w < warp; ++w) base += s_warp[w];
+    for (int b = b0; b < b1; ++b) {
+        base += s_cu[b + 1];
+        s_cu[b + 1] = base;
+    }
+    __syncthreads();
+    const int total = s_cu[a.B];
     const int chunk = tid & 15, sub = tid >> 4, subs = blockDim.x >> 4;
-    for (int k = (from >> a.shift) + first_of; k < blocks; k += a.split) {
+    for (int x = blockIdx.x; x < total; x += gridDim.x) {
+        int b = 0, hi = a.B;                               // the last sequence with s_cu[b] <= x
+        while (hi - b > 1) {
+            const int mid = (b + hi) >> 1;
+            if (s_cu[mid] <= x) b = mid;
+            else hi = mid;
+        }
+        int from;
+        bool ok;
+        const int n = lengths(b, from, ok), k = (from >> a.shift) + (x - s_cu[b]);
         const int page = a.table[b * a.table_stride + k];
         if (page < 0 || page >= a.n_pages) {
             if (tid == 0) report(a.status, DS4A_DEV_BOUNDS);
@@ -103,18 +144,30 @@ __global__ void __launch_bounds__(kKeyThreadsMax) block_keys_kernel(const __grid
 }
 
 // ---- scores
+//     s[u][b] = sum_h w[u][h] max(0, iq[u][h] . bk[table[u][b]])
 // A block of four warps per 128 blocks of a unit: their keys, 256-byte rows anywhere
 // in the store, and the unit's queries come by cp.async into two 64-dim halves of
 // 128-byte rows (128B-swizzled), one UMMA chain gives D[128 blocks x 64 heads] in
-// TMEM, and each thread sums its block's 64 weighted, rectified products.  Four such
-// blocks share an SM, so that one's loads cover another's chain.
-// Bound: HBM on long contexts; a decode step of a small batch is latency.
+// TMEM, and each thread sums its block's 64 weighted, rectified products.  For batches
+// of so few tiles that four of these a SM take them all at once: latency.
 constexpr int kTile = 128;
 constexpr int kScoreThreads = 128;
 constexpr int kHalfA = kTile * 128, kHalfB = kNIdxHead * 128;
 constexpr int kOffA = 0, kOffB = 2 * kHalfA, kOffW = kOffB + 2 * kHalfB, kOffPage = kOffW + kNIdxHead * 4;
 constexpr int kOffBar = kOffPage + kTile * 4, kScoreSmem = kOffBar + 16 + 1024;
 constexpr uint32_t kScoreCols = 64;
+
+// Block b's score (nothing past the unit's n blocks).
+DS4A_DEV void store_score(const BlockScoreArgs &a, int u, int b, int n, bool there, float s) {
+    if (b >= n) return;
+    if (!there) {
+        s = -__int_as_float(0x7f800000);
+        report(a.status, DS4A_DEV_BOUNDS);
+    } else if (b < a.n_first || b >= n - a.n_last) {
+        s = __int_as_float(0x7f800000);
+    }
+    a.scores[static_cast<long long>(u) * a.NB_cap + b] = s;
+}
 
 __global__ void __launch_bounds__(kScoreThreads) block_score_kernel(const __grid_constant__ BlockScoreArgs a) {
     pdl_launch_dependents();
@@ -194,16 +247,7 @@ __global__ void __launch_bounds__(kScoreThreads) block_score_kernel(const __grid
                 s3 = fmaf(w.w, fmaxf(__uint_as_float(v[h + 3]), 0.f), s3);
             }
         }
-        if (b < n) {
-            float s = (s0 + s1) + (s2 + s3);
-            if (page < 0) {
-                s = -__int_as_float(0x7f800000);
-                report(a.status, DS4A_DEV_BOUNDS);
-            } else if (b < a.n_first || b >= n - a.n_last) {
-                s = __int_as_float(0x7f800000);
-            }
-            a.scores[static_cast<long long>(u) * a.NB_cap + b] = s;
-        }
+        store_score(a, u, b, n, page >= 0, (s0 + s1) + (s2 + s3));
     } else {
         if (lane == 0) report(a.status, DS4A_DEV_TIMEOUT);
         wait_drain(bar, 0);
@@ -216,29 +260,301 @@ __global__ void __launch_bounds__(kScoreThreads) block_score_kernel(const __grid
     }
 }
 
+// ---- scores of a large batch
+// One block of threads per SM, persistent over an equal, contiguous share of the
+// batch's 128-block tiles: four warps bring the tiles' keys (and a unit's queries with
+// its first tile) by cp.async into five buffers, one issues the UMMAs into four TMEM
+// accumulators, four sum up.  A tile's copies are handed over three tiles later, so
+// that the copies of four are in flight.
+constexpr int kStages = 5, kAccs = 4, kAhead = 3, kIqBufs = 4;
+static_assert(kIqBufs > kAhead && kStages > kAhead, "a buffer's last user has been handed over before it is waited for");
+constexpr int kMmaWarp = 4, kFirstCopyWarp = 5, kCopyWarps = 4;
+constexpr int kScanThreads = (kFirstCopyWarp + kCopyWarps) * 32;
+constexpr int kOffKeys = 0, kOffIq = kStages * 2 * kHalfA, kOffScanBar = kOffIq + kIqBufs * 2 * kHalfB;
+constexpr int kScanBars = 2 * kStages + 2 * kAccs + kIqBufs + 1;
+constexpr int kOffScanMisc = kOffScanBar + kScanBars * 8, kScanSmem = kOffScanMisc + 16 + 1024;
+static_assert(kScanSmem <= 232448, "shared memory budget");
+
+// The tiles of a share in order: tile t of unit u, of n blocks.
+struct BlockWalk {
+    int u, t, n;
+    long long left;              // tiles of the share from this one on
+};
+DS4A_DEV int blocks_of(const BlockScoreArgs &a, int u) { return min(max(a.n_blocks[u], 0), a.lim); }
+DS4A_DEV void settle_on(const BlockScoreArgs &a, BlockWalk &w) {     // on a unit that has tile t
+    if (w.left <= 0) return;
+    for (w.n = blocks_of(a, w.u); w.t * kTile >= w.n; w.n = blocks_of(a, w.u)) {
+        w.t = 0;
+        if (++w.u >= a.U) {                        // (never: the share's tiles exist)
+            w.left = 0;
+            return;
+        }
+    }
+}
+DS4A_DEV void next_tile(const BlockScoreArgs &a, BlockWalk &w) {
+    --w.left;
+    ++w.t;
+    settle_on(a, w);
+}
+
+// This block's share [c T / G, (c + 1) T / G) of the batch's T tiles.  All threads call it.
+DS4A_DEV BlockWalk share_of(const BlockScoreArgs &a) {
+    __shared__ long long s_warp[kScanThreads / 32];
+    __shared__ int s_at[2];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (a.U + kScanThreads - 1) / kScanThreads, u0 = min(tid * per, a.U), u1 = min(u0 + per, a.U);
+    long long sum = 0;
+    bool ok = true;
+    for (int u = u0; u < u1; ++u) {
+        ok = ok && a.n_blocks[u] == blocks_of(a, u);
+        sum += (blocks_of(a, u) + kTile - 1) / kTile;
+    }
+    if (!ok && blockIdx.x == 0) report(a.status, DS4A_DEV_BOUNDS);
+    long long inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += v;
+    }
+    if (lane == 31) s_warp[warp] = inc;
+    __syncthreads();
+    long long start = inc - sum, T = 0;
+    for (int w = 0; w < kScanThreads / 32; ++w) {
+        if (w < warp) start += s_warp[w];
+        T += s_warp[w];
+    }
+    const long long lo = T * blockIdx.x / gridDim.x, hi = T * (blockIdx.x + 1) / gridDim.x;
+    for (int u = u0; u < u1; ++u) {
+        const int nt = (blocks_of(a, u) + kTile - 1) / kTile;
+        if (start <= lo && lo < start + nt) {
+            s_at[0] = u;
+            s_at[1] = static_cast<int>(lo - start);
+        }
+        start += nt;
+    }
+    __syncthreads();
+    BlockWalk w = {0, 0, 0, hi - lo};
+    if (w.left > 0) {
+        w.u = s_at[0];
+        w.t = s_at[1];
+        settle_on(a, w);
+    }
+    return w;
+}
+
+__global__ void __launch_bounds__(kScanThreads, 1) block_scan_kernel(const __grid_constant__ BlockScoreArgs a) {
+    pdl_launch_dependents();
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kOffScanBar);   // [kStages] keys (and queries) landed
+    uint64_t *empty = full + kStages;                                    // [kStages] read by the UMMAs
+    uint64_t *acc_full = empty + kStages, *acc_empty = acc_full + kAccs; // [kAccs]
+    uint64_t *iq_empty = acc_empty + kAccs;                              // [kIqBufs] a unit's UMMAs done
+    uint64_t *drain = iq_empty + kIqBufs;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + kOffScanMisc);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kOffScanMisc + 4);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&full[s], kCopyWarps);
+            mbar_init(&empty[s], 1);
+        }
+        for (int c = 0; c < kAccs; ++c) {
+            mbar_init(&acc_full[c], 1);
+            mbar_init(&acc_empty[c], 4);
+        }
+        for (int k = 0; k < kIqBufs; ++k) mbar_init(&iq_empty[k], 1);
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        mbar_fence_init();
+    }
+    if (warp == kMmaWarp) tmem_alloc(tmem_slot, kAccs * 64);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    pdl_wait();
+    BlockWalk w = share_of(a);
+    const uint32_t tmem = *tmem_slot, base = smem_u32(smem);
+    bool ok = true;
+    if (warp >= kFirstCopyWarp) {
+        // ------------------------------------------------------------ copies
+        // Copy warp p brings rows 2p, 2p + 1, 8 + 2p, ...: two rows an instruction, lane l
+        // 16-byte chunk l % 16 of row l / 16.  Lane l looks up the page of the tile's row
+        // 2p + l % 2 + 8 (l / 2) one tile ahead.
+        const int p = warp - kFirstCopyWarp, c = lane & 15, half = lane >> 4;
+        auto page_of = [&](const BlockWalk &x) -> int {
+            const int b = x.t * kTile + 2 * p + (lane & 1) + 8 * (lane >> 1);
+            if (x.left <= 0 || b >= x.n) return -1;
+            const int page = __ldg(a.table + x.u * a.table_stride + b);
+            return page < a.n_pages ? page : -1;
+        };
+        uint32_t eph = 0, iqph = 0;
+        int s = 0, ib = 0, last_u = -1, issued = 0, handed = 0;
+        auto hand_over = [&]() {                           // the oldest tile not yet handed over
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&full[handed % kStages]);
+            ++handed;
+        };
+        int page = page_of(w);
+        while (w.left > 0) {
+            BlockWalk n = w;
+            next_tile(a, n);
+            const int next_page = page_of(n);
+            if (!(ok = warp_wait(&empty[s], ((eph >> s) & 1) ^ 1, abort_flag))) break;
+            eph ^= 1u << s;
+            const uint32_t keys = base + kOffKeys + s * 2 * kHalfA + (c >> 3) * kHalfA;
+#pragma unroll 4
+            for (int i = 0; i < kTile / 8; ++i) {
+                const int r = 2 * p + half + 8 * i, pg = __shfl_sync(0xffffffffu, page, 2 * i + half);
+                cp_async16(keys + r * 128 + (((c & 7) ^ (r & 7)) << 4),
+                           a.block_keys + static_cast<long long>(max(pg, 0)) * kIdxDim + c * 8, pg >= 0 ? 16u : 0u);
+            }
+            if (w.u != last_u) {
+                // its first tile in this share: the queries, once the UMMAs of the unit that had
+                // the buffer have read theirs
+                if (!(ok = warp_wait(&iq_empty[ib], ((iqph >> ib) & 1) ^ 1, abort_flag))) break;
+                iqph ^= 1u << ib;
+                const uint32_t dst = base + kOffIq + ib * 2 * kHalfB + (c >> 3) * kHalfB;
+                const uint16_t *iq = a.iq + static_cast<long long>(w.u) * kNIdxHead * kIdxDim + c * 8;
+#pragma unroll
+                for (int i = 0; i < kNIdxHead / 8; ++i) {
+                    const int r = 2 * p + half + 8 * i;
+                    cp_async16(dst + r * 128 + (((c & 7) ^ (r & 7)) << 4), iq + r * kIdxDim, 16u);
+                }
+                ib = ib == kIqBufs - 1 ? 0 : ib + 1;
+                last_u = w.u;
+            }
+            cp_async_commit();
+            if (++issued - handed > kAhead) {
+                cp_async_wait<kAhead>();
+                hand_over();
+            }
+            s = s == kStages - 1 ? 0 : s + 1;
+            w = n;
+            page = next_page;
+        }
+        cp_async_wait<0>();                                // also when a wait gave up
+        if (ok)
+            while (handed < issued) hand_over();
+    } else if (warp == kMmaWarp) {
+        // ------------------------------------------------------------ UMMA issuer
+        constexpr uint32_t id = idesc_bf16_f32(kTile, kNIdxHead);
+        uint32_t fph = 0, aph = 0;
+        int s = 0, ab = 0, ib = -1, last_u = -1;
+        while (w.left > 0) {
+            if (w.u != last_u) {
+                ib = ib == kIqBufs - 1 ? 0 : ib + 1;
+                last_u = w.u;
+            }
+            if (!(ok = warp_wait(&acc_empty[ab], ((aph >> ab) & 1) ^ 1, abort_flag))) break;
+            aph ^= 1u << ab;
+            if (!(ok = warp_wait(&full[s], (fph >> s) & 1, abort_flag))) break;
+            fph ^= 1u << s;
+            tc_fence_after();
+            const uint32_t keys = base + kOffKeys + s * 2 * kHalfA, iq = base + kOffIq + ib * 2 * kHalfB;
+#pragma unroll
+            for (int k = 0; k < kIdxDim / 16; ++k)
+                umma_elect(tmem + ab * 64, sw128_kmajor_desc(keys + (k >> 2) * kHalfA + (k & 3) * 32),
+                           sw128_kmajor_desc(iq + (k >> 2) * kHalfB + (k & 3) * 32), id, k > 0 ? 1u : 0u);
+            commit_elect(&empty[s]);
+            commit_elect(&acc_full[ab]);
+            next_tile(a, w);
+            if (w.left <= 0 || w.u != last_u) commit_elect(&iq_empty[ib]);
+            s = s == kStages - 1 ? 0 : s + 1;
+            ab = ab == kAccs - 1 ? 0 : ab + 1;
+        }
+        commit_elect(drain);
+        wait_drain(drain, 0);
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------ scores
+        uint32_t fph = 0;
+        int ab = 0, last_u = -1;
+        float4 wt[16];
+        auto page_ok = [&](const BlockWalk &x) -> bool {
+            const int b = x.t * kTile + tid;
+            if (x.left <= 0 || b >= x.n) return true;
+            const int page = __ldg(a.table + x.u * a.table_stride + b);
+            return page >= 0 && page < a.n_pages;
+        };
+        bool there = page_ok(w);
+        while (w.left > 0) {
+            if (w.u != last_u) {
+                last_u = w.u;
+                const float *src = a.w + static_cast<long long>(w.u) * kNIdxHead;   // (4-byte aligned)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) wt[i] = make_float4(src[4 * i], src[4 * i + 1], src[4 * i + 2], src[4 * i + 3]);
+            }
+            BlockWalk n = w;
+            next_tile(a, n);
+            const bool next_there = page_ok(n);
+            if (!(ok = warp_wait(&acc_full[ab], (fph >> ab) & 1, abort_flag))) break;
+            fph ^= 1u << ab;
+            tc_fence_after();
+            float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+                uint32_t v[32];
+                tmem_ld32(tmem + (static_cast<uint32_t>(warp * 32) << 16) + ab * 64 + hh * 32, v);
+                tmem_wait_ld(v);
+#pragma unroll
+                for (int h = 0; h < 32; h += 4) {
+                    const float4 q = wt[hh * 8 + h / 4];
+                    s0 = fmaf(q.x, fmaxf(__uint_as_float(v[h]), 0.f), s0);
+                    s1 = fmaf(q.y, fmaxf(__uint_as_float(v[h + 1]), 0.f), s1);
+                    s2 = fmaf(q.z, fmaxf(__uint_as_float(v[h + 2]), 0.f), s2);
+                    s3 = fmaf(q.w, fmaxf(__uint_as_float(v[h + 3]), 0.f), s3);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&acc_empty[ab]);
+            store_score(a, w.u, w.t * kTile + tid, w.n, there, (s0 + s1) + (s2 + s3));
+            ab = ab == kAccs - 1 ? 0 : ab + 1;
+            w = n;
+            there = next_there;
+        }
+    }
+    if (!ok) {
+        *abort_flag = 1;
+        if (lane == 0) report(a.status, DS4A_DEV_TIMEOUT);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kAccs * 64);
+    }
+}
+
 }  // namespace
 
-cudaError_t launch_block_keys(BlockKeysArgs a, int num_sms, cudaStream_t s) {
+cudaError_t launch_block_keys(const BlockKeysArgs &a, int num_sms, cudaStream_t s) {
     // eight keys a thread where the page has them: 2 P threads
     const int P = 1 << a.shift;
     const int threads = 2 * P < 32 ? 32 : 2 * P > kKeyThreadsMax ? kKeyThreadsMax : 2 * P;
-    // enough blocks to fill every SM with threads, at most one a page
-    const long long fill = static_cast<long long>(num_sms) * (2048 / threads < 32 ? 2048 / threads : 32);
-    long long split = (fill + a.B - 1) / a.B;
-    if (split > a.max_pages) split = a.max_pages;
-    if (split * a.B > 0x7fffffffLL) return cudaErrorInvalidValue;
-    a.split = static_cast<int>(split);
-    return launch_k(block_keys_kernel, dim3(static_cast<unsigned>(split * a.B)), dim3(static_cast<unsigned>(threads)), 0, s, a);
+    const size_t smem = (static_cast<size_t>(a.B) + 1) * sizeof(int);
+    // enough blocks for 1,536 threads an SM (fewer where their lists take its shared memory), at most one a page
+    long long per_sm = 1536 / threads < 32 ? 1536 / threads : 32;
+    if (per_sm * (smem + 10240) > 220 * 1024) per_sm = 220 * 1024 / (smem + 10240);
+    const long long most = per_sm * num_sms, want = static_cast<long long>(a.B) * a.max_pages;
+    return launch_k(block_keys_kernel, dim3(static_cast<unsigned>(want < most ? want : most)), dim3(static_cast<unsigned>(threads)),
+                    smem, s, a);
 }
 
 long long block_score_tiles(int NB) { return (static_cast<long long>(NB) + kTile - 1) / kTile; }
 
-cudaError_t launch_block_score(BlockScoreArgs a, cudaStream_t s) {
-    cudaError_t e = cudaFuncSetAttribute(block_score_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kScoreSmem);
-    if (e != cudaSuccess) return e;
+cudaError_t launch_block_score(BlockScoreArgs a, int num_sms, cudaStream_t s) {
     a.tiles = static_cast<int>(block_score_tiles(a.lim));
-    return launch_k(block_score_kernel, dim3(static_cast<unsigned>(static_cast<long long>(a.U) * a.tiles)), dim3(kScoreThreads),
-                    kScoreSmem, s, a);
+    const long long most = static_cast<long long>(a.U) * a.tiles;
+    const bool scan = most > 4LL * num_sms;
+    void (*kern)(BlockScoreArgs) = scan ? block_scan_kernel : block_score_kernel;
+    const int smem = scan ? kScanSmem : kScoreSmem;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    return launch_k(kern, dim3(static_cast<unsigned>(scan ? num_sms : most)), dim3(scan ? kScanThreads : kScoreThreads),
+                    static_cast<size_t>(smem), s, a);
 }
 
 }  // namespace ds4a

@@ -10,8 +10,8 @@
 //
 // evict_select_kernel, a block of 1,024 threads per sequence: the kept rows' smallest
 // key by a radix select (11, 11 and 10 bits of an order-preserving key; keys in shared
-// memory where they fit), then the kept rows' numbers by a count and a fill over the
-// warps' runs of rows, and the masses in their new places.  evict_move_kernel: the
+// memory where they fit), then the kept rows' slots and masses in their new places, by
+// counts over the warps' runs of rows.  evict_move_kernel: the
 // copies, eight rows a warp (all of their loads in flight), and the lists.
 // Bound: the copies HBM; a few sequences the select's chain of passes.
 #include "common.cuh"
@@ -22,6 +22,8 @@ namespace {
 
 constexpr int kThreads = 1024, kWarps = kThreads / 32;
 constexpr int kBins = 2048;
+constexpr int kBatch = 8;                     // rows a thread has in flight in the passes over all rows
+constexpr int kRun = 8;                       // rows a thread places at a time
 constexpr int kKeysMost = 49152;              // keys that fit into shared memory (192 KB)
 
 // ---- workspace (ints): [0] the list's head, then per sequence: rows before (0: left
@@ -104,16 +106,29 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const __grid_
     // ---- the least key that is kept
     const float *mass = a.mass + b * a.mass_stride;
     const long long plane = a.B * a.mass_stride;
-    auto key_of = [&](int r) -> uint32_t {
-        float m = mass[r];
-        for (int p = 1; p < a.n_planes; ++p) m += mass[p * plane + r];
-        return m == m ? float_key(m) : 0u;
-    };
     const int lo = a.first, hi = n - a.recent;             // the rows that compete
+    // Keys of rows r0 + k kThreads, k < kBatch, with all of their loads in flight (0 past hi).
+    auto keys_of = [&](int r0, uint32_t (&key)[kBatch]) {
+        float m[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) m[k] = r0 + k * kThreads < hi ? mass[r0 + k * kThreads] : 0.f;
+        for (int p = 1; p < a.n_planes; ++p) {
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k)
+                if (r0 + k * kThreads < hi) m[k] += mass[p * plane + r0 + k * kThreads];
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) key[k] = m[k] == m[k] ? float_key(m[k]) : 0u;
+    };
     if (a.keys_in_smem) {
-        for (int r = lo + tid; r < hi; r += kThreads) s_keys[r] = key_of(r);
+        for (int r0 = lo + tid; r0 < hi; r0 += kBatch * kThreads) {
+            uint32_t key[kBatch];
+            keys_of(r0, key);
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k)
+                if (r0 + k * kThreads < hi) s_keys[r0 + k * kThreads] = key[k];
+        }
     }
-    auto key_at = [&](int r) -> uint32_t { return a.keys_in_smem ? s_keys[r] : key_of(r); };
     uint32_t left = static_cast<uint32_t>(a.keep - a.first - a.recent);   // of them are kept
     uint32_t least = 0xffffffffu;                          // none: no key is above it, and none of its like is taken
     if (left > 0) {
@@ -125,9 +140,18 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const __grid_
             const uint32_t above = pass == 0 ? 0u : 0xffffffffu << (shift + bits);
             for (int i = tid; i < kBins; i += kThreads) s_hist[i] = 0u;
             __syncthreads();
-            for (int r = lo + tid; r < hi; r += kThreads) {
-                const uint32_t k = key_at(r);
-                if ((k & above) == prefix) atomicAdd(&s_hist[(k >> shift) & ((1u << bits) - 1u)], 1u);
+            for (int r0 = lo + tid; r0 < hi; r0 += kBatch * kThreads) {
+                uint32_t key[kBatch];
+                if (a.keys_in_smem) {
+#pragma unroll
+                    for (int k = 0; k < kBatch; ++k) key[k] = r0 + k * kThreads < hi ? s_keys[r0 + k * kThreads] : 0u;
+                } else {
+                    keys_of(r0, key);
+                }
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k)
+                    if (r0 + k * kThreads < hi && (key[k] & above) == prefix)
+                        atomicAdd(&s_hist[(key[k] >> shift) & ((1u << bits) - 1u)], 1u);
             }
             __syncthreads();
             // thread t: bins 2t and 2t + 1, counted from the top
@@ -141,9 +165,7 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const __grid_
             }
             if (lane == 31) s_gt[warp] = static_cast<int>(inc);
             __syncthreads();
-            uint32_t base = 0;
-            for (int w = 0; w < warp; ++w) base += static_cast<uint32_t>(s_gt[w]);
-            const uint32_t ahead = base + inc - (c1 + c0);
+            const uint32_t ahead = static_cast<uint32_t>(warp_sum(lane < warp ? s_gt[lane] : 0)) + inc - (c1 + c0);
             if (ahead < left && left <= ahead + c1) {
                 s_bin = static_cast<uint32_t>(top);
                 s_left = left - ahead;
@@ -153,81 +175,79 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const __grid_
             }
             __syncthreads();
             prefix |= s_bin << shift;
-            left = s_left;
-            __syncthreads();                               // before the next pass writes them
+            left = s_left;                                 // (s_bin, s_left: written again two barriers later)
         }
         least = prefix;                                    // `left` rows of this key are kept, the lowest
-    } else {
-        __syncthreads();
     }
 
-    // ---- the kept rows' numbers, in order: warp w has rows [w run, (w + 1) run)
-    const int run = ((n + kWarps - 1) / kWarps + 31) & ~31;
-    const int r0 = min(warp * run, n), r1 = min(r0 + run, n);
-    auto is_gt = [&](int r) -> bool { return r < lo || r >= hi || key_at(r) > least; };
-    auto is_eq = [&](int r) -> bool { return r >= lo && r < hi && key_at(r) == least; };
-    int gt = 0, eq = 0;
-    for (int r = r0 + lane; r < r1; r += 32) {
-        gt += is_gt(r);
-        eq += is_eq(r);
-    }
-    gt = warp_sum(gt);
-    eq = warp_sum(eq);
-    __syncthreads();
-    if (lane == 0) {
-        s_gt[warp] = gt;
-        s_eq[warp] = eq;
-    }
-    __syncthreads();
-    int gt0 = 0, eq0 = 0;
-    for (int w = 0; w < warp; ++w) {
-        gt0 += s_gt[w];
-        eq0 += s_eq[w];
-    }
+    // ---- the kept rows' places, slots and masses, kRun x 1,024 rows at a time: warp w has
+    // rows [w kRun 32, (w + 1) kRun 32) of them.  mass_out may be mass: row r's place is
+    // j <= r, so a part's places lie before the rows of the later ones, and within a part
+    // all loads come before all stores.
     int32_t *src = ws.src + static_cast<long long>(b) * a.keep;
+    float *mass_out = a.mass_out + b * a.mass_stride;
     const int take = static_cast<int>(left);               // of the rows with the least key
     const uint32_t below = (1u << lane) - 1u;
-    for (int r = r0; r < r1; r += 32) {                    // (whole warps: the ballots)
-        const bool in = r + lane < r1;
-        const bool g = in && is_gt(r + lane), e = in && is_eq(r + lane);
-        const uint32_t bg = __ballot_sync(0xffffffffu, g), be = __ballot_sync(0xffffffffu, e);
-        const int eq_at = eq0 + __popc(be & below);
-        // kept rows before this one: the greater ones and the taken ones of the least key
-        const int j = gt0 + __popc(bg & below) + min(eq_at, take);
-        if ((g || (e && eq_at < take)) && j < a.keep) src[j] = r + lane;
-        gt0 += __popc(bg);
-        eq0 += __popc(be);
-    }
-    __syncthreads();
-
-    // ---- masses in their new places and slots in place of row numbers.  mass_out may
-    // be mass: entry j comes from row r_j >= j, so a later part's sources lie behind an
-    // earlier part's places, and within a part all loads come before all stores.
-    float *mass_out = a.mass_out + b * a.mass_stride;
-    constexpr int kPart = 4;
-    for (int j0 = 0; j0 < a.keep; j0 += kPart * kThreads) {
-        int row[kPart];
+    int gt_base = 0, eq_base = 0;                          // of the parts before
+    for (int part = 0; part < n; part += kRun * kThreads) {
+        const int r0 = part + warp * kRun * 32 + lane;     // this lane's rows: r0 + 32 k
+        uint32_t bg[kRun], be[kRun];
+        int gt = 0, eq = 0;
+        __syncthreads();                                   // s_keys; s_gt and s_eq of the part before
 #pragma unroll
-        for (int i = 0; i < kPart; ++i) {
-            const int j = j0 + i * kThreads + tid;
-            row[i] = j < a.keep ? src[j] : 0;
+        for (int k = 0; k < kRun; ++k) {
+            const int r = r0 + 32 * k;
+            bool g = r < n && (r < lo || r >= hi), e = false;
+            if (r >= lo && r < hi) {
+                uint32_t key;
+                if (a.keys_in_smem) {
+                    key = s_keys[r];
+                } else {
+                    float m = mass[r];
+                    for (int p = 1; p < a.n_planes; ++p) m += mass[p * plane + r];
+                    key = m == m ? float_key(m) : 0u;
+                }
+                g = key > least;
+                e = key == least;
+            }
+            bg[k] = __ballot_sync(0xffffffffu, g);
+            be[k] = __ballot_sync(0xffffffffu, e);
+            gt += __popc(bg[k]);
+            eq += __popc(be[k]);
+        }
+        if (lane == 0) {
+            s_gt[warp] = gt;
+            s_eq[warp] = eq;
+        }
+        __syncthreads();
+        int gt0 = gt_base + warp_sum(lane < warp ? s_gt[lane] : 0), eq0 = eq_base + warp_sum(lane < warp ? s_eq[lane] : 0);
+        gt_base += warp_sum(s_gt[lane]);
+        eq_base += warp_sum(s_eq[lane]);
+        int place[kRun], page[kRun];                       // place: -1: not kept
+#pragma unroll
+        for (int k = 0; k < kRun; ++k) {
+            const int r = r0 + 32 * k;
+            const bool g = bg[k] >> lane & 1u, e = be[k] >> lane & 1u;
+            const int eq_at = eq0 + __popc(be[k] & below);
+            // kept rows before this one: the greater ones and the taken ones of the least key
+            const int j = gt0 + __popc(bg[k] & below) + min(eq_at, take);
+            place[k] = (g || (e && eq_at < take)) && j < a.keep ? j : -1;
+            page[k] = place[k] >= 0 ? table[r >> a.shift] : 0;
+            gt0 += __popc(bg[k]);
+            eq0 += __popc(be[k]);
         }
         for (int p = 0; p < a.n_planes; ++p) {
-            float m[kPart];
+            float m[kRun];
 #pragma unroll
-            for (int i = 0; i < kPart; ++i) m[i] = mass[p * plane + row[i]];
+            for (int k = 0; k < kRun; ++k) m[k] = place[k] >= 0 ? mass[p * plane + r0 + 32 * k] : 0.f;
             __syncthreads();
 #pragma unroll
-            for (int i = 0; i < kPart; ++i) {
-                const int j = j0 + i * kThreads + tid;
-                if (j < a.keep) mass_out[p * plane + j] = m[i];
-            }
+            for (int k = 0; k < kRun; ++k)
+                if (place[k] >= 0) mass_out[p * plane + place[k]] = m[k];
         }
 #pragma unroll
-        for (int i = 0; i < kPart; ++i) {
-            const int j = j0 + i * kThreads + tid;
-            if (j < a.keep) src[j] = (table[row[i] >> a.shift] << a.shift) + (row[i] & (P - 1));
-        }
+        for (int k = 0; k < kRun; ++k)
+            if (place[k] >= 0) src[place[k]] = (page[k] << a.shift) + ((r0 + 32 * k) & (P - 1));
     }
     __syncthreads();
     for (int p = 0; p < a.n_planes; ++p)
@@ -299,11 +319,20 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
     // ---- copies
     const int n_warps = gridDim.x * kMoveWarps, me = blockIdx.x * kMoveWarps + warp;
     const int parts = (a.keep + kRows - 1) / kRows;
-    for (long long x = me; x < static_cast<long long>(E) * parts; x += n_warps) {
-        const int q = static_cast<int>(x / parts), b = s_seq[q], j0 = static_cast<int>(x - static_cast<long long>(q) * parts) * kRows;
-        const int j = min(j0 + (lane & (kRows - 1)), a.keep - 1);   // (rows past the last repeat it)
-        const int from = ws.src[static_cast<long long>(b) * a.keep + j];
-        const int to = (ws.pages[static_cast<long long>(b) * a.need + (j >> a.shift)] << a.shift) + (j & ((1 << a.shift) - 1));
+    const long long items = static_cast<long long>(E) * parts;
+    // Slots that lane l's row (l % kRows of an item's) comes from and goes to (rows past
+    // the last repeat it); the next item's are looked up while this one's rows arrive.
+    auto look_up = [&](long long x, int &from, int &to) {
+        if (x >= items) return;
+        const int q = static_cast<int>(x / parts), b = s_seq[q];
+        const int j = min(static_cast<int>(x - static_cast<long long>(q) * parts) * kRows + (lane & (kRows - 1)), a.keep - 1);
+        from = ws.src[static_cast<long long>(b) * a.keep + j];
+        to = (ws.pages[static_cast<long long>(b) * a.need + (j >> a.shift)] << a.shift) + (j & ((1 << a.shift) - 1));
+    };
+    int from = 0, to = 0, next_from = 0, next_to = 0;
+    look_up(me, from, to);
+    for (long long x = me; x < items; x += n_warps) {
+        look_up(x + n_warps, next_from, next_to);
         constexpr int kWide = FP8 ? 512 : 1024, kLoads = kWide / 512;
         uint4 v[kRows][kLoads], k[kRows / 2];
         float sc = 0.f;
@@ -337,6 +366,8 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
             }
         }
         if (FP8 && lane < kRows) a.row_scale[to] = sc;
+        from = next_from;
+        to = next_to;
     }
 
     // ---- tables and the free list: a warp per evicted sequence, from the last warp on
