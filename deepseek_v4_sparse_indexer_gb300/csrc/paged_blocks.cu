@@ -262,13 +262,14 @@ __global__ void __launch_bounds__(kScoreThreads) block_score_kernel(const __grid
 
 // ---- scores of a large batch
 // One block of threads per SM, persistent over an equal, contiguous share of the
-// batch's 128-block tiles: four warps bring the tiles' keys (and a unit's queries with
+// batch's 128-block tiles: eight warps bring the tiles' keys (and a unit's queries with
 // its first tile) by cp.async into five buffers, one issues the UMMAs into four TMEM
 // accumulators, four sum up.  A tile's copies are handed over three tiles later, so
 // that the copies of four are in flight.
 constexpr int kStages = 5, kAccs = 4, kAhead = 3, kIqBufs = 4;
 static_assert(kIqBufs > kAhead && kStages > kAhead, "a buffer's last user has been handed over before it is waited for");
-constexpr int kMmaWarp = 4, kFirstCopyWarp = 5, kCopyWarps = 4;
+constexpr int kMmaWarp = 4, kFirstCopyWarp = 5, kCopyWarps = 8;
+constexpr int kPassRows = 2 * kCopyWarps;     // rows that the copy warps bring at a time
 constexpr int kScanThreads = (kFirstCopyWarp + kCopyWarps) * 32;
 constexpr int kOffKeys = 0, kOffIq = kStages * 2 * kHalfA, kOffScanBar = kOffIq + kIqBufs * 2 * kHalfB;
 constexpr int kScanBars = 2 * kStages + 2 * kAccs + kIqBufs + 1;
@@ -378,13 +379,13 @@ __global__ void __launch_bounds__(kScanThreads, 1) block_scan_kernel(const __gri
     bool ok = true;
     if (warp >= kFirstCopyWarp) {
         // ------------------------------------------------------------ copies
-        // Copy warp p brings rows 2p, 2p + 1, 8 + 2p, ...: two rows an instruction, lane l
+        // Copy warp p brings rows 2p and 2p + 1 of every 16: two rows an instruction, lane l
         // 16-byte chunk l % 16 of row l / 16.  Lane l looks up the page of the tile's row
-        // 2p + l % 2 + 8 (l / 2) one tile ahead.
+        // 2p + l % 2 + 16 (l / 2) one tile ahead.
         const int p = warp - kFirstCopyWarp, c = lane & 15, half = lane >> 4;
         auto page_of = [&](const BlockWalk &x) -> int {
-            const int b = x.t * kTile + 2 * p + (lane & 1) + 8 * (lane >> 1);
-            if (x.left <= 0 || b >= x.n) return -1;
+            const int r = 2 * p + (lane & 1) + kPassRows * (lane >> 1), b = x.t * kTile + r;
+            if (x.left <= 0 || r >= kTile || b >= x.n) return -1;
             const int page = __ldg(a.table + x.u * a.table_stride + b);
             return page < a.n_pages ? page : -1;
         };
@@ -404,9 +405,9 @@ __global__ void __launch_bounds__(kScanThreads, 1) block_scan_kernel(const __gri
             if (!(ok = warp_wait(&empty[s], ((eph >> s) & 1) ^ 1, abort_flag))) break;
             eph ^= 1u << s;
             const uint32_t keys = base + kOffKeys + s * 2 * kHalfA + (c >> 3) * kHalfA;
-#pragma unroll 4
-            for (int i = 0; i < kTile / 8; ++i) {
-                const int r = 2 * p + half + 8 * i, pg = __shfl_sync(0xffffffffu, page, 2 * i + half);
+#pragma unroll
+            for (int i = 0; i < kTile / kPassRows; ++i) {
+                const int r = 2 * p + half + kPassRows * i, pg = __shfl_sync(0xffffffffu, page, 2 * i + half);
                 cp_async16(keys + r * 128 + (((c & 7) ^ (r & 7)) << 4),
                            a.block_keys + static_cast<long long>(max(pg, 0)) * kIdxDim + c * 8, pg >= 0 ? 16u : 0u);
             }
@@ -418,8 +419,8 @@ __global__ void __launch_bounds__(kScanThreads, 1) block_scan_kernel(const __gri
                 const uint32_t dst = base + kOffIq + ib * 2 * kHalfB + (c >> 3) * kHalfB;
                 const uint16_t *iq = a.iq + static_cast<long long>(w.u) * kNIdxHead * kIdxDim + c * 8;
 #pragma unroll
-                for (int i = 0; i < kNIdxHead / 8; ++i) {
-                    const int r = 2 * p + half + 8 * i;
+                for (int i = 0; i < kNIdxHead / kPassRows; ++i) {
+                    const int r = 2 * p + half + kPassRows * i;
                     cp_async16(dst + r * 128 + (((c & 7) ^ (r & 7)) << 4), iq + r * kIdxDim, 16u);
                 }
                 ib = ib == kIqBufs - 1 ? 0 : ib + 1;

@@ -58,6 +58,8 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const __grid_
     const int cap = a.max_pages << a.shift;
     const EvictWs ws = evict_ws(a.ws, a.B, a.need);
     pdl_wait();
+    int before = 0;
+    for (int k = tid; k < b; k += kThreads) before += min(max(a.n_rows[k], 0), cap) > a.limit;
     const int n_raw = a.n_rows[b], n = min(max(n_raw, 0), cap);
     const int head = a.free_head[0];
     if (tid == 0) {
@@ -68,9 +70,8 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const __grid_
         if (tid == 0) ws.info[b] = 0;
         return;
     }
-    // ---- this sequence's place among those over the limit, and its new pages
-    int before = 0;
-    for (int k = tid; k < b; k += kThreads) before += min(max(a.n_rows[k], 0), cap) > a.limit;
+    // ---- this sequence's place among those over the limit, and its new pages (whether
+    // they are the pool's is asked once the keys are on their way)
     before = warp_sum(before);
     if (lane == 0) s_gt[warp] = before;
     __syncthreads();
@@ -94,15 +95,6 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const __grid_
         const int page = table[i];
         ok = ok && page >= 0 && page < a.n_pages;
     }
-    if (!__syncthreads_and(ok)) {
-        if (tid == 0) {
-            ws.info[b] = -1;
-            report(a.status, DS4A_DEV_BOUNDS);
-        }
-        return;
-    }
-    if (tid == 0) ws.info[b] = n;
-
     // ---- the least key that is kept
     const float *mass = a.mass + b * a.mass_stride;
     const long long plane = a.B * a.mass_stride;
@@ -113,9 +105,11 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const __grid_
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) m[k] = r0 + k * kThreads < hi ? mass[r0 + k * kThreads] : 0.f;
         for (int p = 1; p < a.n_planes; ++p) {
+            float more[kBatch];
 #pragma unroll
-            for (int k = 0; k < kBatch; ++k)
-                if (r0 + k * kThreads < hi) m[k] += mass[p * plane + r0 + k * kThreads];
+            for (int k = 0; k < kBatch; ++k) more[k] = r0 + k * kThreads < hi ? mass[p * plane + r0 + k * kThreads] : 0.f;
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) m[k] += more[k];
         }
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) key[k] = m[k] == m[k] ? float_key(m[k]) : 0u;
@@ -189,6 +183,14 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const __grid_
     const int take = static_cast<int>(left);               // of the rows with the least key
     const uint32_t below = (1u << lane) - 1u;
     int gt_base = 0, eq_base = 0;                          // of the parts before
+    if (!__syncthreads_and(ok)) {
+        if (tid == 0) {
+            ws.info[b] = -1;
+            report(a.status, DS4A_DEV_BOUNDS);
+        }
+        return;
+    }
+    if (tid == 0) ws.info[b] = n;
     for (int part = 0; part < n; part += kRun * kThreads) {
         const int r0 = part + warp * kRun * 32 + lane;     // this lane's rows: r0 + 32 k
         uint32_t bg[kRun], be[kRun];
