@@ -41,22 +41,19 @@ __host__ __device__ inline EvictWs evict_ws(void *ws, int B, int need) {
     return w;
 }
 
-DS4A_DEV int warp_sum(int v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
-}
+DS4A_DEV int warp_sum(int v) { return __reduce_add_sync(0xffffffffu, v); }
 
 __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const __grid_constant__ EvictArgs a) {
     pdl_launch_dependents();
     extern __shared__ uint32_t s_keys[];                   // the rows' keys, or nothing
-    __shared__ uint32_t s_hist[kBins];
+    __shared__ uint32_t s_hists[3][kBins];                 // one a pass
     __shared__ int s_gt[kWarps], s_eq[kWarps];
     __shared__ uint32_t s_bin, s_left;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, b = blockIdx.x;
     const int P = 1 << a.shift;
     const int cap = a.max_pages << a.shift;
     const EvictWs ws = evict_ws(a.ws, a.B, a.need);
+    for (int i = tid; i < 3 * kBins; i += kThreads) s_hists[0][i] = 0u;
     pdl_wait();
     int before = 0;
     for (int k = tid; k < b; k += kThreads) before += min(max(a.n_rows[k], 0), cap) > a.limit;
@@ -132,8 +129,7 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const __grid_
             const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
             const int bits = pass == 2 ? 10 : 11;
             const uint32_t above = pass == 0 ? 0u : 0xffffffffu << (shift + bits);
-            for (int i = tid; i < kBins; i += kThreads) s_hist[i] = 0u;
-            __syncthreads();
+            uint32_t *s_hist = s_hists[pass];
             for (int r0 = lo + tid; r0 < hi; r0 += kBatch * kThreads) {
                 uint32_t key[kBatch];
                 if (a.keys_in_smem) {
@@ -169,7 +165,7 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const __grid_
             }
             __syncthreads();
             prefix |= s_bin << shift;
-            left = s_left;                                 // (s_bin, s_left: written again two barriers later)
+            left = s_left;                                 // (s_bin, s_left and s_gt: written again a barrier later)
         }
         least = prefix;                                    // `left` rows of this key are kept, the lowest
     }
@@ -195,6 +191,23 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const __grid_
         const int r0 = part + warp * kRun * 32 + lane;     // this lane's rows: r0 + 32 k
         uint32_t bg[kRun], be[kRun];
         int gt = 0, eq = 0;
+        // the rows' masses and pages, kept or not, on their way while the places are counted
+        float m0[kRun], m1[kRun];
+        int page[kRun], place[kRun];                       // place: -1: not kept
+        auto fetch = [&](float (&m)[kRun], int p) {
+#pragma unroll
+            for (int k = 0; k < kRun; ++k) m[k] = r0 + 32 * k < n ? mass[p * plane + r0 + 32 * k] : 0.f;
+        };
+        auto settle = [&](const float (&m)[kRun], int p) {
+            __syncthreads();                               // every thread has read this plane's masses of the part
+#pragma unroll
+            for (int k = 0; k < kRun; ++k)
+                if (place[k] >= 0) mass_out[p * plane + place[k]] = m[k];
+        };
+        fetch(m0, 0);
+        if (a.n_planes > 1) fetch(m1, 1);
+#pragma unroll
+        for (int k = 0; k < kRun; ++k) page[k] = r0 + 32 * k < n ? table[(r0 + 32 * k) >> a.shift] : 0;
         __syncthreads();                                   // s_keys; s_gt and s_eq of the part before
 #pragma unroll
         for (int k = 0; k < kRun; ++k) {
@@ -225,31 +238,27 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const __grid_
         int gt0 = gt_base + warp_sum(lane < warp ? s_gt[lane] : 0), eq0 = eq_base + warp_sum(lane < warp ? s_eq[lane] : 0);
         gt_base += warp_sum(s_gt[lane]);
         eq_base += warp_sum(s_eq[lane]);
-        int place[kRun], page[kRun];                       // place: -1: not kept
 #pragma unroll
         for (int k = 0; k < kRun; ++k) {
-            const int r = r0 + 32 * k;
             const bool g = bg[k] >> lane & 1u, e = be[k] >> lane & 1u;
             const int eq_at = eq0 + __popc(be[k] & below);
             // kept rows before this one: the greater ones and the taken ones of the least key
             const int j = gt0 + __popc(bg[k] & below) + min(eq_at, take);
             place[k] = (g || (e && eq_at < take)) && j < a.keep ? j : -1;
-            page[k] = place[k] >= 0 ? table[r >> a.shift] : 0;
             gt0 += __popc(bg[k]);
             eq0 += __popc(be[k]);
         }
-        for (int p = 0; p < a.n_planes; ++p) {
-            float m[kRun];
 #pragma unroll
-            for (int k = 0; k < kRun; ++k) m[k] = place[k] >= 0 ? mass[p * plane + r0 + 32 * k] : 0.f;
-            __syncthreads();
-#pragma unroll
-            for (int k = 0; k < kRun; ++k)
-                if (place[k] >= 0) mass_out[p * plane + place[k]] = m[k];
+        for (int k = 0; k < kRun; ++k) {
+            if (place[k] < 0) continue;
+            src[place[k]] = (page[k] << a.shift) + ((r0 + 32 * k) & (P - 1));
         }
-#pragma unroll
-        for (int k = 0; k < kRun; ++k)
-            if (place[k] >= 0) src[place[k]] = (page[k] << a.shift) + ((r0 + 32 * k) & (P - 1));
+        settle(m0, 0);
+        if (a.n_planes > 1) settle(m1, 1);
+        for (int p = 2; p < a.n_planes; ++p) {
+            fetch(m0, p);
+            settle(m0, p);
+        }
     }
     __syncthreads();
     for (int p = 0; p < a.n_planes; ++p)
