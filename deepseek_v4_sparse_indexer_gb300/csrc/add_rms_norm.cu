@@ -16,7 +16,10 @@
 // several rows: enough of them share an SM to cover each other's loads and barriers (one
 // a row, two with a scale per row), and the weight comes from L1.
 // Bound: HBM (7 flop for 4 to 17 bytes), with the instructions close behind: products
-// and sums go two at a time (fp32x2).
+// and sums go two at a time (fp32x2).  Measured (GB300): 8,192 x 4,096, bf16 with an fp32
+// residual, into codes 58 us = 6.4 TB/s, 94 % of the copy bandwidth; all bf16, both
+// outputs, 48 us = 93 %; 2,048 x 16,384 47 us = 5.0 TB/s (a row's block of 512 threads,
+// two an SM); one row of 4,096 2.4 us.
 #include <cuda_fp16.h>
 
 #include "common.cuh"
@@ -35,15 +38,21 @@ struct Raw {
     uint32_t v[W == 0 ? 1 : 2 * W];
 };
 
-DS4A_DEV void ld_v4(const void *p, uint32_t *v) {
-    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "l"(p) : "memory");
-}
 template <int W>
 DS4A_DEV void load8(Raw<W> &r, const void *base, long long elem) {
-    if constexpr (W != 0) {
-        const uint8_t *p = static_cast<const uint8_t *>(base) + elem * W;
-        ld_v4(p, r.v);
-        if constexpr (W == 4) ld_v4(p + 16, r.v + 4);
+    const uint8_t *p = static_cast<const uint8_t *>(base) + elem * W;
+    if constexpr (W == 2) {
+        asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(r.v[0]), "=r"(r.v[1]), "=r"(r.v[2]), "=r"(r.v[3])
+                     : "l"(p)
+                     : "memory");
+    } else if constexpr (W == 4) {                         // (the second half of each sector hits L1)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(r.v[4 * k]), "=r"(r.v[4 * k + 1]), "=r"(r.v[4 * k + 2]), "=r"(r.v[4 * k + 3])
+                         : "l"(p + 16 * k)
+                         : "memory");
     }
 }
 
@@ -120,7 +129,7 @@ DS4A_DEV void store8(void *base, long long elem, int type, const F2 (&x)[4]) {
 // XW, RW: bytes of an element of x and of the residual (0: none).  C: octets per thread.
 // blockDim.x: the threads of a row; blockDim.y: rows of a block (above 1: a warp each).
 template <int XW, int RW, int C>
-__global__ void __launch_bounds__(C == 1 ? 1024 : 512, C == 4 && XW + RW <= 4 ? 2 : 1) add_rms_norm_kernel(const __grid_constant__ AddNormArgs a) {
+__global__ void __launch_bounds__(C == 1 ? 1024 : 512, C == 4 && XW + RW <= 4 ? 2 : C == 2 && XW + RW <= 4 ? 3 : 1) add_rms_norm_kernel(const __grid_constant__ AddNormArgs a) {
     pdl_launch_dependents();
     __shared__ float s_sum[kMaxWarps], s_max[kMaxWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
@@ -259,9 +268,10 @@ __global__ void __launch_bounds__(C == 1 ? 1024 : 512, C == 4 && XW + RW <= 4 ? 
 template <int XW, int RW>
 cudaError_t launch_w(const AddNormArgs &a, int num_sms, cudaStream_t s) {
     const int octets = a.D / 8;
-    // Few rows are latency: an octet a thread.  Many: two (four past 4,096 elements), so
-    // that a row's block is small enough for several to share an SM.
-    const int c = a.T <= 2 * num_sms && octets <= 1024 ? 1 : octets <= 512 ? 2 : 4;
+    // Few rows are latency: an octet a thread.  Many: two (four past 8,192 elements), with
+    // registers for two or three blocks an SM (4,000 x 7,168 bf16 38.2 us, fp32 59.6; with
+    // four octets 39.5 and 71).
+    const int c = a.T <= 2 * num_sms && octets <= 1024 ? 1 : octets <= 1024 ? 2 : 4;
     const int tpr = ((octets + c - 1) / c + 31) / 32 * 32;
     const int rows = tpr == 32 ? 4 : 1;
     const long long blocks = (static_cast<long long>(a.T) + rows - 1) / rows;
