@@ -927,7 +927,9 @@ ds4a_status ds4a_paged_block_keys(const uint16_t *ik, int n_pages, int page_size
     if (!ik || !table || !n_rows || !block_keys || !n_blocks || shift < 0 || (first_row && cu_row)) return DS4A_EINVAL;
     if (B < 1 || B > DS4A_MAX_PLAN_SEQS || n_pages < 1 || max_pages < 1 || table_stride < max_pages) return DS4A_EINVAL;
     if (!aligned(ik, 16) || !aligned(block_keys, 16)) return DS4A_EINVAL;
-    if (static_cast<long long>(max_pages) << shift >= (1LL << 30) || static_cast<long long>(n_pages) << shift >= (1LL << 31))
+    // (the blocks of a batch are counted in 32 bits)
+    if (static_cast<long long>(max_pages) << shift >= (1LL << 30) || static_cast<long long>(n_pages) << shift >= (1LL << 31) ||
+        static_cast<long long>(B) * max_pages >= (1LL << 31))
         return DS4A_EINVAL;
     DevInfo *di = nullptr;
     if (ds4a_status st = current_device(&di)) return st;
@@ -999,7 +1001,9 @@ ds4a_status ds4a_paged_evict(const float *mass, int n_planes, int64_t mass_strid
         table_stride < max_pages)
         return DS4A_EINVAL;
     const long long cap = static_cast<long long>(max_pages) << shift, pool = static_cast<long long>(n_pages) << shift;
-    if (cap >= (1LL << 30) || pool >= (1LL << 31) || mass_stride < cap || mass_stride >= (1LL << 40)) return DS4A_EINVAL;
+    if (cap >= (1LL << 30) || pool >= (1LL << 31) || mass_stride < cap || mass_stride >= (1LL << 40) ||
+        static_cast<long long>(B) * max_pages >= (1LL << 31))      // (the pages of a batch are counted in 32 bits)
+        return DS4A_EINVAL;
     if (keep < 1 || keep > cap || limit < keep || first < 0 || recent < 0 || static_cast<long long>(first) + recent > keep)
         return DS4A_EINVAL;
     if (!aligned(rows, 16) || (ik && !aligned(ik, 16)) || !aligned(mass, 4) || !aligned(mass_out, 4)) return DS4A_EINVAL;

@@ -8,7 +8,8 @@
 // list's head.  Rows are copied and not moved within their pages, so that every copy
 // is independent of the others and a page that another sequence reads stays whole.
 //
-// evict_select_kernel, a block of 1,024 threads per sequence: the kept rows' smallest
+// evict_select_kernel, a block of 1,024 threads per sequence over its limit (every block
+// scans the lengths and takes its share of them): the kept rows' smallest
 // key by a radix select (11, 11 and 10 bits of an order-preserving key; keys in shared
 // memory where they fit), then the kept rows' slots and masses in their new places, by
 // counts over the warps' runs of rows.  evict_move_kernel: the
@@ -43,37 +44,13 @@ __host__ __device__ inline EvictWs evict_ws(void *ws, int B, int need) {
 
 DS4A_DEV int warp_sum(int v) { return __reduce_add_sync(0xffffffffu, v); }
 
-__global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const __grid_constant__ EvictArgs a) {
-    pdl_launch_dependents();
-    extern __shared__ uint32_t s_keys[];                   // the rows' keys, or nothing
-    __shared__ uint32_t s_hists[3][kBins];                 // one a pass
-    __shared__ int s_gt[kWarps], s_eq[kWarps];
-    __shared__ uint32_t s_bin, s_left;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, b = blockIdx.x;
+// One sequence, the x-th over the limit, of n rows.  The whole block calls it.
+DS4A_DEV void select_rows(const EvictArgs &a, const EvictWs &ws, int b, int x, int n, int head, uint32_t *s_keys,
+                          uint32_t (*s_hists)[kBins], int *s_gt, int *s_eq, uint32_t *s_bin, uint32_t *s_left) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int P = 1 << a.shift;
-    const int cap = a.max_pages << a.shift;
-    const EvictWs ws = evict_ws(a.ws, a.B, a.need);
-    for (int i = tid; i < 3 * kBins; i += kThreads) s_hists[0][i] = 0u;
-    pdl_wait();
-    int before = 0;
-    for (int k = tid; k < b; k += kThreads) before += min(max(a.n_rows[k], 0), cap) > a.limit;
-    const int n_raw = a.n_rows[b], n = min(max(n_raw, 0), cap);
-    const int head = a.free_head[0];
-    if (tid == 0) {
-        if (n != n_raw || head < 0) report(a.status, DS4A_DEV_BOUNDS);
-        if (b == 0) ws.head[0] = head;
-    }
-    if (n <= a.limit || head < 0) {
-        if (tid == 0) ws.info[b] = 0;
-        return;
-    }
-    // ---- this sequence's place among those over the limit, and its new pages (whether
-    // they are the pool's is asked once the keys are on their way)
-    before = warp_sum(before);
-    if (lane == 0) s_gt[warp] = before;
-    __syncthreads();
-    before = warp_sum(s_gt[lane]);
-    const long long at = head + static_cast<long long>(before) * a.need;
+    // its new pages (whether they are the pool's is asked once the keys are on their way)
+    const long long at = head + static_cast<long long>(x) * a.need;
     if (at + a.need > a.n_free) {
         if (tid == 0) {
             ws.info[b] = 0;
@@ -157,15 +134,15 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const __grid_
             __syncthreads();
             const uint32_t ahead = static_cast<uint32_t>(warp_sum(lane < warp ? s_gt[lane] : 0)) + inc - (c1 + c0);
             if (ahead < left && left <= ahead + c1) {
-                s_bin = static_cast<uint32_t>(top);
-                s_left = left - ahead;
+                *s_bin = static_cast<uint32_t>(top);
+                *s_left = left - ahead;
             } else if (ahead + c1 < left && left <= ahead + c1 + c0) {
-                s_bin = static_cast<uint32_t>(top - 1);
-                s_left = left - ahead - c1;
+                *s_bin = static_cast<uint32_t>(top - 1);
+                *s_left = left - ahead - c1;
             }
             __syncthreads();
-            prefix |= s_bin << shift;
-            left = s_left;                                 // (s_bin, s_left and s_gt: written again a barrier later)
+            prefix |= *s_bin << shift;
+            left = *s_left;                                // (s_bin, s_left and s_gt: written again a barrier later)
         }
         least = prefix;                                    // `left` rows of this key are kept, the lowest
     }
@@ -263,6 +240,58 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const __grid_
     __syncthreads();
     for (int p = 0; p < a.n_planes; ++p)
         for (int j = a.keep + tid; j < n; j += kThreads) mass_out[p * plane + j] = 0.f;
+}
+
+__global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const __grid_constant__ EvictArgs a) {
+    pdl_launch_dependents();
+    extern __shared__ uint32_t s_keys[];                   // the rows' keys, or nothing
+    __shared__ uint32_t s_hists[3][kBins];                 // one a pass
+    __shared__ int s_gt[kWarps], s_eq[kWarps];
+    __shared__ uint32_t s_bin, s_left;
+    __shared__ int s_b[2];                                 // the sequence and its rows
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int cap = a.max_pages << a.shift;
+    const EvictWs ws = evict_ws(a.ws, a.B, a.need);
+    for (int i = tid; i < 3 * kBins; i += kThreads) s_hists[0][i] = 0u;
+    pdl_wait();
+    // ---- the sequences over the limit, in order: thread t scans [t per, (t + 1) per)
+    const int head = a.free_head[0];
+    const int per = (a.B + kThreads - 1) / kThreads, b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
+    auto rows_of = [&](int b) -> int { return min(max(a.n_rows[b], 0), cap); };
+    int mine = 0;
+    for (int b = b0; b < b1; ++b) {
+        const bool over = rows_of(b) > a.limit && head >= 0;
+        mine += over;
+        if (blockIdx.x == 0) {
+            if (!over) ws.info[b] = 0;
+            if (rows_of(b) != a.n_rows[b] || head < 0) report(a.status, DS4A_DEV_BOUNDS);
+        }
+    }
+    if (blockIdx.x == 0 && tid == 0) ws.head[0] = head;
+    int inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += v;
+    }
+    if (lane == 31) s_gt[warp] = inc;
+    __syncthreads();
+    const int start = warp_sum(lane < warp ? s_gt[lane] : 0) + inc - mine, E = warp_sum(s_gt[lane]);
+
+    for (int x = static_cast<int>(blockIdx.x); x < E; x += gridDim.x) {
+        if (x != static_cast<int>(blockIdx.x)) {                             // another: the one before is done with shared memory
+            __syncthreads();
+            for (int i = tid; i < 3 * kBins; i += kThreads) s_hists[0][i] = 0u;
+        }
+        if (start <= x && x < start + mine) {
+            int b = b0;
+            for (int k = start; rows_of(b) <= a.limit || k++ < x; ++b) {}
+            s_b[0] = b;
+            s_b[1] = rows_of(b);
+        }
+        __syncthreads();
+        select_rows(a, ws, s_b[0], x, s_b[1], head, s_keys, s_hists, s_gt, s_eq, &s_bin, &s_left);
+    }
 }
 
 // ---- copies and lists
@@ -426,7 +455,7 @@ cudaError_t launch_evict(EvictArgs a, int num_sms, cudaStream_t s) {
     const size_t smem = a.keys_in_smem ? static_cast<size_t>(cap) * 4 : 0;
     cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
-    e = launch_k(evict_select_kernel, dim3(static_cast<unsigned>(a.B)), dim3(kThreads), smem, s, a);
+    e = launch_k(evict_select_kernel, dim3(static_cast<unsigned>(a.B < num_sms ? a.B : num_sms)), dim3(kThreads), smem, s, a);
     if (e != cudaSuccess) return e;
     void (*kern)(EvictArgs) = a.fp8 ? evict_move_kernel<true> : evict_move_kernel<false>;
     const size_t lists = 2 * static_cast<size_t>(a.B) * sizeof(int);

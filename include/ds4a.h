@@ -749,7 +749,7 @@ ds4a_status ds4a_paged_attn_decode(int n_head, const uint16_t *q, const void *ro
  *    n_blocks    int32 [B] (device, written): ceil(n_rows / page_size).
  *    Lengths out of range are clamped and pages outside the pool left out; each sets
  *    DS4A_DEV_BOUNDS.  1 <= B <= DS4A_MAX_PLAN_SEQS; max_pages * page_size is below
- *    2^30, n_pages * page_size below 2^31.
+ *    2^30, n_pages * page_size and B * max_pages below 2^31.
  */
 ds4a_status ds4a_paged_block_keys(const uint16_t *ik, int n_pages, int page_size,
                                   const int32_t *table, int64_t table_stride, int max_pages,
@@ -768,10 +768,11 @@ ds4a_status ds4a_paged_block_keys(const uint16_t *ik, int n_pages, int page_size
  *
  *    iq, w, table  as in 5c.    block_keys  bf16 [n_pages][128], 16-byte aligned.
  *    n_blocks  int32 [U] (device), 0 .. min(NB_cap, max_pages); a count outside sets
- *              DS4A_DEV_BOUNDS and is clamped.
+ *              DS4A_DEV_BOUNDS and is clamped.  n_first, n_last >= 0.
  *    scores    fp32 [U][NB_cap] (device), written for b < n_blocks[u], the others left
  *              as they were.  A block whose page is not one of the pool's gets -inf and
  *              sets DS4A_DEV_BOUNDS.
+ *    The batch's 128-block tiles, U * ceil(min(NB_cap, max_pages) / 128), are below 2^31.
  */
 ds4a_status ds4a_paged_block_score(const uint16_t *iq, const float *w, const uint16_t *block_keys,
                                    int n_pages, const int32_t *table, int64_t table_stride,
@@ -808,7 +809,8 @@ ds4a_status ds4a_paged_attn_blocks(int n_head, const uint16_t *q, const void *ro
  *
  *    in fp32, the rows and products as in 5d.  The raw window has a part in lse but
  *    gets no mass.  Where lse is -inf a head adds nothing.  A row listed twice is
- *    added to twice.  Bit-identical from call to call.
+ *    added to twice.  Bit-identical from call to call (calls that add to the same mass
+ *    at the same time may round in either order).
  *
  *    q, rows, rows_type, row_scale, table, n_rows, idx, count, top_k, scale   those
  *             of the attention call: 5d, or with list_kind DS4A_LIST_BLOCKS 6c.
@@ -869,7 +871,10 @@ ds4a_status ds4a_paged_attn_mass(int n_head, const uint16_t *q, const void *rows
  *    ws          workspace of ds4a_workspace_bytes(DS4A_OP_PAGED_EVICT, B, 1, max_pages
  *                * page_size, keep) bytes, 256-byte aligned (device).
  *    1 <= keep <= limit, first + recent <= keep <= max_pages * page_size, 1 <= B <=
- *    DS4A_MAX_PLAN_SEQS.  A length out of range is clamped; a free list that runs out
+ *    DS4A_MAX_PLAN_SEQS; max_pages * page_size is below 2^30, n_pages * page_size and
+ *    B * max_pages below 2^31.  The free list's pages are in no table that rows are
+ *    read through, and no two sequences that may be evicted hold the same page but for
+ *    their n_shared ones.  A length out of range is clamped; a free list that runs out
  *    leaves the sequences it does not reach as they are, a negative head all of them,
  *    and a page, old or new, that is not one of the pool's its sequence (whose new
  *    pages are lost to the list); each sets DS4A_DEV_BOUNDS.
@@ -915,8 +920,8 @@ ds4a_status ds4a_paged_evict(const float *mass, int n_planes, int64_t mass_strid
  *             clamped.
  *    D a multiple of 8 up to DS4A_MAX_NORM_DIM (else DS4A_EUNSUPPORTED), T >= 0 (0:
  *    nothing is launched), eps > 0.  Buffers 16-byte aligned (scales 4), strides
- *    at least D and whole multiples of 16 bytes.  out, codes and scales overlap no
- *    other buffer.
+ *    at least D and whole multiples of 16 bytes.  No output overlaps another buffer,
+ *    but for res_out that is res.
  */
 ds4a_status ds4a_add_rms_norm(const void *x, int x_type, int64_t x_stride, const void *res,
                               int res_type, int64_t res_stride, void *res_out,

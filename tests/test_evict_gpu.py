@@ -375,6 +375,17 @@ def test_evict_a_large_batch(cuda_lib):
     c.check()
 
 
+def test_evict_the_largest_batch(cuda_lib):
+    """8,192 sequences, more of them over the limit than there are SMs, and hardly any."""
+    rng = random.Random(8)
+    for share in (0.1, 0.001):
+        lengths = [rng.randint(33, 64) if rng.random() < share else rng.randint(0, 32) for _ in range(8192)]
+        c = Cache(lengths, 8, 1, True, False, max_pages=8)
+        c.run(cuda_lib, 20, 32, 2, 5)
+        status(cuda_lib)
+        c.check()
+
+
 def test_evict_nothing(cuda_lib):
     for lengths in ([0], [100, 64, 0]):
         c = Cache(lengths, 16, max_pages=8)

@@ -50,7 +50,7 @@ def test_plan_evicted_rejects(lib, change):
     dict(ik=None), dict(table=None), dict(n_rows=None), dict(block_keys=None), dict(n_blocks=None), dict(first_row=FAKE),
     dict(page_size=4), dict(page_size=96), dict(B=0), dict(B=B.DS4A_MAX_PLAN_SEQS + 1), dict(n_pages=0), dict(max_pages=0),
     dict(table_stride=3), dict(ik=FAKE + 8), dict(block_keys=FAKE + 2), dict(n_pages=1 << 25),
-    dict(max_pages=1 << 25, table_stride=1 << 25)])
+    dict(max_pages=1 << 25, table_stride=1 << 25), dict(B=8192, max_pages=1 << 18, table_stride=1 << 18, page_size=8)])
 def test_block_keys_rejects(lib, change):
     assert call(lib.ds4a_paged_block_keys, KEYS, **change) == B.DS4A_EINVAL
 
@@ -93,7 +93,8 @@ def test_attention_unsupported(lib, name, args, change):
     dict(n_free=-1), dict(n_planes=0), dict(n_planes=17), dict(mass_stride=255), dict(B=0), dict(B=B.DS4A_MAX_PLAN_SEQS + 1),
     dict(page_size=4), dict(max_pages=0), dict(table_stride=3), dict(n_pages=0), dict(keep=0), dict(keep=257, limit=300),
     dict(limit=99), dict(first=-1), dict(recent=-1), dict(first=50, recent=51), dict(first=2 ** 31 - 1, recent=2 ** 31 - 1),
-    dict(rows=FAKE + 8), dict(ik=FAKE + 8), dict(mass=FAKE + 2), dict(rows_type=B.DS4A_E4M3), dict(gone=FAKE)])
+    dict(rows=FAKE + 8), dict(ik=FAKE + 8), dict(mass=FAKE + 2), dict(rows_type=B.DS4A_E4M3), dict(gone=FAKE),
+    dict(B=8192, max_pages=1 << 18, table_stride=1 << 18, mass_stride=1 << 24)])
 def test_evict_rejects(lib, change):
     assert call(lib.ds4a_paged_evict, EVICT, **change) == B.DS4A_EINVAL
 
