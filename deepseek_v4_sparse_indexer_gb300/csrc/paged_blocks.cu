@@ -264,9 +264,13 @@ __global__ void __launch_bounds__(kScoreThreads) block_score_kernel(const __grid
 // One block of threads per SM, persistent over an equal, contiguous share of the
 // batch's 128-block tiles: eight warps bring the tiles' keys (and a unit's queries with
 // its first tile) by cp.async into five buffers, one issues the UMMAs into four TMEM
-// accumulators, four sum up.  A tile's copies are handed over three tiles later, so
-// that the copies of four are in flight.
-constexpr int kStages = 5, kAccs = 4, kAhead = 3, kIqBufs = 4;
+// accumulators, four sum up.  A tile's copies are handed over two tiles later, so that
+// the copies of three are in flight.
+// Measured (GB300): 64 ragged units of up to 16,384 blocks 28.8 us = 4.8 TB/s, 16 of up to
+// 131,072 50 us = 5.5 TB/s, 82 % of the copy bandwidth: 4 us of start (the lengths' scan,
+// the first pages and keys) and then about 90 %.
+constexpr int kStages = 5, kAccs = 4, kAhead = 2, kIqBufs = 4;
+constexpr int kLook = 4;                      // tiles whose pages are looked up ahead
 static_assert(kIqBufs > kAhead && kStages > kAhead, "a buffer's last user has been handed over before it is waited for");
 constexpr int kMmaWarp = 4, kFirstCopyWarp = 5, kCopyWarps = 8;
 constexpr int kPassRows = 2 * kCopyWarps;     // rows that the copy warps bring at a time
@@ -293,9 +297,9 @@ DS4A_DEV void settle_on(const BlockScoreArgs &a, BlockWalk &w) {     // on a uni
     }
 }
 DS4A_DEV void next_tile(const BlockScoreArgs &a, BlockWalk &w) {
+    if (w.left <= 0) return;
     --w.left;
-    ++w.t;
-    settle_on(a, w);
+    if (++w.t * kTile >= w.n) settle_on(a, w);
 }
 
 // This block's share [c T / G, (c + 1) T / G) of the batch's T tiles.  All threads call it.
@@ -381,13 +385,13 @@ __global__ void __launch_bounds__(kScanThreads, 1) block_scan_kernel(const __gri
         // ------------------------------------------------------------ copies
         // Copy warp p brings rows 2p and 2p + 1 of every 16: two rows an instruction, lane l
         // 16-byte chunk l % 16 of row l / 16.  Lane l looks up the page of the tile's row
-        // 2p + l % 2 + 16 (l / 2) one tile ahead.
+        // 2p + l % 2 + 16 (l / 2) kLook tiles ahead (33 us instead of 28.8 with one tile).
         const int p = warp - kFirstCopyWarp, c = lane & 15, half = lane >> 4;
         auto page_of = [&](const BlockWalk &x) -> int {
             const int r = 2 * p + (lane & 1) + kPassRows * (lane >> 1), b = x.t * kTile + r;
-            if (x.left <= 0 || r >= kTile || b >= x.n) return -1;
-            const int page = __ldg(a.table + x.u * a.table_stride + b);
-            return page < a.n_pages ? page : -1;
+            int page = -1;                                 // (looked at only where it is used: a test here would wait for it)
+            if (x.left > 0 && r < kTile && b < x.n) page = __ldg(a.table + x.u * a.table_stride + b);
+            return page;
         };
         uint32_t eph = 0, iqph = 0;
         int s = 0, ib = 0, last_u = -1, issued = 0, handed = 0;
@@ -397,11 +401,19 @@ __global__ void __launch_bounds__(kScanThreads, 1) block_scan_kernel(const __gri
             if (lane == 0) mbar_arrive(&full[handed % kStages]);
             ++handed;
         };
-        int page = page_of(w);
-        while (w.left > 0) {
-            BlockWalk n = w;
-            next_tile(a, n);
-            const int next_page = page_of(n);
+        int pages[kLook];
+        BlockWalk look = w;
+#pragma unroll
+        for (int k = 0; k < kLook; ++k) {
+            pages[k] = page_of(look);
+            next_tile(a, look);
+        }
+        for (; w.left > 0; next_tile(a, w)) {
+            const int page = pages[0] < a.n_pages ? pages[0] : -1;
+#pragma unroll
+            for (int k = 0; k + 1 < kLook; ++k) pages[k] = pages[k + 1];
+            pages[kLook - 1] = page_of(look);
+            next_tile(a, look);
             if (!(ok = warp_wait(&empty[s], ((eph >> s) & 1) ^ 1, abort_flag))) break;
             eph ^= 1u << s;
             const uint32_t keys = base + kOffKeys + s * 2 * kHalfA + (c >> 3) * kHalfA;
@@ -432,8 +444,6 @@ __global__ void __launch_bounds__(kScanThreads, 1) block_scan_kernel(const __gri
                 hand_over();
             }
             s = s == kStages - 1 ? 0 : s + 1;
-            w = n;
-            page = next_page;
         }
         cp_async_wait<0>();                                // also when a wait gave up
         if (ok)
@@ -473,23 +483,31 @@ __global__ void __launch_bounds__(kScanThreads, 1) block_scan_kernel(const __gri
         uint32_t fph = 0;
         int ab = 0, last_u = -1;
         float4 wt[16];
-        auto page_ok = [&](const BlockWalk &x) -> bool {
+        auto page_of = [&](const BlockWalk &x) -> int {
             const int b = x.t * kTile + tid;
-            if (x.left <= 0 || b >= x.n) return true;
-            const int page = __ldg(a.table + x.u * a.table_stride + b);
-            return page >= 0 && page < a.n_pages;
+            int page = 0;
+            if (x.left > 0 && b < x.n) page = __ldg(a.table + x.u * a.table_stride + b);
+            return page;
         };
-        bool there = page_ok(w);
-        while (w.left > 0) {
+        int pages[kLook];
+        BlockWalk look = w;
+#pragma unroll
+        for (int k = 0; k < kLook; ++k) {
+            pages[k] = page_of(look);
+            next_tile(a, look);
+        }
+        for (; w.left > 0; next_tile(a, w)) {
             if (w.u != last_u) {
                 last_u = w.u;
                 const float *src = a.w + static_cast<long long>(w.u) * kNIdxHead;   // (4-byte aligned)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) wt[i] = make_float4(src[4 * i], src[4 * i + 1], src[4 * i + 2], src[4 * i + 3]);
             }
-            BlockWalk n = w;
-            next_tile(a, n);
-            const bool next_there = page_ok(n);
+            const int page = pages[0];
+#pragma unroll
+            for (int k = 0; k + 1 < kLook; ++k) pages[k] = pages[k + 1];
+            pages[kLook - 1] = page_of(look);
+            next_tile(a, look);
             if (!(ok = warp_wait(&acc_full[ab], (fph >> ab) & 1, abort_flag))) break;
             fph ^= 1u << ab;
             tc_fence_after();
@@ -511,10 +529,8 @@ __global__ void __launch_bounds__(kScanThreads, 1) block_scan_kernel(const __gri
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&acc_empty[ab]);
-            store_score(a, w.u, w.t * kTile + tid, w.n, there, (s0 + s1) + (s2 + s3));
+            store_score(a, w.u, w.t * kTile + tid, w.n, page >= 0 && page < a.n_pages, (s0 + s1) + (s2 + s3));
             ab = ab == kAccs - 1 ? 0 : ab + 1;
-            w = n;
-            there = next_there;
         }
     }
     if (!ok) {

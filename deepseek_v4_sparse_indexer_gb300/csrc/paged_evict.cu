@@ -360,19 +360,20 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
     const int n_warps = gridDim.x * kMoveWarps, me = blockIdx.x * kMoveWarps + warp;
     const int parts = (a.keep + kRows - 1) / kRows;
     const long long items = static_cast<long long>(E) * parts;
-    // Slots that lane l's row (l % kRows of an item's) comes from and goes to (rows past
-    // the last repeat it); the next item's are looked up while this one's rows arrive.
-    auto look_up = [&](long long x, int &from, int &to) {
+    // Lane l's row (l % kRows of an item's; rows past the last repeat it): the slot that it
+    // comes from, its place and the page of that; the next item's are looked up while
+    // this one's rows arrive (and computed with only after).
+    auto look_up = [&](long long x, int &from, int &place, int &page) {
         if (x >= items) return;
         const int q = static_cast<int>(x / parts), b = s_seq[q];
-        const int j = min(static_cast<int>(x - static_cast<long long>(q) * parts) * kRows + (lane & (kRows - 1)), a.keep - 1);
-        from = ws.src[static_cast<long long>(b) * a.keep + j];
-        to = (ws.pages[static_cast<long long>(b) * a.need + (j >> a.shift)] << a.shift) + (j & ((1 << a.shift) - 1));
+        place = min(static_cast<int>(x - static_cast<long long>(q) * parts) * kRows + (lane & (kRows - 1)), a.keep - 1);
+        from = ws.src[static_cast<long long>(b) * a.keep + place];
+        page = ws.pages[static_cast<long long>(b) * a.need + (place >> a.shift)];
     };
-    int from = 0, to = 0, next_from = 0, next_to = 0;
-    look_up(me, from, to);
+    int next_from = 0, next_place = 0, next_page = 0;
+    look_up(me, next_from, next_place, next_page);
     for (long long x = me; x < items; x += n_warps) {
-        look_up(x + n_warps, next_from, next_to);
+        const int from = next_from, to = (next_page << a.shift) + (next_place & ((1 << a.shift) - 1));
         constexpr int kWide = FP8 ? 512 : 1024, kLoads = kWide / 512;
         uint4 v[kRows][kLoads], k[kRows / 2];
         float sc = 0.f;
@@ -391,6 +392,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
             }
         }
         if (FP8 && lane < kRows) sc = a.row_scale[from];
+        look_up(x + n_warps, next_from, next_place, next_page);
         uint8_t *out = static_cast<uint8_t *>(a.rows);
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
@@ -406,8 +408,6 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
             }
         }
         if (FP8 && lane < kRows) a.row_scale[to] = sc;
-        from = next_from;
-        to = next_to;
     }
 
     // ---- tables and the free list: a warp per evicted sequence, from the last warp on
