@@ -15,6 +15,8 @@
 // counts over the warps' runs of rows.  evict_move_kernel: the
 // copies, eight rows a warp (all of their loads in flight), and the lists.
 // Bound: the copies HBM; a few sequences the select's chain of passes.
+#include <type_traits>
+
 #include "common.cuh"
 #include "internal.h"
 
@@ -46,7 +48,7 @@ DS4A_DEV int warp_sum(int v) { return __reduce_add_sync(0xffffffffu, v); }
 
 // One sequence, the x-th over the limit, of n rows.  The whole block calls it.
 DS4A_DEV void select_rows(const EvictArgs &a, const EvictWs &ws, int b, int x, int n, int head, uint32_t *s_keys,
-                          uint32_t (*s_hists)[kBins], int *s_gt, int *s_eq, uint32_t *s_bin, uint32_t *s_left) {
+                          uint32_t (*s_hists)[kBins], int *s_gt, int *s_eq, uint32_t *s_bin, uint32_t *s_left, int *s_all) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int P = 1 << a.shift;
     // its new pages (whether they are the pool's is asked once the keys are on their way)
@@ -96,9 +98,14 @@ DS4A_DEV void select_rows(const EvictArgs &a, const EvictWs &ws, int b, int x, i
             for (int k = 0; k < kBatch; ++k)
                 if (r0 + k * kThreads < hi) s_keys[r0 + k * kThreads] = key[k];
         }
+        // the rows that stay whatever they got: above every key
+        for (int r = tid; r < lo; r += kThreads) s_keys[r] = 0xffffffffu;
+        for (int r = hi + tid; r < n; r += kThreads) s_keys[r] = 0xffffffffu;
     }
     uint32_t left = static_cast<uint32_t>(a.keep - a.first - a.recent);   // of them are kept
-    uint32_t least = 0xffffffffu;                          // none: no key is above it, and none of its like is taken
+    // Kept: keys from `bar` on, and `left` of those equal to `least`, the lowest, unless all are.
+    uint32_t least = 0xffffffffu, bar = 0xffffffffu;
+    bool ties = false;
     if (left > 0) {
         uint32_t prefix = 0;
 #pragma unroll 1
@@ -136,15 +143,19 @@ DS4A_DEV void select_rows(const EvictArgs &a, const EvictWs &ws, int b, int x, i
             if (ahead < left && left <= ahead + c1) {
                 *s_bin = static_cast<uint32_t>(top);
                 *s_left = left - ahead;
+                *s_all = c1 == left - ahead;
             } else if (ahead + c1 < left && left <= ahead + c1 + c0) {
                 *s_bin = static_cast<uint32_t>(top - 1);
                 *s_left = left - ahead - c1;
+                *s_all = c0 == left - ahead - c1;
             }
             __syncthreads();
             prefix |= *s_bin << shift;
-            left = *s_left;                                // (s_bin, s_left and s_gt: written again a barrier later)
+            left = *s_left;                                // (these and s_gt: written again a barrier later)
+            ties = !*s_all;
         }
-        least = prefix;                                    // `left` rows of this key are kept, the lowest
+        least = prefix;
+        bar = ties ? least + 1 : least;                    // (a row's key is below 0xffffffff)
     }
 
     // ---- the kept rows' places, slots and masses, kRun x 1,024 rows at a time: warp w has
@@ -155,7 +166,6 @@ DS4A_DEV void select_rows(const EvictArgs &a, const EvictWs &ws, int b, int x, i
     float *mass_out = a.mass_out + b * a.mass_stride;
     const int take = static_cast<int>(left);               // of the rows with the least key
     const uint32_t below = (1u << lane) - 1u;
-    int gt_base = 0, eq_base = 0;                          // of the parts before
     if (!__syncthreads_and(ok)) {
         if (tid == 0) {
             ws.info[b] = -1;
@@ -164,79 +174,87 @@ DS4A_DEV void select_rows(const EvictArgs &a, const EvictWs &ws, int b, int x, i
         return;
     }
     if (tid == 0) ws.info[b] = n;
-    for (int part = 0; part < n; part += kRun * kThreads) {
-        const int r0 = part + warp * kRun * 32 + lane;     // this lane's rows: r0 + 32 k
-        uint32_t bg[kRun], be[kRun];
-        int gt = 0, eq = 0;
-        // the rows' masses and pages, kept or not, on their way while the places are counted
-        float m0[kRun], m1[kRun];
-        int page[kRun], place[kRun];                       // place: -1: not kept
-        auto fetch = [&](float (&m)[kRun], int p) {
+    auto place_rows = [&](auto with_ties) {
+        constexpr bool kTies = decltype(with_ties)::value;
+        int gt_base = 0, eq_base = 0;                      // of the parts before
+        for (int part = 0; part < n; part += kRun * kThreads) {
+            const int r0 = part + warp * kRun * 32 + lane; // this lane's rows: r0 + 32 k
+            uint32_t bg[kRun], be[kTies ? kRun : 1];
+            int gt = 0, eq = 0;
+            // the rows' masses and pages, kept or not, on their way while the places are counted
+            float m0[kRun], m1[kRun];
+            int page[kRun], place[kRun];                   // place: -1: not kept
+            auto fetch = [&](float (&m)[kRun], int p) {
+                const float *from = mass + p * plane + r0;
 #pragma unroll
-            for (int k = 0; k < kRun; ++k) m[k] = r0 + 32 * k < n ? mass[p * plane + r0 + 32 * k] : 0.f;
-        };
-        auto settle = [&](const float (&m)[kRun], int p) {
-            __syncthreads();                               // every thread has read this plane's masses of the part
+                for (int k = 0; k < kRun; ++k) m[k] = r0 + 32 * k < n ? from[32 * k] : 0.f;
+            };
+            auto settle = [&](const float (&m)[kRun], int p) {
+                __syncthreads();                           // every thread has read this plane's masses of the part
+                float *to = mass_out + p * plane;
 #pragma unroll
-            for (int k = 0; k < kRun; ++k)
-                if (place[k] >= 0) mass_out[p * plane + place[k]] = m[k];
-        };
-        fetch(m0, 0);
-        if (a.n_planes > 1) fetch(m1, 1);
+                for (int k = 0; k < kRun; ++k)
+                    if (place[k] >= 0) to[place[k]] = m[k];
+            };
+            fetch(m0, 0);
+            if (a.n_planes > 1) fetch(m1, 1);
 #pragma unroll
-        for (int k = 0; k < kRun; ++k) page[k] = r0 + 32 * k < n ? table[(r0 + 32 * k) >> a.shift] : 0;
-        __syncthreads();                                   // s_keys; s_gt and s_eq of the part before
+            for (int k = 0; k < kRun; ++k) page[k] = r0 + 32 * k < n ? table[(r0 + 32 * k) >> a.shift] : 0;
+            __syncthreads();                               // s_keys; s_gt and s_eq of the part before
 #pragma unroll
-        for (int k = 0; k < kRun; ++k) {
-            const int r = r0 + 32 * k;
-            bool g = r < n && (r < lo || r >= hi), e = false;
-            if (r >= lo && r < hi) {
-                uint32_t key;
+            for (int k = 0; k < kRun; ++k) {
+                const int r = r0 + 32 * k;
+                uint32_t key = 0u;
                 if (a.keys_in_smem) {
-                    key = s_keys[r];
-                } else {
+                    if (r < n) key = s_keys[r];
+                } else if (r < n) {
                     float m = mass[r];
                     for (int p = 1; p < a.n_planes; ++p) m += mass[p * plane + r];
-                    key = m == m ? float_key(m) : 0u;
+                    key = r < lo || r >= hi ? 0xffffffffu : m == m ? float_key(m) : 0u;
                 }
-                g = key > least;
-                e = key == least;
+                bg[k] = __ballot_sync(0xffffffffu, r < n && key >= bar);
+                gt += __popc(bg[k]);
+                if constexpr (kTies) {
+                    be[k] = __ballot_sync(0xffffffffu, r < n && key == least);
+                    eq += __popc(be[k]);
+                }
             }
-            bg[k] = __ballot_sync(0xffffffffu, g);
-            be[k] = __ballot_sync(0xffffffffu, e);
-            gt += __popc(bg[k]);
-            eq += __popc(be[k]);
-        }
-        if (lane == 0) {
-            s_gt[warp] = gt;
-            s_eq[warp] = eq;
-        }
-        __syncthreads();
-        int gt0 = gt_base + warp_sum(lane < warp ? s_gt[lane] : 0), eq0 = eq_base + warp_sum(lane < warp ? s_eq[lane] : 0);
-        gt_base += warp_sum(s_gt[lane]);
-        eq_base += warp_sum(s_eq[lane]);
+            if (lane == 0) {
+                s_gt[warp] = gt;
+                if constexpr (kTies) s_eq[warp] = eq;
+            }
+            __syncthreads();
+            int gt0 = gt_base + warp_sum(lane < warp ? s_gt[lane] : 0), eq0 = 0;
+            gt_base += warp_sum(s_gt[lane]);
+            if constexpr (kTies) {
+                eq0 = eq_base + warp_sum(lane < warp ? s_eq[lane] : 0);
+                eq_base += warp_sum(s_eq[lane]);
+            }
 #pragma unroll
-        for (int k = 0; k < kRun; ++k) {
-            const bool g = bg[k] >> lane & 1u, e = be[k] >> lane & 1u;
-            const int eq_at = eq0 + __popc(be[k] & below);
-            // kept rows before this one: the greater ones and the taken ones of the least key
-            const int j = gt0 + __popc(bg[k] & below) + min(eq_at, take);
-            place[k] = (g || (e && eq_at < take)) && j < a.keep ? j : -1;
-            gt0 += __popc(bg[k]);
-            eq0 += __popc(be[k]);
+            for (int k = 0; k < kRun; ++k) {
+                // kept rows before this one: those from the bar on, and the taken ones of the least key
+                bool kept = bg[k] >> lane & 1u;
+                int j = gt0 + __popc(bg[k] & below);
+                gt0 += __popc(bg[k]);
+                if constexpr (kTies) {
+                    const int eq_at = eq0 + __popc(be[k] & below);
+                    kept = kept || ((be[k] >> lane & 1u) && eq_at < take);
+                    j += min(eq_at, take);
+                    eq0 += __popc(be[k]);
+                }
+                place[k] = kept && j < a.keep ? j : -1;
+                if (place[k] >= 0) src[j] = (page[k] << a.shift) + ((r0 + 32 * k) & (P - 1));
+            }
+            settle(m0, 0);
+            if (a.n_planes > 1) settle(m1, 1);
+            for (int p = 2; p < a.n_planes; ++p) {
+                fetch(m0, p);
+                settle(m0, p);
+            }
         }
-#pragma unroll
-        for (int k = 0; k < kRun; ++k) {
-            if (place[k] < 0) continue;
-            src[place[k]] = (page[k] << a.shift) + ((r0 + 32 * k) & (P - 1));
-        }
-        settle(m0, 0);
-        if (a.n_planes > 1) settle(m1, 1);
-        for (int p = 2; p < a.n_planes; ++p) {
-            fetch(m0, p);
-            settle(m0, p);
-        }
-    }
+    };
+    if (ties) place_rows(std::true_type{});
+    else place_rows(std::false_type{});
     __syncthreads();
     for (int p = 0; p < a.n_planes; ++p)
         for (int j = a.keep + tid; j < n; j += kThreads) mass_out[p * plane + j] = 0.f;
@@ -248,6 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const __grid_
     __shared__ uint32_t s_hists[3][kBins];                 // one a pass
     __shared__ int s_gt[kWarps], s_eq[kWarps];
     __shared__ uint32_t s_bin, s_left;
+    __shared__ int s_all;                                  // every row of the bin is kept
     __shared__ int s_b[2];                                 // the sequence and its rows
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int cap = a.max_pages << a.shift;
@@ -290,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const __grid_
             s_b[1] = rows_of(b);
         }
         __syncthreads();
-        select_rows(a, ws, s_b[0], x, s_b[1], head, s_keys, s_hists, s_gt, s_eq, &s_bin, &s_left);
+        select_rows(a, ws, s_b[0], x, s_b[1], head, s_keys, s_hists, s_gt, s_eq, &s_bin, &s_left, &s_all);
     }
 }
 
