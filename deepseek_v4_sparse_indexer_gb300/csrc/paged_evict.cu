@@ -327,6 +327,10 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const EvictWs ws = evict_ws(a.ws, a.B, a.need);
     pdl_wait();
+    // (What the select left is checked before it addresses anything: another call that uses
+    // the workspace at the same time must not become a fault.)
+    const int cap = a.max_pages << a.shift;
+    auto rows_before = [&](int b) -> int { return min(ws.info[b], cap); };
     auto returned = [&](int b, int n) -> int {             // old pages of sequence b that go to the list
         const int pages = static_cast<int>((static_cast<long long>(n) + (1 << a.shift) - 1) >> a.shift);
         return pages - (a.n_shared ? min(max(a.n_shared[b], 0), pages) : 0);
@@ -335,7 +339,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
     const int per = (a.B + kMoveThreads - 1) / kMoveThreads, b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
     int ev = 0, pg = 0, tk = 0;
     for (int b = b0; b < b1; ++b) {
-        const int n = ws.info[b];
+        const int n = rows_before(b);
         tk += n != 0;
         if (n > 0) {
             ++ev;
@@ -363,7 +367,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
         taken += s_tk[w];
     }
     for (int b = b0; b < b1; ++b) {
-        const int n = ws.info[b];
+        const int n = rows_before(b);
         if (n > 0) {
             s_seq[e] = b;
             s_ret[e] = g;
@@ -392,7 +396,13 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
     int next_from = 0, next_place = 0, next_page = 0;
     look_up(me, next_from, next_place, next_page);
     for (long long x = me; x < items; x += n_warps) {
+        const bool sound = next_from >= 0 && next_from >> a.shift < a.n_pages && next_page >= 0 && next_page < a.n_pages;
         const int from = next_from, to = (next_page << a.shift) + (next_place & ((1 << a.shift) - 1));
+        if (__any_sync(0xffffffffu, !sound)) {
+            if (lane == 0) report(a.status, DS4A_DEV_BOUNDS);
+            look_up(x + n_warps, next_from, next_place, next_page);
+            continue;
+        }
         constexpr int kWide = FP8 ? 512 : 1024, kLoads = kWide / 512;
         uint4 v[kRows][kLoads], k[kRows / 2];
         float sc = 0.f;
@@ -432,7 +442,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
     // ---- tables and the free list: a warp per evicted sequence, from the last warp on
     // (the first ones have copies).  An entry is read before its place is written.
     for (int q = n_warps - 1 - me; q < E; q += n_warps) {
-        const int b = s_seq[q], n = ws.info[b];
+        const int b = s_seq[q], n = rows_before(b);
         const int pages = static_cast<int>((static_cast<long long>(n) + (1 << a.shift) - 1) >> a.shift);
         const int shared = pages - returned(b, n);
         const int32_t *table = a.table + b * a.table_stride;
@@ -442,7 +452,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
             if (i < a.need) table_out[i] = ws.pages[static_cast<long long>(b) * a.need + i];
             const long long at = head_out + s_ret[q] + (i - shared);
             if (i >= shared) {
-                if (at >= 0) a.free_out[at] = old;
+                if (at >= 0 && at < a.n_free) a.free_out[at] = old;
                 else report(a.status, DS4A_DEV_BOUNDS);
             }
         }
@@ -450,7 +460,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
     // ---- counts
     if (blockIdx.x == gridDim.x - 1) {
         for (int b = tid; b < a.B; b += kMoveThreads) {
-            const int n = ws.info[b], old = a.n_rows[b];
+            const int n = rows_before(b), old = a.n_rows[b];
             if (a.gone_out) a.gone_out[b] = (a.gone ? a.gone[b] : 0) + (n > 0 ? n - a.keep : 0);
             if (a.first_row) a.first_row[b] = n > 0 ? 0 : max(old, 0);
             a.n_rows_out[b] = n > 0 ? a.keep : old;
