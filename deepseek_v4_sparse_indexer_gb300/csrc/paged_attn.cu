@@ -57,6 +57,13 @@
 // two 64-head halves of a share run on neighbouring CTAs, so that the second
 // one's rows come from L2.
 //
+// Two more kernels of the same pipeline.  Blocks: the list names pages of the unit's
+// table, whose rows come by TMA like all rows' (256 units x 2,048 rows 130 us either
+// way, 66 % of the copy bandwidth: the end of each unit, 4 us, weighs more on 45 tiles).
+// Masses: 2^(l - lse) of each row summed over heads, with no values and no window; a
+// row tile is free once its logits are done (256 ragged units of up to 8,192 rows 174 us
+// = 6.3 TB/s, 93 %; 16 x 512 listed rows 12 us).
+//
 // Every wait is bounded (DS4A_DEV_TIMEOUT); on timeout the CTA drains what it
 // issued (bounded), frees TMEM and returns.
 #include "attn_common.cuh"

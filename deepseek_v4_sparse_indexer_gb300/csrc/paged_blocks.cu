@@ -17,7 +17,9 @@ namespace {
 // of their loads in flight), summed in fp32 in a fixed order: the thread's own, then
 // the two halves of a warp, then the warps.  Every block scans the sequences' lengths
 // and takes every gridDim.x-th of the pages that got rows, whosever they are.
-// Bound: HBM (the keys); a decode step latency.
+// Bound: HBM (the keys); a decode step latency.  Measured (GB300): 256 sequences with a
+// new row each 5.1 us, 32 prompts of up to 16,384 rows 13.9 us = 3.9 TB/s (lengths, scan,
+// pages and keys are four latencies, and 3,300 pages make two rounds of blocks).
 constexpr int kKeyThreadsMax = 512;
 
 DS4A_DEV void add8(float (&s)[8], const uint4 &v) {
@@ -149,7 +151,8 @@ __global__ void __launch_bounds__(kKeyThreadsMax) block_keys_kernel(const __grid
 // in the store, and the unit's queries come by cp.async into two 64-dim halves of
 // 128-byte rows (128B-swizzled), one UMMA chain gives D[128 blocks x 64 heads] in
 // TMEM, and each thread sums its block's 64 weighted, rectified products.  For batches
-// of so few tiles that four of these a SM take them all at once: latency.
+// of so few tiles that four of these a SM take them all at once: latency (32 x 1,024
+// blocks 4.7 us; larger batches this way 58 us where the scan below takes 28).
 constexpr int kTile = 128;
 constexpr int kScoreThreads = 128;
 constexpr int kHalfA = kTile * 128, kHalfB = kNIdxHead * 128;
