@@ -562,6 +562,14 @@ def _req_ints(dev, *tensors):
             raise ValueError(f"{name}: must be contiguous int32 on cuda:{dev} with {n} elements")
 
 
+def _ints_ok(dev, n, *tensors):
+    """Whether each is what _req_ints wants; the caller names them to it where one is not."""
+    for t in tensors:
+        if t.dtype is not _I32 or t.numel() != n or t.get_device() != dev or not t.is_contiguous():
+            return False
+    return True
+
+
 def _table_stride(table, U, dev):
     if table.dtype is not _I32 or table.get_device() != dev or table.dim() != 2:
         raise ValueError(f"table: int32 [{U}, max_pages] on cuda:{dev}")
@@ -817,10 +825,12 @@ def ds4a_paged_attn_mass(q, rows, table, n_rows, scale, lse, mass, idx=None, cou
 
 
 def _block_keys(block_keys, n_pages, dev):
-    if block_keys.dtype is not _BF16 or block_keys.get_device() != dev or block_keys.dim() != 2 \
-            or block_keys.shape[1] != IDX_DIM or not block_keys.is_contiguous() \
-            or (n_pages is not None and block_keys.shape[0] != n_pages):
+    """Checks the keys of n_pages (None: as many as there are) pages; their number."""
+    shape = block_keys.shape
+    if len(shape) != 2 or shape[1] != IDX_DIM or block_keys.dtype is not _BF16 or block_keys.get_device() != dev \
+            or not block_keys.is_contiguous() or (n_pages is not None and shape[0] != n_pages):
         raise ValueError("block_keys: contiguous bf16 [n_pages, 128]")
+    return shape[0]
 
 
 def ds4a_paged_block_keys(ik, table, n_rows, block_keys, n_blocks, first_row=None, cu_row=None, stream=None):
@@ -835,13 +845,17 @@ def ds4a_paged_block_keys(ik, table, n_rows, block_keys, n_blocks, first_row=Non
     _block_keys(block_keys, n_pages, dev)
     B = n_rows.numel()
     stride, max_pages = _table_stride(table, B, dev)
-    _req_ints(dev, ("n_rows", n_rows, B), ("n_blocks", n_blocks, B))
+    if not _ints_ok(dev, B, n_rows, n_blocks):
+        _req_ints(dev, ("n_rows", n_rows, B), ("n_blocks", n_blocks, B))
+    first = cu = None
     if first_row is not None:
         _req_ints(dev, ("first_row", first_row, B))
+        first = first_row.data_ptr()
     if cu_row is not None:
         _req_ints(dev, ("cu_row", cu_row, B + 1))
+        cu = cu_row.data_ptr()
     _launch(dev, stream, "ds4a_paged_block_keys", ik.data_ptr(), n_pages, page_size, table.data_ptr(), stride, max_pages,
-            n_rows.data_ptr(), _opt(first_row), _opt(cu_row), block_keys.data_ptr(), n_blocks.data_ptr(), B)
+            n_rows.data_ptr(), first, cu, block_keys.data_ptr(), n_blocks.data_ptr(), B)
 
 
 def ds4a_paged_block_score(iq, w, block_keys, table, n_blocks, scores, n_first=0, n_last=0, stream=None):
@@ -859,10 +873,10 @@ def ds4a_paged_block_score(iq, w, block_keys, table, n_blocks, scores, n_first=0
         raise ValueError("iq: contiguous bf16 [U, 1, 64, 128]")
     if w.dtype is not _F32 or w.get_device() != dev or w.numel() != U * N_IDX_HEAD or not w.is_contiguous():
         raise ValueError("w: contiguous float32 [U, 1, 64]")
-    _block_keys(block_keys, None, dev)
+    n_pages = _block_keys(block_keys, None, dev)
     _req_ints(dev, ("n_blocks", n_blocks, U))
     stride, max_pages = _table_stride(table, U, dev)
-    _launch(dev, stream, "ds4a_paged_block_score", iq.data_ptr(), w.data_ptr(), block_keys.data_ptr(), block_keys.shape[0],
+    _launch(dev, stream, "ds4a_paged_block_score", iq.data_ptr(), w.data_ptr(), block_keys.data_ptr(), n_pages,
             table.data_ptr(), stride, max_pages, n_blocks.data_ptr(), n_first, n_last, scores.data_ptr(), U, NB_cap)
 
 
@@ -878,36 +892,46 @@ def ds4a_paged_evict(mass, n_rows, table, rows, free_pages, free_head, keep, lim
     gone_out, first_row i32 [B] or None; ws uint8 workspace of
     ds4a_workspace_bytes(DS4A_OP_PAGED_EVICT, B, 1, max_pages * P, keep)."""
     dev = _device_index(mass, "mass")
-    B, n_free = n_rows.numel(), free_pages.numel()
+    B, n_free, shape = n_rows.numel(), free_pages.numel(), mass.shape
+    if len(shape) != 3 or shape[1] != B or mass_out.shape != shape:
+        raise ValueError("mass, mass_out: contiguous float32 [planes, B, rows]")
     for t in (mass, mass_out):
-        if t.dtype is not _F32 or t.get_device() != dev or t.dim() != 3 or t.shape != mass.shape or t.shape[1] != B \
-                or not t.is_contiguous():
+        if t.dtype is not _F32 or t.get_device() != dev or not t.is_contiguous():
             raise ValueError("mass, mass_out: contiguous float32 [planes, B, rows]")
-    fp8 = rows.dtype is _U8
-    if not (fp8 or rows.dtype is _BF16) or rows.get_device() != dev or rows.dim() != 3 or rows.shape[2] != HEAD_DIM \
+    fp8, rows_shape = rows.dtype is _U8, rows.shape
+    if not (fp8 or rows.dtype is _BF16) or rows.get_device() != dev or len(rows_shape) != 3 or rows_shape[2] != HEAD_DIM \
             or not rows.is_contiguous():
         raise ValueError("rows: contiguous bf16 or uint8 [n_pages, page_size, 512]")
-    n_pages, page_size, _ = rows.shape
-    if fp8 and (row_scale is None or row_scale.dtype is not _F32 or row_scale.get_device() != dev
-                or row_scale.numel() != n_pages * page_size or not row_scale.is_contiguous()):
-        raise ValueError("row_scale: contiguous float32 [n_pages, page_size]")
-    if ik is not None and (ik.dtype is not _BF16 or ik.get_device() != dev or ik.shape != (n_pages, page_size, IDX_DIM)
-                           or not ik.is_contiguous()):
-        raise ValueError("ik: contiguous bf16 [n_pages, page_size, 128]")
-    stride, max_pages = _table_stride(table, B, dev)
-    if _table_stride(table_out, B, dev) != (stride, max_pages):
+    n_pages, page_size, _ = rows_shape
+    scale_ptr = ik_ptr = None
+    if fp8:
+        if row_scale is None or row_scale.dtype is not _F32 or row_scale.get_device() != dev \
+                or row_scale.numel() != n_pages * page_size or not row_scale.is_contiguous():
+            raise ValueError("row_scale: contiguous float32 [n_pages, page_size]")
+        scale_ptr = row_scale.data_ptr()
+    if ik is not None:
+        if ik.dtype is not _BF16 or ik.get_device() != dev or ik.numel() != n_pages * page_size * IDX_DIM \
+                or not ik.is_contiguous():
+            raise ValueError("ik: contiguous bf16 [n_pages, page_size, 128]")
+        ik_ptr = ik.data_ptr()
+    stride, max_pages = layout = _table_stride(table, B, dev)
+    if table_out is not table and _table_stride(table_out, B, dev) != layout:
         raise ValueError("table_out: laid out as table")
-    _req_ints(dev, ("n_rows", n_rows, B), ("n_rows_out", n_rows_out, B), ("free_pages", free_pages, n_free),
-              ("free_pages_out", free_pages_out, n_free), ("free_head", free_head, 1), ("free_head_out", free_head_out, 1))
-    for name, t in (("n_shared", n_shared), ("gone", gone), ("gone_out", gone_out), ("first_row", first_row)):
+    if not (_ints_ok(dev, B, n_rows, n_rows_out) and _ints_ok(dev, n_free, free_pages, free_pages_out)
+            and _ints_ok(dev, 1, free_head, free_head_out)):
+        _req_ints(dev, ("n_rows", n_rows, B), ("n_rows_out", n_rows_out, B), ("free_pages", free_pages, n_free),
+                  ("free_pages_out", free_pages_out, n_free), ("free_head", free_head, 1), ("free_head_out", free_head_out, 1))
+    opt = [None] * 4
+    for k, t in enumerate((n_shared, gone, gone_out, first_row)):
         if t is not None:
-            _req_ints(dev, (name, t, B))
+            if not _ints_ok(dev, B, t):
+                _req_ints(dev, (("n_shared", "gone", "gone_out", "first_row")[k], t, B))
+            opt[k] = t.data_ptr()
     ws_ptr, ws_bytes = _workspace(ws, dev)
-    _launch(dev, stream, "ds4a_paged_evict", mass.data_ptr(), mass.shape[0], mass.shape[2], mass_out.data_ptr(),
+    _launch(dev, stream, "ds4a_paged_evict", mass.data_ptr(), shape[0], shape[2], mass_out.data_ptr(),
             n_rows.data_ptr(), n_rows_out.data_ptr(), table.data_ptr(), table_out.data_ptr(), stride, max_pages, page_size,
-            n_pages, B, keep, limit, first, recent, rows.data_ptr(), DS4A_E4M3 if fp8 else DS4A_BF16,
-            row_scale.data_ptr() if fp8 else None, _opt(ik), free_pages.data_ptr(), free_pages_out.data_ptr(), n_free,
-            free_head.data_ptr(), free_head_out.data_ptr(), _opt(n_shared), _opt(gone), _opt(gone_out), _opt(first_row),
+            n_pages, B, keep, limit, first, recent, rows.data_ptr(), DS4A_E4M3 if fp8 else DS4A_BF16, scale_ptr, ik_ptr,
+            free_pages.data_ptr(), free_pages_out.data_ptr(), n_free, free_head.data_ptr(), free_head_out.data_ptr(), *opt,
             ws_ptr, ws_bytes)
 
 
@@ -915,17 +939,17 @@ def ds4a_paged_evict(mass, n_rows, table, rows, free_pages, free_head, keep, lim
 # Between layers
 # ----------------------------------------------------------------------------
 
-def _norm_rows(t, name, dev, shape):
-    """(address, type, row stride) of [T, D] rows in 16 or 32 bits; nothing for None."""
-    if t is None:
-        return None, 0, 0
+def _norm_rows(t, name, dev, shape, n):
+    """(address, type, row stride) of n elements as [T, D] rows in 16 or 32 bits.  A contiguous
+    tensor of the right count is the right memory whatever its shape."""
     kind = _TYPES.get(t.dtype, -1)
-    if not DS4A_BF16 <= kind <= DS4A_F32 or t.get_device() != dev or t.shape != shape:
+    if not DS4A_BF16 <= kind <= DS4A_F32 or t.get_device() != dev or t.numel() != n:
         raise ValueError(f"{name}: bf16, fp16 or fp32 [T, D] on cuda:{dev}")
-    stride, one = t.stride()
-    if one != 1 and shape[1] > 1:
-        raise ValueError(f"{name}: contiguous rows")
-    return t.data_ptr(), kind, stride if shape[0] > 1 else shape[1]
+    if t.is_contiguous():
+        return t.data_ptr(), kind, shape[1]
+    if t.shape != shape or t.stride(1) != 1:
+        raise ValueError(f"{name}: [T, D] with contiguous rows")
+    return t.data_ptr(), kind, t.stride(0) if shape[0] > 1 else shape[1]
 
 
 def ds4a_add_rms_norm(x, weight, eps, out=None, residual=None, res_out=None, codes=None, scales=None, group=128,
@@ -937,30 +961,40 @@ def ds4a_add_rms_norm(x, weight, eps, out=None, residual=None, res_out=None, cod
     for every 32, 64 or 128 elements or (group = 0) for a row; n_live i32 [1] or
     None: rows from there on are left as they were."""
     dev = _device_index(x, "x")
-    if x.dim() != 2:
+    shape = x.shape
+    if len(shape) != 2:
         raise ValueError("x: [T, D]")
-    T, D = shape = x.shape
-    x_ptr, x_type, x_stride = _norm_rows(x, "x", dev, shape)
-    res_ptr, res_type, res_stride = _norm_rows(residual, "residual", dev, shape)
-    out_ptr, out_type, out_stride = _norm_rows(out, "out", dev, shape)
-    ro_ptr, ro_type, ro_stride = _norm_rows(res_out, "res_out", dev, shape)
-    if out is not None and out_stride != D:
-        raise ValueError("out: contiguous [T, D]")
-    if res_out is not None and (residual is None or ro_type != res_type):
-        raise ValueError("res_out: with a residual, in its type")
-    if weight is not None and (weight.dtype is not _F32 or weight.get_device() != dev or weight.numel() != D
-                               or not weight.is_contiguous()):
-        raise ValueError(f"weight: contiguous float32 [{D}]")
+    T, D = shape
+    n = T * D
+    x_ptr, x_type, x_stride = _norm_rows(x, "x", dev, shape, n)
+    res_ptr = ro_ptr = out_ptr = w_ptr = codes_ptr = scales_ptr = live_ptr = None
+    res_type = res_stride = ro_stride = out_type = 0
+    if residual is not None:
+        res_ptr, res_type, res_stride = _norm_rows(residual, "residual", dev, shape, n)
+    if res_out is not None:
+        ro_ptr, ro_type, ro_stride = _norm_rows(res_out, "res_out", dev, shape, n)
+        if residual is None or ro_type != res_type:
+            raise ValueError("res_out: with a residual, in its type")
+    if out is not None:
+        out_ptr, out_type, out_stride = _norm_rows(out, "out", dev, shape, n)
+        if out_stride != D:
+            raise ValueError("out: contiguous [T, D]")
+    if weight is not None:
+        if weight.dtype is not _F32 or weight.get_device() != dev or weight.numel() != D or not weight.is_contiguous():
+            raise ValueError(f"weight: contiguous float32 [{D}]")
+        w_ptr = weight.data_ptr()
     if (codes is None) != (scales is None):
         raise ValueError("codes and scales go together")
     if codes is not None:
-        if codes.dtype is not _U8 or codes.get_device() != dev or codes.numel() != T * D or not codes.is_contiguous():
+        if codes.dtype is not _U8 or codes.get_device() != dev or codes.numel() != n or not codes.is_contiguous():
             raise ValueError("codes: contiguous uint8 [T, D]")
         groups = -(-D // group) if group > 0 else 1
         if scales.dtype is not _F32 or scales.get_device() != dev or scales.numel() != T * groups \
                 or not scales.is_contiguous():
             raise ValueError(f"scales: contiguous float32 [T, {groups}]")
+        codes_ptr, scales_ptr = codes.data_ptr(), scales.data_ptr()
     if n_live is not None:
         _req_ints(dev, ("n_live", n_live, 1))
+        live_ptr = n_live.data_ptr()
     _launch(dev, stream, "ds4a_add_rms_norm", x_ptr, x_type, x_stride, res_ptr, res_type, res_stride, ro_ptr, ro_stride,
-            _opt(weight), eps, out_ptr, out_type, _opt(codes), _opt(scales), group, scale_style, _opt(n_live), T, D)
+            w_ptr, eps, out_ptr, out_type, codes_ptr, scales_ptr, group, scale_style, live_ptr, T, D)
