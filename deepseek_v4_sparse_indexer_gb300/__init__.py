@@ -6,7 +6,9 @@ The Python surface is the ctypes binding (same names as the C entry points)
 and DecodeStep / PrefillStep, which chain the three ops on one stream, plus
 DenseStep for the ratio-128 layers (attention over all rows, no indexer) and
 PagedDecodeStep, a decode step over caches in pages (lengths -> block tables and
-slots -> norm and rotation -> score -> select -> attention).
+slots -> norm and rotation -> score -> select -> attention), whose selection may
+go by blocks of rows and whose sequences may be cut by the attention their rows got.
+ds4a_add_rms_norm stands between layers: residual, norm, 8-bit output.
 """
 from ._binding import (Ds4aError, load, ds4a_version, ds4a_workspace_bytes, ds4a_get_device_status,
                        ds4a_debug_inject_error, ds4a_debug_wait_timeout, ds4a_indexer_score, ds4a_topk_select,

@@ -169,6 +169,12 @@ def test_captured_on_another_stream(cuda_lib):
         assert (out[live:] == 0).all() and torch.equal(res[live:], start[live:])
 
 
+def test_no_row(cuda_lib):
+    x = torch.empty(0, 512, dtype=BF, device=DEV)
+    cuda_lib.ds4a_add_rms_norm(x, None, EPS, out=torch.empty_like(x))
+    assert cuda_lib.ds4a_get_device_status() == (0, 0)
+
+
 def test_rejects_other_tensors(cuda_lib):
     x, w = torch.zeros(4, 256, dtype=BF, device=DEV), torch.ones(256, device=DEV)
     out, codes, scales = torch.empty_like(x), torch.empty(4, 256, dtype=torch.uint8, device=DEV), torch.empty(4, 2, device=DEV)

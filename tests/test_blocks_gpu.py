@@ -159,9 +159,19 @@ def test_scores_of_many_and_long_units(cuda_lib):
     s.check(0, 1)
 
 
+def test_scores_of_a_batch_of_short_units(cuda_lib):
+    """Every tile another unit's: queries change with each."""
+    rng = random.Random(4)
+    s = Scores([rng.choice((0, 1, 2, 3, 100, 130)) for _ in range(3000)], 130)
+    s(cuda_lib, n_first=1, n_last=1)
+    status(cuda_lib)
+    s.check(1, 1, units=range(0, 3000, 17))
+
+
+@pytest.mark.parametrize("cap", [300, 60000])        # a block of threads per tile, and the persistent scan
 @pytest.mark.parametrize("bad", [-1, "end", 2 ** 31 - 1])
-def test_scores_of_pages_outside_the_pool(cuda_lib, bad):
-    s = Scores([300, 40], 300)
+def test_scores_of_pages_outside_the_pool(cuda_lib, bad, cap):
+    s = Scores([300, 40], cap, max_pages=cap)
     s.table[0, 130] = s.n_pages if bad == "end" else bad
     s.table[0, 299] = -1                             # a last block too
     s(cuda_lib, n_last=1)
@@ -169,9 +179,11 @@ def test_scores_of_pages_outside_the_pool(cuda_lib, bad):
     s.check(0, 1, bad=((0, 130), (0, 299)))
 
 
-@pytest.mark.parametrize("n,limit", [(-1, 0), (101, 100), (2 ** 31 - 1, 100)])
-def test_block_counts_out_of_range(cuda_lib, n, limit):
-    s = Scores([100, 90], 100)
+@pytest.mark.parametrize("cap", [100, 60000])
+@pytest.mark.parametrize("n,limit", [(-1, 0), ("over", "cap"), (2 ** 31 - 1, "cap")])
+def test_block_counts_out_of_range(cuda_lib, n, limit, cap):
+    n, limit = cap + 1 if n == "over" else n, cap if limit == "cap" else limit
+    s = Scores([cap, 90], cap)
     s.n_blocks[0] = n
     s.blocks[0] = limit
     s(cuda_lib)
@@ -276,7 +288,7 @@ def some_lists(lengths, P, k, seed, order="ascending"):
 LENGTHS = [0, 1, 8, 47, 48, 49, 100, 257, 513, 1000]
 
 
-@pytest.mark.parametrize("P", [8, 16, 32, 64, 128, 512])
+@pytest.mark.parametrize("P", [8, 16, 32, 64, 128, 512, 4096])
 @pytest.mark.parametrize("H,fp8,order", [(64, False, "ascending"), (64, False, "descending"), (128, False, "any"),
                                          (64, True, "any")])
 def test_attention(cuda_lib, P, H, fp8, order):

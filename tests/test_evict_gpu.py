@@ -523,6 +523,35 @@ def test_plan_after_evictions(cuda_lib, form, ratio, P):
         assert o[p].tolist() == [x for x, _ in got] and o[s].tolist() == [y for _, y in got]
 
 
+@pytest.mark.parametrize("form,most", [(0, 3), (0, 70), (3, 1)])
+def test_plan_of_the_largest_batch(cuda_lib, form, most):
+    """8,192 sequences, most of them never cut: the plan of the tokens that are left, on one
+    block, every SM and by sequence."""
+    rng = random.Random(9)
+    B, ratio, P = 8192, 4, 8
+    past, add = [rng.randint(0, 200) for _ in range(B)], [rng.randint(0, most) for _ in range(B)]
+    gone = [rng.choice((0, 0, p // ratio)) for p in past]
+    T = max(sum(add), B)
+
+    def plan(past, **kw):
+        table = torch.full((B, 9), -1, dtype=torch.int32, device=DEV)
+        table[:, :8] = torch.arange(B * 8, device=DEV).view(B, 8)
+        o = [torch.zeros(n, dtype=torch.int32, device=DEV) for n in (B, B, B + 1, B + 1, T, T, T, T, 1)]
+        cuda_lib.ds4a_paged_plan(ints(past), ints(add), ratio, P, ints(list(range(B * 8, B * 24))), ints([0]), table, *o,
+                                 form=form, **kw)
+        status(cuda_lib)
+        return table, o
+    table, o = plan(past, gone=ints(gone))
+    held = [p - g * ratio for p, g in zip(past, gone)]
+    want_table, want = plan(held)
+    assert torch.equal(table, want_table)
+    for k in (0, 2, 3, 7, 8):                        # n_rows, cu_tok, cu_row, row_slot, head: by the rows held
+        assert torch.equal(o[k], want[k]), k
+    same = plan(past)[1]
+    assert torch.equal(o[1], same[1]) and torch.equal(o[4], same[4]) and torch.equal(o[5], same[5])
+    assert torch.equal(o[6], same[6])                # positions: by the tokens
+
+
 def test_plan_with_gone_out_of_range(cuda_lib):
     table = torch.full((2, 8), -1, dtype=torch.int32, device=DEV)
     o = [torch.zeros(n, dtype=torch.int32, device=DEV) for n in (2, 2, 3, 3, 4, 4, 4, 4, 1)]
