@@ -151,8 +151,9 @@ __global__ void __launch_bounds__(kKeyThreadsMax) block_keys_kernel(const __grid
 // in the store, and the unit's queries come by cp.async into two 64-dim halves of
 // 128-byte rows (128B-swizzled), one UMMA chain gives D[128 blocks x 64 heads] in
 // TMEM, and each thread sums its block's 64 weighted, rectified products.  For batches
-// of so few tiles that four of these a SM take them all at once: latency (32 x 1,024
-// blocks 4.7 us; larger batches this way 58 us where the scan below takes 28).
+// of so few tiles that four of these a SM take them all at once: latency (8 x 256 blocks
+// 3.6 us where the scan below takes 4.9, 32 x 1,024 4.7 and 5.3, 75 x 1,024, nearly the
+// most, 6.9 and 7.0; 64 x 16,384 58 and 28).
 constexpr int kTile = 128;
 constexpr int kScoreThreads = 128;
 constexpr int kHalfA = kTile * 128, kHalfB = kNIdxHead * 128;
