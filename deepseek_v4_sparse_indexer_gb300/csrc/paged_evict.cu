@@ -487,14 +487,15 @@ cudaError_t launch_evict(EvictArgs a, int num_sms, cudaStream_t s) {
     a.need = static_cast<int>((static_cast<long long>(a.keep) + (1 << a.shift) - 1) >> a.shift);
     a.keys_in_smem = cap <= kKeysMost;
     const size_t smem = a.keys_in_smem ? static_cast<size_t>(cap) * 4 : 0;
-    cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    // (the most that any call needs, not this one's: a call of another thread must not lower it)
+    cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeysMost * 4);
     if (e != cudaSuccess) return e;
     e = launch_k(evict_select_kernel, dim3(static_cast<unsigned>(a.B < num_sms ? a.B : num_sms)), dim3(kThreads), smem, s, a);
     if (e != cudaSuccess) return e;
     void (*kern)(EvictArgs) = a.fp8 ? evict_move_kernel<true> : evict_move_kernel<false>;
     const size_t lists = 2 * static_cast<size_t>(a.B) * sizeof(int);
     if (lists > 40960) {
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(lists));
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * DS4A_MAX_PLAN_SEQS * static_cast<int>(sizeof(int)));
         if (e != cudaSuccess) return e;
     }
     // two blocks an SM: sixteen warps, 8 to 10 KB of loads each

@@ -304,8 +304,9 @@ cudaError_t launch_paged_plan(PagedPlanArgs a, int num_sms, cudaStream_t s) {
     cudaError_t e = cudaSuccess;
     void (*kern)(PagedPlanArgs) = a.gone ? (a.form & kBySeq ? paged_plan_kernel<true, true> : paged_plan_kernel<false, true>)
                                          : (a.form & kBySeq ? paged_plan_kernel<true, false> : paged_plan_kernel<false, false>);
-    if (smem > 40960)
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (smem > 40960)      // (the most that any call needs, not this one's: a call of another thread must not lower it)
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 ((a.gone ? 6 : 5) * DS4A_MAX_PLAN_SEQS + 3) * static_cast<int>(sizeof(int)));
     if (e != cudaSuccess) return e;
     // One CTA covers a few thousand tokens and rows; more take every SM, or sixteen
     // CTAs as a cluster (a non-portable size) when the head is updated in place

@@ -2,6 +2,7 @@
 walk in Python, and plans after evictions."""
 import math
 import random
+from concurrent.futures import ThreadPoolExecutor
 
 import pytest
 import torch
@@ -481,7 +482,47 @@ def test_evict_captured_and_on_another_stream(cuda_lib):
         c.check()
 
 
+def in_two_threads(*calls):
+    """Each call many times over, in a thread of its own and on a stream of its own."""
+    def many(call):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(2000):
+                call()
+    torch.cuda.synchronize()
+    with ThreadPoolExecutor(len(calls)) as pool:
+        for done in [pool.submit(many, call) for call in calls]:
+            done.result()
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("lengths", [([40000], [500, 100]), ([9] * 8192, [5, 9] * 2700)])
+def test_evict_in_two_threads(cuda_lib, lengths):
+    """Calls of different sizes, whose kernels need different amounts of shared memory."""
+    caches = [Cache(n, 8, seed=k) for k, n in enumerate(lengths)]
+    for c in caches:
+        c.run(cuda_lib, 8, 8, in_place=False)
+    in_two_threads(*(c.call for c in caches))
+    status(cuda_lib)
+    for c in caches:
+        c.check()
+
+
 # ------------------------------------------------------------------------------ plans afterwards
+def test_plan_in_two_threads(cuda_lib):
+    def plan(B):
+        table = torch.full((B, 2), -1, dtype=torch.int32, device=DEV)
+        table[:, 0] = torch.arange(B, device=DEV)
+        o = [torch.zeros(n, dtype=torch.int32, device=DEV) for n in (B, B, B + 1, B + 1, 4 * B, 4 * B, B, B, 1)]
+        args = (ints([40] * B), ints([4] * B), 4, 8, ints(list(range(B, 3 * B))), ints([0]), table, *o)
+        return o, lambda: cuda_lib.ds4a_paged_plan(*args, gone=gone[B])
+    gone = {B: ints([5] * B) for B in (8192, 2000)}
+    plans = {B: plan(B) for B in gone}
+    in_two_threads(*(call for _, call in plans.values()))
+    status(cuda_lib)
+    for B, (o, _) in plans.items():
+        assert o[0].tolist() == [6] * B and o[8].item() == 0
+
+
 @pytest.mark.parametrize("form", [0, 1, 3, 4, 7])
 @pytest.mark.parametrize("ratio,P", [(4, 8), (1, 64), (128, 16)])
 def test_plan_after_evictions(cuda_lib, form, ratio, P):
