@@ -26,9 +26,10 @@ constexpr uint64_t kWaitLimitNs = 2000000000ull;   // 2 s
 // tail; the data order is the stream order, as without it.  The one exception: the
 // top-k kernels read the row counts (n_rows) before the wait.  A kernel starts early
 // only behind a kernel of this library, and the first kernel of such a chain started
-// only once the stream's earlier work had completed.  The one kernel that writes row
-// counts (paged_plan_kernel) never lets its dependents launch early and fences its
-// writes before it ends, so a chain behind it starts with them in place.
+// only once the stream's earlier work had completed.  The kernels that write such
+// counts (paged_plan_kernel, block_keys_kernel, evict_move_kernel) never let their
+// dependents launch early and fence their writes before they end, so a chain behind one
+// starts with them in place.
 DS4A_DEV void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 DS4A_DEV void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 

@@ -902,7 +902,8 @@ ds4a_status ds4a_paged_evict(const float *mass, int n_planes, int64_t mass_strid
  *    With A the largest |y| of the group (NaN elements do not count), s is the
  *    smallest power of two with A <= 448 s, as in 4c (DS4A_SCALE_POW2), or A / 448
  *    (DS4A_SCALE_MAX, at least 2^-126; codes are of y * (448 / A)); 1 where A is 0 or
- *    infinite.  A row whose sum of squares passes the fp32 range gives y = 0.
+ *    infinite.  A row whose sum of squares passes the fp32 range gives y = 0,
+ *    an infinite h itself NaN.
  *
  *    x        bf16, fp16 or fp32 (x_type) [T] rows, x_stride elements apart (device).
  *    res      bf16, fp16 or fp32 (res_type) [T] rows, res_stride apart, or NULL: h = x.
