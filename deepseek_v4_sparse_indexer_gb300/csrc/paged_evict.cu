@@ -326,16 +326,16 @@ template <bool FP8>
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_constant__ EvictArgs a) {
     // It writes row counts that a top-k may read before its own wait: no
     // pdl_launch_dependents here, and a fence before the end.
-    extern __shared__ int s_seq[];                         // [B] the evicted sequences, [B] old pages before each
+    extern __shared__ int s_rows[];                        // [B] rows before, as in the workspace
     __shared__ int s_ev[kMoveWarps], s_pg[kMoveWarps], s_tk[kMoveWarps];
-    int *s_ret = s_seq + a.B;
+    int *s_seq = s_rows + a.B, *s_ret = s_seq + a.B;       // [B] the evicted sequences, [B + 1] old pages before each
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const EvictWs ws = evict_ws(a.ws, a.B, a.need);
     pdl_wait();
-    // (What the select left is checked before it addresses anything: another call that uses
-    // the workspace at the same time must not become a fault.)
+    // What the select left is read once a block and checked before it addresses anything:
+    // another call that uses the workspace at the same time spoils the result, mostly
+    // without a sign of it, but makes no access out of range.
     const int cap = a.max_pages << a.shift;
-    auto rows_before = [&](int b) -> int { return min(ws.info[b], cap); };
     auto returned = [&](int b, int n) -> int {             // old pages of sequence b that go to the list
         const int pages = static_cast<int>((static_cast<long long>(n) + (1 << a.shift) - 1) >> a.shift);
         return pages - (a.n_shared ? min(max(a.n_shared[b], 0), pages) : 0);
@@ -344,7 +344,8 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
     const int per = (a.B + kMoveThreads - 1) / kMoveThreads, b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
     int ev = 0, pg = 0, tk = 0;
     for (int b = b0; b < b1; ++b) {
-        const int n = rows_before(b);
+        const int n = min(ws.info[b], cap);
+        s_rows[b] = n;
         tk += n != 0;
         if (n > 0) {
             ++ev;
@@ -372,7 +373,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
         taken += s_tk[w];
     }
     for (int b = b0; b < b1; ++b) {
-        const int n = rows_before(b);
+        const int n = s_rows[b];
         if (n > 0) {
             s_seq[e] = b;
             s_ret[e] = g;
@@ -380,6 +381,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
             g += returned(b, n);
         }
     }
+    if (tid == 0) s_ret[E] = G;
     __syncthreads();
     const int head = ws.head[0];
     const long long head_out = head < 0 ? head : head + static_cast<long long>(taken) * a.need - G;
@@ -447,14 +449,18 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
     // ---- tables and the free list: a warp per evicted sequence, from the last warp on
     // (the first ones have copies).  An entry is read before its place is written.
     for (int q = n_warps - 1 - me; q < E; q += n_warps) {
-        const int b = s_seq[q], n = rows_before(b);
+        const int b = s_seq[q], n = s_rows[b];
         const int pages = static_cast<int>((static_cast<long long>(n) + (1 << a.shift) - 1) >> a.shift);
-        const int shared = pages - returned(b, n);
+        const int shared = pages - (s_ret[q + 1] - s_ret[q]);
         const int32_t *table = a.table + b * a.table_stride;
         int32_t *table_out = a.table_out + b * a.table_stride;
         for (int i = lane; i < pages; i += 32) {
             const int old = table[i];
-            if (i < a.need) table_out[i] = ws.pages[static_cast<long long>(b) * a.need + i];
+            if (i < a.need) {
+                const int page = ws.pages[static_cast<long long>(b) * a.need + i];
+                if (page >= 0 && page < a.n_pages) table_out[i] = page;
+                else report(a.status, DS4A_DEV_BOUNDS);
+            }
             const long long at = head_out + s_ret[q] + (i - shared);
             if (i >= shared) {
                 if (at >= 0 && at < a.n_free) a.free_out[at] = old;
@@ -465,7 +471,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
     // ---- counts
     if (blockIdx.x == gridDim.x - 1) {
         for (int b = tid; b < a.B; b += kMoveThreads) {
-            const int n = rows_before(b), old = a.n_rows[b];
+            const int n = s_rows[b], old = a.n_rows[b];
             if (a.gone_out) a.gone_out[b] = (a.gone ? a.gone[b] : 0) + (n > 0 ? n - a.keep : 0);
             if (a.first_row) a.first_row[b] = n > 0 ? 0 : max(old, 0);
             a.n_rows_out[b] = n > 0 ? a.keep : old;
@@ -493,9 +499,9 @@ cudaError_t launch_evict(EvictArgs a, int num_sms, cudaStream_t s) {
     e = launch_k(evict_select_kernel, dim3(static_cast<unsigned>(a.B < num_sms ? a.B : num_sms)), dim3(kThreads), smem, s, a);
     if (e != cudaSuccess) return e;
     void (*kern)(EvictArgs) = a.fp8 ? evict_move_kernel<true> : evict_move_kernel<false>;
-    const size_t lists = 2 * static_cast<size_t>(a.B) * sizeof(int);
+    const size_t lists = (3 * static_cast<size_t>(a.B) + 1) * sizeof(int);
     if (lists > 40960) {
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * DS4A_MAX_PLAN_SEQS * static_cast<int>(sizeof(int)));
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (3 * DS4A_MAX_PLAN_SEQS + 1) * static_cast<int>(sizeof(int)));
         if (e != cudaSuccess) return e;
     }
     // two blocks an SM: sixteen warps, 8 to 10 KB of loads each
