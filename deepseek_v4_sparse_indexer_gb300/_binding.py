@@ -51,7 +51,7 @@ EXPORTS = ("ds4a_strerror", "ds4a_version", "ds4a_workspace_bytes", "ds4a_get_de
            "ds4a_rows_to_fp8", "ds4a_sparse_attn_decode_fp8", "ds4a_sparse_attn_prefill_fp8", "ds4a_indexer_topk",
            "ds4a_paged_plan", "ds4a_paged_plan_form", "ds4a_qk_norm_rope", "ds4a_paged_indexer_score",
            "ds4a_paged_attn_decode", "ds4a_paged_block_keys", "ds4a_paged_block_score", "ds4a_paged_attn_blocks",
-           "ds4a_paged_attn_mass", "ds4a_paged_evict", "ds4a_add_rms_norm", "ds4a_paged_plan_evicted")
+           "ds4a_paged_attn_mass", "ds4a_paged_evict", "ds4a_paged_evict_shared", "ds4a_add_rms_norm", "ds4a_paged_plan_evicted")
 DS4A_TOPK_NOALLOC_SCRATCH_BYTES = 8 << 20
 DS4A_MAX_TOP_K = 2048
 
@@ -156,6 +156,8 @@ def load(build_if_missing: bool = True):
                                    _i32, _i32, _vp, _i32, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                                    _sz, _vp]
     L.ds4a_paged_evict.restype = _i32
+    L.ds4a_paged_evict_shared.argtypes = L.ds4a_paged_evict.argtypes[:27] + [_vp] + L.ds4a_paged_evict.argtypes[27:]
+    L.ds4a_paged_evict_shared.restype = _i32
     L.ds4a_add_rms_norm.argtypes = [_vp, _i32, _i64, _vp, _i32, _i64, _vp, _i64, _vp, _f32, _vp, _i32, _vp, _vp, _i32,
                                     _i32, _vp, _i32, _i32, _vp]
     L.ds4a_add_rms_norm.restype = _i32
@@ -882,14 +884,16 @@ def ds4a_paged_block_score(iq, w, block_keys, table, n_blocks, scores, n_first=0
 
 def ds4a_paged_evict(mass, n_rows, table, rows, free_pages, free_head, keep, limit, mass_out, n_rows_out, table_out,
                      free_pages_out, free_head_out, ws, first=0, recent=0, row_scale=None, ik=None, n_shared=None,
-                     gone=None, gone_out=None, first_row=None, stream=None):
+                     gone=None, gone_out=None, first_row=None, stream=None, n_shared_out=None):
     """Cuts every sequence of more than `limit` rows to `keep`: its first `first`, its
     last `recent` and those of the greatest mass, copied to pages of the free list;
     the old pages go back to it.  mass f32 [planes,B,>= max_pages * P]; n_rows i32
     [B]; table i32 [B,max_pages]; rows bf16 or uint8 [n_pages,P,512] with row_scale
     f32 [n_pages,P], ik bf16 [n_pages,P,128] or None (all updated); free_pages i32
     [n_free], free_head i32 [1]; each *_out may be its input; n_shared, gone,
-    gone_out, first_row i32 [B] or None; ws uint8 workspace of
+    gone_out, first_row i32 [B] or None; n_shared_out i32 [B] or None (written, with
+    n_shared: 0 for the sequences cut, whose pages are their own now; a sequence cut
+    again with its old number loses pages); ws uint8 workspace of
     ds4a_workspace_bytes(DS4A_OP_PAGED_EVICT, B, 1, max_pages * P, keep)."""
     dev = _device_index(mass, "mass")
     B, n_free, shape = n_rows.numel(), free_pages.numel(), mass.shape
@@ -927,8 +931,15 @@ def ds4a_paged_evict(mass, n_rows, table, rows, free_pages, free_head, keep, lim
             if not _ints_ok(dev, B, t):
                 _req_ints(dev, (("n_shared", "gone", "gone_out", "first_row")[k], t, B))
             opt[k] = t.data_ptr()
+    name = "ds4a_paged_evict"
+    if n_shared_out is not None:
+        _req_ints(dev, ("n_shared_out", n_shared_out, B))
+        if n_shared is None:
+            raise ValueError("n_shared_out: with n_shared")
+        name = "ds4a_paged_evict_shared"
+        opt.insert(1, n_shared_out.data_ptr())
     ws_ptr, ws_bytes = _workspace(ws, dev)
-    _launch(dev, stream, "ds4a_paged_evict", mass.data_ptr(), shape[0], shape[2], mass_out.data_ptr(),
+    _launch(dev, stream, name, mass.data_ptr(), shape[0], shape[2], mass_out.data_ptr(),
             n_rows.data_ptr(), n_rows_out.data_ptr(), table.data_ptr(), table_out.data_ptr(), stride, max_pages, page_size,
             n_pages, B, keep, limit, first, recent, rows.data_ptr(), DS4A_E4M3 if fp8 else DS4A_BF16, scale_ptr, ik_ptr,
             free_pages.data_ptr(), free_pages_out.data_ptr(), n_free, free_head.data_ptr(), free_head_out.data_ptr(), *opt,

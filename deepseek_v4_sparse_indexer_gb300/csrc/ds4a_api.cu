@@ -982,20 +982,21 @@ ds4a_status ds4a_paged_block_score(const uint16_t *iq, const float *w, const uin
     return launch_block_score(a, di->sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? DS4A_OK : DS4A_ECUDA;
 }
 
-ds4a_status ds4a_paged_evict(const float *mass, int n_planes, int64_t mass_stride, float *mass_out,
-                             const int32_t *n_rows, int32_t *n_rows_out, const int32_t *table, int32_t *table_out,
-                             int64_t table_stride, int max_pages, int page_size, int n_pages, int B, int keep,
-                             int limit, int first, int recent, void *rows, int rows_type, float *row_scale,
-                             uint16_t *ik, const int32_t *free_pages, int32_t *free_pages_out, int n_free,
-                             const int32_t *free_head, int32_t *free_head_out, const int32_t *n_shared,
-                             const int32_t *gone, int32_t *gone_out, int32_t *first_row, void *ws, size_t ws_bytes,
-                             void *stream) {
-    const NvtxRange nvtx_range("ds4a_paged_evict");
+namespace {
+ds4a_status evict_call(const char *name, const float *mass, int n_planes, int64_t mass_stride, float *mass_out,
+                       const int32_t *n_rows, int32_t *n_rows_out, const int32_t *table, int32_t *table_out,
+                       int64_t table_stride, int max_pages, int page_size, int n_pages, int B, int keep, int limit,
+                       int first, int recent, void *rows, int rows_type, float *row_scale, uint16_t *ik,
+                       const int32_t *free_pages, int32_t *free_pages_out, int n_free, const int32_t *free_head,
+                       int32_t *free_head_out, const int32_t *n_shared, int32_t *n_shared_out, const int32_t *gone,
+                       int32_t *gone_out, int32_t *first_row, void *ws, size_t ws_bytes, void *stream) {
+    const NvtxRange nvtx_range(name);
     if (ds4a_status inj = take_injected()) return inj;
     if (rows_type != DS4A_BF16 && rows_type != DS4A_E4M3) return DS4A_EUNSUPPORTED;
     const int shift = page_shift(page_size);
     if (!mass || !mass_out || !n_rows || !n_rows_out || !table || !table_out || !rows || !free_head || !free_head_out ||
-        shift < 0 || n_free < 0 || (n_free > 0 && (!free_pages || !free_pages_out)) || (gone && !gone_out))
+        shift < 0 || n_free < 0 || (n_free > 0 && (!free_pages || !free_pages_out)) || (gone && !gone_out) ||
+        (n_shared_out && !n_shared))
         return DS4A_EINVAL;
     if (n_planes < 1 || n_planes > 16 || B < 1 || B > DS4A_MAX_PLAN_SEQS || n_pages < 1 || max_pages < 1 ||
         table_stride < max_pages)
@@ -1039,12 +1040,43 @@ ds4a_status ds4a_paged_evict(const float *mass, int n_planes, int64_t mass_strid
     a.free_head = free_head;
     a.head_out = free_head_out;
     a.n_shared = n_shared;
+    a.n_shared_out = n_shared_out;
     a.gone = gone;
     a.gone_out = gone_out;
     a.first_row = first_row;
     a.ws = ws;
     a.status = di->status;
     return launch_evict(a, di->sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? DS4A_OK : DS4A_ECUDA;
+}
+}  // namespace
+
+ds4a_status ds4a_paged_evict(const float *mass, int n_planes, int64_t mass_stride, float *mass_out,
+                             const int32_t *n_rows, int32_t *n_rows_out, const int32_t *table, int32_t *table_out,
+                             int64_t table_stride, int max_pages, int page_size, int n_pages, int B, int keep,
+                             int limit, int first, int recent, void *rows, int rows_type, float *row_scale,
+                             uint16_t *ik, const int32_t *free_pages, int32_t *free_pages_out, int n_free,
+                             const int32_t *free_head, int32_t *free_head_out, const int32_t *n_shared,
+                             const int32_t *gone, int32_t *gone_out, int32_t *first_row, void *ws, size_t ws_bytes,
+                             void *stream) {
+    return evict_call("ds4a_paged_evict", mass, n_planes, mass_stride, mass_out, n_rows, n_rows_out, table, table_out,
+                      table_stride, max_pages, page_size, n_pages, B, keep, limit, first, recent, rows, rows_type,
+                      row_scale, ik, free_pages, free_pages_out, n_free, free_head, free_head_out, n_shared, nullptr, gone,
+                      gone_out, first_row, ws, ws_bytes, stream);
+}
+
+ds4a_status ds4a_paged_evict_shared(const float *mass, int n_planes, int64_t mass_stride, float *mass_out,
+                                    const int32_t *n_rows, int32_t *n_rows_out, const int32_t *table, int32_t *table_out,
+                                    int64_t table_stride, int max_pages, int page_size, int n_pages, int B, int keep,
+                                    int limit, int first, int recent, void *rows, int rows_type, float *row_scale,
+                                    uint16_t *ik, const int32_t *free_pages, int32_t *free_pages_out, int n_free,
+                                    const int32_t *free_head, int32_t *free_head_out, const int32_t *n_shared,
+                                    int32_t *n_shared_out, const int32_t *gone, int32_t *gone_out, int32_t *first_row,
+                                    void *ws, size_t ws_bytes, void *stream) {
+    if (!n_shared || !n_shared_out) return DS4A_EINVAL;
+    return evict_call("ds4a_paged_evict_shared", mass, n_planes, mass_stride, mass_out, n_rows, n_rows_out, table, table_out,
+                      table_stride, max_pages, page_size, n_pages, B, keep, limit, first, recent, rows, rows_type,
+                      row_scale, ik, free_pages, free_pages_out, n_free, free_head, free_head_out, n_shared, n_shared_out,
+                      gone, gone_out, first_row, ws, ws_bytes, stream);
 }
 
 ds4a_status ds4a_add_rms_norm(const void *x, int x_type, int64_t x_stride, const void *res, int res_type,

@@ -248,6 +248,7 @@ struct EvictArgs {
     const int32_t *free_head;
     int32_t *head_out;
     const int32_t *n_shared;     // [B] or null
+    int32_t *n_shared_out;       // [B] or null
     const int32_t *gone;         // [B] or null
     int32_t *gone_out;           // [B] or null
     int32_t *first_row;          // [B] or null

@@ -34,7 +34,7 @@ constexpr int kRun = 8;                       // rows a thread places at a time
 // again in every pass 162.
 constexpr int kKeysMost = 49152;
 
-// ---- workspace (ints): [0] the list's head, then per sequence: rows before (0: left
+// ---- workspace (ints): [0] the list's head, [1] blocks that have read n_shared, then per sequence: rows before (0: left
 // alone, -1: refused behind its place in the list); new pages; the kept rows' slots
 struct EvictWs {
     int32_t *head, *info, *pages, *src;
@@ -291,7 +291,10 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const __grid_
             if (rows_of(b) != a.n_rows[b] || head < 0) report(a.status, DS4A_DEV_BOUNDS);
         }
     }
-    if (blockIdx.x == 0 && tid == 0) ws.head[0] = head;
+    if (blockIdx.x == 0 && tid == 0) {
+        ws.head[0] = head;
+        ws.head[1] = 0;
+    }
     int inc = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -328,6 +331,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
     // pdl_launch_dependents here, and a fence before the end.
     extern __shared__ int s_rows[];                        // [B] rows before, as in the workspace
     __shared__ int s_ev[kMoveWarps], s_pg[kMoveWarps], s_tk[kMoveWarps];
+    __shared__ int s_last;
     int *s_seq = s_rows + a.B, *s_ret = s_seq + a.B;       // [B] the evicted sequences, [B + 1] old pages before each
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const EvictWs ws = evict_ws(a.ws, a.B, a.need);
@@ -467,6 +471,14 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
                 else report(a.status, DS4A_DEV_BOUNDS);
             }
         }
+    }
+    // ---- a cut sequence shares nothing any more: written by the last block that has read the
+    // old numbers, which may lie in the same place
+    if (a.n_shared_out) {
+        if (tid == 0) s_last = atomicAdd(&ws.head[1], 1) == static_cast<int>(gridDim.x) - 1;
+        __syncthreads();
+        if (s_last)
+            for (int b = tid; b < a.B; b += kMoveThreads) a.n_shared_out[b] = s_rows[b] > 0 ? 0 : a.n_shared[b];
     }
     // ---- counts
     if (blockIdx.x == gridDim.x - 1) {

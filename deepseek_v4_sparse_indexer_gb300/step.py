@@ -211,7 +211,8 @@ class PagedDecodeStep:
     evict = (keep, limit, first, recent), evict(x) cuts the sequences that the last
     step left with more than limit rows to keep of them (ds4a_paged_evict, in
     place); x["gone"] i32 [U] (zeros for a new sequence) counts the rows evicted,
-    which later steps' plans go by.  x may hold n_shared i32 [U].
+    which later steps' plans go by.  x may hold n_shared i32 [U], the leading pages that
+    other sequences hold too: zeros afterwards for those that were cut.
     """
 
     def __init__(self, U, max_pages, page_size, top_k=512, ratio=4, device="cuda", n_head=B.N_HEAD, fp8=False, eps=1e-6,
@@ -321,7 +322,7 @@ class PagedDecodeStep:
                            x["mass"], self.n_rows, x["table"], x["free_pages"], x["free_head"], self.ws_evict, first=first,
                            recent=recent, row_scale=x["row_scale"] if self.fp8 else None,
                            ik=x["ik"] if self.listed else None, n_shared=x.get("n_shared"), gone=x["gone"],
-                           gone_out=x["gone"], first_row=self.first_row, stream=stream)
+                           gone_out=x["gone"], first_row=self.first_row, stream=stream, n_shared_out=x.get("n_shared"))
         if self.blocks:
             B.ds4a_paged_block_keys(x["ik"], x["table"], self.n_rows, x["block_keys"], self.n_blocks,
                                     first_row=self.first_row, stream=stream)

@@ -862,7 +862,10 @@ ds4a_status ds4a_paged_attn_mass(int n_head, const uint16_t *q, const void *rows
  *                start is dropped and sets DS4A_DEV_BOUNDS.
  *    n_shared    int32 [B] or NULL (device): leading pages of a sequence that other
  *                sequences hold too; they are not returned (their rows are copied, so
- *                the others read them as before).
+ *                the others read them as before; a page that its last holder has let
+ *                go is the program's to put back).  A cut sequence's new pages are its
+ *                own: its entry has to be 0 from then on, else as many of them are not
+ *                returned when it is cut again.  ds4a_paged_evict_shared sees to that.
  *    gone        int32 [B] or NULL (device): rows evicted earlier (zeros when NULL).
  *                gone_out int32 [B] or NULL (device, written; may be gone): with this
  *                call's added, for ds4a_paged_plan_evicted.
@@ -888,6 +891,26 @@ ds4a_status ds4a_paged_evict(const float *mass, int n_planes, int64_t mass_strid
                              const int32_t *free_head, int32_t *free_head_out,
                              const int32_t *n_shared, const int32_t *gone, int32_t *gone_out,
                              int32_t *first_row, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * 7c. 7b with the shared pages kept up to date, for sequences that may be cut again
+ *    (which ones were is known on the device only).
+ *
+ *    n_shared, n_shared_out  int32 [B] (device; the second written, may be the first):
+ *                n_shared_out is 0 for an evicted sequence, n_shared for another.
+ *                Neither is NULL.
+ *    Everything else is as in 7b.
+ */
+ds4a_status ds4a_paged_evict_shared(const float *mass, int n_planes, int64_t mass_stride,
+                                    float *mass_out, const int32_t *n_rows, int32_t *n_rows_out,
+                                    const int32_t *table, int32_t *table_out, int64_t table_stride,
+                                    int max_pages, int page_size, int n_pages, int B, int keep,
+                                    int limit, int first, int recent, void *rows, int rows_type,
+                                    float *row_scale, uint16_t *ik, const int32_t *free_pages,
+                                    int32_t *free_pages_out, int n_free, const int32_t *free_head,
+                                    int32_t *free_head_out, const int32_t *n_shared,
+                                    int32_t *n_shared_out, const int32_t *gone, int32_t *gone_out,
+                                    int32_t *first_row, void *ws, size_t ws_bytes, void *stream);
 
 /*
  * 8. The residual's addition, RMS norm and 8-bit output, in one pass over T rows of
