@@ -11,7 +11,7 @@
 // evict_select_kernel, a block of 1,024 threads per sequence over its limit (every block
 // scans the lengths and takes its share of them): the kept rows' smallest
 // key by a radix select (11, 11 and 10 bits of an order-preserving key; keys in shared
-// memory where they fit), then the kept rows' slots and masses in their new places, by
+// memory where the table's rows fit), then the kept rows' slots and masses in their new places, by
 // counts over the warps' runs of rows.  evict_move_kernel: the
 // copies, eight rows a warp (all of their loads in flight), and the lists.
 // Bound: the copies HBM; a few sequences the select's chain of passes.  Measured (GB300):
@@ -30,8 +30,11 @@ constexpr int kThreads = 1024, kWarps = kThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kBatch = 8;                     // rows a thread has in flight in the passes over all rows
 constexpr int kRun = 8;                       // rows a thread places at a time
-// Keys that fit into shared memory (192 KB): 64 x 16,384 rows 150 us, with the masses read
-// again in every pass 162.
+// Rows of a table whose keys fit into shared memory (192 KB): 64 x 16,384 rows 150 us, with
+// the masses read again in every pass 162.  By the table's rows and not each sequence's: with
+// 192 KB taken for the sequences that fit, in tables of 65,536 rows, 64 x 16,384 took 176 us
+// instead of 166 and 2 x 65,536 (re-read, through what was left of L1) 78 instead of 74; 4 x
+// 4,096 took 14.8 instead of 15.8.
 constexpr int kKeysMost = 49152;
 
 // ---- workspace (ints): [0] the list's head, [1] blocks that have read n_shared, then per sequence: rows before (0: left
