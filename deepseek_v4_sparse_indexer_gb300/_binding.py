@@ -864,7 +864,8 @@ def ds4a_paged_block_score(iq, w, block_keys, table, n_blocks, scores, n_first=0
     """Indexer scores of one query per unit over its blocks' mean keys: iq bf16
     [U,1,64,128]; w f32 [U,1,64]; block_keys bf16 [n_pages,128]; table i32
     [U,max_pages]; n_blocks i32 [U]; scores f32 [U,1,NB_cap] (written for b <
-    n_blocks[u]; +inf for the first n_first and last n_last blocks)."""
+    n_blocks[u]; +inf for the first n_first and last n_last blocks, which a list of at
+    least n_first + n_last then holds)."""
     dev = _device_index(iq, "iq")
     if scores.dim() != 3:
         raise ValueError("scores: [U, 1, NB_cap]")

@@ -203,7 +203,7 @@ class PagedDecodeStep:
 
     blocks = k (with top_k = 0) selects k blocks, whole pages, instead of rows, by the
     indexer's score of each block's mean key, keep_blocks = (first, last) of them
-    whatever they score; x also holds block_keys bf16 [n_pages,128], kept by the
+    whatever they score (at most k together); x also holds block_keys bf16 [n_pages,128], kept by the
     program.
 
     mass = True adds the weights of each step's attention to x["mass"] f32
@@ -220,6 +220,8 @@ class PagedDecodeStep:
                  rotate_iq=True, blocks=0, keep_blocks=(0, 0), mass=False, evict=None):
         if blocks and top_k:
             raise ValueError("blocks: with top_k = 0")
+        if blocks and (min(keep_blocks) < 0 or sum(keep_blocks) > blocks):
+            raise ValueError("keep_blocks: (first, last), at most `blocks` together")
         if evict is not None and not mass:
             raise ValueError("evict: with mass = True")
         self.U, self.page_size, self.top_k, self.ratio, self.n_head = U, page_size, top_k, ratio, n_head
