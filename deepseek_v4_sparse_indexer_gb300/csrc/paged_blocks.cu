@@ -161,6 +161,13 @@ constexpr int kOffA = 0, kOffB = 2 * kHalfA, kOffW = kOffB + 2 * kHalfB, kOffPag
 constexpr int kOffBar = kOffPage + kTile * 4, kScoreSmem = kOffBar + 16 + 1024;
 constexpr uint32_t kScoreCols = 64;
 
+// max(0, x), NaN where x is: a page with such a key must not pass for one that scores 0.
+DS4A_DEV float rectified(uint32_t x) {
+    float y;
+    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(y) : "f"(__uint_as_float(x)));
+    return y;
+}
+
 // Block b's score (nothing past the unit's n blocks).
 DS4A_DEV void store_score(const BlockScoreArgs &a, int u, int b, int n, bool there, float s) {
     if (b >= n) return;
@@ -245,10 +252,10 @@ __global__ void __launch_bounds__(kScoreThreads) block_score_kernel(const __grid
 #pragma unroll
             for (int h = 0; h < 32; h += 4) {
                 const float4 w = *reinterpret_cast<const float4 *>(sW + hh * 32 + h);
-                s0 = fmaf(w.x, fmaxf(__uint_as_float(v[h]), 0.f), s0);
-                s1 = fmaf(w.y, fmaxf(__uint_as_float(v[h + 1]), 0.f), s1);
-                s2 = fmaf(w.z, fmaxf(__uint_as_float(v[h + 2]), 0.f), s2);
-                s3 = fmaf(w.w, fmaxf(__uint_as_float(v[h + 3]), 0.f), s3);
+                s0 = fmaf(w.x, rectified(v[h]), s0);
+                s1 = fmaf(w.y, rectified(v[h + 1]), s1);
+                s2 = fmaf(w.z, rectified(v[h + 2]), s2);
+                s3 = fmaf(w.w, rectified(v[h + 3]), s3);
             }
         }
         store_score(a, u, b, n, page >= 0, (s0 + s1) + (s2 + s3));
@@ -524,10 +531,10 @@ __global__ void __launch_bounds__(kScanThreads, 1) block_scan_kernel(const __gri
 #pragma unroll
                 for (int h = 0; h < 32; h += 4) {
                     const float4 q = wt[hh * 8 + h / 4];
-                    s0 = fmaf(q.x, fmaxf(__uint_as_float(v[h]), 0.f), s0);
-                    s1 = fmaf(q.y, fmaxf(__uint_as_float(v[h + 1]), 0.f), s1);
-                    s2 = fmaf(q.z, fmaxf(__uint_as_float(v[h + 2]), 0.f), s2);
-                    s3 = fmaf(q.w, fmaxf(__uint_as_float(v[h + 3]), 0.f), s3);
+                    s0 = fmaf(q.x, rectified(v[h]), s0);
+                    s1 = fmaf(q.y, rectified(v[h + 1]), s1);
+                    s2 = fmaf(q.z, rectified(v[h + 2]), s2);
+                    s3 = fmaf(q.w, rectified(v[h + 3]), s3);
                 }
             }
             tc_fence_before();

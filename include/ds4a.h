@@ -766,7 +766,9 @@ ds4a_status ds4a_paged_block_keys(const uint16_t *ik, int n_pages, int page_size
  *    then selected whatever they score, as long as n_first + n_last <= top_k and no
  *    other block scores +inf (equal scores go to the lower block, so that with a
  *    shorter list the last blocks are lost).  ds4a_topk_select over [U][1][NB_cap]
- *    with n_blocks for its n_rows gives the lists that 6c reads.
+ *    with n_blocks for its n_rows gives the lists that 6c reads.  A NaN in a block's
+ *    mean key (or in the unit's iq or w) makes its score NaN, which the select never
+ *    takes; 1 and 5c count a NaN product of a row's key as 0.
  *
  *    iq, w, table  as in 5c.    block_keys  bf16 [n_pages][128], 16-byte aligned.
  *    n_blocks  int32 [U] (device), 0 .. min(NB_cap, max_pages); a count outside sets
