@@ -968,7 +968,7 @@ def ds4a_add_rms_norm(x, weight, eps, out=None, residual=None, res_out=None, cod
                       scale_style=DS4A_SCALE_POW2, n_live=None, stream=None):
     """h = x + residual; y = h * weight / sqrt(mean h^2 + eps): x [T,D], residual
     [T,D] or None and res_out [T,D] (h; may be residual) in bf16, fp16 or fp32, rows
-    any stride apart; weight f32 [D] or None; out [T,D] in 16 or 32 bits and / or
+    any stride apart; weight f32 [D] or None; out [T,D] in 16 or 32 bits (may be x) and / or
     codes uint8 [T,D] E4M3 with scales f32 [T,ceil(D / group)] (written), a scale
     for every 32, 64 or 128 elements or (group = 0) for a row; n_live i32 [1] or
     None: rows from there on are left as they were."""

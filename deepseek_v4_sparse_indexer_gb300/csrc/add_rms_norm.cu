@@ -12,7 +12,9 @@
 //
 // A row is a block's (rows of up to 512 elements a warp's, four to a block): a thread
 // holds C octets of elements, octet c of the row in thread c % threads, so that a
-// group's maximum is a butterfly over neighbouring lanes.  Blocks are not kept for
+// group's maximum is a butterfly over neighbouring lanes.  It has read all of its
+// elements of x and r before it writes the first, so h and y may lie in their place.
+// Blocks are not kept for
 // several rows: enough of them share an SM to cover each other's loads and barriers (one
 // a row, two with a scale per row), and the weight comes from L1.
 // Bound: HBM (7 flop for 4 to 17 bytes), with the instructions close behind: products

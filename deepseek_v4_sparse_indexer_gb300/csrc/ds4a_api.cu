@@ -11,6 +11,7 @@
 
 #include "../../include/ds4a.h"
 #include "internal.h"
+#include "span.h"
 
 using namespace ds4a;
 
@@ -1104,6 +1105,22 @@ ds4a_status ds4a_add_rms_norm(const void *x, int x_type, int64_t x_stride, const
         (res_out && !stride_ok(res_out_stride, res_type)))
         return DS4A_EINVAL;
     if (res_out == res && res && T > 1 && res_out_stride != res_stride) return DS4A_EINVAL;
+    const long long groups = codes && group ? (D + group - 1) / group : 1;
+    auto rows_of = [&](const void *p, int type, int64_t stride) -> Span {
+        const int size = type == DS4A_F32 ? 4 : 2;
+        return {p, T, T > 1 ? stride * size : 0, static_cast<long long>(D) * size, type};
+    };
+    const Span in[] = {rows_of(x, x_type, x_stride), rows_of(res, res_type, res_stride), {weight, 1, 0, 4LL * D, -1},
+                       {n_live, 1, 0, 4, -1}};
+    const Span to[] = {rows_of(res_out, res_type, res_out_stride), rows_of(out, out_type, D),
+                       {codes, 1, 0, static_cast<long long>(T) * D, -2}, {codes ? scales : nullptr, 1, 0, 4 * groups * T, -2}};
+    // (an output in the place of x or res: each element is read by the thread that writes it)
+    for (int i = 0; i < 4; ++i) {
+        for (const Span &r : in)
+            if (overlap(to[i], r) && !same(to[i], r)) return DS4A_EINVAL;
+        for (int k = 0; k < i; ++k)
+            if (overlap(to[i], to[k])) return DS4A_EINVAL;
+    }
     DevInfo *di = nullptr;
     if (ds4a_status st = current_device(&di)) return st;
     AddNormArgs a{};
@@ -1122,7 +1139,7 @@ ds4a_status ds4a_add_rms_norm(const void *x, int x_type, int64_t x_stride, const
     a.codes = codes;
     a.scales = scales;
     a.group = group;
-    a.n_groups = codes && group ? (D + group - 1) / group : 1;
+    a.n_groups = static_cast<int>(groups);
     a.scale_style = scale_style;
     a.n_live = n_live;
     a.T = T;

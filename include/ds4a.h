@@ -935,7 +935,7 @@ ds4a_status ds4a_paged_evict_shared(const float *mass, int n_planes, int64_t mas
  *    x        bf16, fp16 or fp32 (x_type) [T] rows, x_stride elements apart (device).
  *    res      bf16, fp16 or fp32 (res_type) [T] rows, res_stride apart, or NULL: h = x.
  *    res_out  [T] rows of res_type, res_out_stride apart, or NULL (device, written; may
- *             be res itself, with its stride).
+ *             be res itself, with its stride, or x, with its type and stride).
  *    weight   fp32 [D] or NULL: all ones (device).
  *    out      bf16, fp16 or fp32 (out_type) [T][D], contiguous, or NULL (device, written).
  *    codes    uint8 [T][D], contiguous, or NULL (device, written).  At least one of out
@@ -948,8 +948,9 @@ ds4a_status ds4a_paged_evict_shared(const float *mass, int n_planes, int64_t mas
  *             clamped.
  *    D a multiple of 8 up to DS4A_MAX_NORM_DIM (else DS4A_EUNSUPPORTED), T >= 0 (0:
  *    nothing is launched), eps > 0.  Buffers 16-byte aligned (scales 4), strides
- *    at least D and whole multiples of 16 bytes.  No output overlaps another buffer,
- *    but for res_out that is res.
+ *    at least D and whole multiples of 16 bytes.  No output overlaps another buffer
+ *    (DS4A_EINVAL), but that res_out and out may each be x or res itself: the same
+ *    address, type and stride (in place; not both the same one).
  */
 ds4a_status ds4a_add_rms_norm(const void *x, int x_type, int64_t x_stride, const void *res,
                               int res_type, int64_t res_stride, void *res_out,
