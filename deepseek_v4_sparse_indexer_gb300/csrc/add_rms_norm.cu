@@ -10,18 +10,18 @@
 //
 // Sums, norm and scales in fp32; one rounding to each output's type.
 //
-// A row is a block's (rows of up to 512 elements a warp's, four to a block): a thread
-// holds C octets of elements, octet c of the row in thread c % threads, so that a
-// group's maximum is a butterfly over neighbouring lanes.  It has read all of its
-// elements of x and r before it writes the first, so h and y may lie in their place.
-// Blocks are not kept for
-// several rows: enough of them share an SM to cover each other's loads and barriers (one
-// a row, two with a scale per row), and the weight comes from L1.
-// Bound: HBM (7 flop for 4 to 17 bytes), with the instructions close behind: products
+// A row is a block's; short ones (up to 256 elements in a batch of few rows, up to 512 in
+// one of many) are a warp's, four to a block.  A thread holds C octets of elements, octet
+// c of the row in thread c % threads, so that a group's maximum is a butterfly over
+// neighbouring lanes.  It has read all of its elements of x and r before it writes the
+// first, so h and y may lie in their place.  Blocks are not kept for several rows:
+// enough of them share an SM to cover each other's loads and barriers (one a row, two
+// with a scale per row), and the weight comes from L1.
+// Bound: HBM (7 flop for 3 to 17 bytes), with the instructions close behind: products
 // and sums go two at a time (fp32x2).  Measured (GB300): 8,192 x 4,096, bf16 with an fp32
 // residual, into codes 58 us = 6.4 TB/s, 94 % of the copy bandwidth; all bf16, both
 // outputs, 48 us = 93 %; 2,048 x 16,384 47 us = 5.0 TB/s (a row's block of 512 threads,
-// two an SM); one row of 4,096 2.4 us.
+// two an SM); one row of 4,096 2.5 us.
 #include <cuda_fp16.h>
 
 #include "common.cuh"
