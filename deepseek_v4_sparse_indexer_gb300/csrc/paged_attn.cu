@@ -62,7 +62,8 @@
 // way, 66 % of the copy bandwidth: the end of each unit, 4 us, weighs more on 45 tiles).
 // Masses: 2^(l - lse) of each row summed over heads, with no values and no window; a
 // row tile is free once its logits are done (256 ragged units of up to 8,192 rows 174 us
-// = 6.3 TB/s, 93 %; 16 x 512 listed rows 12 us).
+// = 6.3 TB/s, 93 %; FP8 rows 222, the pass that writes the codes out; 16 x 512 listed
+// rows 12 us).
 //
 // Every wait is bounded (DS4A_DEV_TIMEOUT); on timeout the CTA drains what it
 // issued (bounded), frees TMEM and returns.

@@ -826,6 +826,11 @@ ds4a_status ds4a_paged_attn_blocks(int n_head, const uint16_t *q, const void *ro
  *             mass_stride >= max_pages * page_size.  A program keeps it beside its
  *             tables and starts a sequence's row with zeros.
  *    A masked row (5d, 6c) is not added to.  No workspace.
+ *    One query a unit: a prompt's tokens add nothing by themselves.  A program that
+ *    wants their weights gives them as units (q and lse of the token, the sequence's
+ *    table, n_rows the rows before it, a mass row each) and adds those rows up; else
+ *    the first eviction ranks a prompt's rows by the decode steps since, and those
+ *    that got nothing by age (7b keeps the lower of equal masses).
  */
 ds4a_status ds4a_paged_attn_mass(int n_head, const uint16_t *q, const void *rows, int rows_type,
                                  const float *row_scale, int n_pages, int page_size,
