@@ -216,27 +216,24 @@ struct Lens {
 };
 template <int KIND>
 DS4A_DEV Lens lens_of(const PagedAttnArgs &a, int u) {
+    constexpr bool kWindow = KIND != kMassKind;    // the window gets no mass
     Lens l;
-    const int n = a.n_rows[u], c = a.idx ? a.count[u] : n;
+    const int n = a.n_rows[u], c = a.idx ? a.count[u] : n, r = kWindow ? a.n_raw[u] : 0;
+    l.ring = !kWindow ? 0 : a.ring ? a.ring[u] : u;
     l.lim = min(max(n, 0), a.N_cap);
     if (lists_blocks<KIND>(a)) {                   // the last block's rows counted whole
         const int listed = min(max(c, 0), a.idx_stride);
         l.cnt = listed << a.page_shift;
-        l.ok = l.lim == n && listed == c;
+        l.ok = listed == c;
     } else {
         l.cnt = min(max(c, 0), a.list_cap);
-        l.ok = l.lim == n && l.cnt == c;
+        l.ok = l.cnt == c;
     }
-    l.nrw = l.ring = 0;
-    if constexpr (KIND == kMassKind) {             // the window gets no mass, nor a unit without a token
-        if (a.tok_pos && a.tok_pos[u] < 0) l.cnt = 0;
-        return l;
-    }
-    const int r = a.n_raw[u];
-    l.ring = a.ring ? a.ring[u] : u;
     l.nrw = min(max(r, 0), kNSwa);
-    l.ok = l.ok && l.nrw == r;
-    if (l.ring < 0 || l.ring >= a.n_ring) {
+    l.ok = l.ok && l.lim == n && l.nrw == r;
+    if (!kWindow) {                                // nor does a unit without a token
+        if (a.tok_pos && a.tok_pos[u] < 0) l.cnt = 0;
+    } else if (l.ring < 0 || l.ring >= a.n_ring) {
         l.ok = l.ok && l.nrw == 0;     // a unit without raw rows needs no ring
         l.nrw = l.ring = 0;
     }
