@@ -549,7 +549,7 @@ def ds4a_sparse_attn_prefill_fp8(q, q_pos, rows8, row_scale, idx, count, raw, ra
 # Paged caches
 # ----------------------------------------------------------------------------
 
-_I32, _F32, _F64, _BF16, _U8 = torch.int32, torch.float32, torch.float64, torch.bfloat16, torch.uint8
+_I32, _F32, _F64, _BF16, _F16, _U8 = torch.int32, torch.float32, torch.float64, torch.bfloat16, torch.float16, torch.uint8
 _TYPES = {torch.bfloat16: DS4A_BF16, torch.float16: DS4A_F16, torch.float32: DS4A_F32, torch.uint8: DS4A_E4M3}
 
 
@@ -724,33 +724,37 @@ def ds4a_paged_indexer_score(iq, w, ik, table, n_rows, scores, stream=None):
 def _paged_rows(q, rows, row_scale, table, n_rows, idx, count):
     """What the attention calls over paged rows share: (device, U, H, the arguments
     from n_head to n_rows, those of the list)."""
-    dev = _device_index(q, "q")
-    if q.dtype is not _BF16 or q.dim() != 3 or not q.is_contiguous():
+    dev, shape = _device_index(q, "q"), q.shape
+    if q.dtype is not _BF16 or len(shape) != 3 or shape[2] != HEAD_DIM or not q.is_contiguous():
         raise ValueError("q: contiguous bf16 [U, H, 512]")
-    U, H, width = q.shape
-    if width != HEAD_DIM:
-        raise ValueError("q: contiguous bf16 [U, H, 512]")
-    fp8 = rows.dtype is _U8
-    if not (fp8 or rows.dtype is _BF16) or rows.get_device() != dev or rows.dim() != 3 \
+    U, H, _ = shape
+    kind, shape, scale_ptr = rows.dtype, rows.shape, None
+    fp8 = kind is _U8
+    if not (fp8 or kind is _BF16) or rows.get_device() != dev or len(shape) != 3 or shape[2] != HEAD_DIM \
             or not rows.is_contiguous():
         raise ValueError("rows: contiguous bf16 or uint8 [n_pages, page_size, 512]")
-    n_pages, page_size, width = rows.shape
-    if width != HEAD_DIM:
-        raise ValueError("rows: contiguous bf16 or uint8 [n_pages, page_size, 512]")
-    if fp8 and (row_scale is None or row_scale.dtype is not _F32 or row_scale.get_device() != dev
-                or row_scale.numel() != n_pages * page_size or not row_scale.is_contiguous()):
-        raise ValueError("row_scale: contiguous float32 [n_pages, page_size]")
+    n_pages, page_size, _ = shape
+    if fp8:
+        if row_scale is None or row_scale.dtype is not _F32 or row_scale.get_device() != dev \
+                or row_scale.numel() != n_pages * page_size or not row_scale.is_contiguous():
+            raise ValueError("row_scale: contiguous float32 [n_pages, page_size]")
+        scale_ptr = row_scale.data_ptr()
     stride, max_pages = _table_stride(table, U, dev)
-    _req_ints(dev, ("n_rows", n_rows, U))
-    top_k = 0
-    if (idx is None) != (count is None):
-        raise ValueError("idx and count go together")
-    if idx is not None:
+    if idx is None:
+        if count is not None:
+            raise ValueError("idx and count go together")
+        if not _ints_ok(dev, U, n_rows):
+            _req_ints(dev, ("n_rows", n_rows, U))
+        lists = None, None, 0
+    else:
+        if count is None:
+            raise ValueError("idx and count go together")
         top_k = idx.shape[-1]
-        _req_ints(dev, ("idx", idx, U * top_k), ("count", count, U))
-    return dev, U, H, (H, q.data_ptr(), rows.data_ptr(), DS4A_E4M3 if fp8 else DS4A_BF16, row_scale.data_ptr() if fp8 else None,
-                       n_pages, page_size, table.data_ptr(), stride, max_pages, n_rows.data_ptr()), \
-        (_opt(idx), _opt(count), top_k)
+        if not (_ints_ok(dev, U, n_rows, count) and _ints_ok(dev, U * top_k, idx)):
+            _req_ints(dev, ("n_rows", n_rows, U), ("idx", idx, U * top_k), ("count", count, U))
+        lists = idx.data_ptr(), count.data_ptr(), top_k
+    return dev, U, H, (H, q.data_ptr(), rows.data_ptr(), DS4A_E4M3 if fp8 else DS4A_BF16, scale_ptr, n_pages, page_size,
+                       table.data_ptr(), stride, max_pages, n_rows.data_ptr()), lists
 
 
 def _workspace(ws, dev):
@@ -766,21 +770,26 @@ def _paged_attn(name, q, rows, table, n_rows, raw, n_raw, scale, out, lse, ws, i
     if out.dtype is not _BF16 or out.get_device() != dev or out.numel() != U * H * HEAD_DIM \
             or not out.is_contiguous():
         raise ValueError("out: contiguous bf16 [U, H, 512]")
-    if raw.dtype is not torch.float16 or raw.get_device() != dev or raw.dim() != 3 or raw.shape[1:] != (N_SWA, HEAD_DIM) \
+    shape = raw.shape
+    if raw.dtype is not _F16 or raw.get_device() != dev or len(shape) != 3 or shape[1] != N_SWA or shape[2] != HEAD_DIM \
             or not raw.is_contiguous():
         raise ValueError("raw: contiguous fp16 [n_ring, 128, 512]")
-    n_ring = raw.shape[0]
-    _req_ints(dev, ("n_raw", n_raw, U))
+    n_ring, ring_ptr, lse_ptr = shape[0], None, None
     if ring is not None:
-        _req_ints(dev, ("ring", ring, U))
-    elif n_ring < U:
-        raise ValueError("raw: a ring per unit, or give ring")
-    if lse is not None and (lse.dtype is not _F32 or lse.get_device() != dev or lse.numel() != U * H
-                            or not lse.is_contiguous()):
-        raise ValueError("lse: contiguous float32 [U, H]")
-    ws_ptr, ws_bytes = _workspace(ws, dev)
-    _launch(dev, stream, name, *lead, *lists, raw.data_ptr(), n_ring, _opt(ring), n_raw.data_ptr(), scale,
-            out.data_ptr(), _opt(lse), U, ws_ptr, ws_bytes)
+        if not _ints_ok(dev, U, n_raw, ring):
+            _req_ints(dev, ("n_raw", n_raw, U), ("ring", ring, U))
+        ring_ptr = ring.data_ptr()
+    else:
+        if not _ints_ok(dev, U, n_raw):
+            _req_ints(dev, ("n_raw", n_raw, U))
+        if n_ring < U:
+            raise ValueError("raw: a ring per unit, or give ring")
+    if lse is not None:
+        if lse.dtype is not _F32 or lse.get_device() != dev or lse.numel() != U * H or not lse.is_contiguous():
+            raise ValueError("lse: contiguous float32 [U, H]")
+        lse_ptr = lse.data_ptr()
+    _launch(dev, stream, name, *lead, *lists, raw.data_ptr(), n_ring, ring_ptr, n_raw.data_ptr(), scale, out.data_ptr(),
+            lse_ptr, U, *_workspace(ws, dev))
 
 
 def ds4a_paged_attn_decode(q, rows, table, n_rows, raw, n_raw, scale, out, lse=None, ws=None, idx=None, count=None,
